@@ -335,10 +335,137 @@ pq_status pq_w4a4_gemm_launch_count(int64_t T, int64_t N, int64_t D, int* launch
 pq_status pq_w4a4_gemm_launch_count_g(int64_t T, int64_t N, int64_t D, int g, int* launches);
 
 /*
+ * 8-bit products: one symmetric scale per token and per output channel.  ParoQuant page §4.1 keeps in
+ * 8 bits what 4 bits lose; here a whole layer (the down projection, the output head) does.
+ *
+ * pq_quant_rows8 — rows of bf16 to signed 8-bit codes, activations and weights alike:
+ *   y = x H_g / sqrt(g) per block of g channels (g = 64, 128, 256; g = 0: y = x), scales[t] =
+ *   max|y[t]| / 127 over the whole row, codes = RNE(y / scale) in -127..127.  A row whose maximum is
+ *   below 1e-36 counts as zero (scale 0, codes 0).  H is symmetric, so rotated activations against
+ *   weights rotated with the same g leave the product unchanged before quantisation.
+ *   X       device bf16 [T][ldx] (first D columns used), ldx >= D, ldx % 8 == 0; finite.
+ *   D       16..65536, a multiple of 16 and of g.  T >= 1.
+ *   codes   device int8 [T][D];  scales device float32 [T] (both dense, 16-byte aligned).
+ */
+pq_status pq_quant_rows8(const void* X, int64_t T, int64_t D, int64_t ldx, int g, int8_t* codes,
+                         float* scales, void* stream);
+
+/*
+ * pq_w8a8_gemm — Y[t][n] = scales_A[t] * scales_W[n] * d[t][n], d = sum_k codes_A[t][k] codes_W[n][k],
+ *   exact in int32 for any codes in -128..127 (D <= 65536: |d| <= 2^30); then converted to float32
+ *   (one rounding above 2^24), multiplied with the two scales in float32 and stored.
+ *   codes_A int8 [T][D], scales_A float32 [T], codes_W int8 [N][D], scales_W float32 [N]: device, dense.
+ *   T, N >= 1 (any N; no multiple is asked), D 16..65536 and a multiple of 16.  Scales must be finite.
+ *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense.  No scratch, one launch.
+ *
+ * pq_w8a8_linear — pq_quant_rows8(X, T, D, ldx, g, codes_A, scales_A) followed by pq_w8a8_gemm, in one
+ *   call: the product is launched as a programmatic dependent and its first weight loads overlap the
+ *   quantisation.  codes_A and scales_A are caller-owned and written.  codes_W and scales_W must be
+ *   complete when the call is made (written by work enqueued on `stream` before it, or earlier); Y
+ *   must not overlap X, codes_A or scales_A.
+ */
+pq_status pq_w8a8_gemm(const int8_t* codes_A, const float* scales_A, const int8_t* codes_W, const float* scales_W,
+                       int64_t T, int64_t N, int64_t D, void* Y, pq_out_dtype out_dtype, void* stream);
+pq_status pq_w8a8_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g, int8_t* codes_A, float* scales_A,
+                         const int8_t* codes_W, const float* scales_W, int64_t N, void* Y, pq_out_dtype out_dtype,
+                         void* stream);
+
+/*
+ * The cache of keys and values in 4 bits (RRS page, set-up of the experiments: the cache quantised in
+ * groups of 128, here one group per head), in pages:
+ *   k_codes, v_codes    device uint8 [pages][heads][page_size][head_dim / 2], nibbles as everywhere.
+ *   k_scales, v_scales  device float32 [pages][heads][page_size].
+ *   A slot is page * page_size + place in the page.  page_size 16, 32, 64, 128 or 256; head_dim 64 or
+ *   128; heads 1..1024; all four 16-byte aligned and owned by the caller.
+ *   flags  PQ_KV4_ROTATE_K: keys (and queries) are held rotated, k H / sqrt(head_dim), after the
+ *          position rotation (OSTQuant page: Hadamard on Q and K after RoPE); q . k is unchanged.
+ *          PQ_KV4_ROTATE_V: values are held rotated; pq_kv4_attention rotates its output back.
+ *
+ * Indices are read on the device.  One that lies outside its table (a slot or page beyond the cache, a
+ * position beyond the rope table, a length beyond the block table) is never followed: the access is
+ * skipped as told below and the next pq_check_status returns PQ_ERR_INVALID_ARG.
+ */
+#define PQ_KV4_ROTATE_K 0x1u
+#define PQ_KV4_ROTATE_V 0x2u
+typedef struct pq_kv4_cache {
+  uint8_t* k_codes;
+  float* k_scales;
+  uint8_t* v_codes;
+  float* v_scales;
+  int64_t pages;
+  int32_t page_size;
+  int32_t heads;
+  int32_t head_dim;
+  uint32_t flags;
+} pq_kv4_cache;
+
+/*
+ * pq_kv4_append — one pass from a projection's output to attention's operands.  Per token t and head:
+ *   queries, keys: x <- x / sqrt(mean(x^2) + eps) * norm weight           (if q_norm / k_norm is given)
+ *   queries, keys: the first rope_dim channels turned by the token's position, pairs (i, i + rope_dim/2),
+ *                  or (2i, 2i + 1) with PQ_KV4_INTERLEAVED: (a, b) -> (a cos - b sin, b cos + a sin)
+ *   rotated caches: y = x H / sqrt(head_dim)  (queries and keys: ROTATE_K; values: ROTATE_V)
+ *   queries: Q_out = bf16(y).   Keys, values: scale = max|y| / 7, codes = RNE(y / scale), into the slot
+ *   (a head whose maximum is below 1e-36 counts as zero: scale 0, codes 0).
+ *   All in float32, each product and sum rounded on its own; nothing but Q_out is rounded to bf16.
+ *   Q, K, V     device bf16 [T][heads_q | heads | heads][head_dim], row strides ldq, ldk, ldv (elements,
+ *               multiples of 4; 8-byte aligned): columns of one projection's output will do.
+ *   heads_q     a multiple of cache->heads.
+ *   q_norm, k_norm  device bf16 [head_dim] or NULL each.
+ *   rope        device float32 [rope_rows][rope_dim]: the cosines of a position, then its sines; or NULL.
+ *               rope_dim a multiple of 8, <= head_dim (ignored without a table).
+ *   positions   device int32 [T] (may be NULL without a table).  A position outside the table: Q_out of
+ *               the token is 0 and nothing is cached for it.
+ *   slots       device int64 [T]: where each token goes.  Negative: nowhere (padding; Q_out is still
+ *               written).  Slots must be distinct: of a repeated one, codes and scale may come from
+ *               different tokens.  Slots not listed stay as they were.
+ *   Q_out       device bf16 [T][heads_q][head_dim], dense; may not overlap Q, K or V.
+ *
+ * pq_kv4_read — cached rows back: K_out[t], V_out[t] (device bf16 [T][heads][head_dim]) = bf16(code *
+ *   scale) at slots[t], in the cache's own (rotated) basis; rows of negative slots, and of slots outside
+ *   the cache, become 0.
+ */
+#define PQ_KV4_INTERLEAVED 0x1u
+pq_status pq_kv4_append(const pq_kv4_cache* cache, const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                        const void* V, int64_t ldv, int64_t T, int heads_q, const void* q_norm, const void* k_norm,
+                        float eps, const float* rope, int64_t rope_rows, int rope_dim, const int32_t* positions,
+                        const int64_t* slots, uint32_t flags, void* Q_out, void* stream);
+pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T, void* K_out, void* V_out,
+                      void* stream);
+
+/*
+ * pq_kv4_attention — causal attention of the newest tokens of B sequences over the cache.  Sequence b
+ *   has seq_lens[b] cached tokens, its new ones (already appended) being the last; rows q_start[b] ..
+ *   q_start[b + 1] - 1 of Q are theirs.  Row i of q_len sits at position p = seq_lens[b] - q_len + i and
+ *   sees the tokens t <= p, with a window also t > p - window:
+ *     s_t = scale * (q . k_t),  O = softmax(s) v   (times H / sqrt(head_dim) for ROTATE_V),
+ *   k_t, v_t = code * scale of the slot block_table[b][t / page_size] * page_size + t % page_size; query
+ *   head h reads key/value head h / (heads_q / heads).  A row that sees nothing becomes 0.
+ *   Codes enter the products exactly; scores, maxima, sums and the output run in float32; the queries
+ *   are bf16 and the probabilities are rounded to bf16 for the second product.
+ *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
+ *   q_start     device int32 [B + 1], ascending, within 0..T.  Rows outside every sequence stay as they were.
+ *   seq_lens    device int32 [B];  block_table device int32 [B][table_width].  Entries behind a
+ *               sequence's last page are not read.  A listed page outside the cache counts as 16-token
+ *               pieces that nobody sees; a length beyond table_width pages is cut to them.
+ *   max_q, max_len  upper bounds of the sequences' new tokens and lengths (>= 1): they size the launch.
+ *               A sequence beyond them is still computed in full, only more slowly.
+ *   window      0: none.
+ *   O           device bf16 [T][heads_q][head_dim], row stride ldo (a multiple of 8).
+ *   Scratch: when long contexts are cut over several blocks, float32 partial results of
+ *   4 (head_dim + 2) bytes per row, query head and piece, from the library's stream-ordered pool.
+ */
+pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q, const int32_t* q_start,
+                           const int32_t* seq_lens, const int32_t* block_table, int64_t table_width, int64_t B,
+                           int64_t T, int64_t max_q, int64_t max_len, float scale, int64_t window, void* O,
+                           int64_t ldo, void* stream);
+
+/*
  * pq_check_status — synchronises `stream`, then reads and clears the device status words
  * (the plan's, if plan != NULL, and the GEMM's).  Returns PQ_ERR_TIMEOUT if a bounded
  * device-side wait gave up since the last check (the affected output is incomplete),
- * PQ_ERR_CUDA if the stream reports an error, PQ_OK otherwise.
+ * PQ_ERR_INVALID_ARG if a cache index was out of range (see pq_kv4_cache), PQ_ERR_CUDA if the
+ * stream reports an error, PQ_OK otherwise.
  */
 pq_status pq_check_status(const pq_plan* plan, void* stream);
 

@@ -629,6 +629,8 @@ pq_status make_operand_map(CUtensorMap* map, const uint8_t* base, int64_t rows, 
   return PQ_OK;
 }
 
+}  // namespace
+
 // Library-owned stream-ordered pool per device.  Its release threshold is unlimited, so memory
 // freed at the end of one call is reused by the next instead of being unmapped at every
 // synchronisation (which made each call pay for fresh page mappings).
@@ -659,6 +661,8 @@ cudaError_t scratch_pool(cudaMemPool_t* out) {
   *out = pools[dev];
   return cudaSuccess;
 }
+
+namespace {
 
 // CTA pairs (clusters of 2) of w4a4_gemm_kernel resident at once on the current device: one
 // per SM pair when every pair can host one.

@@ -20,6 +20,7 @@ constexpr int kSmoothBlock = 128;      // rows per runtime-smoothing block
 
 // Device status word bits.
 #define PQ_DEV_TIMEOUT 0x1u
+#define PQ_DEV_BAD_INDEX 0x2u   // a slot, page, position or length lay outside its table (the access was skipped)
 
 struct pq_plan {
   pq_kind kind;
@@ -202,6 +203,15 @@ pq_status gemm_run_linear(transform_launcher transform, const void* ctx, const u
                           const uint8_t* codes_W, const float* scales_W, int64_t T, int64_t N, int64_t D, int g,
                           void* Y, pq_out_dtype out_dtype, cudaStream_t stream);
 pq_status gemm_read_and_clear_status(unsigned int* bits);
+// The current device's stream-ordered scratch pool (gemm.cu).
+cudaError_t scratch_pool(cudaMemPool_t* out);
+// 8-bit codes with one scale a row (quant8.cu) and their product (w8a8.cu).  pdl: launch the product as
+// the programmatic dependent of the kernel before it on `stream`, the one that writes codes_A and scales_A.
+cudaError_t launch_quant_rows8(const void* X, int64_t rows, int D, int64_t ldx, int g, int8_t* codes, float* scales,
+                               cudaStream_t stream);
+pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t* codes_W, const float* scales_W,
+                      int64_t T, int64_t N, int64_t D, void* Y, pq_out_dtype out_dtype, cudaStream_t stream,
+                      bool pdl);
 // Launches the bounded-wait diagnostic (a wait that cannot complete, limited to limit_ns).
 pq_status gemm_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream);
 // Device address of the GEMM's status word on the current device.

@@ -1,0 +1,613 @@
+// Attention over the paged 4-bit cache for a few query rows a sequence (decode; sm_100a).
+//
+// Per query row (token at position p, query head) and cached token t of its key/value head, t <= p (and t > p - window):
+//   s_t = scale (q . kc_t) ks_t,  P = softmax(s),  o = sum_t P_t vs_t vc_t   (then o H / sqrt(hd) for rotated values)
+// kc, vc: 4-bit codes, ks, vs: their scales.  The codes are exact in bf16, so the products run on the tensor cores on
+// the codes themselves; ks multiplies the finished dot product and vs the probability, both in float32.
+//
+// The cache is read once for all query rows of a key/value head (the group's heads x the sequence's new tokens), 64
+// bytes a token for keys and as much for values, and HBM bounds the kernel.  A warp owns blocks of 64 tokens:
+//   - keys are the A operand (16 tokens x 16 channels), the query rows the 8-column B operand: a thread's 16-byte
+//     load of one token is its share of the A operands of all 8 channel steps, because the channels of a dot product
+//     may be taken in any order as long as the queries follow the same one (set up once).  No shared memory.
+//   - the scores come out tokens x rows; the softmax runs over the warp's registers with one running maximum per row;
+//   - probabilities go back in as B operand (movmatrix transposes 8 x 8 of them) against the values as A operand
+//     (16 channels x 16 tokens): two tokens' words are byte-permuted together, then masked.
+//   - keys become bf16, as the queries are: nibble ^ 8 under 0x4300 is 128 + (code + 8), and the offset 136 leaves
+//     with the query's sum (136 sum(q) is subtracted from the score, in float32).
+//   - values become fp16: nibble ^ 8 under 0x6400 is 1024 + (code + 8), and 1032 is subtracted from the operand
+//     itself, exactly, since a long sum of probabilities times 1032 would drown the result.
+//   - the loads of the next block are issued as soon as this block's registers are free.
+// The second product takes P_t vs_t / mv as fp16, mv the largest scale of the values that the row has seen so far
+// (the running output is rescaled when it grows, as for the maximum): at most 1, so it neither overflows nor, where it
+// matters, leaves the normal range; rounding it costs half a step of fp16, 2^-11, an eighth of what bf16 would.
+// Maxima, sums and the running output are float32.
+//
+// A block's warps join their maxima, sums and outputs through shared memory.  Long contexts are cut into chunks of
+// tokens, one block each; a second kernel joins the chunks' float32 partial results.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "internal.h"
+#include "kv4.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace pq {
+namespace {
+
+constexpr int AT_WARPS = 4;
+constexpr int AT_BLOCK = 64;            // tokens a warp takes at a time
+constexpr int AT_TILES = AT_BLOCK / 16;
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
+                                         const uint32_t a3, const uint32_t b0, const uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
+                                        const uint32_t a3, const uint32_t b0, const uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code.
+__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) {
+  return ((x >> s) & 0x000F000Fu) ^ 0x43084308u;
+}
+
+// The same two nibbles -> two fp16 codes (1032 + code, less 1032: exact).
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, int s) {
+  const uint32_t b = ((x >> s) & 0x000F000Fu) ^ 0x64086408u, k = 0x64086408u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 2^x; results below the smallest normal number become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A value scale as far as it counts toward the largest one: not if it is infinite (NaN drops out of fmaxf).
+__device__ __forceinline__ float finite_or_0(float x) {
+  const float y = fabsf(x);
+  return y < 3.0e38f ? y : 0.0f;
+}
+__device__ __forceinline__ float inverse_or_0(float x) { return x > 1.2e-38f ? 1.0f / x : 0.0f; }
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+template <int W>
+__device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
+  if constexpr (W == 4) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else if constexpr (W == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    x[0] = v.x, x[1] = v.y;
+  } else {
+    x[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+// One query row's output from its un-normalised float32 sums: lane l of the warp holds channels E l .. E l + E - 1
+// (E = HD / 32).  Divides by the sum of the probabilities (none: 0), rotates back, stores bf16.
+template <int HD>
+__device__ __forceinline__ void finish_row(float (&o)[HD / 32], float l, int rotate, uint16_t* dst, int lane) {
+  constexpr int E = HD / 32;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (rotate) {
+    if constexpr (E == 4) {
+      const float p0 = o[0] + o[1], p1 = o[0] - o[1], p2 = o[2] + o[3], p3 = o[2] - o[3];
+      o[0] = p0 + p2, o[1] = p1 + p3, o[2] = p0 - p2, o[3] = p1 - p3;
+    } else {
+      const float p0 = o[0] + o[1], p1 = o[0] - o[1];
+      o[0] = p0, o[1] = p1;
+    }
+#pragma unroll
+    for (int b = 1; b < 32; b <<= 1)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float p = __shfl_xor_sync(0xffffffffu, o[i], b);
+        o[i] = (lane & b) ? p - o[i] : o[i] + p;
+      }
+  }
+  const float f = rotate ? inv * (HD == 128 ? 0.08838834764831845f : 0.125f) : inv;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+  else
+    *reinterpret_cast<uint32_t*>(dst + 2 * lane) = pack_bf16(o[0] * f, o[1] * f);
+}
+
+// Partial results of one chunk: un-normalised output [HD], then maximum (log2 domain) and sum, per (token, query head).
+struct Partials {
+  float* o;       // [chunk][T * heads_q][HD]
+  float2* ml;     // [chunk][T * heads_q]
+  int chunks;     // 1: no partials, the output is written directly
+  int chunk_len;  // tokens, a multiple of AT_BLOCK
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
+                                                                int row_tiles) {
+  constexpr int R = 8 * NT;              // query rows per tile
+  constexpr int KS = HD / 16;            // channel steps of the first product = channel tiles of the second
+  constexpr int KW = HD / 32;            // words of a token's key a thread holds
+  constexpr int VW = HD / 64;            // words of a token's value a thread holds
+  constexpr int HB = HD / 2;             // bytes a token
+  __shared__ float sm_o[AT_WARPS][R][HD];
+  __shared__ float sm_m[AT_WARPS][R], sm_l[AT_WARPS][R];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int b = blockIdx.z, kvh = blockIdx.y;
+  const int chunk = blockIdx.x % part.chunks;
+  const int group = a.heads_q / a.cache.heads;
+  const int q0 = max(0, a.q_start[b]);
+  const int qlen = min((int)a.T, a.q_start[b + 1]) - q0;
+  const int ps = a.cache.page_shift;
+  const int rows = qlen * group;
+  if (rows <= 0) return;
+  int n = max(0, a.seq_lens[b]);
+  {
+    const int64_t cap = (int64_t)a.table_width << ps;
+    if (n > cap) {
+      n = (int)cap;
+      if (threadIdx.x == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
+    }
+  }
+  const int32_t* table = a.table + b * a.table_stride;
+  const float c_log2 = a.scale * kLog2e;
+
+  for (int rt = blockIdx.x / part.chunks; rt * R < rows; rt += row_tiles) {
+    const int r0 = rt * R;
+    // positions of the tile's first and last row, and the tokens the tile sees
+    const int p_first = n - qlen + r0 / group, p_last = n - qlen + min(rows - 1, r0 + R - 1) / group;
+    const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+    const int hi = min(n, p_last + 1);
+    // this chunk's part of [lo, hi); chunk borders are fixed multiples of chunk_len
+    const int c_lo = part.chunks > 1 ? max(lo, chunk * part.chunk_len) : lo;
+    const int c_hi = part.chunks > 1 && chunk < part.chunks - 1 ? min(hi, (chunk + 1) * part.chunk_len) : hi;
+
+    // ---- query operands: B fragment of step (w, h): channels (d, d + 4), (d + 1, d + 5), d = 8 (KW t + w) + 2 h
+    uint32_t qb[NT][KS][2];
+    float bq[NT][2];                     // 136 * sum of the query, for this thread's two columns
+    int pos[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = r0 + 8 * nt + g;
+      uint32_t x[KW][4];
+      if (r < rows) {
+        const uint16_t* src = a.Q + (int64_t)(q0 + r / group) * a.ldq + (kvh * group + r % group) * HD + 8 * KW * t;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) load_words<4>(x[w], reinterpret_cast<const uint8_t*>(src + 8 * w));
+      } else {
+#pragma unroll
+        for (int w = 0; w < KW; ++w) x[w][0] = x[w][1] = x[w][2] = x[w][3] = 0u;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          qb[nt][2 * w + h][0] = __byte_perm(x[w][h], x[w][h + 2], 0x5410);   // channels 2h, 2h + 4
+          qb[nt][2 * w + h][1] = __byte_perm(x[w][h], x[w][h + 2], 0x7632);   // channels 2h + 1, 2h + 5
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          sum += __uint_as_float(x[w][k] << 16) + __uint_as_float(x[w][k] & 0xFFFF0000u);
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        bq[nt][e] = 136.0f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        pos[nt][e] = n - qlen + min(rows - 1, r0 + 8 * nt + 2 * t + e) / group;
+      }
+    }
+
+    float o[NT][KS][4];
+    float m[NT][2], l[NT][2], mv[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = mv[nt][0] = mv[nt][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
+    }
+
+    // ---- the warp's blocks of 64 tokens
+    uint32_t kx[AT_TILES][2][KW], vx[AT_TILES][4][VW];
+    float ks[AT_TILES][2], vs[AT_TILES][2];
+    int lim[AT_TILES];                   // tokens of the 16-token tile that exist
+    int64_t base[AT_TILES];              // first token's row in the cache
+    auto locate = [&](int tok0) {
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) {
+        const int tok = tok0 + 16 * i;
+        int k = min(16, n - tok);
+        int64_t at = 0;
+        if (k > 0) {
+          const int page = table[tok >> ps];
+          if (page < 0 || page >= a.cache.pages) {
+            k = 0;
+            if (lane == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
+          } else {
+            at = (((int64_t)page * a.cache.heads + kvh) << ps) + (tok & ((1 << ps) - 1));
+          }
+        }
+        lim[i] = max(k, 0);
+        base[i] = at;
+      }
+    };
+    auto load_k = [&]() {
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (g + 8 * h < lim[i]) {
+            const int64_t row = base[i] + g + 8 * h;
+            load_words<KW>(kx[i][h], a.cache.k_codes + row * HB + 4 * KW * t);
+            ks[i][h] = __ldg(a.cache.k_scales + row);
+          } else {
+#pragma unroll
+            for (int w = 0; w < KW; ++w) kx[i][h][w] = 0u;
+            ks[i][h] = 0.0f;
+          }
+        }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
+          if (tok < lim[i]) {
+            load_words<VW>(vx[i][k], a.cache.v_codes + (base[i] + tok) * HB + 4 * VW * g);
+          } else {
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vx[i][k][w] = 0u;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) vs[i][h] = g + 8 * h < lim[i] ? __ldg(a.cache.v_scales + base[i] + g + 8 * h) : 0.0f;
+      }
+    };
+
+    const int first = (c_lo & ~(AT_BLOCK - 1)) + AT_BLOCK * warp;
+    if (first < c_hi) {
+      locate(first);
+      load_k();
+      load_v();
+    }
+    for (int tok0 = first; tok0 < c_hi; tok0 += AT_BLOCK * AT_WARPS) {
+      int cur_lim[AT_TILES];
+      bool whole = tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
+                   (a.window <= 0 || tok0 > p_last - a.window);
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) {
+        cur_lim[i] = lim[i];
+        whole = whole && lim[i] == 16;
+      }
+      float s[AT_TILES][NT][4];
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a0 = biased_pair(kx[i][0][w], 8 * h), a2 = biased_pair(kx[i][0][w], 8 * h + 4);
+            const uint32_t a1 = biased_pair(kx[i][1][w], 8 * h), a3 = biased_pair(kx[i][1][w], 8 * h + 4);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_bf16(s[i][nt], a0, a1, a2, a3, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
+          }
+        const float f0 = ks[i][0] * c_log2, f1 = ks[i][1] * c_log2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[i][nt][0] = (s[i][nt][0] - bq[nt][0]) * f0;
+          s[i][nt][1] = (s[i][nt][1] - bq[nt][1]) * f0;
+          s[i][nt][2] = (s[i][nt][2] - bq[nt][0]) * f1;
+          s[i][nt][3] = (s[i][nt][3] - bq[nt][1]) * f1;
+        }
+      }
+      // the next block's keys
+      const int next = tok0 + AT_BLOCK * AT_WARPS;
+      if (next < c_hi) {
+        locate(next);
+        load_k();
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int tok = tok0 + 16 * i + 8 * h + g;
+            const bool in = 8 * h + g < cur_lim[i] && tok >= c_lo && tok < c_hi;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (!(in && tok <= pos[nt][e] && (a.window <= 0 || tok > pos[nt][e] - a.window)))
+                  s[i][nt][2 * h + e] = -INFINITY;
+          }
+      }
+      // the block's largest value scale
+      float v_block = 0.0f;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < AT_TILES; ++i) v_block = fmaxf(v_block, fmaxf(finite_or_0(vs[i][0]), finite_or_0(vs[i][1])));
+        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 4));
+        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 8));
+        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 16));
+      }
+      uint32_t pb[AT_TILES][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float alpha[2], mu[2], rmv[2];
+        bool grew = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = m[nt][e];
+#pragma unroll
+          for (int i = 0; i < AT_TILES; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mu[e] = x == -INFINITY ? 0.0f : x;
+          alpha[e] = ex2(m[nt][e] - mu[e]);
+          // the row's own largest value scale: in a block with hidden tokens, over those it sees
+          float y = v_block;
+          if (!whole) {
+#pragma unroll
+            for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (s[i][nt][2 * h + e] != -INFINITY) y = fmaxf(y, finite_or_0(vs[i][h]));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+          }
+          grew = grew || x > m[nt][e] || y > mv[nt][e];
+          m[nt][e] = x;
+          y = fmaxf(y, mv[nt][e]);
+          rmv[e] = inverse_or_0(y);
+          l[nt][e] *= alpha[e];
+          alpha[e] *= mv[nt][e] * rmv[e];
+          mv[nt][e] = y;
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            o[nt][j][0] *= alpha[0];
+            o[nt][j][1] *= alpha[1];
+            o[nt][j][2] *= alpha[0];
+            o[nt][j][3] *= alpha[1];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float s0 = s[i][nt][2 * h], s1 = s[i][nt][2 * h + 1];
+            const float p0 = ex2(s0 - mu[0]), p1 = ex2(s1 - mu[1]);
+            l[nt][0] += p0;
+            l[nt][1] += p1;
+            // a hidden token's value scale may be anything: select, do not multiply
+            const float w0 = whole || s0 != -INFINITY ? p0 * (vs[i][h] * rmv[0]) : 0.0f;
+            const float w1 = whole || s1 != -INFINITY ? p1 * (vs[i][h] * rmv[1]) : 0.0f;
+            pb[i][nt][h] = movmatrix_trans(pack_f16(w0, w1));
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          // words of tokens 2t and 2t + 1 (and + 8), their low or high 16 bits side by side
+          uint32_t x[VW][2];
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            x[w][0] = __byte_perm(vx[i][0][w], vx[i][1][w], half ? 0x7632 : 0x5410);
+            x[w][1] = __byte_perm(vx[i][2][w], vx[i][3][w], half ? 0x7632 : 0x5410);
+          }
+          if constexpr (VW == 2) {
+            // channel tile j: rows g <-> channel 16 g + j, rows g + 8 <-> 16 g + 8 + j
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int j = 4 * half + k;
+              const uint32_t a0 = code_pair(x[0][0], 4 * k), a1 = code_pair(x[1][0], 4 * k);
+              const uint32_t a2 = code_pair(x[0][1], 4 * k), a3 = code_pair(x[1][1], 4 * k);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][j], a0, a1, a2, a3, pb[i][nt][0], pb[i][nt][1]);
+            }
+          } else {
+            // channel tile j: rows g <-> channel 8 g + 2 j, rows g + 8 <-> 8 g + 2 j + 1
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = 2 * half + k;
+              const uint32_t a0 = code_pair(x[0][0], 8 * k), a1 = code_pair(x[0][0], 8 * k + 4);
+              const uint32_t a2 = code_pair(x[0][1], 8 * k), a3 = code_pair(x[0][1], 8 * k + 4);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][j], a0, a1, a2, a3, pb[i][nt][0], pb[i][nt][1]);
+            }
+          }
+        }
+      if (next < c_hi) load_v();
+    }
+
+    // ---- join the block's warps
+    __syncthreads();                     // the previous row tile's reads are done
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          o[nt][j][e] *= mv[nt][e];
+          o[nt][j][2 + e] *= mv[nt][e];
+        }
+        float x = l[nt][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        const int r = 8 * nt + 2 * t + e;
+        if (g == 0) {
+          sm_m[warp][r] = m[nt][e];
+          sm_l[warp][r] = x;
+        }
+        float* dst = &sm_o[warp][r][(HD / 8) * g];
+        if constexpr (VW == 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+              *reinterpret_cast<float4*>(dst + 8 * h + j) =
+                  make_float4(o[nt][j][2 * h + e], o[nt][j + 1][2 * h + e], o[nt][j + 2][2 * h + e], o[nt][j + 3][2 * h + e]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; j += 2)
+            *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nt][j][e], o[nt][j][2 + e], o[nt][j + 1][e], o[nt][j + 1][2 + e]);
+        }
+      }
+    __syncthreads();
+    for (int r = warp; r < R && r0 + r < rows; r += AT_WARPS) {
+      constexpr int E = HD / 32;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) mx = fmaxf(mx, sm_m[w][r]);
+      const float mu = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f, y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) {
+        const float f = ex2(sm_m[w][r] - mu);
+        sum = fmaf(sm_l[w][r], f, sum);
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w][r][E * lane + i], f, y[i]);
+      }
+      const int64_t token = q0 + (r0 + r) / group;
+      const int head = kvh * group + (r0 + r) % group;
+      if (part.chunks == 1) {
+        finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + head * HD, lane);
+      } else {
+        const int64_t row = ((int64_t)chunk * a.T + token) * a.heads_q + head;
+        if (lane == 0) part.ml[row] = make_float2(mx, sum);
+        if (mx != -INFINITY || sum != 0.0f) {
+#pragma unroll
+          for (int i = 0; i < E; ++i) part.o[row * HD + E * lane + i] = y[i];
+        }
+      }
+    }
+  }
+}
+
+// Joins the chunks of each query row; one warp a row.  Rows of tokens outside every sequence stay as they were.
+template <int HD>
+__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a, const Partials part) {
+  constexpr int E = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int64_t total = a.T * a.heads_q;
+  if (row >= total) return;
+  const int64_t token = row / a.heads_q;
+  if (token < a.q_start[0] || token >= a.q_start[a.B]) return;
+  float mx = -INFINITY;
+  for (int c = 0; c < part.chunks; ++c) mx = fmaxf(mx, part.ml[c * total + row].x);
+  const float mu = mx == -INFINITY ? 0.0f : mx;
+  float sum = 0.0f, y[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) y[i] = 0.0f;
+  for (int c = 0; c < part.chunks; ++c) {
+    const float2 ml = part.ml[c * total + row];
+    if (ml.x == -INFINITY && ml.y == 0.0f) continue;          // nothing seen: its output was not written
+    const float f = ex2(ml.x - mu);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = fmaf(part.o[(c * total + row) * HD + E * lane + i], f, y[i]);
+  }
+  finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + (row - token * a.heads_q) * HD, lane);
+}
+
+template <int HD, int NT>
+cudaError_t launch_rows(const Kv4AttnArgs& a, const Partials& part, int row_tiles, cudaStream_t stream) {
+  const dim3 grid((unsigned)(part.chunks * row_tiles), (unsigned)a.cache.heads, (unsigned)a.B);
+  kv4_rows_kernel<HD, NT><<<grid, 32 * AT_WARPS, 0, stream>>>(a, part, row_tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream) {
+  const int group = a.heads_q / a.cache.heads;
+  const int64_t max_rows = max_q * group;
+  const int nt = max_rows > 8 ? 2 : 1;
+  const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
+  // Chunks: about four blocks for each multiprocessor when every sequence has max_len tokens, at least 256 tokens each.
+  const int64_t units = (int64_t)a.B * a.cache.heads * row_tiles;
+  const int64_t want = (4 * (int64_t)device_sm_count() + units - 1) / units;
+  const int64_t most = (max_len + 255) / 256;
+  Partials part = {};
+  part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
+  part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + AT_BLOCK - 1) / AT_BLOCK * AT_BLOCK);
+  void* ws = nullptr;
+  cudaError_t e;
+  if (part.chunks > 1) {
+    const size_t rows = (size_t)part.chunks * a.T * a.heads_q;
+    const size_t bytes = rows * (a.cache.head_dim * sizeof(float) + sizeof(float2));
+    cudaMemPool_t pool = nullptr;
+    e = scratch_pool(&pool);
+    if (e != cudaSuccess) return cuda_fail(e, "scratch memory pool");
+    e = cudaMallocFromPoolAsync(&ws, bytes, pool, stream);
+    if (e != cudaSuccess) {
+      set_error("cudaMallocFromPoolAsync(%zu bytes of attention workspace): %s", bytes, cudaGetErrorString(e));
+      return PQ_ERR_ALLOC;
+    }
+    part.o = static_cast<float*>(ws);
+    part.ml = reinterpret_cast<float2*>(part.o + rows * a.cache.head_dim);
+  }
+  const bool wide = a.cache.head_dim == 128;
+  e = wide ? (nt == 1 ? launch_rows<128, 1>(a, part, row_tiles, stream) : launch_rows<128, 2>(a, part, row_tiles, stream))
+           : (nt == 1 ? launch_rows<64, 1>(a, part, row_tiles, stream) : launch_rows<64, 2>(a, part, row_tiles, stream));
+  if (e == cudaSuccess && part.chunks > 1) {
+    const unsigned grid = (unsigned)((a.T * a.heads_q + 3) / 4);
+    if (wide) kv4_join_kernel<128><<<grid, 128, 0, stream>>>(a, part);
+    else kv4_join_kernel<64><<<grid, 128, 0, stream>>>(a, part);
+    e = cudaGetLastError();
+  }
+  pq_status st = cuda_fail(e, "pq_kv4_attention launch");
+  if (ws) {
+    e = cudaFreeAsync(ws, stream);
+    if (st == PQ_OK && e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync(attention workspace)");
+  }
+  return st;
+}
+
+}  // namespace pq

@@ -662,5 +662,9 @@ extern "C" pq_status pq_check_status(const pq_plan* plan, void* stream) {
     set_error("a device-side bounded wait timed out (status bits 0x%x)", bits);
     return PQ_ERR_TIMEOUT;
   }
+  if (bits & PQ_DEV_BAD_INDEX) {
+    set_error("a slot, page, position or length lay outside its cache or table and was skipped (status bits 0x%x)", bits);
+    return PQ_ERR_INVALID_ARG;
+  }
   return PQ_OK;
 }

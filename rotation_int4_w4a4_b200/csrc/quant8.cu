@@ -1,0 +1,131 @@
+// Rows of bf16 -> signed 8-bit codes with one symmetric scale a row (sm_100a):
+//   y = x H_g / sqrt(g) per block of g channels (g = 64, 128 or 256; g = 0: y = x),
+//   scale = max|y| / 127, codes = RNE(y / scale) in -127..127.
+// The row scale of the RRS page's set-up (per-token activation quantisation) at 8 bits (ParoQuant
+// page §4.1 keeps in 8 bits what 4 bits lose); weights take the same pass, one scale an output channel.
+//
+// The scale needs the whole row before the first code, so a row stays in registers between its one
+// read and its one write: 3 bytes move per element (2 in, 1 out) and HBM bounds the kernel.  A
+// thread holds SLOTS pieces of 8 channels, piece s of thread t at channel 8 (t + s TPR), so every
+// load and store instruction of a warp covers contiguous memory (512 and 256 bytes).  Three
+// butterfly stages of the Hadamard transform run inside the thread, the other 3 to 5 across the
+// g / 8 lanes of the block by xor shuffles (float32 sums, the factor 1/sqrt(g) goes into the scale:
+// the codes do not depend on it).
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace pq {
+namespace {
+
+constexpr int Q8_SLOTS = 4;           // 8-channel pieces a thread holds for rows up to 32 * 1024 channels
+constexpr int Q8_SLOTS_LONG = 8;      // for longer rows
+constexpr int Q8_BLOCK = 256;         // threads a block gets by stacking short rows
+// Rows whose maximum is below this are taken as zero: 127 / max would overflow float32.
+constexpr float kQ8Tiny = 1e-36f;
+
+template <int G, int SLOTS>
+__global__ void __launch_bounds__(1024) quant_rows8_kernel(const uint16_t* __restrict__ X, int64_t rows, int64_t ldx,
+                                                           int D, int tpr, float scale_mult,
+                                                           int8_t* __restrict__ codes, float* __restrict__ scales) {
+  __shared__ float red[32];
+  ptx::griddep_launch_dependents();
+  const int sub = threadIdx.x / tpr;                       // row within the block
+  const int t = threadIdx.x - sub * tpr;
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + sub;
+  const bool live = row < rows;
+  const int pieces = D / 8;
+  const uint4* src = reinterpret_cast<const uint4*>(X + (live ? row : 0) * ldx);
+  uint4 raw[SLOTS];
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int c = t + s * tpr;
+    raw[s] = live && c < pieces ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float v[SLOTS][8];
+  float m = 0.0f;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    row_bf16x8(raw[s], v[s]);
+    if (G > 0) {
+#pragma unroll
+      for (int h = 1; h < 8; h <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if ((i & h) == 0) {
+            const float a = v[s][i], b = v[s][i + h];
+            v[s][i] = a + b;
+            v[s][i + h] = a - b;
+          }
+#pragma unroll
+      for (int l = 1; l < G / 8; l <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = __shfl_xor_sync(0xffffffffu, v[s][i], l);
+          v[s][i] = (lane & l) ? o - v[s][i] : v[s][i] + o;
+        }
+    }
+    m = fmaxf(m, row_absmax<8>(v[s]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (tpr > 32) {                                          // the same for the whole block
+    if (lane == 0) red[threadIdx.x >> 5] = m;
+    __syncthreads();
+    const int w0 = sub * (tpr / 32);
+    m = lane < tpr / 32 ? red[w0 + lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  if (!live) return;
+  const bool zero = !(m >= kQ8Tiny);
+  const float inv = zero ? 0.0f : 127.0f / m;
+  if (t == 0) scales[row] = zero ? 0.0f : m * scale_mult;
+  uint2* dst = reinterpret_cast<uint2*>(codes + row * D);
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int c = t + s * tpr;
+    if (c >= pieces) continue;
+    uint32_t b[8];                                          // codes in the low bytes (1.5 * 2^23 added)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[s][i], inv, kRowRoundMagic));
+    dst[c] = make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                        __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+  }
+}
+
+template <int G>
+cudaError_t launch_g(const void* X, int64_t rows, int D, int64_t ldx, int8_t* codes, float* scales,
+                     cudaStream_t stream) {
+  const int pieces = D / 8;
+  const int slots = pieces <= 1024 * Q8_SLOTS ? Q8_SLOTS : Q8_SLOTS_LONG;
+  const int tpr = (pieces + 32 * slots - 1) / (32 * slots) * 32;
+  const int per_block = tpr < Q8_BLOCK ? Q8_BLOCK / tpr : 1;
+  const unsigned grid = (unsigned)((rows + per_block - 1) / per_block);
+  const float mult = (float)(1.0 / (127.0 * (G == 0 ? 1.0 : G == 64 ? 8.0 : G == 256 ? 16.0 : 11.313708498984761)));
+  const uint16_t* x = static_cast<const uint16_t*>(X);
+  if (slots == Q8_SLOTS)
+    quant_rows8_kernel<G, Q8_SLOTS><<<grid, tpr * per_block, 0, stream>>>(x, rows, ldx, D, tpr, mult, codes, scales);
+  else
+    quant_rows8_kernel<G, Q8_SLOTS_LONG><<<grid, tpr * per_block, 0, stream>>>(x, rows, ldx, D, tpr, mult, codes, scales);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quant_rows8(const void* X, int64_t rows, int D, int64_t ldx, int g, int8_t* codes, float* scales,
+                               cudaStream_t stream) {
+  switch (g) {
+    case 64: return launch_g<64>(X, rows, D, ldx, codes, scales, stream);
+    case 128: return launch_g<128>(X, rows, D, ldx, codes, scales, stream);
+    case 256: return launch_g<256>(X, rows, D, ldx, codes, scales, stream);
+    default: return launch_g<0>(X, rows, D, ldx, codes, scales, stream);
+  }
+}
+
+}  // namespace pq

@@ -22,6 +22,8 @@ PQ_HADAMARD, PQ_GIVENS, PQ_SMOOTH_HADAMARD = range(3)
 PQ_OUT_F32, PQ_OUT_BF16 = range(2)
 PQ_FLAG_SMOOTH_AFTER_ROTATE = 0x1
 PQ_NO_PAIR = 0xFF
+PQ_KV4_ROTATE_K, PQ_KV4_ROTATE_V = 0x1, 0x2
+PQ_KV4_INTERLEAVED = 0x1
 KINDS = {"hadamard": PQ_HADAMARD, "givens": PQ_GIVENS, "smooth_hadamard": PQ_SMOOTH_HADAMARD}
 
 # Every symbol the header declares.
@@ -29,6 +31,8 @@ EXPORTS = ("pq_select_pairs", "pq_make_plan", "pq_destroy_plan", "pq_transform_q
            "pq_pack_weights", "pq_w4a4_gemm", "pq_w4a4_gemm_noalloc", "pq_w4a4_gemm_launch_count",
            "pq_w4a4_gemm_launch_count_g", "pq_w4a4_linear", "pq_make_plan_outliers",
            "pq_rrs_prepare", "pq_rrs_transform_quant", "pq_rrs_pack_weights", "pq_rrs_gemm",
+           "pq_quant_rows8", "pq_w8a8_gemm", "pq_w8a8_linear",
+           "pq_kv4_append", "pq_kv4_read", "pq_kv4_attention",
            "pq_check_status",
            "pq_selftest_wait_timeout", "pq_status_string", "pq_last_error")
 
@@ -64,6 +68,28 @@ lib.pq_rrs_pack_weights.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]
 lib.pq_rrs_pack_weights.restype = _i32
 lib.pq_rrs_gemm.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp]
 lib.pq_rrs_gemm.restype = _i32
+_f32 = _c.c_float
+lib.pq_quant_rows8.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp]
+lib.pq_quant_rows8.restype = _i32
+lib.pq_w8a8_gemm.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _vp]
+lib.pq_w8a8_gemm.restype = _i32
+lib.pq_w8a8_linear.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp]
+lib.pq_w8a8_linear.restype = _i32
+
+
+class _KV4Struct(_c.Structure):
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp), ("pages", _i64),
+                ("page_size", _c.c_int32), ("heads", _c.c_int32), ("head_dim", _c.c_int32), ("flags", _u32)]
+
+
+lib.pq_kv4_append.argtypes = [_vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _vp, _vp, _f32, _vp, _i64, _i32, _vp,
+                              _vp, _u32, _vp, _vp]
+lib.pq_kv4_append.restype = _i32
+lib.pq_kv4_read.argtypes = [_vp, _vp, _i64, _vp, _vp, _vp]
+lib.pq_kv4_read.restype = _i32
+lib.pq_kv4_attention.argtypes = [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _i64, _vp,
+                                 _i64, _vp]
+lib.pq_kv4_attention.restype = _i32
 lib.pq_selftest_wait_timeout.argtypes = [_u64, _vp]
 lib.pq_selftest_wait_timeout.restype = _i32
 lib.pq_check_status.argtypes = [_vp, _vp]
@@ -112,8 +138,8 @@ def _arg(x, name, dtype, need, rows_strided=False):
     if x is None or isinstance(x, int):
         return _ptr(x)
     import torch
-    want = {"bf16": (torch.bfloat16,), "u8": (torch.uint8,), "f32": (torch.float32,),
-            "i32": (torch.int32,), "y": (torch.float32, torch.bfloat16)}[dtype]
+    want = {"bf16": (torch.bfloat16,), "u8": (torch.uint8,), "i8": (torch.int8,), "f32": (torch.float32,),
+            "i32": (torch.int32,), "i64": (torch.int64,), "y": (torch.float32, torch.bfloat16)}[dtype]
     if x.dtype not in want:
         raise ValueError(f"{name}: dtype {x.dtype} is not accepted (expected {' or '.join(map(str, want))})")
     p = _ptr(x, rows_strided)
@@ -325,6 +351,166 @@ def pq_rrs_gemm(codes_A, token_scales, codes_W, scales_W, Y, T=None, N=None, D=N
     T, N, D, out_dtype, ptrs = _gemm_args(codes_A, token_scales, codes_W, scales_W, Y, T, N, D, g, out_dtype,
                                           sa_per_token=True)
     _check(lib.pq_rrs_gemm(*ptrs[:4], T, N, D, g, ptrs[4], out_dtype, _stream(stream)), "pq_rrs_gemm")
+
+
+def pq_quant_rows8(X, codes, scales, g=0, T=None, D=None, ldx=None, stream=None) -> None:
+    """X bf16 [T, ldx] -> codes int8 [T, D], scales float32 [T] (one a row); rows rotated in blocks of g
+    channels by a Hadamard matrix first (g = 0: not)."""
+    T = X.shape[0] if T is None else T
+    D = X.shape[1] if D is None else D
+    ldx = _row_stride(X, "X") if ldx is None else ldx
+    xp = _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
+    _check(lib.pq_quant_rows8(xp, T, D, ldx, g, _arg(codes, "codes", "i8", T * D),
+                              _arg(scales, "scales", "f32", T), _stream(stream)), "pq_quant_rows8")
+
+
+def _row_stride(x, name):
+    """Row stride of a 2-D activation tensor; a single row's stride says nothing, so its length stands in."""
+    if x.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype):
+    if not isinstance(Y, int):
+        import torch
+        y_kind = PQ_OUT_BF16 if Y.dtype == torch.bfloat16 else PQ_OUT_F32
+        if out_dtype is None:
+            out_dtype = y_kind
+        elif out_dtype != y_kind:
+            raise ValueError(f"Y: dtype {Y.dtype} does not match out_dtype={out_dtype}")
+    elif out_dtype is None:
+        out_dtype = PQ_OUT_F32
+    return out_dtype, (_arg(codes_A, "codes_A", "i8", T * D), _arg(scales_A, "scales_A", "f32", T),
+                       _arg(codes_W, "codes_W", "i8", N * D), _arg(scales_W, "scales_W", "f32", N),
+                       _arg(Y, "Y", "y", T * N))
+
+
+def pq_w8a8_gemm(codes_A, scales_A, codes_W, scales_W, Y, T=None, N=None, D=None, out_dtype=None, stream=None) -> None:
+    """Y [T, N] = scales_A[t] scales_W[n] (codes_A codes_W^T), codes int8 [T, D] and [N, D]."""
+    T = codes_A.shape[0] if T is None else T
+    N = codes_W.shape[0] if N is None else N
+    D = codes_A.shape[1] if D is None else D
+    out_dtype, p = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype)
+    _check(lib.pq_w8a8_gemm(p[0], p[1], p[2], p[3], T, N, D, p[4], out_dtype, _stream(stream)), "pq_w8a8_gemm")
+
+
+def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=None, D=None, ldx=None, out_dtype=None,
+                   stream=None) -> None:
+    """:func:`pq_quant_rows8` of X into codes_A / scales_A and :func:`pq_w8a8_gemm` into Y, one call."""
+    T = X.shape[0] if T is None else T
+    N = codes_W.shape[0] if N is None else N
+    D = X.shape[1] if D is None else D
+    ldx = _row_stride(X, "X") if ldx is None else ldx
+    xp = _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
+    out_dtype, p = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype)
+    _check(lib.pq_w8a8_linear(xp, T, D, ldx, g, p[0], p[1], p[2], p[3], N, p[4], out_dtype, _stream(stream)),
+           "pq_w8a8_linear")
+
+
+class KV4Cache:
+    """The paged 4-bit cache of one layer: four device tensors and how they are to be read.
+
+    k_codes, v_codes uint8 [pages, heads, page_size, head_dim / 2]; k_scales, v_scales float32 [pages, heads,
+    page_size].  rotate_k / rotate_v: keys (and queries) / values are held rotated by a Hadamard matrix per head.
+    """
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, rotate_k=True, rotate_v=True):
+        shape = tuple(k_codes.shape)
+        if len(shape) != 4:
+            raise ValueError("k_codes: expected [pages, heads, page_size, head_dim / 2]")
+        if tuple(v_codes.shape) != shape or tuple(k_scales.shape) != shape[:3] or tuple(v_scales.shape) != shape[:3]:
+            raise ValueError("k_codes, v_codes, k_scales and v_scales do not have the shapes of one cache")
+        if len({x.device for x in (k_codes, k_scales, v_codes, v_scales)}) != 1:
+            raise ValueError("the cache's tensors are on different devices")
+        n = k_scales.numel()
+        self.tensors = (k_codes, k_scales, v_codes, v_scales)
+        self.pages, self.heads, self.page_size, self.head_dim = shape[0], shape[1], shape[2], 2 * shape[3]
+        self.rotate_k, self.rotate_v = bool(rotate_k), bool(rotate_v)
+        flags = (PQ_KV4_ROTATE_K if rotate_k else 0) | (PQ_KV4_ROTATE_V if rotate_v else 0)
+        self._s = _KV4Struct(_arg(k_codes, "k_codes", "u8", n * shape[3]), _arg(k_scales, "k_scales", "f32", n),
+                             _arg(v_codes, "v_codes", "u8", n * shape[3]), _arg(v_scales, "v_scales", "f32", n),
+                             self.pages, self.page_size, self.heads, self.head_dim, flags)
+        self.handle = _c.addressof(self._s)
+
+    @classmethod
+    def empty(cls, pages, heads, page_size, head_dim, rotate_k=True, rotate_v=True, device="cuda"):
+        """A cache of zeros."""
+        import torch
+        codes = [torch.zeros(pages, heads, page_size, head_dim // 2, dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.zeros(pages, heads, page_size, dtype=torch.float32, device=device) for _ in "kv"]
+        return cls(codes[0], scales[0], codes[1], scales[1], rotate_k, rotate_v)
+
+
+def _rows_of(x, name, width, T):
+    """Pointer and row stride of [T, width] bf16 rows (or [T, heads, head_dim] with dense heads)."""
+    import torch
+    if x.dtype != torch.bfloat16:
+        raise ValueError(f"{name}: dtype {x.dtype} is not accepted (expected torch.bfloat16)")
+    if not x.is_cuda:
+        raise ValueError("expected a CUDA tensor: the library takes device pointers")
+    if x.dim() == 3 and (x.stride(1) == x.shape[2] or x.shape[1] == 1):
+        cols = x.shape[1] * x.shape[2]
+    elif x.dim() == 2:
+        cols = x.shape[1]
+    else:
+        raise ValueError(f"{name}: expected [T, heads * head_dim] or [T, heads, head_dim] with dense heads")
+    if x.stride(-1) != 1 or cols != width or x.shape[0] != T:
+        raise ValueError(f"{name}: shape {tuple(x.shape)} (strides {x.stride()}) is not {T} rows of {width} channels")
+    return x.data_ptr(), (x.stride(0) if T > 1 else width)
+
+
+def pq_kv4_append(cache: KV4Cache, Q, K, V, Q_out, positions, slots, rope=None, q_norm=None, k_norm=None, eps=1e-6,
+                  interleaved=False, stream=None) -> None:
+    """Queries, keys and values of T new tokens (bf16 rows, any row stride): norms, position rotation and Hadamard
+    into Q_out bf16 [T, heads_q, head_dim] and, as 4-bit codes, into the cache at slots (int64 [T], negative: nowhere).
+
+    rope float32 [positions, rope_dim] (cosines, then sines), positions int32 [T]; q_norm, k_norm bf16 [head_dim].
+    """
+    T, hd = Q.shape[0], cache.head_dim
+    wq, wk = Q.shape[1] * (Q.shape[2] if Q.dim() == 3 else 1), cache.heads * hd
+    (qp, ldq), (kp, ldk), (vp, ldv) = _rows_of(Q, "Q", wq, T), _rows_of(K, "K", wk, T), _rows_of(V, "V", wk, T)
+    if wq % hd:
+        raise ValueError(f"Q: rows of {wq} channels are not whole heads of {hd}")
+    if rope is not None and rope.dim() != 2:
+        raise ValueError("rope: expected [positions, rope_dim]")
+    _check(lib.pq_kv4_append(cache.handle, qp, ldq, kp, ldk, vp, ldv, T, wq // hd,
+                             _arg(q_norm, "q_norm", "bf16", hd), _arg(k_norm, "k_norm", "bf16", hd), eps,
+                             _arg(rope, "rope", "f32", 0), 0 if rope is None else rope.shape[0],
+                             0 if rope is None else rope.shape[1], _arg(positions, "positions", "i32", T),
+                             _arg(slots, "slots", "i64", T), PQ_KV4_INTERLEAVED if interleaved else 0,
+                             _arg(Q_out, "Q_out", "bf16", T * wq), _stream(stream)), "pq_kv4_append")
+
+
+def pq_kv4_read(cache: KV4Cache, slots, K_out, V_out, stream=None) -> None:
+    """Cached rows at slots (int64 [T]) as bf16 values in the cache's basis; negative slots give zeros."""
+    T = slots.shape[0]
+    n = T * cache.heads * cache.head_dim
+    _check(lib.pq_kv4_read(cache.handle, _arg(slots, "slots", "i64", T), T, _arg(K_out, "K_out", "bf16", n),
+                           _arg(V_out, "V_out", "bf16", n), _stream(stream)), "pq_kv4_read")
+
+
+def pq_kv4_attention(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_q, max_len, scale=None, window=0,
+                     stream=None) -> None:
+    """O = causal attention of the newest tokens of each sequence over its cached tokens.
+
+    Q bf16 [T, heads_q, head_dim] as Q_out of :func:`pq_kv4_append`; q_start int32 [B + 1], seq_lens int32 [B],
+    block_table int32 [B, pages of a sequence]; max_q, max_len: upper bounds (they size the launch); scale defaults
+    to 1 / sqrt(head_dim); window > 0: each token sees itself and the window - 1 before it.
+    """
+    T, hd = Q.shape[0], cache.head_dim
+    wq = Q.shape[1] * (Q.shape[2] if Q.dim() == 3 else 1)
+    (qp, ldq), (op, ldo) = _rows_of(Q, "Q", wq, T), _rows_of(O, "O", wq, T)
+    if wq % hd:
+        raise ValueError(f"Q: rows of {wq} channels are not whole heads of {hd}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [sequences, pages]")
+    B, width = block_table.shape
+    _check(lib.pq_kv4_attention(cache.handle, qp, ldq, wq // hd, _arg(q_start, "q_start", "i32", B + 1),
+                                _arg(seq_lens, "seq_lens", "i32", B),
+                                _arg(block_table, "block_table", "i32", B * width), width, B, T, max_q, max_len,
+                                hd ** -0.5 if scale is None else scale, window, op, ldo, _stream(stream)),
+           "pq_kv4_attention")
 
 
 def pq_w4a4_gemm_launch_count_g(T: int, N: int, D: int, g: int) -> int:
