@@ -1,7 +1,31 @@
-// W8A8 GEMM with one scale per token and one per output channel (sm_100a):
-//   Y[t][n] = fl(d sa[t] sw[n]),  d = sum_k qa[t][k] qw[n][k]  (exact in int32 for D <= 65536).
+// W8A8 GEMM with one scale per token and one per output channel on tcgen05 tensor cores (sm_100a):
+//   Y[t][n] = fl(fl(fl(d) sa[t]) sw[n]),  d = sum_k qa[t][k] qw[n][k]
+// d is exact: int8 products summed in int32 (D <= 65536, so |d| <= 2^30).  Integer sums do not depend on their order,
+// so neither the split of the reduction nor the tile changes a bit of the result.
+//
+// Both kernels take weights as MMA operand A (output channels = tensor-memory lanes) and tokens as operand B, both as
+// they lie in memory: K-major rows of 128 bytes by TMA into the 128-byte-swizzled operand layout, zero-filled past
+// the last row and the last code.  A warp's store of one token then covers 32 consecutive channels.
+//
+// w8a8_pair_kernel (many output tiles): persistent, one CTA per SM, clusters of two CTAs that share every MMA
+//   (cta_group::2, M256 N256 K32; each SM loads 128 weight rows and 128 tokens per 128-code step).  The whole
+//   reduction of a 256 x 256 tile runs in one accumulator, and there are two (512 columns of tensor memory), so the
+//   epilogue of a tile overlaps the next tile's reduction.  Tensor-bound.
+//   warp 0: TMA producer; warp 1: tensor memory, MMA issue (even CTA); warps 4..11: epilogue, two a lane quarter.
+//
+// w8a8_tile_kernel (few tiles: decode batches, short prompts, narrow layers): tiles of 128 channels x NP tokens (16 to
+//   128), the reduction cut into ranges over the 1 to 8 CTAs of a cluster, each with its own part of the weights in
+//   flight: at these sizes streaming the weights is the work, and it takes every SM's loads to fill HBM.  The CTAs
+//   leave their int32 partial tiles in shared memory, meet, and each adds one slice of the tokens over the cluster's
+//   shared memory: one launch, no workspace.
+//   warp 0: TMA producer; warp 1: tensor memory, MMA issue; warps 2..5: epilogue.
+//
+// Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains what it has in flight, meets
+// its cluster, frees tensor memory and returns.
+#include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "internal.h"
@@ -10,45 +34,398 @@
 namespace pq {
 namespace {
 
-// 64 tokens x 64 channels per block of 256 threads, 64 codes of K at a time in shared memory;
-// a thread forms 4 x 4 outputs with __dp4a.
-constexpr int TB = 64;
+constexpr int KB = 128;                 // codes per K step = bytes of a swizzle row
+constexpr uint64_t kWaitNs = 2000000000ull;
 
-__global__ void __launch_bounds__(256) w8a8_dp4a_kernel(const int8_t* __restrict__ A, const float* __restrict__ sa,
-                                                        const int8_t* __restrict__ W, const float* __restrict__ sw,
-                                                        void* __restrict__ Y, int64_t T, int64_t N, int D,
-                                                        int out_bf16) {
-  __shared__ int as[TB][TB / 4 + 1], ws[TB][TB / 4 + 1];
-  const int64_t t0 = (int64_t)blockIdx.y * TB, n0 = (int64_t)blockIdx.x * TB;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  ptx::griddep_wait();
-  for (int k0 = 0; k0 < D; k0 += TB) {
-    const int r = threadIdx.x >> 2, c = threadIdx.x & 3;      // row, 16-byte piece
-    const bool in = k0 + 16 * c < D;
-    const int4 a = in && t0 + r < T ? *reinterpret_cast<const int4*>(A + (t0 + r) * D + k0 + 16 * c) : make_int4(0, 0, 0, 0);
-    const int4 w = in && n0 + r < N ? *reinterpret_cast<const int4*>(W + (n0 + r) * D + k0 + 16 * c) : make_int4(0, 0, 0, 0);
-    __syncthreads();
-    as[r][4 * c] = a.x, as[r][4 * c + 1] = a.y, as[r][4 * c + 2] = a.z, as[r][4 * c + 3] = a.w;
-    ws[r][4 * c] = w.x, ws[r][4 * c + 1] = w.y, ws[r][4 * c + 2] = w.z, ws[r][4 * c + 3] = w.w;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TB / 4; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __dp4a(as[ty + 16 * i][k], ws[tx + 16 * j][k], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t t = t0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (t >= T || n >= N) continue;
-      const float y = (float)acc[i][j] * sa[t] * sw[n];
-      if (out_bf16) static_cast<__nv_bfloat16*>(Y)[t * N + n] = __float2bfloat16_rn(y);
-      else static_cast<float*>(Y)[t * N + n] = y;
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
+  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs)) return true;
+  *abort_flag = 1;
+  atomicOr(status, PQ_DEV_TIMEOUT);
+  return false;
+}
+
+// One lane polls for the warp.
+__device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                                   unsigned int* status) {
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, abort_flag, status) ? 1 : 0;
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  __syncwarp();
+  return ok != 0;
+}
+
+// While draining: bounded in time only.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+  int never = 0;
+  (void)ptx::mbar_wait_bounded(bar, parity, &never, kWaitNs);
+}
+
+__device__ __forceinline__ void store_y(void* Y, int64_t idx, int d, float sa, float sw, int out_bf16) {
+  const float y = (float)d * sa * sw;
+  if (out_bf16) static_cast<__nv_bfloat16*>(Y)[idx] = __float2bfloat16_rn(y);
+  else static_cast<float*>(Y)[idx] = y;
+}
+
+// ------------------------------------------------------------------------------------ pair kernel
+constexpr int PM = 128;                 // weight rows per CTA
+constexpr int PN = 256;                 // tokens per tile
+constexpr int PN_HALF = PN / 2;         // tokens each CTA stages
+constexpr int P_STAGES = 6;
+constexpr int P_THREADS = 384;
+constexpr int P_EPI_WARP0 = 4;
+constexpr int P_EPI_COLS = PN / 2;      // tokens per epilogue warp
+constexpr uint32_t P_TX = 2 * (PM + PN_HALF) * KB;   // both CTAs' bytes, on the even CTA's barrier
+
+struct __align__(1024) PairSmem {
+  uint8_t a[P_STAGES][PM * KB];
+  uint8_t b[P_STAGES][PN_HALF * KB];
+  uint64_t full[P_STAGES], empty[P_STAGES];
+  uint64_t acc_full[2], acc_empty[2];
+  uint64_t mma_done, pair_done;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+constexpr size_t kPairSmem = sizeof(PairSmem) + 1024;
+static_assert(kPairSmem <= 232448, "shared memory exceeds 227 KB");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_pair_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const float* __restrict__ scales_A,
+    const float* __restrict__ scales_W, void* __restrict__ Y, int T, int N, int steps, int m_tiles, int tiles,
+    int out_bf16, int pdl, unsigned int* status) {
+  extern __shared__ unsigned char smem_raw[];
+  PairSmem& S = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
     }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&S.acc_full[b], 1);
+      ptx::mbar_init(&S.acc_empty[b], 2 * 8);            // both CTAs' epilogue warps
+    }
+    ptx::mbar_init(&S.mma_done, 1);
+    ptx::mbar_init(&S.pair_done, 1);
+    S.abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmA);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&S.tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // Launched as the dependent of the quantisation: it reads the codes only once that is complete.
+      if (pdl) ptx::griddep_wait();
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
+      int step = 0;
+      bool ok = true;
+      for (int u = first; u < tiles && ok; u += stride) {
+        const int m0 = (u % m_tiles) * 2 * PM + PM * rank, n0 = (u / m_tiles) * PN + PN_HALF * rank;
+        for (int kb = 0; kb < steps; ++kb, ++step) {
+          const int s = step % P_STAGES;
+          if (!wait_or_abort(&S.empty[s], ((uint32_t)(step / P_STAGES) & 1u) ^ 1u, &S.abort_flag, status)) { ok = false; break; }
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[s], P_TX);
+          ptx::tma_load_2d_pair(S.a[s], &tmW, full0 + 8u * s, kb * KB, m0);
+          ptx::tma_load_2d_pair(S.b[s], &tmA, full0 + 8u * s, kb * KB, n0);
+        }
+      }
+      // Every load issued has landed and every release aimed at this CTA has arrived before it may exit.
+      const int j0 = step > P_STAGES ? step - P_STAGES : 0;
+      if (rank == 0)
+        for (int j = j0; j < step; ++j) drain_wait(&S.full[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
+      for (int j = j0; j < step; ++j) drain_wait(&S.empty[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = ptx::idesc_s8_s32(2 * PM, PN);
+      int step = 0, tile = 0;
+      bool ok = true;
+      for (int u = first; u < tiles && ok; u += stride, ++tile) {
+        const int b = tile & 1;
+        if (!wait_or_abort(&S.acc_empty[b], ((uint32_t)(tile >> 1) & 1u) ^ 1u, &S.abort_flag, status)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)b * PN;
+        for (int kb = 0; kb < steps; ++kb, ++step) {
+          const int s = step % P_STAGES;
+          if (!wait_or_abort(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t a0 = ptx::smem_addr(S.a[s]), b0 = ptx::smem_addr(S.b[s]);
+#pragma unroll
+          for (int k = 0; k < KB / 32; ++k)
+            ptx::umma_s8_pair(d, ptx::smem_desc_sw128(a0 + 32 * k), ptx::smem_desc_sw128(b0 + 32 * k), idesc,
+                              kb > 0 || k > 0 ? 1u : 0u);
+          ptx::umma_commit_pair(&S.empty[s], 0x3);
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(&S.acc_full[b], 0x3);
+      }
+      ptx::umma_commit_pair(&S.mma_done, 0x1);
+      drain_wait(&S.mma_done, 0);
+      for (int j = (tile > 2 ? tile - 2 : 0); j < tile; ++j) drain_wait(&S.acc_empty[j & 1], (uint32_t)(j >> 1) & 1u);
+    }
+  } else if (warp >= P_EPI_WARP0) {
+    // Lane quarter warp % 4 (channels), token half of the tile.
+    if (pdl) ptx::griddep_wait();
+    const int ew = warp - P_EPI_WARP0;
+    const int sub = warp & 3, half = ew >> 2;
+    const uint32_t acc_empty0 = ptx::mapa_shared(ptx::smem_addr(&S.acc_empty[0]), 0);
+    int tile = 0;
+    for (int u = first; u < tiles; u += stride, ++tile) {
+      const int b = tile & 1;
+      const int n = (u % m_tiles) * 2 * PM + PM * rank + 32 * sub + lane;       // this thread's channel
+      const int t0 = (u / m_tiles) * PN + P_EPI_COLS * half;
+      const float sw = n < N ? __ldg(scales_W + n) : 0.0f;
+      // The token scales of this half (its four warps write and read their own copy of 32 each).
+      float sa_l[P_EPI_COLS / 32];
+#pragma unroll
+      for (int i = 0; i < P_EPI_COLS / 32; ++i) sa_l[i] = t0 + 32 * i + lane < T ? __ldg(scales_A + t0 + 32 * i + lane) : 0.0f;
+      if (!warp_wait_or_abort(&S.acc_full[b], (uint32_t)(tile >> 1) & 1u, &S.abort_flag, status)) break;
+      ptx::tc_fence_after();
+      const uint32_t col0 = tmem + ((uint32_t)(32 * sub) << 16) + (uint32_t)(b * PN + half * P_EPI_COLS);
+#pragma unroll 1
+      for (int c = 0; c < P_EPI_COLS / 32; ++c) {
+        uint32_t r[32];
+        ptx::tmem_ld32(col0 + 32 * c, r);
+        ptx::tmem_ld_wait();
+        if (c == P_EPI_COLS / 32 - 1) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_remote(acc_empty0 + 8u * b);
+        }
+        const float sa_c = c == 0 ? sa_l[0] : c == 1 ? sa_l[1] : c == 2 ? sa_l[2] : sa_l[3];
+        const int t = t0 + 32 * c;
+        const int live = min(32, T - t);
+        const int64_t base = (int64_t)t * N + n;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float sa = __shfl_sync(0xffffffffu, sa_c, i);
+          if (i < live && n < N) store_y(Y, base + (int64_t)i * N, (int)r[i], sa, sw, out_bf16);
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves while its peer may still arrive on its barriers or read its tiles.
+  if (threadIdx.x == 0) {
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&S.pair_done), (uint32_t)rank ^ 1u));
+    int never = 0;
+    if (!ptx::mbar_wait_bounded_cl(&S.pair_done, 0, &never, kWaitNs)) atomicOr(status, PQ_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------ tile kernel
+constexpr int TM = 128;                 // weight rows per tile
+constexpr int T_THREADS = 192;
+
+// NP: token columns of a tile.  The stages leave room for two CTAs per SM.
+template <int NP> struct TileGeom {
+  static constexpr int STAGES = NP == 16 ? 6 : NP == 32 ? 5 : NP == 64 ? 4 : 3;
+  static constexpr uint32_t TX = (TM + NP) * KB;
+  static constexpr uint32_t COLS = NP < 32 ? 32 : NP;
+};
+
+template <int NP> struct __align__(1024) TileSmem {
+  uint8_t a[TileGeom<NP>::STAGES][TM * KB];
+  uint8_t b[TileGeom<NP>::STAGES][NP * KB];
+  uint64_t full[TileGeom<NP>::STAGES], empty[TileGeom<NP>::STAGES];
+  uint64_t acc_full;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+// Grid: x = tile * split + range (the cluster), tiles channel-fastest.
+template <int NP>
+__global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const float* __restrict__ scales_A,
+    const float* __restrict__ scales_W, void* __restrict__ Y, int T, int N, int steps, int m_tiles, int split,
+    int out_bf16, int pdl, unsigned int* status) {
+  constexpr int STAGES = TileGeom<NP>::STAGES;
+  extern __shared__ unsigned char smem_raw[];
+  TileSmem<NP>& S = *reinterpret_cast<TileSmem<NP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  static_assert(sizeof(S.a) + sizeof(S.b) >= sizeof(int) * TM * NP, "partial tile overlays the stages");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = (int)blockIdx.x / split, rank = (int)blockIdx.x % split;
+  const int m0 = (tile % m_tiles) * TM, t0 = (tile / m_tiles) * NP;
+  const int per = (steps + split - 1) / split;
+  const int k0 = min(steps, rank * per), k1 = min(steps, k0 + per);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
+    }
+    ptx::mbar_init(&S.acc_full, 1);
+    S.abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmA);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&S.tmem_slot, TileGeom<NP>::COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // The first ring of weights is requested before the wait for the kernel that writes the token codes.
+      const int head = min(STAGES, k1 - k0);
+      for (int i = 0; i < head; ++i) {
+        ptx::mbar_arrive_expect_tx(&S.full[i], TileGeom<NP>::TX);
+        ptx::tma_load_2d(S.a[i], &tmW, &S.full[i], (k0 + i) * KB, m0);
+      }
+      if (pdl) ptx::griddep_wait();
+      for (int i = 0; i < head; ++i) ptx::tma_load_2d(S.b[i], &tmA, &S.full[i], (k0 + i) * KB, t0);
+      int step = head;
+      for (int kb = k0 + head; kb < k1; ++kb, ++step) {
+        const int s = step % STAGES;
+        if (!wait_or_abort(&S.empty[s], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &S.abort_flag, status)) break;
+        ptx::mbar_arrive_expect_tx(&S.full[s], TileGeom<NP>::TX);
+        ptx::tma_load_2d(S.a[s], &tmW, &S.full[s], kb * KB, m0);
+        ptx::tma_load_2d(S.b[s], &tmA, &S.full[s], kb * KB, t0);
+      }
+      // Every load has landed and every stage's release has arrived before the CTA may exit.
+      for (int j = (step > STAGES ? step - STAGES : 0); j < step; ++j) {
+        drain_wait(&S.full[j % STAGES], (uint32_t)(j / STAGES) & 1u);
+        drain_wait(&S.empty[j % STAGES], (uint32_t)(j / STAGES) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = ptx::idesc_s8_s32(TM, NP);
+      for (int kb = k0, step = 0; kb < k1; ++kb, ++step) {
+        const int s = step % STAGES;
+        if (!wait_or_abort(&S.full[s], (uint32_t)(step / STAGES) & 1u, &S.abort_flag, status)) break;
+        ptx::tc_fence_after();
+        const uint32_t a0 = ptx::smem_addr(S.a[s]), b0 = ptx::smem_addr(S.b[s]);
+#pragma unroll
+        for (int k = 0; k < KB / 32; ++k)
+          ptx::umma_s8(tmem, ptx::smem_desc_sw128(a0 + 32 * k), ptx::smem_desc_sw128(b0 + 32 * k), idesc,
+                       step > 0 || k > 0 ? 1u : 0u);
+        ptx::umma_commit(&S.empty[s]);
+      }
+      ptx::umma_commit(&S.acc_full);
+      drain_wait(&S.acc_full, 0);
+    }
+  } else {
+    if (pdl) ptx::griddep_wait();
+    const int sub = warp & 3;
+    const int n = m0 + 32 * sub + lane;
+    const bool some = k1 > k0;                            // an empty range contributes zeros
+    bool ok = true;
+    if (some) ok = warp_wait_or_abort(&S.acc_full, 0, &S.abort_flag, status);
+    ptx::tc_fence_after();
+    const uint32_t col0 = tmem + ((uint32_t)(32 * sub) << 16);
+    int* part = reinterpret_cast<int*>(S.a);              // [token][128 channels], over the finished stages
+    const float sw = n < N ? __ldg(scales_W + n) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < NP; c += 16) {
+      uint32_t r[16];
+      if (some && ok) {
+        ptx::tmem_ld32x16(col0 + c, r);
+        ptx::tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (split > 1) {
+          part[(c + i) * TM + 32 * sub + lane] = (int)r[i];
+        } else {
+          const int t = t0 + c + i;
+          if (t < T && n < N) store_y(Y, (int64_t)t * N + n, (int)r[i], __ldg(scales_A + t), sw, out_bf16);
+        }
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  if (split > 1) {
+    ptx::cluster_sync();                                  // every partial tile is written
+    // This CTA adds token columns rank, rank + split, ... over the cluster; a warp takes 32 channels of one.
+    if (pdl) ptx::griddep_wait();
+    const uint32_t mine = ptx::smem_addr(S.a);
+    for (int w = warp; w < 4 * ((NP - rank + split - 1) / split); w += T_THREADS / 32) {
+      const int c = rank + split * (w >> 2), row = 32 * (w & 3) + lane;
+      const int t = t0 + c, n = m0 + row;
+      if (t < T && n < N) {
+        int d = 0;
+        for (int p = 0; p < split; ++p)
+          d += ptx::ld_cluster_s32(ptx::mapa_shared(mine + 4u * (uint32_t)(c * TM + row), (uint32_t)p));
+        store_y(Y, (int64_t)t * N + n, d, __ldg(scales_A + t), __ldg(scales_W + n), out_bf16);
+      }
+    }
+    ptx::cluster_sync();                                  // nobody leaves while its tile is read
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, TileGeom<NP>::COLS);
+  }
+}
+
+// ----------------------------------------------------------------------------------------- launch
+pq_status operand_map(CUtensorMap* map, const int8_t* base, int64_t rows, int64_t D, int box_rows) {
+  const cudaError_t e = make_u8_tile_map(map, base, rows, D, KB, box_rows, /*swizzle128=*/true);
+  return cuda_fail(e, "8-bit operand tensor map");
+}
+
+void pdl_attribute(cudaLaunchAttribute* a) {
+  a->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a->val.programmaticStreamSerializationAllowed = 1;
+}
+
+template <int NP>
+pq_status launch_tile(const CUtensorMap& tmW, const CUtensorMap& tmA, const float* scales_A, const float* scales_W,
+                      void* Y, int T, int N, int steps, int m_tiles, int64_t tiles, int split, int bf16, bool pdl,
+                      unsigned int* status, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(TileSmem<NP>) + 1024;
+  static_assert(2 * smem <= 232448, "two CTAs of the tile kernel share an SM");
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(w8a8_tile_kernel<NP>), (int)smem, done);
+  if (e != cudaSuccess) return cuda_fail(e, "w8a8_tile_kernel attributes");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
+  cfg.blockDim = dim3(T_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  pdl_attribute(&attr[1]);
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_tile_kernel<NP>, tmW, tmA, scales_A, scales_W, Y, T, N, steps, m_tiles,
+                                      split, bf16, pdl ? 1 : 0, status),
+                   "w8a8_tile_kernel launch");
 }
 
 }  // namespace
@@ -56,11 +433,47 @@ __global__ void __launch_bounds__(256) w8a8_dp4a_kernel(const int8_t* __restrict
 pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t* codes_W, const float* scales_W,
                       int64_t T, int64_t N, int64_t D, void* Y, pq_out_dtype out_dtype, cudaStream_t stream,
                       bool pdl) {
-  (void)pdl;
-  const dim3 grid((unsigned)((N + TB - 1) / TB), (unsigned)((T + TB - 1) / TB), 1);
-  w8a8_dp4a_kernel<<<grid, 256, 0, stream>>>(codes_A, scales_A, codes_W, scales_W, Y, T, N, (int)D,
-                                             out_dtype == PQ_OUT_BF16 ? 1 : 0);
-  return cuda_fail(cudaGetLastError(), "w8a8_dp4a_kernel launch");
+  unsigned int* status = nullptr;
+  cudaError_t e = gemm_status_address(&status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  const int sms = device_sm_count();
+  const int steps = (int)((D + KB - 1) / KB);
+  const int bf16 = out_dtype == PQ_OUT_BF16 ? 1 : 0;
+  const int64_t pair_m = (N + 2 * PM - 1) / (2 * PM), pair_tiles = pair_m * ((T + PN - 1) / PN);
+  CUtensorMap tmW, tmA;
+  // The pair kernel needs enough 256 x 256 tiles to occupy most SM pairs.
+  if (T > 128 && pair_tiles * 4 >= 3 * (sms / 2)) {
+    if (pair_tiles >= ((int64_t)1 << 30)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
+    pq_status st = operand_map(&tmW, codes_W, N, D, PM);
+    if (st == PQ_OK) st = operand_map(&tmA, codes_A, T, D, PN_HALF);
+    if (st != PQ_OK) return st;
+    static std::atomic<bool> done[kMaxDevices];
+    e = set_kernel_attributes(reinterpret_cast<const void*>(w8a8_pair_kernel), (int)kPairSmem, done);
+    if (e != cudaSuccess) return cuda_fail(e, "w8a8_pair_kernel attributes");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(pair_tiles, sms / 2)), 1, 1);
+    cfg.blockDim = dim3(P_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = kPairSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    pdl_attribute(&attr);
+    cfg.attrs = &attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_pair_kernel, tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps,
+                                        (int)pair_m, (int)pair_tiles, bf16, pdl ? 1 : 0, status),
+                     "w8a8_pair_kernel launch");
+  }
+  const int np = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
+  // Ranges of the reduction: as long as the CTAs still fit next to each other (two an SM) and each keeps some steps.
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * sms && steps >= 4 * split) split *= 2;
+  pq_status st = operand_map(&tmW, codes_W, N, D, TM);
+  if (st == PQ_OK) st = operand_map(&tmA, codes_A, T, D, np);
+  if (st != PQ_OK) return st;
+#define PQ_TILE_CASE(NP) launch_tile<NP>(tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps, (int)m_tiles, tiles, split, bf16, pdl, status, stream)
+  return np == 16 ? PQ_TILE_CASE(16) : np == 32 ? PQ_TILE_CASE(32) : np == 64 ? PQ_TILE_CASE(64) : PQ_TILE_CASE(128);
+#undef PQ_TILE_CASE
 }
 
 }  // namespace pq
