@@ -62,6 +62,10 @@ struct Kv4AttnArgs {
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_kv4_read(const Kv4View& c, const int64_t* slots, int64_t T, uint16_t* K_out, uint16_t* V_out,
                             unsigned int* status, cudaStream_t stream);
+// The kernel for many query rows (kv4_prompt.cu): tiles of 256 (token, head) rows at most, and its launch.
+struct Partials;
+int64_t kv4_prompt_tiles(const Kv4AttnArgs& a);
+pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream);
 pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream);
 
 }  // namespace pq

@@ -18,21 +18,18 @@
 //   - values become fp16: nibble ^ 8 under 0x6400 is 1024 + (code + 8), and 1032 is subtracted from the operand
 //     itself, exactly, since a long sum of probabilities times 1032 would drown the result.
 //   - the loads of the next block are issued as soon as this block's registers are free.
-// The second product takes P_t vs_t / mv as fp16, mv the largest scale of the values that the row has seen so far
-// (the running output is rescaled when it grows, as for the maximum): at most 1, so it neither overflows nor, where it
-// matters, leaves the normal range; rounding it costs half a step of fp16, 2^-11, an eighth of what bf16 would.
-// Maxima, sums and the running output are float32.
+// The second product takes P_t vs_t as fp16, relative to the row's largest score and to the exponent of the largest
+// value scale it has seen: at most 1, so it neither overflows nor, where it matters, leaves the normal range; rounding
+// it costs half a step of fp16, 2^-11, an eighth of what bf16 would.  Maxima, sums and the output are float32.
 //
 // A block's warps join their maxima, sums and outputs through shared memory.  Long contexts are cut into chunks of
 // tokens, one block each; a second kernel joins the chunks' float32 partial results.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <algorithm>
 #include <cstdint>
 
 #include "internal.h"
 #include "kv4.h"
+#include "kv4_device.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -42,8 +39,8 @@ namespace {
 constexpr int AT_WARPS = 4;
 constexpr int AT_BLOCK = 64;            // tokens a warp takes at a time
 constexpr int AT_TILES = AT_BLOCK / 16;
-constexpr float kLog2e = 1.4426950408889634f;
-
+// Query rows a key/value head and sequence from which on the tensor-core kernel of kv4_prompt.cu takes the call.
+constexpr int64_t kPromptRows = 64;
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                          const uint32_t a3, const uint32_t b0, const uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -66,42 +63,6 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
   return y;
 }
 
-// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code.
-__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) {
-  return ((x >> s) & 0x000F000Fu) ^ 0x43084308u;
-}
-
-// The same two nibbles -> two fp16 codes (1032 + code, less 1032: exact).
-__device__ __forceinline__ uint32_t code_pair(uint32_t x, int s) {
-  const uint32_t b = ((x >> s) & 0x000F000Fu) ^ 0x64086408u, k = 0x64086408u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 p = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
-// 2^x; results below the smallest normal number become 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// A value scale as far as it counts toward the largest one: not if it is infinite (NaN drops out of fmaxf).
-__device__ __forceinline__ float finite_or_0(float x) {
-  const float y = fabsf(x);
-  return y < 3.0e38f ? y : 0.0f;
-}
-__device__ __forceinline__ float inverse_or_0(float x) { return x > 1.2e-38f ? 1.0f / x : 0.0f; }
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&p);
-}
-
 template <int W>
 __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
   if constexpr (W == 4) {
@@ -114,43 +75,6 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
     x[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
   }
 }
-
-// One query row's output from its un-normalised float32 sums: lane l of the warp holds channels E l .. E l + E - 1
-// (E = HD / 32).  Divides by the sum of the probabilities (none: 0), rotates back, stores bf16.
-template <int HD>
-__device__ __forceinline__ void finish_row(float (&o)[HD / 32], float l, int rotate, uint16_t* dst, int lane) {
-  constexpr int E = HD / 32;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (rotate) {
-    if constexpr (E == 4) {
-      const float p0 = o[0] + o[1], p1 = o[0] - o[1], p2 = o[2] + o[3], p3 = o[2] - o[3];
-      o[0] = p0 + p2, o[1] = p1 + p3, o[2] = p0 - p2, o[3] = p1 - p3;
-    } else {
-      const float p0 = o[0] + o[1], p1 = o[0] - o[1];
-      o[0] = p0, o[1] = p1;
-    }
-#pragma unroll
-    for (int b = 1; b < 32; b <<= 1)
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const float p = __shfl_xor_sync(0xffffffffu, o[i], b);
-        o[i] = (lane & b) ? p - o[i] : o[i] + p;
-      }
-  }
-  const float f = rotate ? inv * (HD == 128 ? 0.08838834764831845f : 0.125f) : inv;
-  if constexpr (E == 4)
-    *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
-  else
-    *reinterpret_cast<uint32_t*>(dst + 2 * lane) = pack_bf16(o[0] * f, o[1] * f);
-}
-
-// Partial results of one chunk: un-normalised output [HD], then maximum (log2 domain) and sum, per (token, query head).
-struct Partials {
-  float* o;       // [chunk][T * heads_q][HD]
-  float2* ml;     // [chunk][T * heads_q]
-  int chunks;     // 1: no partials, the output is written directly
-  int chunk_len;  // tokens, a multiple of AT_BLOCK
-};
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
@@ -232,11 +156,11 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
     }
 
     float o[NT][KS][4];
-    float m[NT][2], l[NT][2], mv[NT][2];
+    float m[NT][2], l[NT][2];            // reference exponent (score maximum + scale exponent) and sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = mv[nt][0] = mv[nt][1] = 0.0f;
+      l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int j = 0; j < KS; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
     }
@@ -371,19 +295,17 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       uint32_t pb[AT_TILES][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2], mu[2], rmv[2];
+        float alpha[2], mu[2];
         bool grew = false;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = m[nt][e];
+          float x = -INFINITY;
 #pragma unroll
           for (int i = 0; i < AT_TILES; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          mu[e] = x == -INFINITY ? 0.0f : x;
-          alpha[e] = ex2(m[nt][e] - mu[e]);
-          // the row's own largest value scale: in a block with hidden tokens, over those it sees
+          // the largest value scale: in a block with hidden tokens, over those the row sees
           float y = v_block;
           if (!whole) {
 #pragma unroll
@@ -395,13 +317,11 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
           }
-          grew = grew || x > m[nt][e] || y > mv[nt][e];
+          x = fmaxf(m[nt][e], x + scale_exponent(y));
+          mu[e] = x == -INFINITY ? 0.0f : x;
+          alpha[e] = ex2(m[nt][e] - mu[e]);
+          grew = grew || x > m[nt][e];
           m[nt][e] = x;
-          y = fmaxf(y, mv[nt][e]);
-          rmv[e] = inverse_or_0(y);
-          l[nt][e] *= alpha[e];
-          alpha[e] *= mv[nt][e] * rmv[e];
-          mv[nt][e] = y;
         }
         if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -411,6 +331,8 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
             o[nt][j][2] *= alpha[0];
             o[nt][j][3] *= alpha[1];
           }
+          l[nt][0] *= alpha[0];
+          l[nt][1] *= alpha[1];
         }
 #pragma unroll
         for (int i = 0; i < AT_TILES; ++i)
@@ -421,8 +343,8 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
             l[nt][0] += p0;
             l[nt][1] += p1;
             // a hidden token's value scale may be anything: select, do not multiply
-            const float w0 = whole || s0 != -INFINITY ? p0 * (vs[i][h] * rmv[0]) : 0.0f;
-            const float w1 = whole || s1 != -INFINITY ? p1 * (vs[i][h] * rmv[1]) : 0.0f;
+            const float w0 = whole || s0 != -INFINITY ? p0 * vs[i][h] : 0.0f;
+            const float w1 = whole || s1 != -INFINITY ? p1 * vs[i][h] : 0.0f;
             pb[i][nt][h] = movmatrix_trans(pack_f16(w0, w1));
           }
       }
@@ -468,11 +390,6 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          o[nt][j][e] *= mv[nt][e];
-          o[nt][j][2 + e] *= mv[nt][e];
-        }
         float x = l[nt][e];
         x += __shfl_xor_sync(0xffffffffu, x, 4);
         x += __shfl_xor_sync(0xffffffffu, x, 8);
@@ -568,15 +485,26 @@ cudaError_t launch_rows(const Kv4AttnArgs& a, const Partials& part, int row_tile
 pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream) {
   const int group = a.heads_q / a.cache.heads;
   const int64_t max_rows = max_q * group;
+  const int sms = device_sm_count();
+  const bool prompt = max_rows > kPromptRows;
   const int nt = max_rows > 8 ? 2 : 1;
   const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
-  // Chunks: about four blocks for each multiprocessor when every sequence has max_len tokens, at least 256 tokens each.
-  const int64_t units = (int64_t)a.B * a.cache.heads * row_tiles;
-  const int64_t want = (4 * (int64_t)device_sm_count() + units - 1) / units;
-  const int64_t most = (max_len + 255) / 256;
+  int64_t units, want, unit_len;
+  if (prompt) {
+    // One block an SM: chunks only where the tiles leave SMs idle, at least four steps of 128 tokens each.
+    units = kv4_prompt_tiles(a) * a.cache.heads;
+    want = sms / std::max<int64_t>(units, 1);
+    unit_len = 512;
+  } else {
+    // Chunks: about four blocks for each multiprocessor when every sequence has max_len tokens, at least 256 tokens each.
+    units = (int64_t)a.B * a.cache.heads * row_tiles;
+    want = (4 * (int64_t)sms + units - 1) / units;
+    unit_len = 256;
+  }
+  const int64_t most = (max_len + unit_len - 1) / unit_len;
   Partials part = {};
   part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
-  part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + AT_BLOCK - 1) / AT_BLOCK * AT_BLOCK);
+  part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);
   void* ws = nullptr;
   cudaError_t e;
   if (part.chunks > 1) {
@@ -594,15 +522,20 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     part.ml = reinterpret_cast<float2*>(part.o + rows * a.cache.head_dim);
   }
   const bool wide = a.cache.head_dim == 128;
-  e = wide ? (nt == 1 ? launch_rows<128, 1>(a, part, row_tiles, stream) : launch_rows<128, 2>(a, part, row_tiles, stream))
-           : (nt == 1 ? launch_rows<64, 1>(a, part, row_tiles, stream) : launch_rows<64, 2>(a, part, row_tiles, stream));
-  if (e == cudaSuccess && part.chunks > 1) {
+  pq_status st;
+  if (prompt) {
+    st = launch_kv4_prompt(a, part, stream);
+  } else {
+    e = wide ? (nt == 1 ? launch_rows<128, 1>(a, part, row_tiles, stream) : launch_rows<128, 2>(a, part, row_tiles, stream))
+             : (nt == 1 ? launch_rows<64, 1>(a, part, row_tiles, stream) : launch_rows<64, 2>(a, part, row_tiles, stream));
+    st = cuda_fail(e, "kv4_rows_kernel launch");
+  }
+  if (st == PQ_OK && part.chunks > 1) {
     const unsigned grid = (unsigned)((a.T * a.heads_q + 3) / 4);
     if (wide) kv4_join_kernel<128><<<grid, 128, 0, stream>>>(a, part);
     else kv4_join_kernel<64><<<grid, 128, 0, stream>>>(a, part);
-    e = cudaGetLastError();
+    st = cuda_fail(cudaGetLastError(), "kv4_join_kernel launch");
   }
-  pq_status st = cuda_fail(e, "pq_kv4_attention launch");
   if (ws) {
     e = cudaFreeAsync(ws, stream);
     if (st == PQ_OK && e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync(attention workspace)");

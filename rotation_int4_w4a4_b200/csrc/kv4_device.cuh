@@ -1,0 +1,102 @@
+// Device code shared by the attention kernels over the 4-bit cache.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+namespace pq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Partial results of one chunk of a context, per (token, query head): the un-normalised output [HD], then the
+// reference exponent (log2) that output and sum are relative to, and the sum.
+struct Partials {
+  float* o;       // [chunk][T * heads_q][HD]
+  float2* ml;     // [chunk][T * heads_q]
+  int chunks;     // 1: no partials, the output is written directly
+  int chunk_len;  // tokens of a chunk
+};
+
+// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code: nibble ^ 8 is code + 8, under 0x4300
+// (128, whose last mantissa bit counts 1).
+__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) {
+  return ((x >> s) & 0x000F000Fu) ^ 0x43084308u;
+}
+
+// The same, 136 taken off: the codes (exact).
+__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t x, int s) {
+  const uint32_t b = biased_pair(x, s), k = 0x43084308u;
+  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// The same two nibbles -> two fp16 codes (0x6400 is 1024; 1032 + code, less 1032: exact).
+__device__ __forceinline__ uint32_t code_pair(uint32_t x, int s) {
+  const uint32_t b = ((x >> s) & 0x000F000Fu) ^ 0x64086408u, k = 0x64086408u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 p = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// 2^x; results below the smallest normal number become 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A value scale as far as it counts toward the largest one: not if it is infinite (NaN drops out of fmaxf).
+__device__ __forceinline__ float finite_or_0(float x) {
+  const float y = fabsf(x);
+  return y < 3.0e38f ? y : 0.0f;
+}
+
+// An exponent e with x < 2^e (x >= 0), within -100..100; 0 for x = 0.  Scores taken relative to (largest score + e)
+// make probability times value scale at most 1, which fp16 holds; output and sum carry the same factor, so it
+// leaves with their quotient.
+__device__ __forceinline__ float scale_exponent(float x) {
+  const int e = (int)(__float_as_uint(x) >> 23) - 126;
+  return x == 0.0f ? 0.0f : (float)max(-100, min(100, e));
+}
+
+// One query row's output from its un-normalised float32 sums: lane l of the warp holds channels E l .. E l + E - 1
+// (E = HD / 32).  Divides by the sum of the probabilities (none: 0), rotates back, stores bf16.
+template <int HD>
+__device__ __forceinline__ void finish_row(float (&o)[HD / 32], float l, int rotate, uint16_t* dst, int lane) {
+  constexpr int E = HD / 32;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (rotate) {
+    if constexpr (E == 4) {
+      const float p0 = o[0] + o[1], p1 = o[0] - o[1], p2 = o[2] + o[3], p3 = o[2] - o[3];
+      o[0] = p0 + p2, o[1] = p1 + p3, o[2] = p0 - p2, o[3] = p1 - p3;
+    } else {
+      const float p0 = o[0] + o[1], p1 = o[0] - o[1];
+      o[0] = p0, o[1] = p1;
+    }
+#pragma unroll
+    for (int b = 1; b < 32; b <<= 1)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const float p = __shfl_xor_sync(0xffffffffu, o[i], b);
+        o[i] = (lane & b) ? p - o[i] : o[i] + p;
+      }
+  }
+  const float f = rotate ? inv * (HD == 128 ? 0.08838834764831845f : 0.125f) : inv;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2*>(dst + 4 * lane) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+  else
+    *reinterpret_cast<uint32_t*>(dst + 2 * lane) = pack_bf16(o[0] * f, o[1] * f);
+}
+
+}  // namespace pq
