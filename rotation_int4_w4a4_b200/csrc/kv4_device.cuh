@@ -25,13 +25,6 @@ __device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) {
   return ((x >> s) & 0x000F000Fu) ^ 0x43084308u;
 }
 
-// The same, 136 taken off: the codes (exact).
-__device__ __forceinline__ uint32_t code_pair_bf16(uint32_t x, int s) {
-  const uint32_t b = biased_pair(x, s), k = 0x43084308u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&b), *reinterpret_cast<const __nv_bfloat162*>(&k));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
 // The same two nibbles -> two fp16 codes (0x6400 is 1024; 1032 + code, less 1032: exact).
 __device__ __forceinline__ uint32_t code_pair(uint32_t x, int s) {
   const uint32_t b = ((x >> s) & 0x000F000Fu) ^ 0x64086408u, k = 0x64086408u;

@@ -1,21 +1,31 @@
 // Attention over the paged 4-bit cache for many query rows a sequence (prompts and long chunks) on tcgen05 tensor
 // cores, sm_100a.  The mathematics is that of the few-row kernel (kv4_attention.cu): per row
-//   s_t = scale (q . kc_t) ks_t,  o = sum_t softmax(s)_t vs_t vc_t,  codes exact, all sums float32.
+//   s_t = scale (q . kc_t) ks_t,  o = sum_t softmax(s)_t vs_t vc_t,  all sums float32.
 //
 // The query rows of one key/value head (row = new token x head of the group) come in tiles of 128 = the lanes of tensor
 // memory; a CTA takes two tiles (256 rows) and walks the cached tokens 128 at a time:
-//   S_i = Q_i K^T   (bf16, M128 N128)       into 128 columns of tensor memory, i = 0, 1
-//   P_i = softmax numerators times vs, fp16, written over S_i's columns
-//   O_i += P_i V    (fp16, A from tensor memory, M128 N head_dim) into head_dim more columns
+//   S_i = Q_i K^T   (fp16, M128 N128)       into 128 columns of tensor memory, i = 0, 1
+//   P_i = softmax numerators, fp16, written over S_i's columns
+//   O_i += P_i V    (A from tensor memory, M128 N head_dim) into head_dim more columns
 // While the tensor cores work for one tile, the other's softmax runs; both tiles share each 128 keys and values, so a
 // code is unpacked once per 256 rows.  The tensor cores and the exponentials (16 a clock and SM) are about evenly
 // loaded: 2 x 128 x 128 x head_dim multiply-adds against 128 x 128 exponentials a tile and step.
 //   warps 0..3, 4..7   softmax of tile 0, 1: a thread owns a row: its scores from tensor memory, maximum, exponentials,
 //                      P back; O is rescaled in tensor memory only when the row's reference grows by more than 2^8
 //                      (P stays below 2^8, which fp16 holds); at the end its output row.
-//   warps 8..11        producers: 128 tokens' codes from the pages, unpacked to bf16 keys and fp16 values in the
-//                      swizzled operand layout, two stages each; their scales beside them.
+//   warps 8..11        producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
+//                      operand layout, two stages each; their scales beside them.
 //   warp 12            tensor memory and MMA issue.
+// Nothing may spill: the operands leave so little of the L1 cache that a spilled register comes back from L2.
+//
+// Where the scales go.  A step whose 128 tokens every row of the block sees takes keys and values with their scales
+// multiplied in, as fp16 relative to a power of two for each 32 tokens (a key: one rounding of code * scale; a value:
+// the scale's and the product's; half a step is 2^-11, an eighth of a bf16 cache's).  With the scales left to the
+// softmax, every thread would read two scales a token from shared memory, a broadcast that costs four times its bytes:
+// measured, 3800 of 6200 shared-memory cycles a step.  Steps with tokens that some row must not see (the diagonal, a
+// window's edge, the ends of a sequence) keep the bare codes, exact, and the scales in the softmax, where a hidden
+// token's can be left out whatever it holds.  Queries become fp16 relative to their row's largest channel (exact but
+// for channels below 2^-14 of it).
 // Channels sit in the operands in the order 0 4 1 5 2 6 3 7 of each 8 (the order in which nibbles come out of a word);
 // queries are staged in the same order and the output is read back through it.
 // Keys are rows of 128 bytes, K-major; values lie the same way and enter as an MN-major operand.
@@ -37,19 +47,16 @@ namespace pq {
 namespace {
 
 constexpr int PT = 128;                  // rows per tile and tokens per step
-constexpr int PR_THREADS = 512;
+constexpr int PR_THREADS = 416;
+constexpr int PR_PROD0 = 8, PR_MMA = 12;                 // first producer warp, MMA warp
 constexpr int PR_STAGES = 2;             // key and value stages
 constexpr int SC_RING = 4;               // scale stages: a step's scales outlive its keys by at most one step
 constexpr uint64_t kPrWaitNs = 2000000000ull;
 constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i, O_i at 256 + 128 i
 constexpr float kLazy = 8.0f;            // log2 growth of the reference that is let pass
-constexpr uint32_t PR_REG_LAUNCH = 128, PR_REG_SOFT = 184, PR_REG_PROD = 96, PR_REG_CTRL = 48;
-static_assert(256 * PR_REG_SOFT + 128 * PR_REG_PROD + 128 * PR_REG_CTRL <= PR_THREADS * PR_REG_LAUNCH,
-              "setmaxnreg shares exceed the launch allocation");
-
-// kind::f16 with a float32 accumulator: A and B types at bits 7 and 10 (0 fp16, 1 bf16), B MN-major at bit 16.
-__host__ __device__ constexpr uint32_t idesc_f16(int bf16, int b_mn_major, int N) {
-  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)b_mn_major << 16) |
+// kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
+__host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
+  return (1u << 4) | ((uint32_t)b_mn_major << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(PT >> 4) << 24);
 }
 
@@ -59,9 +66,11 @@ struct __align__(1024) PromptSmem {
   uint8_t q[2][KBLK][PT * 128];
   uint8_t k[PR_STAGES][KBLK][PT * 128];
   uint8_t v[PR_STAGES][KBLK][PT * 128];
-  float ks[SC_RING][PT], vs[SC_RING][PT];                // ks already times scale * log2(e)
+  // What multiplies a token's score, and its probability: its scales, or (scales multiplied in) its group's powers of 2.
+  float ks[SC_RING][PT], vs[SC_RING][PT];
   uint32_t valid[SC_RING][4];                            // which tokens exist, a bit each
-  float vmax[SC_RING][4];                                // largest value scale of each 32
+  int scaled[SC_RING];                                   // every row sees all tokens: scales are in the operands
+  float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
   uint64_t sc_full[SC_RING];
@@ -72,7 +81,7 @@ struct __align__(1024) PromptSmem {
 };
 
 __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
-  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs)) return true;
+  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, 16)) return true;
   *abort_flag = 1;
   atomicOr(status, PQ_DEV_TIMEOUT);
   return false;
@@ -146,6 +155,140 @@ __device__ __forceinline__ void fwht(float (&v)[N]) {
 // Swizzled place of 16-byte chunk c of row r in a block of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
+// What a row's thread keeps of a step's tokens when some are hidden: which the row sees, and their scales.
+struct StepView {
+  const float4* ks;        // 4 tokens a vector
+  const float4* vs;
+  const uint32_t* valid;   // a bit a token
+  float c;                 // score units: |scale| log2(e) times the row's power of two
+  int tok0, row_lo, row_hi;
+  __device__ __forceinline__ bool sees(int t) const {    // token t of the step
+    const int tok = tok0 + t;
+    return ((valid[t >> 5] >> (t & 31)) & 1u) && tok >= row_lo && tok <= row_hi;
+  }
+};
+
+// First column of the probabilities of 32 tokens (chunk c of 4) within a tile's 128 score columns: chunks 0 and 1 are
+// read a second time after the probabilities of 2 and 3 have been written, so those stay clear of their columns.
+__host__ __device__ constexpr int p_col(int c) { return 64 + 16 * ((c + 2) & 3); }
+
+// Largest of 32 raw scores.
+__device__ __forceinline__ float chunk_max(const uint32_t (&r)[32]) {
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    m[k % 4] = ptx::max3(m[k % 4], __uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// 2^(c s + off) of 32 scores: as 16 columns of fp16 pairs, and their sum.
+__device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], float c, float off, uint32_t col) {
+  const uint64_t c2 = ptx::f2_pack(c, c), off2 = ptx::f2_pack(off, off);
+  uint64_t sum0 = 0ull, sum1 = 0ull;
+  uint32_t p[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float e[4];
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), c2, off2), e[0], e[1]);
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), c2, off2), e[2], e[3]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
+    sum0 = ptx::f2_add(sum0, ptx::f2_pack(e[0], e[1]));
+    sum1 = ptx::f2_add(sum1, ptx::f2_pack(e[2], e[3]));
+    p[2 * k] = pack_f16(e[0], e[1]);
+    p[2 * k + 1] = pack_f16(e[2], e[3]);
+  }
+  ptx::tmem_st32x16(col, p);
+  float a0, a1, a2, a3;
+  ptx::f2_unpack(sum0, a0, a1);
+  ptx::f2_unpack(sum1, a2, a3);
+  return (a0 + a1) + (a2 + a3);
+}
+
+// The same with hidden tokens: 16 scores in log2 units, -inf where the row does not see.
+__device__ __forceinline__ void masked_scores(const uint32_t (&r)[16], int t, const StepView& v, float (&e)[16]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 ks = v.ks[t / 4 + k];
+    const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      e[4 * k + q] = v.sees(t + 4 * k + q) ? __uint_as_float(r[4 * k + q]) * (kk[q] * v.c) : -INFINITY;
+  }
+}
+
+// Maximum of the row's 128 scores of a step with hidden tokens (log2 units), and the largest value scale seen.
+__device__ __forceinline__ float step_max_masked(uint32_t s_col, const StepView& v, float& vm) {
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int t = 0; t < PT; t += 16) {
+    uint32_t r[16];
+    float e[16];
+    ptx::tmem_ld32x16(s_col + t, r);
+    ptx::tmem_ld_wait(r);
+    masked_scores(r, t, v, e);
+    const float* vs = reinterpret_cast<const float*>(v.vs) + t;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      top = fmaxf(top, e[k]);
+      if (v.sees(t + k)) vm = fmaxf(vm, finite_or_0(vs[k]));
+    }
+  }
+  return top;
+}
+
+// Their probabilities, written over scores already read; returns their sum.
+__device__ __forceinline__ float step_exp_masked(uint32_t s_col, const StepView& v, float ref) {
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int d = 0; d < PT; d += 16) {
+    const int t = (d + 64) & 127;                        // chunks 2, 3, 0, 1: none is overwritten before it is read
+    uint32_t r[16], p[8];
+    float e[16];
+    ptx::tmem_ld32x16(s_col + t, r);
+    ptx::tmem_ld_wait(r);
+    masked_scores(r, t, v, e);
+    const float* vs = reinterpret_cast<const float*>(v.vs) + t;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = ex2(e[k] - ref);
+      sum += x;
+      e[k] = v.sees(t + k) ? x * vs[k] : 0.0f;           // a hidden token's value scale may be anything
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = pack_f16(e[2 * k], e[2 * k + 1]);
+    ptx::tmem_st32x8(s_col + 64 + d / 2, p);
+  }
+  return sum;
+}
+
+// 32 output columns in channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4.
+__device__ __forceinline__ void load_channels(float (&o)[32], uint32_t col) {
+  uint32_t x[32];
+  ptx::tmem_ld32(col, x);
+  ptx::tmem_ld_wait(x);
+#pragma unroll
+  for (int c = 0; c < 32; c += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      o[c + k] = __uint_as_float(x[c + 2 * k]);
+      o[c + k + 4] = __uint_as_float(x[c + 2 * k + 1]);
+    }
+}
+__device__ __forceinline__ uint4 bf16x8(const float* o, float f) {
+  return make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
+                    pack_bf16(o[6] * f, o[7] * f));
+}
+
+// Whether every row of the block sees all tokens of the step: known from the lengths alone, so producers and softmax
+// agree on it.
+struct Interior {
+  int c_lo, c_hi, p_first, p_last, window;
+  __device__ __forceinline__ bool operator()(int tok0) const {
+    return tok0 >= c_lo && tok0 + PT <= c_hi && tok0 + PT - 1 <= p_first && (window <= 0 || tok0 > p_last - window);
+  }
+};
+
 template <int HD>
 __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4AttnArgs a, const Partials part) {
   using Smem = PromptSmem<HD>;
@@ -172,6 +315,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   const int j0 = c_lo / PT;
   const int steps = c_hi > c_lo ? (c_hi + PT - 1) / PT - j0 : 0;
   const int tiles = w.rows - w.r0 > PT ? 2 : 1;          // row tiles that hold rows
+  const Interior interior{c_lo, c_hi, p_first, p_last, a.window};
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(&S.q_full, 8);
@@ -191,7 +335,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     S.abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == PR_MMA) {
     ptx::tmem_alloc(&S.tmem_slot, 512);
     ptx::tmem_relinquish();
   }
@@ -200,37 +344,54 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_slot;
 
-  if (warp < 8) {
+  if (warp < PR_PROD0) {
     // ------------------------------------------------------------------------------- softmax
-    ptx::setmaxnreg_inc<PR_REG_SOFT>();
     const int i = warp >> 2;                             // row tile
     const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
     const int r = w.r0 + PT * i + row;
     const bool live = r < w.rows;
     const int rr = min(r, w.rows - 1);
-    const int64_t token = w.q0 + rr / group;
     const int head = w.kvh * group + rr % group;
+    float c_row;                                         // raw scores to log2 units, but for the keys' power of two
     {
-      const uint4* src = reinterpret_cast<const uint4*>(a.Q + token * a.ldq + head * HD);
-#pragma unroll
+      const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(w.q0 + rr / group) * a.ldq + head * HD);
+      float mq = 0.0f;
+#pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
-        const uint4 x = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = __ldg(src + c);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mq = fmaxf(mq, fmaxf(finite_or_0(__uint_as_float(y[q] << 16)), finite_or_0(__uint_as_float(y[q] & 0xFFFF0000u))));
+      }
+      const float eq = scale_exponent(mq);
+      const float f = live ? (a.scale < 0.0f ? -ex2(-eq) : ex2(-eq)) : 0.0f;
+      c_row = fabsf(a.scale) * kLog2e * ex2(eq);
+#pragma unroll 4
+      for (int c = 0; c < HD / 8; ++c) {
+        const uint4 x = __ldg(src + c);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[2 * q] = __uint_as_float(y[q] << 16) * f;
+          v[2 * q + 1] = __uint_as_float(y[q] & 0xFFFF0000u) * f;
+        }
         // channels 0 4 | 1 5 | 2 6 | 3 7
-        const uint4 y = make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
-                                   __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-        *reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(row, c % 8)) = y;
+        *reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(row, c % 8)) =
+            make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]), pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.q_full);
     }
-    const int pos = n - w.qlen + rr / group;
-    const int row_hi = min(pos, c_hi - 1), row_lo = a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo;
-    // whole tiles: every row of this warp's tile sees every token
-    const int t_first = n - w.qlen + min(w.rows - 1, w.r0 + PT * i) / group;
-    const int t_last = n - w.qlen + min(w.rows - 1, w.r0 + PT * i + PT - 1) / group;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_col = lane_base + S_COL + 128 * i, o_col = lane_base + O_COL + 128 * i;
+    auto view = [&](int j) {
+      const int sc = j % SC_RING, pos = n - w.qlen + rr / group;
+      return StepView{reinterpret_cast<const float4*>(S.ks[sc]), reinterpret_cast<const float4*>(S.vs[sc]), S.valid[sc], c_row,
+                      (j0 + j) * PT, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1)};
+    };
     float m = -INFINITY, l = 0.0f;
     bool ok = i < tiles;
     for (int j = 0; j < steps && ok; ++j) {
@@ -239,63 +400,32 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
            pr_warp_wait(&S.s_full[i], (uint32_t)j & 1u, &S.abort_flag, a.status);
       if (!ok) break;
       ptx::tc_fence_after();
-      const int tok0 = (j0 + j) * PT;
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
-      const bool whole = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && tok0 >= c_lo && tok0 + PT <= c_hi &&
-                         tok0 + PT - 1 <= t_first && (a.window <= 0 || tok0 > t_last - a.window);
-      uint64_t x[PT / 2];                                // scores in pairs, log2 domain
-      {
-        uint32_t* xr = reinterpret_cast<uint32_t*>(x);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(xr + 32 * c));
-        ptx::tmem_ld_wait();
-      }
-      float mx = -INFINITY, vm;
-      const float4* ks4 = reinterpret_cast<const float4*>(S.ks[sc]);
-      const float4* vs4 = reinterpret_cast<const float4*>(S.vs[sc]);
-#pragma unroll
-      for (int c = 0; c < PT / 4; ++c) {
-        const float4 k = ks4[c];
-        x[2 * c] = ptx::f2_mul(x[2 * c], ptx::f2_pack(k.x, k.y));
-        x[2 * c + 1] = ptx::f2_mul(x[2 * c + 1], ptx::f2_pack(k.z, k.w));
-      }
+      const bool whole = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && S.scaled[sc] != 0;
+      float mx, ve;
+      uint32_t xa[32], xb[32];                           // chunks 2 and 3 stay from the maximum to the exponentials
       if (whole) {
-        const float4 v4 = *reinterpret_cast<const float4*>(S.vmax[sc]);
-        vm = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
+        ptx::tmem_ld32(s_col, xa);
+        ptx::tmem_ld32(s_col + 32, xb);
+        const float4 kp = *reinterpret_cast<const float4*>(S.k_pow[sc]);
+        const float4 v4 = *reinterpret_cast<const float4*>(S.v_exp[sc]);
+        ve = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
+        ptx::tmem_ld_wait(xa);
+        mx = chunk_max(xa) * kp.x;
+        ptx::tmem_ld32(s_col + 64, xa);
+        ptx::tmem_ld_wait(xb);
+        mx = fmaxf(mx, chunk_max(xb) * kp.y);
+        ptx::tmem_ld32(s_col + 96, xb);
+        ptx::tmem_ld_wait(xa);
+        ptx::tmem_ld_wait(xb);
+        mx = fmaxf(mx, fmaxf(chunk_max(xa) * kp.z, chunk_max(xb) * kp.w)) * c_row;
       } else {
-        vm = 0.0f;
-#pragma unroll
-        for (int c = 0; c < PT / 4; ++c) {
-          const float4 v4 = vs4[c];
-          const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
-          const uint32_t bits = (c < 8 ? valid.x : c < 16 ? valid.y : c < 24 ? valid.z : valid.w) >> (4 * (c & 7));
-          float e[4];
-          ptx::f2_unpack(x[2 * c], e[0], e[1]);
-          ptx::f2_unpack(x[2 * c + 1], e[2], e[3]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int tok = tok0 + 4 * c + k;
-            const bool seen = ((bits >> k) & 1u) && tok >= row_lo && tok <= row_hi;
-            e[k] = seen ? e[k] : -INFINITY;
-            if (seen) vm = fmaxf(vm, finite_or_0(vv[k]));
-          }
-          x[2 * c] = ptx::f2_pack(e[0], e[1]);
-          x[2 * c + 1] = ptx::f2_pack(e[2], e[3]);
-        }
-      }
-      {
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < PT / 2; ++c) {
-          float e0, e1;
-          ptx::f2_unpack(x[c], e0, e1);
-          m0 = fmaxf(m0, e0);
-          m1 = fmaxf(m1, e1);
-        }
-        mx = fmaxf(m0, m1);
+        float vm = 0.0f;
+        mx = step_max_masked(s_col, view(j), vm);
+        ve = scale_exponent(vm);
       }
       // the reference: largest score plus the exponent of the largest value scale
-      const float cand = mx + scale_exponent(vm);
+      const float cand = mx + ve;
       const bool grow = cand > m + kLazy || (m == -INFINITY && cand > m);
       if (__any_sync(0xffffffffu, grow)) {
         const float m_new = grow ? cand : m;
@@ -310,7 +440,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           for (int c = 0; c < HD; c += 16) {
             uint32_t o[16];
             ptx::tmem_ld32x16(o_col + c, o);
-            ptx::tmem_ld_wait();
+            ptx::tmem_ld_wait(o);
 #pragma unroll
             for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
             ptx::tmem_st32x16(o_col + c, o);
@@ -318,138 +448,181 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      const uint64_t ref2 = ptx::f2_pack(-ref, -ref);
-      uint64_t sum0 = 0ull, sum1 = 0ull;
-#pragma unroll
-      for (int c = 0; c < PT / 32; ++c) {                // 32 tokens -> 16 columns of P
-        uint32_t p[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float4 v4 = vs4[8 * c + k];
-          float e[4];
-          ptx::f2_unpack(ptx::f2_add(x[16 * c + 2 * k], ref2), e[0], e[1]);
-          ptx::f2_unpack(ptx::f2_add(x[16 * c + 2 * k + 1], ref2), e[2], e[3]);
-          const uint64_t p0 = ptx::f2_pack(ex2(e[0]), ex2(e[1])), p1 = ptx::f2_pack(ex2(e[2]), ex2(e[3]));
-          sum0 = ptx::f2_add(sum0, p0);
-          sum1 = ptx::f2_add(sum1, p1);
-          float y[4];
-          ptx::f2_unpack(ptx::f2_mul(p0, ptx::f2_pack(v4.x, v4.y)), y[0], y[1]);
-          ptx::f2_unpack(ptx::f2_mul(p1, ptx::f2_pack(v4.z, v4.w)), y[2], y[3]);
-          if (!whole) {                                  // a hidden token's value scale may be anything
-#pragma unroll
-            for (int q = 0; q < 4; ++q) y[q] = e[q] == -INFINITY ? 0.0f : y[q];
-          }
-          p[2 * k] = pack_f16(y[0], y[1]);
-          p[2 * k + 1] = pack_f16(y[2], y[3]);
-        }
-        ptx::tmem_st32x16(s_col + 16 * c, p);
+      if (whole) {
+        const float4 kp = *reinterpret_cast<const float4*>(S.k_pow[sc]);
+        const float4 v4 = *reinterpret_cast<const float4*>(S.v_exp[sc]);
+        // each sum without its values' power of two
+        l = fmaf(chunk_exp(xa, c_row * kp.z, v4.z - ref, s_col + p_col(2)), ex2(-v4.z), l);
+        ptx::tmem_ld32(s_col, xa);
+        l = fmaf(chunk_exp(xb, c_row * kp.w, v4.w - ref, s_col + p_col(3)), ex2(-v4.w), l);
+        ptx::tmem_ld_wait(xa);
+        ptx::tmem_ld32(s_col + 32, xb);
+        l = fmaf(chunk_exp(xa, c_row * kp.x, v4.x - ref, s_col + p_col(0)), ex2(-v4.x), l);
+        ptx::tmem_ld_wait(xb);
+        l = fmaf(chunk_exp(xb, c_row * kp.y, v4.y - ref, s_col + p_col(1)), ex2(-v4.y), l);
+      } else {
+        l += step_exp_masked(s_col, view(j), ref);
       }
-      float a0, a1, a2, a3;
-      ptx::f2_unpack(sum0, a0, a1);
-      ptx::f2_unpack(sum1, a2, a3);
-      l += (a0 + a1) + (a2 + a3);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.p_full[i]);
     }
-    // ---- the row's output
+    // ---- the row's output, 32 channels at a time
     if (i < tiles) {
-      float o[HD];
       if (ok && steps > 0) ok = pr_warp_wait(&S.o_full[i], (uint32_t)(steps - 1) & 1u, &S.abort_flag, a.status);
-      if (ok && steps > 0) {
-        ptx::tc_fence_after();
-        uint32_t* od = reinterpret_cast<uint32_t*>(o);
+      ptx::tc_fence_after();
+      const bool some = ok && steps > 0;
+      const int64_t token = w.q0 + rr / group;
+      if (part.chunks > 1) {
+        const int64_t at = ((int64_t)w.chunk * a.T + token) * a.heads_q + head;
+        if (live) part.ml[at] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
+        if (some) {
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            load_channels(o, o_col + c);
+            if (live) {
+              float4* dst = reinterpret_cast<float4*>(part.o + at * HD + c);
 #pragma unroll
-        for (int c = 0; c < HD / 32; ++c) ptx::tmem_ld32(o_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(od + 32 * c));
-        ptx::tmem_ld_wait();
-        ptx::tc_fence_before();
-      } else {
-#pragma unroll
-        for (int c = 0; c < HD; ++c) o[c] = 0.0f;
-      }
-      if (live) {
-        // operand order -> channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4
-#pragma unroll
-        for (int c = 0; c < HD; c += 8) {
-          const float t1 = o[c + 1], t2 = o[c + 2], t3 = o[c + 3], t4 = o[c + 4], t5 = o[c + 5], t6 = o[c + 6];
-          o[c + 1] = t2, o[c + 2] = t4, o[c + 3] = t6, o[c + 4] = t1, o[c + 5] = t3, o[c + 6] = t5;
+              for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
         }
-        if (part.chunks > 1) {
-          const int64_t at = ((int64_t)w.chunk * a.T + token) * a.heads_q + head;
-          part.ml[at] = make_float2(m, l);
-          if (m != -INFINITY || l != 0.0f) {
-            float4* dst = reinterpret_cast<float4*>(part.o + at * HD);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(a.O + token * a.ldo + head * HD);
+        float f = l == 0.0f ? 0.0f : 1.0f / l;
+        if (!some) {
+          if (live)
+            for (int c = 0; c < HD / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+        } else if (!a.cache.rotate_v) {
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            load_channels(o, o_col + c);
+            if (live) {
 #pragma unroll
-            for (int c = 0; c < HD / 4; ++c) dst[c] = make_float4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+              for (int k = 0; k < 4; ++k) dst[c / 8 + k] = bf16x8(o + 8 * k, f);
+            }
           }
         } else {
-          float f = l == 0.0f ? 0.0f : 1.0f / l;
-          if (a.cache.rotate_v) {
+          // x H / sqrt(head_dim): the stages within 32 channels go back to tensor memory, those across them follow 8
+          // channels of each 32 at a time
+          f *= HD == 128 ? 0.08838834764831845f : 0.125f;
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            load_channels(o, o_col + c);
             fwht(o);
-            f *= HD == 128 ? 0.08838834764831845f : 0.125f;
-          }
-          uint4* dst = reinterpret_cast<uint4*>(a.O + token * a.ldo + head * HD);
 #pragma unroll
-          for (int c = 0; c < HD / 8; ++c)
-            dst[c] = make_uint4(pack_bf16(o[8 * c] * f, o[8 * c + 1] * f), pack_bf16(o[8 * c + 2] * f, o[8 * c + 3] * f),
-                                pack_bf16(o[8 * c + 4] * f, o[8 * c + 5] * f), pack_bf16(o[8 * c + 6] * f, o[8 * c + 7] * f));
+            for (int h = 0; h < 2; ++h) {
+              uint32_t y[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[16 * h + k]);
+              ptx::tmem_st32x16(o_col + c + 16 * h, y);
+            }
+          }
+          ptx::tmem_st_wait();
+#pragma unroll 1
+          for (int c = 0; c < 32; c += 16) {
+            constexpr int N32 = HD / 32;
+            float o[16][N32];
+#pragma unroll
+            for (int b = 0; b < N32; ++b) {
+              uint32_t x[16];
+              ptx::tmem_ld32x16(o_col + 32 * b + c, x);
+              ptx::tmem_ld_wait(x);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k][b] = __uint_as_float(x[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) fwht(o[k]);
+            if (live) {
+#pragma unroll
+              for (int b = 0; b < N32; ++b)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float y[8];
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) y[k] = o[8 * h + k][b];
+                  dst[4 * b + c / 8 + h] = bf16x8(y, f);
+                }
+            }
+          }
         }
       }
+      ptx::tc_fence_before();
     }
-  } else if (warp < 12) {
+  } else if (warp < PR_MMA) {
     // ----------------------------------------------------------------------------- producers
-    ptx::setmaxnreg_dec<PR_REG_PROD>();
-    const int t = threadIdx.x - 256;                     // token of the step
-    const int wq = warp - 8;
+    const int t = threadIdx.x - 32 * PR_PROD0;           // token of the step
+    const int wq = warp - PR_PROD0;
     const int32_t* table = a.table + w.b * a.table_stride;
-    const float c_log2 = a.scale * kLog2e;
     uint4 kx[HB / 16], vx[HB / 16];
-    float ks = 0.0f, vs = 0.0f;
-    bool valid = false;
-    auto load = [&](int j) {
+    float ks, vs;
+    int64_t at = -1, at_next = -1;                       // cache row of the token (-1: none), one step ahead
+    auto locate = [&](int j) {
       const int tok = (j0 + j) * PT + t;
-      valid = false;
-      int64_t at = 0;
-      if (tok < n) {
+      at_next = -1;
+      if (tok < n && j < steps) {
         const int page = table[tok >> ps];
         if (page < 0 || page >= a.cache.pages) atomicOr(a.status, PQ_DEV_BAD_INDEX);
-        else {
-          valid = true;
-          at = (((int64_t)page * a.cache.heads + w.kvh) << ps) + (tok & ((1 << ps) - 1));
-        }
+        else at_next = (((int64_t)page * a.cache.heads + w.kvh) << ps) + (tok & ((1 << ps) - 1));
       }
-#pragma unroll
-      for (int c = 0; c < HB / 16; ++c) {
-        kx[c] = valid ? __ldg(reinterpret_cast<const uint4*>(a.cache.k_codes + at * HB) + c) : make_uint4(0u, 0u, 0u, 0u);
-        vx[c] = valid ? __ldg(reinterpret_cast<const uint4*>(a.cache.v_codes + at * HB) + c) : make_uint4(0u, 0u, 0u, 0u);
-      }
-      ks = valid ? __ldg(a.cache.k_scales + at) * c_log2 : 0.0f;
-      vs = valid ? __ldg(a.cache.v_scales + at) : 0.0f;
     };
-    if (steps > 0) load(0);
+    auto load = [&](uint4 (&x)[HB / 16], float& sc, const uint8_t* codes, const float* scales, int64_t r) {
+#pragma unroll
+      for (int c = 0; c < HB / 16; ++c)
+        x[c] = r >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + r * HB) + c) : make_uint4(0u, 0u, 0u, 0u);
+      sc = r >= 0 ? __ldg(scales + r) : 0.0f;
+    };
+    locate(0);
+    at = at_next;
+    load(kx, ks, a.cache.k_codes, a.cache.k_scales, at);
+    load(vx, vs, a.cache.v_codes, a.cache.v_scales, at);
+    locate(1);
     for (int j = 0; j < steps; ++j) {
       const int s = j % PR_STAGES, sc = j % SC_RING;
       const uint32_t reuse = ((uint32_t)(j / PR_STAGES) & 1u) ^ 1u;
       if (!pr_warp_wait(&S.k_empty[s], reuse, &S.abort_flag, a.status)) break;
-      S.ks[sc][t] = ks;
-      S.vs[sc][t] = vs;
-      const uint32_t bits = __ballot_sync(0xffffffffu, valid);
-      float vm = finite_or_0(vs);
+      const bool scaled = interior((j0 + j) * PT);
+      const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
+      float km = finite_or_0(ks), vm = finite_or_0(vs);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-      if (lane == 0) {
-        S.valid[sc][wq] = bits;
-        S.vmax[sc][wq] = vm;
+      for (int o = 16; o > 0; o >>= 1) {
+        km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
+        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
       }
+      const float ke = scale_exponent(km), ve = scale_exponent(vm);
+      S.ks[sc][t] = scaled ? ex2(ke) : ks;
+      S.vs[sc][t] = scaled ? ex2(ve) : vs;
+      if (lane == 0) {
+        if (wq == 0) S.scaled[sc] = scaled ? 1 : 0;
+        S.valid[sc][wq] = bits;
+        S.k_pow[sc][wq] = ex2(ke);
+        S.v_exp[sc][wq] = ve;
+      }
+      // code * scale in one rounding: scale as fp16 high and low parts, code * low below the fused multiply-add
+      const float kn = ks * ex2(-ke);
+      const __half2 k_hi = __float2half2_rn(kn), k_lo = __float2half2_rn(kn - __low2float(k_hi));
+      const __half2 v_hi = __float2half2_rn(vs * ex2(-ve));
 #pragma unroll
       for (int c = 0; c < HB / 16; ++c) {
         const uint32_t x[4] = {kx[c].x, kx[c].y, kx[c].z, kx[c].w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {                    // a word: 8 channels, one 16-byte chunk
           const int ch = 4 * c + q;
-          *reinterpret_cast<uint4*>(S.k[s][ch / 8] + sw128(t, ch % 8)) =
-              make_uint4(code_pair_bf16(x[q], 0), code_pair_bf16(x[q], 4), code_pair_bf16(x[q], 8), code_pair_bf16(x[q], 12));
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[k] = code_pair(x[q], 4 * k);
+            if (scaled) {
+              const __half2 code = *reinterpret_cast<const __half2*>(&y[k]);
+              const __half2 z = __hfma2(code, k_hi, __hmul2(code, k_lo));
+              y[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          *reinterpret_cast<uint4*>(S.k[s][ch / 8] + sw128(t, ch % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       ptx::fence_proxy_async_smem();
@@ -458,6 +631,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         ptx::mbar_arrive(&S.sc_full[sc]);
         ptx::mbar_arrive(&S.k_full[s]);
       }
+      // the next step's keys, under this step's values (and the other way round below)
+      load(kx, ks, a.cache.k_codes, a.cache.k_scales, at_next);
       if (!pr_warp_wait(&S.v_empty[s], reuse, &S.abort_flag, a.status)) break;
 #pragma unroll
       for (int c = 0; c < HB / 16; ++c) {
@@ -465,69 +640,101 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int ch = 4 * c + q;
-          *reinterpret_cast<uint4*>(S.v[s][ch / 8] + sw128(t, ch % 8)) =
-              make_uint4(code_pair(x[q], 0), code_pair(x[q], 4), code_pair(x[q], 8), code_pair(x[q], 12));
+          uint32_t y[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            y[k] = code_pair(x[q], 4 * k);
+            if (scaled) {
+              const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), v_hi);
+              y[k] = *reinterpret_cast<const uint32_t*>(&z);
+            }
+          }
+          *reinterpret_cast<uint4*>(S.v[s][ch / 8] + sw128(t, ch % 8)) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&S.v_full[s]);
-      if (j + 1 < steps) load(j + 1);
+      load(vx, vs, a.cache.v_codes, a.cache.v_scales, at_next);
+      at = at_next;
+      locate(j + 2);
     }
-  } else {
-    ptx::setmaxnreg_dec<PR_REG_CTRL>();
-    if (warp == 12 && lane == 0 && steps > 0) {
+  } else if (warp == PR_MMA) {
+    if (steps > 0) {
       // ------------------------------------------------------------------------- MMA issue
-      constexpr uint32_t id_s = idesc_f16(1, 0, PT), id_o = idesc_f16(0, 1, HD);
+      // The whole warp walks the steps and one elected lane issues: descriptors stay in uniform registers.
+      constexpr uint32_t id_s = idesc_f16(0, PT), id_o = idesc_f16(1, HD);
+      // Descriptors of the operands' first tiles; an offset of b bytes adds b / 16 to the address field.
+      const uint64_t dq = ptx::smem_desc_sw128(ptx::smem_addr(S.q[0][0])), dk = ptx::smem_desc_sw128(ptx::smem_addr(S.k[0][0]));
+      const uint64_t dv = ptx::smem_desc_sw128_mn(ptx::smem_addr(S.v[0][0]), PT * 128);
+      constexpr uint64_t kTile = Smem::KBLK * PT * 128 / 16;
       auto mma_s = [&](int i, int s) {
-        const uint32_t q0 = ptx::smem_addr(S.q[i][0]), k0 = ptx::smem_addr(S.k[s][0]);
+        const uint64_t q = dq + (uint64_t)i * kTile, k0 = dk + (uint64_t)s * kTile;
+        if (ptx::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < HD / 16; ++k) {
-          const uint32_t off = (uint32_t)((k / 4) * PT * 128 + 32 * (k % 4));
-          ptx::umma_f16(tmem + S_COL + 128 * i, ptx::smem_desc_sw128(q0 + off), ptx::smem_desc_sw128(k0 + off), id_s,
-                        k > 0 ? 1u : 0u);
+          for (int k = 0; k < HD / 16; ++k) {
+            constexpr uint64_t kBlock = PT * 128 / 16;
+            const uint64_t off = (uint64_t)(k / 4) * kBlock + 2 * (k % 4);
+            ptx::umma_f16(tmem + S_COL + 128 * i, q + off, k0 + off, id_s, k > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit(&S.s_full[i]);
         }
-        ptx::umma_commit(&S.s_full[i]);
+        __syncwarp();
       };
       auto mma_o = [&](int i, int s, bool first) {
-        const uint32_t v0 = ptx::smem_addr(S.v[s][0]);
+        const uint64_t v0 = dv + (uint64_t)s * kTile;
+        if (ptx::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < PT / 16; ++k)
-          ptx::umma_f16_ts(tmem + O_COL + 128 * i, tmem + S_COL + 128 * i + 8 * k,
-                           ptx::smem_desc_sw128_mn(v0 + 2048 * k, PT * 128), id_o, first && k == 0 ? 0u : 1u);
-        ptx::umma_commit(&S.o_full[i]);
+          for (int k = 0; k < PT / 16; ++k)
+            ptx::umma_f16_ts(tmem + O_COL + 128 * i, tmem + S_COL + 128 * i + p_col(k / 2) + 8 * (k % 2), v0 + 128 * k, id_o,
+                             first && k == 0 ? 0u : 1u);
+          ptx::umma_commit(&S.o_full[i]);
+        }
+        __syncwarp();
       };
-      bool ok = pr_wait(&S.q_full, 0, &S.abort_flag, a.status) && pr_wait(&S.k_full[0], 0, &S.abort_flag, a.status);
+      auto commit = [&](uint64_t* bar) {
+        if (ptx::elect_one()) ptx::umma_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return pr_warp_wait(bar, parity, &S.abort_flag, a.status); };
+      bool ok = wait(&S.q_full, 0) && wait(&S.k_full[0], 0);
       if (ok) {
         ptx::tc_fence_after();
         for (int i = 0; i < tiles; ++i) mma_s(i, 0);
-        ptx::umma_commit(&S.k_empty[0]);
+        commit(&S.k_empty[0]);
       }
       for (int j = 0; j < steps && ok; ++j) {
         const int s = j % PR_STAGES, s1 = (j + 1) % PR_STAGES;
         const bool more = j + 1 < steps;
-        if (!(ok = pr_wait(&S.v_full[s], (uint32_t)(j / PR_STAGES) & 1u, &S.abort_flag, a.status))) break;
-        if (more && !(ok = pr_wait(&S.k_full[s1], (uint32_t)((j + 1) / PR_STAGES) & 1u, &S.abort_flag, a.status))) break;
+        if (!(ok = wait(&S.v_full[s], (uint32_t)(j / PR_STAGES) & 1u))) break;
         for (int i = 0; i < tiles; ++i) {
-          if (!(ok = pr_wait(&S.p_full[i], (uint32_t)j & 1u, &S.abort_flag, a.status))) break;
+          if (!(ok = wait(&S.p_full[i], (uint32_t)j & 1u))) break;
           ptx::tc_fence_after();
           mma_o(i, s, j == 0);
           // MMAs of one thread run in order: S_i is overwritten after its probabilities have been read
-          if (more) mma_s(i, s1);
+          if (more) {
+            if (i == 0) {
+              if (!(ok = wait(&S.k_full[s1], (uint32_t)((j + 1) / PR_STAGES) & 1u))) break;
+              ptx::tc_fence_after();
+            }
+            mma_s(i, s1);
+          }
         }
         if (!ok) break;
-        ptx::umma_commit(&S.v_empty[s]);
-        if (more) ptx::umma_commit(&S.k_empty[s1]);
+        commit(&S.v_empty[s]);
+        if (more) commit(&S.k_empty[s1]);
       }
-      ptx::umma_commit(&S.mma_done);
-      int never = 0;
-      (void)ptx::mbar_wait_bounded(&S.mma_done, 0, &never, kPrWaitNs);
+      commit(&S.mma_done);
+      if (lane == 0) {
+        int never = 0;
+        (void)ptx::mbar_wait_bounded(&S.mma_done, 0, &never, kPrWaitNs);
+      }
     }
   }
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == PR_MMA) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
@@ -540,18 +747,6 @@ pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tile
   static std::atomic<bool> done[kMaxDevices];
   cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(kv4_prompt_kernel<HD>), (int)smem, done);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_prompt_kernel attributes");
-  // The warp roles re-divide the launch's registers, which works only if it was compiled with exactly that many.
-  static std::atomic<int> regs{-1};
-  if (regs.load(std::memory_order_relaxed) < 0) {
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, kv4_prompt_kernel<HD>);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(prompt)");
-    regs.store(fa.numRegs, std::memory_order_relaxed);
-  }
-  if (regs.load(std::memory_order_relaxed) != (int)PR_REG_LAUNCH) {
-    set_error("kv4_prompt_kernel compiled with %d registers per thread, %u expected", regs.load(), PR_REG_LAUNCH);
-    return PQ_ERR_CUDA;
-  }
   const int64_t grid = tiles * a.cache.heads * part.chunks;
   if (grid >= ((int64_t)1 << 31)) { set_error("too many query tiles for one call"); return PQ_ERR_INVALID_ARG; }
   kv4_prompt_kernel<HD><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);

@@ -197,7 +197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_p
       for (int c = 0; c < P_EPI_COLS / 32; ++c) {
         uint32_t r[32];
         ptx::tmem_ld32(col0 + 32 * c, r);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(r);
         if (c == P_EPI_COLS / 32 - 1) {
           ptx::tc_fence_before();
           __syncwarp();
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
       uint32_t r[16];
       if (some && ok) {
         ptx::tmem_ld32x16(col0 + c, r);
-        ptx::tmem_ld_wait();
+        ptx::tmem_ld_wait(r);
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = 0u;

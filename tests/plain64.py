@@ -91,13 +91,18 @@ def unpack(codes, scales):
 
 
 # ------------------------------------------------------------------------------------- attention
-def attention64(cache, Q, q_start, seq_lens, table, scale, window, out):
+def attention64(cache, Q, q_start, seq_lens, table, scale, window, out, fp16_operands=False):
     """(output, bound) in float64: `out` (float64) with the sequences' rows replaced.
 
     The bound per element: each probability's fp16 rounding (2^-11 relative, and 2^-25 of the largest scale
     where it leaves fp16's normal range), the scores' float32 sums (the operands 136 + code are summed with the
     queries, so 16 * 9 magnitudes per channel; the exponent sees them twice, in the numerator and the sum),
-    float32 accumulation over the tokens, and half a bf16 step of the result."""
+    float32 accumulation over the tokens, and half a bf16 step of the result.
+
+    fp16_operands (calls of many rows, where scales are multiplied into fp16 keys and values): each product of a code
+    and its key scale is off by 2^-11 of it at most (one rounding; the low part of the scale adds 2^-21), or 2^-25 of
+    the largest scale below fp16's normal range, and so is each query channel; each value by 2^-11 twice (its scale,
+    then the product), or 2^-25 of the largest."""
     kc, ks, vc, vs = cache.tensors
     hd, hkv, page = cache.head_dim, cache.heads, cache.page_size
     T = Q.shape[0]
@@ -129,16 +134,21 @@ def attention64(cache, Q, q_start, seq_lens, table, scale, window, out):
             x = q[first:last, h]
             s = (x @ k_code[kv].t()) * k_s[kv] * scale
             s_err = (x.abs().sum(-1, keepdim=True) * 144 * 140 * 2 * U) * k_s[kv].abs() * abs(scale) + 4 * U * s.abs()
+            if fp16_operands:
+                mag = k_code[kv].abs()
+                small = x.abs().amax(-1, keepdim=True) * 2.0 ** -24
+                s_err = s_err + abs(scale) * ((x.abs() @ mag.t()) * (2.0 ** -11 + 2.0 ** -20) * k_s[kv] +
+                                              x.abs().sum(-1, keepdim=True) * 8 * 2.0 ** -24 * k_s[kv].max() + small * mag.sum(-1) * k_s[kv])
             s = s.masked_fill(hidden, -math.inf)
             top = s.amax(-1, keepdim=True)
             p = torch.where(hidden, torch.zeros_like(s), torch.exp(s - torch.where(top.isfinite(), top, torch.zeros_like(top))))
             total = p.sum(-1, keepdim=True)
             p = torch.where(total > 0, p / total, torch.zeros_like(p))
             vv = torch.where(hidden.all(0)[:, None], torch.zeros_like(v[kv]), v[kv])   # never seen: anything may be there
-            pe = p * (2.0 ** -11 + 2 * torch.where(hidden, torch.zeros_like(s_err), s_err).amax(-1, keepdim=True) + (n + 64) * 2 * U)
+            pe = p * ((3 if fp16_operands else 1) * 2.0 ** -11 + 2 * torch.where(hidden, torch.zeros_like(s_err), s_err).amax(-1, keepdim=True) + (n + 64) * 2 * U)
             seen_vs = torch.where(hidden, torch.zeros_like(s), v_s[kv].expand_as(s)).amax(-1, keepdim=True)
             o = p @ vv
-            e = pe @ vv.abs() + torch.where(total > 0, 8 * n * seen_vs * 2.0 ** -25 / total.clamp_min(1e-300), torch.zeros_like(total))
+            e = pe @ vv.abs() + torch.where(total > 0, (2 if fp16_operands else 1) * 8 * n * seen_vs * 2.0 ** -25 / total.clamp_min(1e-300), torch.zeros_like(total))
             if H is not None:
                 o = o @ H
                 e = (e.sum(-1, keepdim=True) / math.sqrt(hd) * (1 + 10 * U)).expand_as(o) + 16 * U * o.abs().amax(-1, keepdim=True)
