@@ -3,19 +3,21 @@
 //   s_t = scale (q . kc_t) ks_t,  o = sum_t softmax(s)_t vs_t vc_t,  all sums float32.
 //
 // The query rows of one key/value head (row = new token x head of the group) come in tiles of 128 = the lanes of tensor
-// memory; a CTA takes two tiles (256 rows) and walks the cached tokens 128 at a time:
-//   S_i = Q_i K^T   (fp16, M128 N128)       into 128 columns of tensor memory, i = 0, 1
+// memory; a CTA takes two tiles (256 rows, i = 0, 1) and walks the cached tokens 128 at a time, staged once for both,
+// in halves of 64:
+//   S_i = Q_i K^T   (fp16, M128 N64)        into 64 columns of tensor memory, two buffers a tile
 //   P_i = softmax numerators, fp16, written over S_i's columns
 //   O_i += P_i V    (A from tensor memory, M128 N head_dim) into head_dim more columns
-// While the tensor cores work for one tile, the other's softmax runs; both tiles share each 128 keys and values, so a
-// code is unpacked once per 256 rows.  The tensor cores and the exponentials (16 a clock and SM) are about evenly
-// loaded: 2 x 128 x 128 x head_dim multiply-adds against 128 x 128 exponentials a tile and step.
+// The scores of the next half are computed before the probabilities of this one are awaited, so a tile's softmax finds
+// them ready: with one buffer of 128 it waited for the products of every step (5000 of 9000 cycles, measured).  The
+// tensor cores and the exponentials (16 a clock and SM) are about evenly loaded: 2 x 128 x 128 x head_dim multiply-adds
+// against 128 x 128 exponentials a tile and step.
 //   warps 0..3, 4..7   softmax of tile 0, 1: a thread owns a row: its scores from tensor memory, maximum, exponentials,
 //                      P back; O is rescaled in tensor memory only when the row's reference grows by more than 2^8
 //                      (P stays below 2^8, which fp16 holds); at the end its output row.
 //   warps 8..11        producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
-//   warp 12            tensor memory and MMA issue.
+//   warps 12, 13       MMA issue for tile 0, 1 (12: tensor memory).
 // Nothing may spill: the operands leave so little of the L1 cache that a spilled register comes back from L2.
 //
 // Where the scales go.  A step whose 128 tokens every row of the block sees takes keys and values with their scales
@@ -47,12 +49,13 @@ namespace pq {
 namespace {
 
 constexpr int PT = 128;                  // rows per tile and tokens per step
-constexpr int PR_THREADS = 416;
-constexpr int PR_PROD0 = 8, PR_MMA = 12;                 // first producer warp, MMA warp
+constexpr int PR_THREADS = 448;
+constexpr int PR_PROD0 = 8, PR_MMA = 12;                 // first producer warp, first MMA warp
+constexpr int HT = PT / 2;               // tokens of a half step
 constexpr int PR_STAGES = 2;             // key and value stages
 constexpr int SC_RING = 4;               // scale stages: a step's scales outlive its keys by at most one step
 constexpr uint64_t kPrWaitNs = 2000000000ull;
-constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i, O_i at 256 + 128 i
+constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i + 64 (half & 1), O_i at 256 + 128 i
 constexpr float kLazy = 8.0f;            // log2 growth of the reference that is let pass
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
@@ -74,14 +77,14 @@ struct __align__(1024) PromptSmem {
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
   uint64_t sc_full[SC_RING];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2][2], p_full[2][2], o_full[2][2];     // [tile][half step & 1]
   uint64_t mma_done;
   uint32_t tmem_slot;
   int abort_flag;
 };
 
 __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
-  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, 16)) return true;
+  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, 200)) return true;
   *abort_flag = 1;
   atomicOr(status, PQ_DEV_TIMEOUT);
   return false;
@@ -168,10 +171,6 @@ struct StepView {
   }
 };
 
-// First column of the probabilities of 32 tokens (chunk c of 4) within a tile's 128 score columns: chunks 0 and 1 are
-// read a second time after the probabilities of 2 and 3 have been written, so those stay clear of their columns.
-__host__ __device__ constexpr int p_col(int c) { return 64 + 16 * ((c + 2) & 3); }
-
 // Largest of 32 raw scores.
 __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -217,47 +216,47 @@ __device__ __forceinline__ void masked_scores(const uint32_t (&r)[16], int t, co
   }
 }
 
-// Maximum of the row's 128 scores of a step with hidden tokens (log2 units), and the largest value scale seen.
-__device__ __forceinline__ float step_max_masked(uint32_t s_col, const StepView& v, float& vm) {
+// Maximum of the row's 64 scores of a half step with hidden tokens (log2 units; tokens t0 .. of the step), and the
+// largest value scale seen.
+__device__ __forceinline__ float half_max_masked(uint32_t s_col, int t0, const StepView& v, float& vm) {
   float top = -INFINITY;
 #pragma unroll 1
-  for (int t = 0; t < PT; t += 16) {
+  for (int t = 0; t < HT; t += 16) {
     uint32_t r[16];
     float e[16];
     ptx::tmem_ld32x16(s_col + t, r);
     ptx::tmem_ld_wait(r);
-    masked_scores(r, t, v, e);
-    const float* vs = reinterpret_cast<const float*>(v.vs) + t;
+    masked_scores(r, t0 + t, v, e);
+    const float* vs = reinterpret_cast<const float*>(v.vs) + t0 + t;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       top = fmaxf(top, e[k]);
-      if (v.sees(t + k)) vm = fmaxf(vm, finite_or_0(vs[k]));
+      if (v.sees(t0 + t + k)) vm = fmaxf(vm, finite_or_0(vs[k]));
     }
   }
   return top;
 }
 
 // Their probabilities, written over scores already read; returns their sum.
-__device__ __forceinline__ float step_exp_masked(uint32_t s_col, const StepView& v, float ref) {
+__device__ __forceinline__ float half_exp_masked(uint32_t s_col, int t0, const StepView& v, float ref) {
   float sum = 0.0f;
 #pragma unroll 1
-  for (int d = 0; d < PT; d += 16) {
-    const int t = (d + 64) & 127;                        // chunks 2, 3, 0, 1: none is overwritten before it is read
+  for (int t = 0; t < HT; t += 16) {
     uint32_t r[16], p[8];
     float e[16];
     ptx::tmem_ld32x16(s_col + t, r);
     ptx::tmem_ld_wait(r);
-    masked_scores(r, t, v, e);
-    const float* vs = reinterpret_cast<const float*>(v.vs) + t;
+    masked_scores(r, t0 + t, v, e);
+    const float* vs = reinterpret_cast<const float*>(v.vs) + t0 + t;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float x = ex2(e[k] - ref);
       sum += x;
-      e[k] = v.sees(t + k) ? x * vs[k] : 0.0f;           // a hidden token's value scale may be anything
+      e[k] = v.sees(t0 + t + k) ? x * vs[k] : 0.0f;      // a hidden token's value scale may be anything
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) p[k] = pack_f16(e[2 * k], e[2 * k + 1]);
-    ptx::tmem_st32x8(s_col + 64 + d / 2, p);
+    ptx::tmem_st32x8(s_col + t / 2, p);
   }
   return sum;
 }
@@ -321,17 +320,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     ptx::mbar_init(&S.q_full, 8);
     for (int s = 0; s < PR_STAGES; ++s) {
       ptx::mbar_init(&S.k_full[s], 4);
-      ptx::mbar_init(&S.k_empty[s], 1);
+      ptx::mbar_init(&S.k_empty[s], tiles);
       ptx::mbar_init(&S.v_full[s], 4);
-      ptx::mbar_init(&S.v_empty[s], 1);
+      ptx::mbar_init(&S.v_empty[s], tiles);
     }
     for (int s = 0; s < SC_RING; ++s) ptx::mbar_init(&S.sc_full[s], 4);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&S.s_full[i], 1);
-      ptx::mbar_init(&S.p_full[i], 4);
-      ptx::mbar_init(&S.o_full[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        ptx::mbar_init(&S.s_full[i][b], 1);
+        ptx::mbar_init(&S.p_full[i][b], 4);
+        ptx::mbar_init(&S.o_full[i][b], 1);
+      }
     }
-    ptx::mbar_init(&S.mma_done, 1);
+    ptx::mbar_init(&S.mma_done, tiles);
     S.abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -394,34 +395,31 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     };
     float m = -INFINITY, l = 0.0f;
     bool ok = i < tiles;
-    for (int j = 0; j < steps && ok; ++j) {
-      const int sc = j % SC_RING;
-      ok = pr_warp_wait(&S.sc_full[sc], (uint32_t)(j / SC_RING) & 1u, &S.abort_flag, a.status) &&
-           pr_warp_wait(&S.s_full[i], (uint32_t)j & 1u, &S.abort_flag, a.status);
+    for (int h = 0; h < 2 * steps && ok; ++h) {            // half steps
+      const int j = h >> 1, sc = j % SC_RING, t0 = HT * (h & 1);
+      const uint32_t s_buf = s_col + HT * (h & 1);
+      if (t0 == 0) ok = pr_warp_wait(&S.sc_full[sc], (uint32_t)(j / SC_RING) & 1u, &S.abort_flag, a.status);
+      ok = ok && pr_warp_wait(&S.s_full[i][h & 1], (uint32_t)j & 1u, &S.abort_flag, a.status);
       if (!ok) break;
       ptx::tc_fence_after();
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
       const bool whole = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && S.scaled[sc] != 0;
       float mx, ve;
-      uint32_t xa[32], xb[32];                           // chunks 2 and 3 stay from the maximum to the exponentials
+      float2 kp, v2;                                     // of the half's two groups of 32 tokens
+      uint32_t xa[32], xb[32];                           // their scores
       if (whole) {
-        ptx::tmem_ld32(s_col, xa);
-        ptx::tmem_ld32(s_col + 32, xb);
-        const float4 kp = *reinterpret_cast<const float4*>(S.k_pow[sc]);
-        const float4 v4 = *reinterpret_cast<const float4*>(S.v_exp[sc]);
-        ve = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
-        ptx::tmem_ld_wait(xa);
-        mx = chunk_max(xa) * kp.x;
-        ptx::tmem_ld32(s_col + 64, xa);
-        ptx::tmem_ld_wait(xb);
-        mx = fmaxf(mx, chunk_max(xb) * kp.y);
-        ptx::tmem_ld32(s_col + 96, xb);
+        ptx::tmem_ld32(s_buf, xa);
+        ptx::tmem_ld32(s_buf + 32, xb);
+        kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
+        v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
+        kp.x *= c_row, kp.y *= c_row;
+        ve = fmaxf(v2.x, v2.y);
         ptx::tmem_ld_wait(xa);
         ptx::tmem_ld_wait(xb);
-        mx = fmaxf(mx, fmaxf(chunk_max(xa) * kp.z, chunk_max(xb) * kp.w)) * c_row;
+        mx = fmaxf(chunk_max(xa) * kp.x, chunk_max(xb) * kp.y);
       } else {
         float vm = 0.0f;
-        mx = step_max_masked(s_col, view(j), vm);
+        mx = half_max_masked(s_buf, t0, view(j), vm);
         ve = scale_exponent(vm);
       }
       // the reference: largest score plus the exponent of the largest value scale
@@ -432,8 +430,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         const float f = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
         m = m_new;
         l *= f;
-        if (j > 0) {
-          ok = pr_warp_wait(&S.o_full[i], (uint32_t)(j - 1) & 1u, &S.abort_flag, a.status);
+        if (h > 0) {
+          ok = pr_warp_wait(&S.o_full[i][(h - 1) & 1], (uint32_t)((h - 1) >> 1) & 1u, &S.abort_flag, a.status);
           if (!ok) break;
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -449,28 +447,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       }
       const float ref = m == -INFINITY ? 0.0f : m;
       if (whole) {
-        const float4 kp = *reinterpret_cast<const float4*>(S.k_pow[sc]);
-        const float4 v4 = *reinterpret_cast<const float4*>(S.v_exp[sc]);
         // each sum without its values' power of two
-        l = fmaf(chunk_exp(xa, c_row * kp.z, v4.z - ref, s_col + p_col(2)), ex2(-v4.z), l);
-        ptx::tmem_ld32(s_col, xa);
-        l = fmaf(chunk_exp(xb, c_row * kp.w, v4.w - ref, s_col + p_col(3)), ex2(-v4.w), l);
-        ptx::tmem_ld_wait(xa);
-        ptx::tmem_ld32(s_col + 32, xb);
-        l = fmaf(chunk_exp(xa, c_row * kp.x, v4.x - ref, s_col + p_col(0)), ex2(-v4.x), l);
-        ptx::tmem_ld_wait(xb);
-        l = fmaf(chunk_exp(xb, c_row * kp.y, v4.y - ref, s_col + p_col(1)), ex2(-v4.y), l);
+        l = fmaf(chunk_exp(xa, kp.x, v2.x - ref, s_buf), ex2(-v2.x), l);
+        l = fmaf(chunk_exp(xb, kp.y, v2.y - ref, s_buf + 16), ex2(-v2.y), l);
       } else {
-        l += step_exp_masked(s_col, view(j), ref);
+        l += half_exp_masked(s_buf, t0, view(j), ref);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&S.p_full[i]);
+      if (lane == 0) ptx::mbar_arrive(&S.p_full[i][h & 1]);
     }
     // ---- the row's output, 32 channels at a time
     if (i < tiles) {
-      if (ok && steps > 0) ok = pr_warp_wait(&S.o_full[i], (uint32_t)(steps - 1) & 1u, &S.abort_flag, a.status);
+      if (ok && steps > 0) ok = pr_warp_wait(&S.o_full[i][1], (uint32_t)(steps - 1) & 1u, &S.abort_flag, a.status);
       ptx::tc_fence_after();
       const bool some = ok && steps > 0;
       const int64_t token = w.q0 + rr / group;
@@ -659,72 +649,67 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       at = at_next;
       locate(j + 2);
     }
-  } else if (warp == PR_MMA) {
-    if (steps > 0) {
+  } else {
+    const int i = warp - PR_MMA;                         // row tile
+    if (i < tiles && steps > 0) {
       // ------------------------------------------------------------------------- MMA issue
-      // The whole warp walks the steps and one elected lane issues: descriptors stay in uniform registers.
-      constexpr uint32_t id_s = idesc_f16(0, PT), id_o = idesc_f16(1, HD);
+      // The whole warp walks the half steps and one elected lane issues: descriptors stay in uniform registers.
+      constexpr uint32_t id_s = idesc_f16(0, HT), id_o = idesc_f16(1, HD);
       // Descriptors of the operands' first tiles; an offset of b bytes adds b / 16 to the address field.
-      const uint64_t dq = ptx::smem_desc_sw128(ptx::smem_addr(S.q[0][0])), dk = ptx::smem_desc_sw128(ptx::smem_addr(S.k[0][0]));
+      constexpr uint64_t kTile = Smem::KBLK * PT * 128 / 16, kBlock = PT * 128 / 16, kHalf = HT * 128 / 16;
+      const uint64_t dq = ptx::smem_desc_sw128(ptx::smem_addr(S.q[i][0]));
+      const uint64_t dk = ptx::smem_desc_sw128(ptx::smem_addr(S.k[0][0]));
       const uint64_t dv = ptx::smem_desc_sw128_mn(ptx::smem_addr(S.v[0][0]), PT * 128);
-      constexpr uint64_t kTile = Smem::KBLK * PT * 128 / 16;
-      auto mma_s = [&](int i, int s) {
-        const uint64_t q = dq + (uint64_t)i * kTile, k0 = dk + (uint64_t)s * kTile;
+      const uint32_t s_col = tmem + S_COL + 128 * i, o_col = tmem + O_COL + 128 * i;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return pr_warp_wait(bar, parity, &S.abort_flag, a.status); };
+      // Scores of half step h; its second half is the last to read the keys' stage.
+      auto scores = [&](int h) {
+        const int j = h >> 1, st = j % PR_STAGES;
+        const uint64_t k0 = dk + (uint64_t)st * kTile + (uint64_t)(h & 1) * kHalf;
+        const uint32_t d = s_col + HT * (h & 1);
         if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
-            constexpr uint64_t kBlock = PT * 128 / 16;
             const uint64_t off = (uint64_t)(k / 4) * kBlock + 2 * (k % 4);
-            ptx::umma_f16(tmem + S_COL + 128 * i, q + off, k0 + off, id_s, k > 0 ? 1u : 0u);
+            ptx::umma_f16(d, dq + off, k0 + off, id_s, k > 0 ? 1u : 0u);
           }
-          ptx::umma_commit(&S.s_full[i]);
+          ptx::umma_commit(&S.s_full[i][h & 1]);
+          if (h & 1) ptx::umma_commit(&S.k_empty[st]);
         }
         __syncwarp();
       };
-      auto mma_o = [&](int i, int s, bool first) {
-        const uint64_t v0 = dv + (uint64_t)s * kTile;
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < PT / 16; ++k)
-            ptx::umma_f16_ts(tmem + O_COL + 128 * i, tmem + S_COL + 128 * i + p_col(k / 2) + 8 * (k % 2), v0 + 128 * k, id_o,
-                             first && k == 0 ? 0u : 1u);
-          ptx::umma_commit(&S.o_full[i]);
-        }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (ptx::elect_one()) ptx::umma_commit(bar);
-        __syncwarp();
-      };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return pr_warp_wait(bar, parity, &S.abort_flag, a.status); };
       bool ok = wait(&S.q_full, 0) && wait(&S.k_full[0], 0);
       if (ok) {
         ptx::tc_fence_after();
-        for (int i = 0; i < tiles; ++i) mma_s(i, 0);
-        commit(&S.k_empty[0]);
+        scores(0);
       }
-      for (int j = 0; j < steps && ok; ++j) {
-        const int s = j % PR_STAGES, s1 = (j + 1) % PR_STAGES;
-        const bool more = j + 1 < steps;
-        if (!(ok = wait(&S.v_full[s], (uint32_t)(j / PR_STAGES) & 1u))) break;
-        for (int i = 0; i < tiles; ++i) {
-          if (!(ok = wait(&S.p_full[i], (uint32_t)j & 1u))) break;
-          ptx::tc_fence_after();
-          mma_o(i, s, j == 0);
-          // MMAs of one thread run in order: S_i is overwritten after its probabilities have been read
-          if (more) {
-            if (i == 0) {
-              if (!(ok = wait(&S.k_full[s1], (uint32_t)((j + 1) / PR_STAGES) & 1u))) break;
-              ptx::tc_fence_after();
-            }
-            mma_s(i, s1);
+      for (int h = 0; h < 2 * steps && ok; ++h) {
+        const int j = h >> 1, st = j % PR_STAGES;
+        if (h + 1 < 2 * steps) {
+          // MMAs of one thread run in order: the buffer's last probabilities have been read by then
+          if (h & 1) {
+            const int j1 = j + 1;
+            if (!(ok = wait(&S.k_full[j1 % PR_STAGES], (uint32_t)(j1 / PR_STAGES) & 1u))) break;
+            ptx::tc_fence_after();
           }
+          scores(h + 1);
         }
-        if (!ok) break;
-        commit(&S.v_empty[s]);
-        if (more) commit(&S.k_empty[s1]);
+        if ((h & 1) == 0 && !(ok = wait(&S.v_full[st], (uint32_t)(j / PR_STAGES) & 1u))) break;
+        if (!(ok = wait(&S.p_full[i][h & 1], (uint32_t)j & 1u))) break;
+        ptx::tc_fence_after();
+        const uint64_t v0 = dv + (uint64_t)st * kTile + (uint64_t)(h & 1) * kHalf;
+        const uint32_t p = s_col + HT * (h & 1);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < HT / 16; ++k)
+            ptx::umma_f16_ts(o_col, p + 8 * k, v0 + 128 * k, id_o, h == 0 && k == 0 ? 0u : 1u);
+          ptx::umma_commit(&S.o_full[i][h & 1]);
+          if (h & 1) ptx::umma_commit(&S.v_empty[st]);
+        }
+        __syncwarp();
       }
-      commit(&S.mma_done);
+      if (ptx::elect_one()) ptx::umma_commit(&S.mma_done);
+      __syncwarp();
       if (lane == 0) {
         int never = 0;
         (void)ptx::mbar_wait_bounded(&S.mma_done, 0, &never, kPrWaitNs);
