@@ -83,15 +83,19 @@ struct __align__(1024) PromptSmem {
   int abort_flag;
 };
 
-__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
-  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, 200)) return true;
+// spins: polls before the waiting lane sleeps between them.  Softmax and MMA issue poll (a sleeping lane comes back
+// late); the producers, two stages ahead, sleep: their polls would take issue slots from the others.
+constexpr int kSpin = 200;
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status, int spins) {
+  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, spins)) return true;
   *abort_flag = 1;
   atomicOr(status, PQ_DEV_TIMEOUT);
   return false;
 }
-__device__ __forceinline__ bool pr_warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
+__device__ __forceinline__ bool pr_warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status,
+                                             int spins = kSpin) {
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = pr_wait(bar, parity, abort_flag, status) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = pr_wait(bar, parity, abort_flag, status, spins) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
@@ -574,7 +578,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     for (int j = 0; j < steps; ++j) {
       const int s = j % PR_STAGES, sc = j % SC_RING;
       const uint32_t reuse = ((uint32_t)(j / PR_STAGES) & 1u) ^ 1u;
-      if (!pr_warp_wait(&S.k_empty[s], reuse, &S.abort_flag, a.status)) break;
+      if (!pr_warp_wait(&S.k_empty[s], reuse, &S.abort_flag, a.status, 0)) break;
       const bool scaled = interior((j0 + j) * PT);
       const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
       float km = finite_or_0(ks), vm = finite_or_0(vs);
@@ -623,7 +627,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       }
       // the next step's keys, under this step's values (and the other way round below)
       load(kx, ks, a.cache.k_codes, a.cache.k_scales, at_next);
-      if (!pr_warp_wait(&S.v_empty[s], reuse, &S.abort_flag, a.status)) break;
+      if (!pr_warp_wait(&S.v_empty[s], reuse, &S.abort_flag, a.status, 0)) break;
 #pragma unroll
       for (int c = 0; c < HB / 16; ++c) {
         const uint32_t x[4] = {vx[c].x, vx[c].y, vx[c].z, vx[c].w};
