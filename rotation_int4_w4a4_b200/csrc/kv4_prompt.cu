@@ -56,7 +56,8 @@ constexpr int PR_STAGES = 2;             // key and value stages
 constexpr int SC_RING = 4;               // scale stages: a step's scales outlive its keys by at most one step
 constexpr uint64_t kPrWaitNs = 2000000000ull;
 constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i + 64 (half & 1), O_i at 256 + 128 i
-constexpr float kLazy = 8.0f;            // log2 growth of the reference that is let pass
+constexpr float kLazy = 8.0f;            // log2 growth of the reference that is let pass where the maximum is taken
+constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 65504) from which it is taken elsewhere
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) |
@@ -408,54 +409,61 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       ptx::tc_fence_after();
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
       const bool whole = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && S.scaled[sc] != 0;
-      float mx, ve;
-      float2 kp, v2;                                     // of the half's two groups of 32 tokens
-      uint32_t xa[32], xb[32];                           // their scores
-      if (whole) {
-        ptx::tmem_ld32(s_buf, xa);
-        ptx::tmem_ld32(s_buf + 32, xb);
-        kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
-        v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
-        kp.x *= c_row, kp.y *= c_row;
-        ve = fmaxf(v2.x, v2.y);
-        ptx::tmem_ld_wait(xa);
-        ptx::tmem_ld_wait(xb);
-        mx = fmaxf(chunk_max(xa) * kp.x, chunk_max(xb) * kp.y);
-      } else {
-        float vm = 0.0f;
-        mx = half_max_masked(s_buf, t0, view(j), vm);
-        ve = scale_exponent(vm);
-      }
-      // the reference: largest score plus the exponent of the largest value scale
-      const float cand = mx + ve;
-      const bool grow = cand > m + kLazy || (m == -INFINITY && cand > m);
-      if (__any_sync(0xffffffffu, grow)) {
+      // Raises rows' references to cand (largest score plus the exponent of the largest value scale), in the sum and in O.
+      auto raise = [&](bool grow, float cand) {
         const float m_new = grow ? cand : m;
         const float f = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
         m = m_new;
         l *= f;
-        if (h > 0) {
-          ok = pr_warp_wait(&S.o_full[i][(h - 1) & 1], (uint32_t)((h - 1) >> 1) & 1u, &S.abort_flag, a.status);
-          if (!ok) break;
-          ptx::tc_fence_after();
+        if (h == 0) return true;
+        if (!pr_warp_wait(&S.o_full[i][(h - 1) & 1], (uint32_t)((h - 1) >> 1) & 1u, &S.abort_flag, a.status)) return false;
+        ptx::tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 16) {
-            uint32_t o[16];
-            ptx::tmem_ld32x16(o_col + c, o);
-            ptx::tmem_ld_wait(o);
+        for (int c = 0; c < HD; c += 16) {
+          uint32_t o[16];
+          ptx::tmem_ld32x16(o_col + c, o);
+          ptx::tmem_ld_wait(o);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            ptx::tmem_st32x16(o_col + c, o);
-          }
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+          ptx::tmem_st32x16(o_col + c, o);
         }
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
+        return true;
+      };
       if (whole) {
+        uint32_t xa[32], xb[32];                         // the scores of the half's two groups of 32 tokens
+        ptx::tmem_ld32(s_buf, xa);
+        ptx::tmem_ld32(s_buf + 32, xb);
+        float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
+        const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
+        kp.x *= c_row, kp.y *= c_row;
+        ptx::tmem_ld_wait(xa);
+        ptx::tmem_ld_wait(xb);
+        // The maximum is not taken first: the reference of the steps before serves until a row's probabilities outgrow
+        // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
+        bool over = m == -INFINITY;
+        float sum0 = 0.0f, sum1 = 0.0f;
+        for (int pass = 0; pass < 2; ++pass) {
+          if (__any_sync(0xffffffffu, over)) {
+            const float cand = fmaxf(chunk_max(xa) * kp.x, chunk_max(xb) * kp.y) + fmaxf(v2.x, v2.y);
+            if (!(ok = raise(over && cand > m, cand))) break;
+          } else if (pass > 0) {
+            break;
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+          sum0 = chunk_exp(xa, kp.x, v2.x - ref, s_buf);
+          sum1 = chunk_exp(xb, kp.y, v2.y - ref, s_buf + 16);
+          over = pass == 0 && sum0 + sum1 > kTop;
+        }
+        if (!ok) break;
         // each sum without its values' power of two
-        l = fmaf(chunk_exp(xa, kp.x, v2.x - ref, s_buf), ex2(-v2.x), l);
-        l = fmaf(chunk_exp(xb, kp.y, v2.y - ref, s_buf + 16), ex2(-v2.y), l);
+        l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
       } else {
-        l += half_exp_masked(s_buf, t0, view(j), ref);
+        float vm = 0.0f;
+        const float mx = half_max_masked(s_buf, t0, view(j), vm);
+        const float cand = mx + scale_exponent(vm);
+        const bool grow = cand > m + kLazy || (m == -INFINITY && cand > m);
+        if (__any_sync(0xffffffffu, grow) && !(ok = raise(grow, cand))) break;
+        l += half_exp_masked(s_buf, t0, view(j), m == -INFINITY ? 0.0f : m);
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
