@@ -12,12 +12,13 @@
 // them ready: with one buffer of 128 it waited for the products of every step (5000 of 9000 cycles, measured).  The
 // tensor cores and the exponentials (16 a clock and SM) are about evenly loaded: 2 x 128 x 128 x head_dim multiply-adds
 // against 128 x 128 exponentials a tile and step.
-//   warps 0..3, 4..7   softmax of tile 0, 1: a thread owns a row: its scores from tensor memory, maximum, exponentials,
-//                      P back; O is rescaled in tensor memory only when the row's reference grows by more than 2^8
-//                      (P stays below 2^8, which fp16 holds); at the end its output row.
-//   warps 8..11        producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
+//   warps 0, 1         MMA issue for tile 0, 1 (0: tensor memory).  The oldest warps: the others' waiting polls must
+//                      not take their issue slots.
+//   warps 4..7, 8..11  softmax of tile 0, 1: a thread owns a row: its scores from tensor memory, exponentials, P back;
+//                      the reference they are taken against moves, and O is rescaled in tensor memory, only when a
+//                      row's P would outgrow fp16; at the end its output row.
+//   warps 12..15       producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
-//   warps 12, 13       MMA issue for tile 0, 1 (12: tensor memory).
 // Nothing may spill: the operands leave so little of the L1 cache that a spilled register comes back from L2.
 //
 // Where the scales go.  A step whose 128 tokens every row of the block sees takes keys and values with their scales
@@ -49,8 +50,8 @@ namespace pq {
 namespace {
 
 constexpr int PT = 128;                  // rows per tile and tokens per step
-constexpr int PR_THREADS = 448;
-constexpr int PR_PROD0 = 8, PR_MMA = 12;                 // first producer warp, first MMA warp
+constexpr int PR_THREADS = 512;
+constexpr int PR_SOFT0 = 4, PR_PROD0 = 12;               // first softmax and producer warps; 0 and 1 issue MMAs
 constexpr int HT = PT / 2;               // tokens of a half step
 constexpr int PR_STAGES = 2;             // key and value stages
 constexpr int SC_RING = 4;               // scale stages: a step's scales outlive its keys by at most one step
@@ -185,28 +186,22 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32]) {
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// 2^(c s + off) of 32 scores: as 16 columns of fp16 pairs, and their sum.
-__device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], float c, float off, uint32_t col) {
+// 2^(c s + off) of 32 scores: 16 registers of fp16 pairs, and their sum.
+__device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], float c, float off, uint32_t (&p)[16]) {
   const uint64_t c2 = ptx::f2_pack(c, c), off2 = ptx::f2_pack(off, off);
-  uint64_t sum0 = 0ull, sum1 = 0ull;
-  uint32_t p[16];
+  uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    float e[4];
-    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1])), c2, off2), e[0], e[1]);
-    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[4 * k + 2]), __uint_as_float(r[4 * k + 3])), c2, off2), e[2], e[3]);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
-    sum0 = ptx::f2_add(sum0, ptx::f2_pack(e[0], e[1]));
-    sum1 = ptx::f2_add(sum1, ptx::f2_pack(e[2], e[3]));
-    p[2 * k] = pack_f16(e[0], e[1]);
-    p[2 * k + 1] = pack_f16(e[2], e[3]);
+  for (int k = 0; k < 16; ++k) {
+    float e0, e1;
+    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, off2), e0, e1);
+    e0 = ex2(e0);
+    e1 = ex2(e1);
+    sum[k & 3] = ptx::f2_add(sum[k & 3], ptx::f2_pack(e0, e1));
+    p[k] = pack_f16(e0, e1);
   }
-  ptx::tmem_st32x16(col, p);
-  float a0, a1, a2, a3;
-  ptx::f2_unpack(sum0, a0, a1);
-  ptx::f2_unpack(sum1, a2, a3);
-  return (a0 + a1) + (a2 + a3);
+  float a0, a1;
+  ptx::f2_unpack(ptx::f2_add(ptx::f2_add(sum[0], sum[1]), ptx::f2_add(sum[2], sum[3])), a0, a1);
+  return a0 + a1;
 }
 
 // The same with hidden tokens: 16 scores in log2 units, -inf where the row does not see.
@@ -321,7 +316,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   const int tiles = w.rows - w.r0 > PT ? 2 : 1;          // row tiles that hold rows
   const Interior interior{c_lo, c_hi, p_first, p_last, a.window};
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     ptx::mbar_init(&S.q_full, 8);
     for (int s = 0; s < PR_STAGES; ++s) {
       ptx::mbar_init(&S.k_full[s], 4);
@@ -341,7 +336,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     S.abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == PR_MMA) {
+  if (warp == 0) {
     ptx::tmem_alloc(&S.tmem_slot, 512);
     ptx::tmem_relinquish();
   }
@@ -350,9 +345,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   ptx::tc_fence_after();
   const uint32_t tmem = S.tmem_slot;
 
-  if (warp < PR_PROD0) {
+  if (warp >= PR_SOFT0 && warp < PR_PROD0) {
     // ------------------------------------------------------------------------------- softmax
-    const int i = warp >> 2;                             // row tile
+    const int i = (warp - PR_SOFT0) >> 2;                // row tile
     const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
     const int r = w.r0 + PT * i + row;
     const bool live = r < w.rows;
@@ -430,31 +425,33 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         return true;
       };
       if (whole) {
-        uint32_t xa[32], xb[32];                         // the scores of the half's two groups of 32 tokens
-        ptx::tmem_ld32(s_buf, xa);
-        ptx::tmem_ld32(s_buf + 32, xb);
         float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
         const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
         kp.x *= c_row, kp.y *= c_row;
-        ptx::tmem_ld_wait(xa);
-        ptx::tmem_ld_wait(xb);
         // The maximum is not taken first: the reference of the steps before serves until a row's probabilities outgrow
         // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
         bool over = m == -INFINITY;
-        float sum0 = 0.0f, sum1 = 0.0f;
-        for (int pass = 0; pass < 2; ++pass) {
+        float sum0, sum1;
+        uint32_t pa[16], pb[16];
+        for (int pass = 0;; ++pass) {
+          uint32_t xa[32], xb[32];                       // the scores of the half's two groups of 32 tokens
+          ptx::tmem_ld32(s_buf, xa);
+          ptx::tmem_ld32(s_buf + 32, xb);
+          ptx::tmem_ld_wait(xa);
+          ptx::tmem_ld_wait(xb);
           if (__any_sync(0xffffffffu, over)) {
             const float cand = fmaxf(chunk_max(xa) * kp.x, chunk_max(xb) * kp.y) + fmaxf(v2.x, v2.y);
             if (!(ok = raise(over && cand > m, cand))) break;
-          } else if (pass > 0) {
-            break;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
-          sum0 = chunk_exp(xa, kp.x, v2.x - ref, s_buf);
-          sum1 = chunk_exp(xb, kp.y, v2.y - ref, s_buf + 16);
-          over = pass == 0 && sum0 + sum1 > kTop;
+          sum0 = chunk_exp(xa, kp.x, v2.x - ref, pa);
+          sum1 = chunk_exp(xb, kp.y, v2.y - ref, pb);
+          over = sum0 + sum1 > kTop;
+          if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
         if (!ok) break;
+        ptx::tmem_st32x16(s_buf, pa);
+        ptx::tmem_st32x16(s_buf + 16, pb);
         // each sum without its values' power of two
         l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
       } else {
@@ -555,7 +552,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       }
       ptx::tc_fence_before();
     }
-  } else if (warp < PR_MMA) {
+  } else if (warp >= PR_PROD0) {
     // ----------------------------------------------------------------------------- producers
     const int t = threadIdx.x - 32 * PR_PROD0;           // token of the step
     const int wq = warp - PR_PROD0;
@@ -662,7 +659,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       locate(j + 2);
     }
   } else {
-    const int i = warp - PR_MMA;                         // row tile
+    const int i = warp;                                  // row tile
     if (i < tiles && steps > 0) {
       // ------------------------------------------------------------------------- MMA issue
       // The whole warp walks the half steps and one elected lane issues: descriptors stay in uniform registers.
@@ -731,7 +728,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == PR_MMA) {
+  if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
   }
