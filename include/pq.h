@@ -376,7 +376,8 @@ pq_status pq_w8a8_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g
  *   k_codes, v_codes    device uint8 [pages][heads][page_size][head_dim / 2], nibbles as everywhere.
  *   k_scales, v_scales  device float32 [pages][heads][page_size].
  *   A slot is page * page_size + place in the page.  page_size 16, 32, 64, 128 or 256; head_dim 64 or
- *   128; heads 1..1024; all four 16-byte aligned and owned by the caller.
+ *   128; heads 1..1024; pages * heads * page_size < 2^32; all four 16-byte aligned and owned by the
+ *   caller.
  *   flags  PQ_KV4_ROTATE_K: keys (and queries) are held rotated, k H / sqrt(head_dim), after the
  *          position rotation (OSTQuant page: Hadamard on Q and K after RoPE); q . k is unchanged.
  *          PQ_KV4_ROTATE_V: values are held rotated; pq_kv4_attention rotates its output back.

@@ -6,21 +6,24 @@
 // the codes themselves; ks multiplies the finished dot product and vs the probability, both in float32.
 //
 // The cache is read once for all query rows of a key/value head (the group's heads x the sequence's new tokens), 64
-// bytes a token for keys and as much for values, and HBM bounds the kernel.  A warp owns blocks of 64 tokens:
+// bytes a token for keys and as much for values, and HBM bounds the kernel, with the unpacking close behind (about 14
+// instructions a token and warp).  A warp owns blocks of 32 tokens:
 //   - keys are the A operand (16 tokens x 16 channels), the query rows the 8-column B operand: a thread's 16-byte
 //     load of one token is its share of the A operands of all 8 channel steps, because the channels of a dot product
 //     may be taken in any order as long as the queries follow the same one (set up once).  No shared memory.
-//   - the scores come out tokens x rows; the softmax runs over the warp's registers with one running maximum per row;
+//   - the scores come out tokens x rows and stay in the warp's registers;
 //   - probabilities go back in as B operand (movmatrix transposes 8 x 8 of them) against the values as A operand
 //     (16 channels x 16 tokens): two tokens' words are byte-permuted together, then masked.
 //   - keys become bf16, as the queries are: nibble ^ 8 under 0x4300 is 128 + (code + 8), and the offset 136 leaves
-//     with the query's sum (136 sum(q) is subtracted from the score, in float32).
+//     with the query's sum: the accumulator starts at -136 sum(q).
 //   - values become fp16: nibble ^ 8 under 0x6400 is 1024 + (code + 8), and 1032 is subtracted from the operand
 //     itself, exactly, since a long sum of probabilities times 1032 would drown the result.
-//   - the loads of the next block are issued as soon as this block's registers are free.
-// The second product takes P_t vs_t as fp16, relative to the row's largest score and to the exponent of the largest
-// value scale it has seen: at most 1, so it neither overflows nor, where it matters, leaves the normal range; rounding
-// it costs half a step of fp16, 2^-11, an eighth of what bf16 would.  Maxima, sums and the output are float32.
+//   - the loads of the next block are issued as soon as this block's registers are free; 16 warps an SM (128 registers a
+//     thread) keep 64 KB in flight.
+// The second product takes P_t vs_t as fp16.  Both are relative to a reference (a score plus the exponent of a value
+// scale) that a row keeps until its products outgrow fp16; only then, and at first, are the block's maximum score and
+// value scale reduced over the warp.  Rounding a product costs half a step of fp16, 2^-11, an eighth of what bf16 would.
+// Sums and the output are float32.
 //
 // A block's warps join their maxima, sums and outputs through shared memory.  Long contexts are cut into chunks of
 // tokens, one block each; a second kernel joins the chunks' float32 partial results.
@@ -37,10 +40,11 @@ namespace pq {
 namespace {
 
 constexpr int AT_WARPS = 4;
-constexpr int AT_BLOCK = 64;            // tokens a warp takes at a time
+constexpr int AT_BLOCK = 32;            // tokens a warp takes at a time
 constexpr int AT_TILES = AT_BLOCK / 16;
 // Query rows a key/value head and sequence from which on the tensor-core kernel of kv4_prompt.cu takes the call.
 constexpr int64_t kPromptRows = 64;
+constexpr float kRowsTop = 16384.0f;    // a product of probability and value scale from which the reference is raised (fp16: 65504)
 __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                          const uint32_t a3, const uint32_t b0, const uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -77,7 +81,7 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
+__global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
                                                                 int row_tiles) {
   constexpr int R = 8 * NT;              // query rows per tile
   constexpr int KS = HD / 16;            // channel steps of the first product = channel tiles of the second
@@ -87,6 +91,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
   __shared__ float sm_o[AT_WARPS][R][HD];
   __shared__ float sm_m[AT_WARPS][R], sm_l[AT_WARPS][R];
 
+  ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int b = blockIdx.z, kvh = blockIdx.y;
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
 
     // ---- query operands: B fragment of step (w, h): channels (d, d + 4), (d + 1, d + 5), d = 8 (KW t + w) + 2 h
     uint32_t qb[NT][KS][2];
-    float bq[NT][2];                     // 136 * sum of the query, for this thread's two columns
+    float bq[NT][2];                     // -136 * sum of the query, for this thread's two columns
     int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        bq[nt][e] = 136.0f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        bq[nt][e] = -136.0f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
         pos[nt][e] = n - qlen + min(rows - 1, r0 + 8 * nt + 2 * t + e) / group;
       }
     }
@@ -165,27 +170,33 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       for (int j = 0; j < KS; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
     }
 
-    // ---- the warp's blocks of 64 tokens
+    // ---- the warp's blocks of 32 tokens
     uint32_t kx[AT_TILES][2][KW], vx[AT_TILES][4][VW];
     float ks[AT_TILES][2], vs[AT_TILES][2];
     int lim[AT_TILES];                   // tokens of the 16-token tile that exist
-    int64_t base[AT_TILES];              // first token's row in the cache
+    bool all;                            // every token of the block does
+    uint32_t base[AT_TILES];             // cache row of the tile's first token (a cache has fewer than 2^32)
+    const uint8_t* const kp = a.cache.k_codes + (HB * g + 4 * KW * t);   // this thread's part of a tile
+    const uint8_t* const vp = a.cache.v_codes + (HB * 2 * t + 4 * VW * g);
+    const float *const ksp = a.cache.k_scales + g, *const vsp = a.cache.v_scales + g;
     auto locate = [&](int tok0) {
+      all = tok0 + AT_BLOCK <= n;
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
         const int tok = tok0 + 16 * i;
         int k = min(16, n - tok);
-        int64_t at = 0;
+        uint32_t at = 0;
         if (k > 0) {
           const int page = table[tok >> ps];
           if (page < 0 || page >= a.cache.pages) {
             k = 0;
+            all = false;
             if (lane == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
           } else {
-            at = (((int64_t)page * a.cache.heads + kvh) << ps) + (tok & ((1 << ps) - 1));
+            at = (((uint32_t)page * (uint32_t)a.cache.heads + kvh) << ps) + (tok & ((1 << ps) - 1));
           }
         }
-        lim[i] = max(k, 0);
+        lim[i] = k;
         base[i] = at;
       }
     };
@@ -194,10 +205,9 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (g + 8 * h < lim[i]) {
-            const int64_t row = base[i] + g + 8 * h;
-            load_words<KW>(kx[i][h], a.cache.k_codes + row * HB + 4 * KW * t);
-            ks[i][h] = __ldg(a.cache.k_scales + row);
+          if (all || g + 8 * h < lim[i]) {
+            load_words<KW>(kx[i][h], kp + (uint64_t)base[i] * HB + HB * 8 * h);
+            ks[i][h] = __ldg(ksp + base[i] + 8 * h);
           } else {
 #pragma unroll
             for (int w = 0; w < KW; ++w) kx[i][h][w] = 0u;
@@ -210,16 +220,15 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       for (int i = 0; i < AT_TILES; ++i) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int tok = 2 * t + (k & 1) + 8 * (k >> 1);
-          if (tok < lim[i]) {
-            load_words<VW>(vx[i][k], a.cache.v_codes + (base[i] + tok) * HB + 4 * VW * g);
+          if (all || 2 * t + (k & 1) + 8 * (k >> 1) < lim[i]) {
+            load_words<VW>(vx[i][k], vp + (uint64_t)base[i] * HB + HB * ((k & 1) + 8 * (k >> 1)));
           } else {
 #pragma unroll
             for (int w = 0; w < VW; ++w) vx[i][k][w] = 0u;
           }
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) vs[i][h] = g + 8 * h < lim[i] ? __ldg(a.cache.v_scales + base[i] + g + 8 * h) : 0.0f;
+        for (int h = 0; h < 2; ++h) vs[i][h] = all || g + 8 * h < lim[i] ? __ldg(vsp + base[i] + 8 * h) : 0.0f;
       }
     };
 
@@ -230,19 +239,13 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
       load_v();
     }
     for (int tok0 = first; tok0 < c_hi; tok0 += AT_BLOCK * AT_WARPS) {
-      int cur_lim[AT_TILES];
-      bool whole = tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
-                   (a.window <= 0 || tok0 > p_last - a.window);
-#pragma unroll
-      for (int i = 0; i < AT_TILES; ++i) {
-        cur_lim[i] = lim[i];
-        whole = whole && lim[i] == 16;
-      }
+      const bool whole = all && tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
+                         (a.window <= 0 || tok0 > p_last - a.window);
       float s[AT_TILES][NT][4];
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][1] = s[i][nt][2] = s[i][nt][3] = 0.0f;
+        for (int nt = 0; nt < NT; ++nt) s[i][nt][0] = s[i][nt][2] = bq[nt][0], s[i][nt][1] = s[i][nt][3] = bq[nt][1];
 #pragma unroll
         for (int w = 0; w < KW; ++w)
 #pragma unroll
@@ -256,17 +259,11 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
         const float f0 = ks[i][0] * c_log2, f1 = ks[i][1] * c_log2;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          s[i][nt][0] = (s[i][nt][0] - bq[nt][0]) * f0;
-          s[i][nt][1] = (s[i][nt][1] - bq[nt][1]) * f0;
-          s[i][nt][2] = (s[i][nt][2] - bq[nt][0]) * f1;
-          s[i][nt][3] = (s[i][nt][3] - bq[nt][1]) * f1;
+          s[i][nt][0] *= f0;
+          s[i][nt][1] *= f0;
+          s[i][nt][2] *= f1;
+          s[i][nt][3] *= f1;
         }
-      }
-      // the next block's keys
-      const int next = tok0 + AT_BLOCK * AT_WARPS;
-      if (next < c_hi) {
-        locate(next);
-        load_k();
       }
       if (!whole) {
 #pragma unroll
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int tok = tok0 + 16 * i + 8 * h + g;
-            const bool in = 8 * h + g < cur_lim[i] && tok >= c_lo && tok < c_hi;
+            const bool in = 8 * h + g < lim[i] && tok >= c_lo && tok < c_hi;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -283,70 +280,78 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
                   s[i][nt][2 * h + e] = -INFINITY;
           }
       }
-      // the block's largest value scale
-      float v_block = 0.0f;
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < AT_TILES; ++i) v_block = fmaxf(v_block, fmaxf(finite_or_0(vs[i][0]), finite_or_0(vs[i][1])));
-        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 4));
-        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 8));
-        v_block = fmaxf(v_block, __shfl_xor_sync(0xffffffffu, v_block, 16));
+      // the next block's keys (its values follow below)
+      const int next = tok0 + AT_BLOCK * AT_WARPS;
+      if (next < c_hi) {
+        locate(next);
+        load_k();
       }
       uint32_t pb[AT_TILES][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2], mu[2];
-        bool grew = false;
+        bool over = m[nt][0] == -INFINITY || m[nt][1] == -INFINITY;
+        float sum[2];
+        for (int pass = 0;; ++pass) {
+          if (__any_sync(0xffffffffu, over)) {
+            // Raise the references to this block's largest score plus the exponent of the largest value scale, both over
+            // the tokens that the row sees.
+            float alpha[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float x = -INFINITY;
+            for (int e = 0; e < 2; ++e) {
+              float x = -INFINITY, y = 0.0f;
 #pragma unroll
-          for (int i = 0; i < AT_TILES; ++i) x = fmaxf(x, fmaxf(s[i][nt][e], s[i][nt][2 + e]));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          // the largest value scale: in a block with hidden tokens, over those the row sees
-          float y = v_block;
-          if (!whole) {
+              for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
-            for (int i = 0; i < AT_TILES; ++i)
+                for (int h = 0; h < 2; ++h) {
+                  const float z = s[i][nt][2 * h + e];
+                  x = fmaxf(x, z);
+                  if (z != -INFINITY) y = fmaxf(y, finite_or_0(vs[i][h]));
+                }
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
-                if (s[i][nt][2 * h + e] != -INFINITY) y = fmaxf(y, finite_or_0(vs[i][h]));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
-            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+              for (int b = 4; b < 32; b <<= 1) {
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, b));
+                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, b));
+              }
+              x = fmaxf(m[nt][e], x + scale_exponent(y));
+              alpha[e] = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
+              m[nt][e] = x;
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              o[nt][j][0] *= alpha[0];
+              o[nt][j][1] *= alpha[1];
+              o[nt][j][2] *= alpha[0];
+              o[nt][j][3] *= alpha[1];
+            }
+            l[nt][0] *= alpha[0];
+            l[nt][1] *= alpha[1];
           }
-          x = fmaxf(m[nt][e], x + scale_exponent(y));
-          mu[e] = x == -INFINITY ? 0.0f : x;
-          alpha[e] = ex2(m[nt][e] - mu[e]);
-          grew = grew || x > m[nt][e];
-          m[nt][e] = x;
-        }
-        if (__any_sync(0xffffffffu, grew)) {
+          const float r0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], r1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+          sum[0] = sum[1] = 0.0f;
+          float top = 0.0f;
 #pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            o[nt][j][0] *= alpha[0];
-            o[nt][j][1] *= alpha[1];
-            o[nt][j][2] *= alpha[0];
-            o[nt][j][3] *= alpha[1];
-          }
-          l[nt][0] *= alpha[0];
-          l[nt][1] *= alpha[1];
+          for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float s0 = s[i][nt][2 * h], s1 = s[i][nt][2 * h + 1];
+              const float p0 = ex2(s0 - r0), p1 = ex2(s1 - r1);
+              sum[0] += p0;
+              sum[1] += p1;
+              // a hidden token's value scale may be anything: select, do not multiply
+              const float w0 = whole || s0 != -INFINITY ? p0 * vs[i][h] : 0.0f;
+              const float w1 = whole || s1 != -INFINITY ? p1 * vs[i][h] : 0.0f;
+              top = ptx::max3(top, w0, w1);
+              pb[i][nt][h] = pack_f16(w0, w1);
+            }
+          over = top > kRowsTop;
+          if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
+        l[nt][0] += sum[0];
+        l[nt][1] += sum[1];
 #pragma unroll
         for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float s0 = s[i][nt][2 * h], s1 = s[i][nt][2 * h + 1];
-            const float p0 = ex2(s0 - mu[0]), p1 = ex2(s1 - mu[1]);
-            l[nt][0] += p0;
-            l[nt][1] += p1;
-            // a hidden token's value scale may be anything: select, do not multiply
-            const float w0 = whole || s0 != -INFINITY ? p0 * vs[i][h] : 0.0f;
-            const float w1 = whole || s1 != -INFINITY ? p1 * vs[i][h] : 0.0f;
-            pb[i][nt][h] = movmatrix_trans(pack_f16(w0, w1));
-          }
+          for (int h = 0; h < 2; ++h) pb[i][nt][h] = movmatrix_trans(pb[i][nt][h]);
       }
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i)
@@ -446,29 +451,59 @@ __global__ void __launch_bounds__(32 * AT_WARPS) kv4_rows_kernel(const Kv4AttnAr
   }
 }
 
-// Joins the chunks of each query row; one warp a row.  Rows of tokens outside every sequence stay as they were.
+// Joins the chunks of each query row, a block a row: its warps take every fourth chunk each.  Rows of tokens outside
+// every sequence stay as they were.  Launched as the programmatic dependent of the kernel that writes the chunks.
+constexpr int JN_WARPS = 4;
 template <int HD>
-__global__ void __launch_bounds__(128) kv4_join_kernel(const Kv4AttnArgs a, const Partials part) {
+__global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_kernel(const Kv4AttnArgs a, const Partials part) {
   constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int64_t total = a.T * a.heads_q;
-  if (row >= total) return;
+  __shared__ float sm_o[JN_WARPS][HD];
+  __shared__ float sm_m[JN_WARPS], sm_l[JN_WARPS];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x, total = a.T * a.heads_q;
   const int64_t token = row / a.heads_q;
-  if (token < a.q_start[0] || token >= a.q_start[a.B]) return;
+  ptx::griddep_wait();
+  if (token < a.q_start[0] || token >= a.q_start[a.B]) return;   // the whole block
   float mx = -INFINITY;
-  for (int c = 0; c < part.chunks; ++c) mx = fmaxf(mx, part.ml[c * total + row].x);
+  for (int c = warp + JN_WARPS * lane; c < part.chunks; c += 32 * JN_WARPS) mx = fmaxf(mx, part.ml[c * total + row].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.0f : mx;
   float sum = 0.0f, y[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) y[i] = 0.0f;
-  for (int c = 0; c < part.chunks; ++c) {
+#pragma unroll 4
+  for (int c = warp; c < part.chunks; c += JN_WARPS) {
     const float2 ml = part.ml[c * total + row];
-    if (ml.x == -INFINITY && ml.y == 0.0f) continue;          // nothing seen: its output was not written
-    const float f = ex2(ml.x - mu);
+    const bool some = ml.x != -INFINITY || ml.y != 0.0f;     // otherwise nothing seen and no output written
+    const float f = some ? ex2(ml.x - mu) : 0.0f;
     sum = fmaf(ml.y, f, sum);
+    float x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = fmaf(part.o[(c * total + row) * HD + E * lane + i], f, y[i]);
+    for (int i = 0; i < E; ++i) x[i] = some ? part.o[(c * total + row) * HD + E * lane + i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = fmaf(x[i], f, y[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < E; ++i) sm_o[warp][E * lane + i] = y[i];
+  if (lane == 0) {
+    sm_m[warp] = mx;
+    sm_l[warp] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < JN_WARPS; ++w) mx = fmaxf(mx, sm_m[w]);
+  const float all = mx == -INFINITY ? 0.0f : mx;
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) y[i] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < JN_WARPS; ++w) {
+    const float f = sm_m[w] == -INFINITY ? (sm_l[w] == 0.0f ? 0.0f : 1.0f) : ex2(sm_m[w] - all);
+    sum = fmaf(sm_l[w], f, sum);
+#pragma unroll
+    for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w][E * lane + i], f, y[i]);
   }
   finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + (row - token * a.heads_q) * HD, lane);
 }
@@ -504,6 +539,7 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   const int64_t most = (max_len + unit_len - 1) / unit_len;
   Partials part = {};
   part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
+  if (a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;    // the joining kernel takes a block a row
   part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);
   void* ws = nullptr;
   cudaError_t e;
@@ -531,10 +567,17 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     st = cuda_fail(e, "kv4_rows_kernel launch");
   }
   if (st == PQ_OK && part.chunks > 1) {
-    const unsigned grid = (unsigned)((a.T * a.heads_q + 3) / 4);
-    if (wide) kv4_join_kernel<128><<<grid, 128, 0, stream>>>(a, part);
-    else kv4_join_kernel<64><<<grid, 128, 0, stream>>>(a, part);
-    st = cuda_fail(cudaGetLastError(), "kv4_join_kernel launch");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.T * a.heads_q), 1, 1);
+    cfg.blockDim = dim3(32 * JN_WARPS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = wide ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, a, part) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, a, part);
+    st = cuda_fail(e, "kv4_join_kernel launch");
   }
   if (ws) {
     e = cudaFreeAsync(ws, stream);

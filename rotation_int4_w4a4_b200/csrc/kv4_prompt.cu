@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  ptx::griddep_launch_dependents();                      // the kernel that joins chunks waits for this one
   Work w;
   if (!find_work(a, part, w)) return;                    // the whole block agrees
   const int group = a.heads_q / a.cache.heads;

@@ -83,6 +83,10 @@ pq_status check_cache(const pq_kv4_cache* c, Kv4View* v) {
     set_error("pages=%lld must be in 1..2^31-1", (long long)c->pages);
     return PQ_ERR_INVALID_ARG;
   }
+  if (c->pages * c->heads >= ((int64_t)1 << 32) / c->page_size) {
+    set_error("pages * heads * page_size must be below 2^32");
+    return PQ_ERR_INVALID_ARG;
+  }
   if (c->flags & ~(PQ_KV4_ROTATE_K | PQ_KV4_ROTATE_V)) { set_error("unknown cache flags 0x%x", c->flags); return PQ_ERR_INVALID_ARG; }
   *v = Kv4View{c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->pages, shift, c->heads, c->head_dim,
                (c->flags & PQ_KV4_ROTATE_K) ? 1 : 0, (c->flags & PQ_KV4_ROTATE_V) ? 1 : 0};
