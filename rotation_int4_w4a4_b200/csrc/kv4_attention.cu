@@ -200,35 +200,50 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
         base[i] = at;
       }
     };
+    // Loads of a block whose tokens all exist carry no predicates.
     auto load_k = [&]() {
+      if (all) {
 #pragma unroll
-      for (int i = 0; i < AT_TILES; ++i)
+        for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (all || g + 8 * h < lim[i]) {
+          for (int h = 0; h < 2; ++h) {
             load_words<KW>(kx[i][h], kp + (uint64_t)base[i] * HB + HB * 8 * h);
             ks[i][h] = __ldg(ksp + base[i] + 8 * h);
-          } else {
-#pragma unroll
-            for (int w = 0; w < KW; ++w) kx[i][h][w] = 0u;
-            ks[i][h] = 0.0f;
           }
-        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool in = g + 8 * h < lim[i];
+            // codes of a token that does not exist are never used: the cache's first bytes stand in
+            load_words<KW>(kx[i][h], in ? kp + (uint64_t)base[i] * HB + HB * 8 * h : a.cache.k_codes);
+            ks[i][h] = in ? __ldg(ksp + base[i] + 8 * h) : 0.0f;
+          }
+      }
     };
     auto load_v = [&]() {
+      if (all) {
 #pragma unroll
-      for (int i = 0; i < AT_TILES; ++i) {
+        for (int i = 0; i < AT_TILES; ++i) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (all || 2 * t + (k & 1) + 8 * (k >> 1) < lim[i]) {
+          for (int k = 0; k < 4; ++k)
             load_words<VW>(vx[i][k], vp + (uint64_t)base[i] * HB + HB * ((k & 1) + 8 * (k >> 1)));
-          } else {
 #pragma unroll
-            for (int w = 0; w < VW; ++w) vx[i][k][w] = 0u;
-          }
+          for (int h = 0; h < 2; ++h) vs[i][h] = __ldg(vsp + base[i] + 8 * h);
         }
+      } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) vs[i][h] = all || g + 8 * h < lim[i] ? __ldg(vsp + base[i] + 8 * h) : 0.0f;
+        for (int i = 0; i < AT_TILES; ++i) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = (k & 1) + 8 * (k >> 1);
+            const bool in = 2 * t + tok < lim[i];
+            load_words<VW>(vx[i][k], in ? vp + (uint64_t)base[i] * HB + HB * tok : a.cache.v_codes);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) vs[i][h] = g + 8 * h < lim[i] ? __ldg(vsp + base[i] + 8 * h) : 0.0f;
+        }
       }
     };
 
@@ -358,31 +373,29 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           // words of tokens 2t and 2t + 1 (and + 8), their low or high 16 bits side by side
-          uint32_t x[VW][2];
+          uint32_t y[VW][2][4];
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
-            x[w][0] = __byte_perm(vx[i][0][w], vx[i][1][w], half ? 0x7632 : 0x5410);
-            x[w][1] = __byte_perm(vx[i][2][w], vx[i][3][w], half ? 0x7632 : 0x5410);
+            code_pairs(__byte_perm(vx[i][0][w], vx[i][1][w], half ? 0x7632 : 0x5410), y[w][0]);
+            code_pairs(__byte_perm(vx[i][2][w], vx[i][3][w], half ? 0x7632 : 0x5410), y[w][1]);
           }
           if constexpr (VW == 2) {
             // channel tile j: rows g <-> channel 16 g + j, rows g + 8 <-> 16 g + 8 + j
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const int j = 4 * half + k;
-              const uint32_t a0 = code_pair(x[0][0], 4 * k), a1 = code_pair(x[1][0], 4 * k);
-              const uint32_t a2 = code_pair(x[0][1], 4 * k), a3 = code_pair(x[1][1], 4 * k);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][j], a0, a1, a2, a3, pb[i][nt][0], pb[i][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[nt][j], y[0][0][k], y[1][0][k], y[0][1][k], y[1][1][k], pb[i][nt][0], pb[i][nt][1]);
             }
           } else {
             // channel tile j: rows g <-> channel 8 g + 2 j, rows g + 8 <-> 8 g + 2 j + 1
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int j = 2 * half + k;
-              const uint32_t a0 = code_pair(x[0][0], 8 * k), a1 = code_pair(x[0][0], 8 * k + 4);
-              const uint32_t a2 = code_pair(x[0][1], 8 * k), a3 = code_pair(x[0][1], 8 * k + 4);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][j], a0, a1, a2, a3, pb[i][nt][0], pb[i][nt][1]);
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(o[nt][j], y[0][0][2 * k], y[0][0][2 * k + 1], y[0][1][2 * k], y[0][1][2 * k + 1], pb[i][nt][0], pb[i][nt][1]);
             }
           }
         }
@@ -403,6 +416,17 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
         if (g == 0) {
           sm_m[warp][r] = m[nt][e];
           sm_l[warp][r] = x;
+        }
+        // odd nibbles' channels come 16 times too large
+        if constexpr (VW == 2) {
+#pragma unroll
+          for (int j = 1; j < KS; j += 2) {
+            o[nt][j][e] *= kOddNibble;
+            o[nt][j][2 + e] *= kOddNibble;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < KS; ++j) o[nt][j][2 + e] *= kOddNibble;
         }
         float* dst = &sm_o[warp][r][(HD / 8) * g];
         if constexpr (VW == 2) {
@@ -533,7 +557,7 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   } else {
     // Chunks: about four blocks for each multiprocessor when every sequence has max_len tokens, at least 256 tokens each.
     units = (int64_t)a.B * a.cache.heads * row_tiles;
-    want = (4 * (int64_t)sms + units - 1) / units;
+    want = (8 * (int64_t)sms + units - 1) / units;
     unit_len = 256;
   }
   const int64_t most = (max_len + unit_len - 1) / unit_len;

@@ -19,18 +19,33 @@ struct Partials {
   int chunk_len;  // tokens of a chunk
 };
 
-// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code: nibble ^ 8 is code + 8, under 0x4300
-// (128, whose last mantissa bit counts 1).
-__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) {
-  return ((x >> s) & 0x000F000Fu) ^ 0x43084308u;
+// (x & mask) ^ flip in one instruction (of two constants the compiler would make two).
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(y) : "r"(x), "r"(mask), "r"(flip));
+  return y;
 }
 
-// The same two nibbles -> two fp16 codes (0x6400 is 1024; 1032 + code, less 1032: exact).
-__device__ __forceinline__ uint32_t code_pair(uint32_t x, int s) {
-  const uint32_t b = ((x >> s) & 0x000F000Fu) ^ 0x64086408u, k = 0x64086408u;
-  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
+// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code: nibble ^ 8 is code + 8, under 0x4300
+// (128, whose last mantissa bit counts 1).
+__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) { return and_xor(x >> s, 0x000F000Fu, 0x43084308u); }
+
+__device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+
+// Nibbles k and k + 4 of a word (k = 0..3) -> fp16 pairs, exactly: the codes for even k (1024 + code + 8 under 0x6400,
+// less 1032) and 16 times the codes for odd k, whose bits stay four places up in the mantissa (less 1152): one shift
+// a word instead of three.  The factor is taken out of the other operand (queries) or of the result (outputs).
+__device__ __forceinline__ void code_pairs(uint32_t x, uint32_t (&y)[4]) {
+  const uint32_t z = x >> 8;
+  y[0] = hsub2_bits(and_xor(x, 0x000F000Fu, 0x64086408u), 0x64086408u);
+  y[1] = hsub2_bits(and_xor(x, 0x00F000F0u, 0x64806480u), 0x64806480u);
+  y[2] = hsub2_bits(and_xor(z, 0x000F000Fu, 0x64086408u), 0x64086408u);
+  y[3] = hsub2_bits(and_xor(z, 0x00F000F0u, 0x64806480u), 0x64806480u);
+}
+constexpr float kOddNibble = 0.0625f;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);

@@ -28,7 +28,7 @@
 // measured, 3800 of 6200 shared-memory cycles a step.  Steps with tokens that some row must not see (the diagonal, a
 // window's edge, the ends of a sequence) keep the bare codes, exact, and the scales in the softmax, where a hidden
 // token's can be left out whatever it holds.  Queries become fp16 relative to their row's largest channel (exact but
-// for channels below 2^-14 of it).
+// for channels below 2^-10 of it).
 // Channels sit in the operands in the order 0 4 1 5 2 6 3 7 of each 8 (the order in which nibbles come out of a word);
 // queries are staged in the same order and the output is read back through it.
 // Keys are rows of 128 bytes, K-major; values lie the same way and enter as an MN-major operand.
@@ -261,7 +261,7 @@ __device__ __forceinline__ float half_exp_masked(uint32_t s_col, int t0, const S
   return sum;
 }
 
-// 32 output columns in channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4.
+// 32 output columns in channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4 (odd k: 16 times).
 __device__ __forceinline__ void load_channels(float (&o)[32], uint32_t col) {
   uint32_t x[32];
   ptx::tmem_ld32(col, x);
@@ -270,8 +270,9 @@ __device__ __forceinline__ void load_channels(float (&o)[32], uint32_t col) {
   for (int c = 0; c < 32; c += 8)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      o[c + k] = __uint_as_float(x[c + 2 * k]);
-      o[c + k + 4] = __uint_as_float(x[c + 2 * k + 1]);
+      const float f = k & 1 ? kOddNibble : 1.0f;
+      o[c + k] = __uint_as_float(x[c + 2 * k]) * f;
+      o[c + k + 4] = __uint_as_float(x[c + 2 * k + 1]) * f;
     }
 }
 __device__ __forceinline__ uint4 bf16x8(const float* o, float f) {
@@ -379,9 +380,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           v[2 * q] = __uint_as_float(y[q] << 16) * f;
           v[2 * q + 1] = __uint_as_float(y[q] & 0xFFFF0000u) * f;
         }
-        // channels 0 4 | 1 5 | 2 6 | 3 7
+        // channels 0 4 | 1 5 | 2 6 | 3 7; the keys' odd channels come 16 times too large
         *reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(row, c % 8)) =
-            make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1], v[5]), pack_f16(v[2], v[6]), pack_f16(v[3], v[7]));
+            make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1] * kOddNibble, v[5] * kOddNibble), pack_f16(v[2], v[6]),
+                       pack_f16(v[3] * kOddNibble, v[7] * kOddNibble));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -613,9 +615,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         for (int q = 0; q < 4; ++q) {                    // a word: 8 channels, one 16-byte chunk
           const int ch = 4 * c + q;
           uint32_t y[4];
+          code_pairs(x[q], y);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[k] = code_pair(x[q], 4 * k);
             if (scaled) {
               const __half2 code = *reinterpret_cast<const __half2*>(&y[k]);
               const __half2 z = __hfma2(code, k_hi, __hmul2(code, k_lo));
@@ -641,9 +643,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         for (int q = 0; q < 4; ++q) {
           const int ch = 4 * c + q;
           uint32_t y[4];
+          code_pairs(x[q], y);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            y[k] = code_pair(x[q], 4 * k);
             if (scaled) {
               const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&y[k]), v_hi);
               y[k] = *reinterpret_cast<const uint32_t*>(&z);
