@@ -81,7 +81,7 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
+__global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
                                                                 int row_tiles) {
   constexpr int R = 8 * NT;              // query rows per tile
   constexpr int KS = HD / 16;            // channel steps of the first product = channel tiles of the second
@@ -179,6 +179,11 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
     const uint8_t* const kp = a.cache.k_codes + (HB * g + 4 * KW * t);   // this thread's part of a tile
     const uint8_t* const vp = a.cache.v_codes + (HB * 2 * t + 4 * VW * g);
     const float *const ksp = a.cache.k_scales + g, *const vsp = a.cache.v_scales + g;
+    int page_of[AT_TILES];               // pages of the block to be located next: read a block ahead
+    auto look_up = [&](int tok0) {
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) page_of[i] = tok0 + 16 * i < n ? __ldg(table + ((tok0 + 16 * i) >> ps)) : 0;
+    };
     auto locate = [&](int tok0) {
       all = tok0 + AT_BLOCK <= n;
 #pragma unroll
@@ -187,7 +192,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
         int k = min(16, n - tok);
         uint32_t at = 0;
         if (k > 0) {
-          const int page = table[tok >> ps];
+          const int page = page_of[i];
           if (page < 0 || page >= a.cache.pages) {
             k = 0;
             all = false;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
           }
       }
     };
-    auto load_v = [&]() {
+    auto load_v = [&](uint32_t (&vx)[AT_TILES][4][VW], float (&vs)[AT_TILES][2]) {
       if (all) {
 #pragma unroll
         for (int i = 0; i < AT_TILES; ++i) {
@@ -249,9 +254,11 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
 
     const int first = (c_lo & ~(AT_BLOCK - 1)) + AT_BLOCK * warp;
     if (first < c_hi) {
+      look_up(first);
       locate(first);
       load_k();
-      load_v();
+      load_v(vx, vs);
+      look_up(first + AT_BLOCK * AT_WARPS);
     }
     for (int tok0 = first; tok0 < c_hi; tok0 += AT_BLOCK * AT_WARPS) {
       const bool whole = all && tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
@@ -295,11 +302,15 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
                   s[i][nt][2 * h + e] = -INFINITY;
           }
       }
-      // the next block's keys (its values follow below)
+      // the next block's keys and values
       const int next = tok0 + AT_BLOCK * AT_WARPS;
+      uint32_t vn[AT_TILES][4][VW];
+      float vsn[AT_TILES][2];
       if (next < c_hi) {
         locate(next);
         load_k();
+        load_v(vn, vsn);
+        look_up(next + AT_BLOCK * AT_WARPS);
       }
       uint32_t pb[AT_TILES][NT][2];
 #pragma unroll
@@ -399,7 +410,14 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 4 : 2) kv4_rows_kerne
             }
           }
         }
-      if (next < c_hi) load_v();
+#pragma unroll
+      for (int i = 0; i < AT_TILES; ++i) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vx[i][k][w] = vn[i][k][w];
+        vs[i][0] = vsn[i][0], vs[i][1] = vsn[i][1];
+      }
     }
 
     // ---- join the block's warps
@@ -555,9 +573,12 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     want = sms / std::max<int64_t>(units, 1);
     unit_len = 512;
   } else {
-    // Chunks: about four blocks for each multiprocessor when every sequence has max_len tokens, at least 256 tokens each.
+    // Three blocks an SM run at once.  Few sequences: as many chunks as make one full round of blocks (one token over
+    // 65536: 33 us, 42 with three rounds); from 8 sequences on two, since their lengths differ and short chunks even that
+    // out (16 of up to 4096: 26 us against 30); many: about three (64 of up to 8192: 92 us, 110 with one chunk each).
     units = (int64_t)a.B * a.cache.heads * row_tiles;
-    want = (8 * (int64_t)sms + units - 1) / units;
+    const int64_t slots = 3 * (int64_t)sms;
+    want = units * 2 > slots ? (8 * (int64_t)sms + units - 1) / units : (a.B < 8 ? slots : 2 * slots) / units;
     unit_len = 256;
   }
   const int64_t most = (max_len + unit_len - 1) / unit_len;

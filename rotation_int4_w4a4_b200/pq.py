@@ -353,27 +353,59 @@ def pq_rrs_gemm(codes_A, token_scales, codes_W, scales_W, Y, T=None, N=None, D=N
     _check(lib.pq_rrs_gemm(*ptrs[:4], T, N, D, g, ptrs[4], out_dtype, _stream(stream)), "pq_rrs_gemm")
 
 
+def _here():
+    """Index of the current CUDA device (-1 without one) and torch, for the calls below."""
+    import torch
+    return (torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1), torch
+
+
+def _raw_stream(stream, dev, torch):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on(x, name, kind, dtype, need, dev):
+    """:func:`_arg` and that the tensor lives on the current device (the library launches there)."""
+    if x is None:
+        return None
+    if not isinstance(x, int) and x.dtype is dtype and x.is_contiguous() and x.numel() >= need and x.get_device() == dev:
+        return x.data_ptr()
+    p = _arg(x, name, kind, need)              # names what is wrong, if it is the tensor's type, layout or size
+    if not isinstance(x, int) and x.get_device() != dev:
+        raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{dev}")
+    return p
+
+
 def pq_quant_rows8(X, codes, scales, g=0, T=None, D=None, ldx=None, stream=None) -> None:
     """X bf16 [T, ldx] -> codes int8 [T, D], scales float32 [T] (one a row); rows rotated in blocks of g
     channels by a Hadamard matrix first (g = 0: not)."""
-    T = X.shape[0] if T is None else T
-    D = X.shape[1] if D is None else D
-    ldx = _row_stride(X, "X") if ldx is None else ldx
-    xp = _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
-    _check(lib.pq_quant_rows8(xp, T, D, ldx, g, _arg(codes, "codes", "i8", T * D),
-                              _arg(scales, "scales", "f32", T), _stream(stream)), "pq_quant_rows8")
+    dev, torch = _here()
+    xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
+    _check(lib.pq_quant_rows8(xp, T, D, ldx, g, _on(codes, "codes", "i8", torch.int8, T * D, dev),
+                              _on(scales, "scales", "f32", torch.float32, T, dev), _raw_stream(stream, dev, torch)),
+           "pq_quant_rows8")
 
 
-def _row_stride(x, name):
-    """Row stride of a 2-D activation tensor; a single row's stride says nothing, so its length stands in."""
-    if x.dim() != 2:
-        raise ValueError(f"{name}: expected a 2-D tensor")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+def _rows8(X, T, D, ldx, dev, torch):
+    """Pointer, rows, channels and row stride of bf16 rows (a single row's stride says nothing: its length stands in)."""
+    if isinstance(X, int):
+        return X, T, D, D if ldx is None else ldx
+    if X.dim() != 2:
+        raise ValueError("X: expected a 2-D tensor")
+    rows, cols = X.shape
+    T, D = rows if T is None else T, cols if D is None else D
+    if ldx is None:
+        ldx = X.stride(0) if rows > 1 else cols
+    if X.dtype is not torch.bfloat16 or X.stride(1) != 1 or T > rows or D > cols or X.get_device() != dev:
+        _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
+        if X.get_device() != dev:
+            raise ValueError(f"X: on {X.device}, but the current device is cuda:{dev}")
+    return X.data_ptr(), T, D, ldx
 
 
-def _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype):
+def _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype, dev, torch):
     if not isinstance(Y, int):
-        import torch
         y_kind = PQ_OUT_BF16 if Y.dtype == torch.bfloat16 else PQ_OUT_F32
         if out_dtype is None:
             out_dtype = y_kind
@@ -381,30 +413,30 @@ def _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype):
             raise ValueError(f"Y: dtype {Y.dtype} does not match out_dtype={out_dtype}")
     elif out_dtype is None:
         out_dtype = PQ_OUT_F32
-    return out_dtype, (_arg(codes_A, "codes_A", "i8", T * D), _arg(scales_A, "scales_A", "f32", T),
-                       _arg(codes_W, "codes_W", "i8", N * D), _arg(scales_W, "scales_W", "f32", N),
-                       _arg(Y, "Y", "y", T * N))
+    f32, i8 = torch.float32, torch.int8
+    return (out_dtype, _on(codes_A, "codes_A", "i8", i8, T * D, dev), _on(scales_A, "scales_A", "f32", f32, T, dev),
+            _on(codes_W, "codes_W", "i8", i8, N * D, dev), _on(scales_W, "scales_W", "f32", f32, N, dev),
+            _on(Y, "Y", "y", torch.bfloat16 if out_dtype == PQ_OUT_BF16 else f32, T * N, dev))
 
 
 def pq_w8a8_gemm(codes_A, scales_A, codes_W, scales_W, Y, T=None, N=None, D=None, out_dtype=None, stream=None) -> None:
     """Y [T, N] = scales_A[t] scales_W[n] (codes_A codes_W^T), codes int8 [T, D] and [N, D]."""
+    dev, torch = _here()
     T = codes_A.shape[0] if T is None else T
     N = codes_W.shape[0] if N is None else N
     D = codes_A.shape[1] if D is None else D
-    out_dtype, p = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype)
-    _check(lib.pq_w8a8_gemm(p[0], p[1], p[2], p[3], T, N, D, p[4], out_dtype, _stream(stream)), "pq_w8a8_gemm")
+    out, ca, sa, cw, sw, y = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype, dev, torch)
+    _check(lib.pq_w8a8_gemm(ca, sa, cw, sw, T, N, D, y, out, _raw_stream(stream, dev, torch)), "pq_w8a8_gemm")
 
 
 def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=None, D=None, ldx=None, out_dtype=None,
                    stream=None) -> None:
     """:func:`pq_quant_rows8` of X into codes_A / scales_A and :func:`pq_w8a8_gemm` into Y, one call."""
-    T = X.shape[0] if T is None else T
+    dev, torch = _here()
+    xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
     N = codes_W.shape[0] if N is None else N
-    D = X.shape[1] if D is None else D
-    ldx = _row_stride(X, "X") if ldx is None else ldx
-    xp = _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
-    out_dtype, p = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype)
-    _check(lib.pq_w8a8_linear(xp, T, D, ldx, g, p[0], p[1], p[2], p[3], N, p[4], out_dtype, _stream(stream)),
+    out, ca, sa, cw, sw, y = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype, dev, torch)
+    _check(lib.pq_w8a8_linear(xp, T, D, ldx, g, ca, sa, cw, sw, N, y, out, _raw_stream(stream, dev, torch)),
            "pq_w8a8_linear")
 
 
@@ -432,6 +464,13 @@ class KV4Cache:
                              _arg(v_codes, "v_codes", "u8", n * shape[3]), _arg(v_scales, "v_scales", "f32", n),
                              self.pages, self.page_size, self.heads, self.head_dim, flags)
         self.handle = _c.addressof(self._s)
+        self.device = k_codes.get_device()
+
+    def on(self, dev):
+        """The handle, for a call on device `dev`."""
+        if dev != self.device:
+            raise ValueError(f"the cache is on cuda:{self.device}, but the current device is cuda:{dev}")
+        return self.handle
 
     @classmethod
     def empty(cls, pages, heads, page_size, head_dim, rotate_k=True, rotate_v=True, device="cuda"):
@@ -442,22 +481,32 @@ class KV4Cache:
         return cls(codes[0], scales[0], codes[1], scales[1], rotate_k, rotate_v)
 
 
-def _rows_of(x, name, width, T):
+def _rows_of(x, name, width, T, dev, torch):
     """Pointer and row stride of [T, width] bf16 rows (or [T, heads, head_dim] with dense heads)."""
-    import torch
-    if x.dtype != torch.bfloat16:
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3:
+        cols = shape[1] * shape[2]
+        dense = stride[2] == 1 and (stride[1] == shape[2] or shape[1] == 1)
+    elif len(shape) == 2:
+        cols, dense = shape[1], stride[1] == 1
+    else:
+        raise ValueError(f"{name}: expected [T, heads * head_dim] or [T, heads, head_dim] with dense heads")
+    if x.dtype is not torch.bfloat16:
         raise ValueError(f"{name}: dtype {x.dtype} is not accepted (expected torch.bfloat16)")
     if not x.is_cuda:
         raise ValueError("expected a CUDA tensor: the library takes device pointers")
-    if x.dim() == 3 and (x.stride(1) == x.shape[2] or x.shape[1] == 1):
-        cols = x.shape[1] * x.shape[2]
-    elif x.dim() == 2:
-        cols = x.shape[1]
-    else:
-        raise ValueError(f"{name}: expected [T, heads * head_dim] or [T, heads, head_dim] with dense heads")
-    if x.stride(-1) != 1 or cols != width or x.shape[0] != T:
-        raise ValueError(f"{name}: shape {tuple(x.shape)} (strides {x.stride()}) is not {T} rows of {width} channels")
-    return x.data_ptr(), (x.stride(0) if T > 1 else width)
+    if not dense or cols != width or shape[0] != T:
+        raise ValueError(f"{name}: shape {tuple(shape)} (strides {stride}) is not {T} rows of {width} channels")
+    if x.get_device() != dev:
+        raise ValueError(f"{name}: on {x.device}, but the current device is cuda:{dev}")
+    return x.data_ptr(), (stride[0] if T > 1 else width)
+
+
+def _query_width(Q, hd):
+    w = Q.shape[1] * (Q.shape[2] if Q.dim() == 3 else 1)
+    if w % hd:
+        raise ValueError(f"Q: rows of {w} channels are not whole heads of {hd}")
+    return w
 
 
 def pq_kv4_append(cache: KV4Cache, Q, K, V, Q_out, positions, slots, rope=None, q_norm=None, k_norm=None, eps=1e-6,
@@ -467,27 +516,36 @@ def pq_kv4_append(cache: KV4Cache, Q, K, V, Q_out, positions, slots, rope=None, 
 
     rope float32 [positions, rope_dim] (cosines, then sines), positions int32 [T]; q_norm, k_norm bf16 [head_dim].
     """
+    dev, torch = _here()
     T, hd = Q.shape[0], cache.head_dim
-    wq, wk = Q.shape[1] * (Q.shape[2] if Q.dim() == 3 else 1), cache.heads * hd
-    (qp, ldq), (kp, ldk), (vp, ldv) = _rows_of(Q, "Q", wq, T), _rows_of(K, "K", wk, T), _rows_of(V, "V", wk, T)
-    if wq % hd:
-        raise ValueError(f"Q: rows of {wq} channels are not whole heads of {hd}")
-    if rope is not None and rope.dim() != 2:
-        raise ValueError("rope: expected [positions, rope_dim]")
-    _check(lib.pq_kv4_append(cache.handle, qp, ldq, kp, ldk, vp, ldv, T, wq // hd,
-                             _arg(q_norm, "q_norm", "bf16", hd), _arg(k_norm, "k_norm", "bf16", hd), eps,
-                             _arg(rope, "rope", "f32", 0), 0 if rope is None else rope.shape[0],
-                             0 if rope is None else rope.shape[1], _arg(positions, "positions", "i32", T),
-                             _arg(slots, "slots", "i64", T), PQ_KV4_INTERLEAVED if interleaved else 0,
-                             _arg(Q_out, "Q_out", "bf16", T * wq), _stream(stream)), "pq_kv4_append")
+    wq, wk = _query_width(Q, hd), cache.heads * hd
+    qp, ldq = _rows_of(Q, "Q", wq, T, dev, torch)
+    kp, ldk = _rows_of(K, "K", wk, T, dev, torch)
+    vp, ldv = _rows_of(V, "V", wk, T, dev, torch)
+    rope_rows = rope_dim = 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError("rope: expected [positions, rope_dim]")
+        rope_rows, rope_dim = rope.shape
+    bf16 = torch.bfloat16
+    _check(lib.pq_kv4_append(cache.on(dev), qp, ldq, kp, ldk, vp, ldv, T, wq // hd,
+                             _on(q_norm, "q_norm", "bf16", bf16, hd, dev), _on(k_norm, "k_norm", "bf16", bf16, hd, dev), eps,
+                             _on(rope, "rope", "f32", torch.float32, 0, dev), rope_rows, rope_dim,
+                             _on(positions, "positions", "i32", torch.int32, T, dev),
+                             _on(slots, "slots", "i64", torch.int64, T, dev), PQ_KV4_INTERLEAVED if interleaved else 0,
+                             _on(Q_out, "Q_out", "bf16", bf16, T * wq, dev), _raw_stream(stream, dev, torch)),
+           "pq_kv4_append")
 
 
 def pq_kv4_read(cache: KV4Cache, slots, K_out, V_out, stream=None) -> None:
     """Cached rows at slots (int64 [T]) as bf16 values in the cache's basis; negative slots give zeros."""
+    dev, torch = _here()
     T = slots.shape[0]
     n = T * cache.heads * cache.head_dim
-    _check(lib.pq_kv4_read(cache.handle, _arg(slots, "slots", "i64", T), T, _arg(K_out, "K_out", "bf16", n),
-                           _arg(V_out, "V_out", "bf16", n), _stream(stream)), "pq_kv4_read")
+    _check(lib.pq_kv4_read(cache.on(dev), _on(slots, "slots", "i64", torch.int64, T, dev), T,
+                           _on(K_out, "K_out", "bf16", torch.bfloat16, n, dev),
+                           _on(V_out, "V_out", "bf16", torch.bfloat16, n, dev), _raw_stream(stream, dev, torch)),
+           "pq_kv4_read")
 
 
 def pq_kv4_attention(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_q, max_len, scale=None, window=0,
@@ -498,18 +556,19 @@ def pq_kv4_attention(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_
     block_table int32 [B, pages of a sequence]; max_q, max_len: upper bounds (they size the launch); scale defaults
     to 1 / sqrt(head_dim); window > 0: each token sees itself and the window - 1 before it.
     """
+    dev, torch = _here()
     T, hd = Q.shape[0], cache.head_dim
-    wq = Q.shape[1] * (Q.shape[2] if Q.dim() == 3 else 1)
-    (qp, ldq), (op, ldo) = _rows_of(Q, "Q", wq, T), _rows_of(O, "O", wq, T)
-    if wq % hd:
-        raise ValueError(f"Q: rows of {wq} channels are not whole heads of {hd}")
+    wq = _query_width(Q, hd)
+    qp, ldq = _rows_of(Q, "Q", wq, T, dev, torch)
+    op, ldo = _rows_of(O, "O", wq, T, dev, torch)
     if block_table.dim() != 2:
         raise ValueError("block_table: expected [sequences, pages]")
     B, width = block_table.shape
-    _check(lib.pq_kv4_attention(cache.handle, qp, ldq, wq // hd, _arg(q_start, "q_start", "i32", B + 1),
-                                _arg(seq_lens, "seq_lens", "i32", B),
-                                _arg(block_table, "block_table", "i32", B * width), width, B, T, max_q, max_len,
-                                hd ** -0.5 if scale is None else scale, window, op, ldo, _stream(stream)),
+    i32 = torch.int32
+    _check(lib.pq_kv4_attention(cache.on(dev), qp, ldq, wq // hd, _on(q_start, "q_start", "i32", i32, B + 1, dev),
+                                _on(seq_lens, "seq_lens", "i32", i32, B, dev),
+                                _on(block_table, "block_table", "i32", i32, B * width, dev), width, B, T, max_q, max_len,
+                                hd ** -0.5 if scale is None else scale, window, op, ldo, _raw_stream(stream, dev, torch)),
            "pq_kv4_attention")
 
 
