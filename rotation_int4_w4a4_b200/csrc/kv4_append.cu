@@ -10,9 +10,9 @@
 // set-up of the experiments: the cache quantised in groups of 128, here the head.)
 //
 // Bytes bound it: every input is read and every output written once (4 bytes a query channel, 2.5 + 4/hd a key or
-// value channel), all else stays in registers.  A head is hd / 4 lanes of 4 channels: the norm's sum and the head's
-// maximum are shuffle trees over those lanes, the rotation's partner and the Hadamard stages beyond 4 channels are
-// shuffles too, so nothing goes through shared memory.
+// value channel), all else stays in registers.  A head is spread over a few lanes: the norm's sum and the head's
+// maximum are shuffle trees over those lanes, the rotation's partner and the Hadamard stages beyond a lane's channels
+// are shuffles too, so nothing goes through shared memory.
 //
 // A code sits next to a rounding border now and then, so the arithmetic is pinned: products and sums are rounded one by
 // one (no contraction into FMAs), sums are taken over neighbours first, and the factor of each head is
@@ -29,133 +29,219 @@
 namespace pq {
 namespace {
 
-constexpr int AP_WARPS = 8;
 // Heads whose maximum is below this are taken as zero (7 / max would overflow float32).
 constexpr float kKv4Tiny = 1e-36f;
 
-__device__ __forceinline__ float4 ap_load4(const uint16_t* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
+// bf16 channels of a lane: 4 consecutive (8-byte aligned), or 8 of the head's first half and the same 8 of its second.
+template <int HD, int E, bool WIDE>
+__device__ __forceinline__ void ap_load(float (&v)[E], const uint16_t* head, int e0) {
+#pragma unroll
+  for (int c = 0; c < E; c += 8) {
+    const uint16_t* p = head + e0 + c * (HD / 16);      // c = 8: HD / 2 further on
+    if constexpr (WIDE) {
+      row_bf16x8(__ldg(reinterpret_cast<const uint4*>(p)), v + c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < (E < 8 ? E : 8); k += 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(p + k));
+        v[c + k] = __uint_as_float(w.x << 16), v[c + k + 1] = __uint_as_float(w.x & 0xFFFF0000u);
+        v[c + k + 2] = __uint_as_float(w.y << 16), v[c + k + 3] = __uint_as_float(w.y & 0xFFFF0000u);
+      }
+    }
+  }
 }
 
-__device__ __forceinline__ uint2 ap_bf16x4(const float (&v)[4]) {
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+__device__ __forceinline__ uint32_t ap_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&p);
 }
 
-// A warp takes 32 / LANES heads of one token; HD = 4 LANES.
-template <int LANES>
-__global__ void __launch_bounds__(32 * AP_WARPS) kv4_append_kernel(const Kv4AppendArgs a) {
-  constexpr int HD = 4 * LANES;
+// Products of pairs, each rounded on its own (mul.rn: as __fmul_rn).
+__device__ __forceinline__ void ap_mul2(float& a, float& b, float c, float d) {
+  ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(a, b), ptx::f2_pack(c, d)), a, b);
+}
+
+// (a, b) -> (a cos - b sin, b cos + a sin) of N channel pairs.
+template <int N>
+__device__ __forceinline__ void ap_turn(float* a, float* b, const float* cos, const float* sin) {
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(cos + c)), s4 = __ldg(reinterpret_cast<const float4*>(sin + c));
+    const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const uint64_t x = ptx::f2_pack(a[c + k], a[c + k + 1]), y = ptx::f2_pack(b[c + k], b[c + k + 1]);
+      const uint64_t co = ptx::f2_pack(cc[k], cc[k + 1]), si = ptx::f2_pack(ss[k], ss[k + 1]);
+      ptx::f2_unpack(ptx::f2_sub(ptx::f2_mul(x, co), ptx::f2_mul(y, si)), a[c + k], a[c + k + 1]);
+      ptx::f2_unpack(ptx::f2_add(ptx::f2_mul(y, co), ptx::f2_mul(x, si)), b[c + k], b[c + k + 1]);
+    }
+  }
+}
+
+// A head is LANES lanes of E channels, a warp takes 32 / LANES heads of one kind (queries, keys or values) of one token,
+// a block one token's warps (blockIdx.x; more than 16 warps: blockIdx.y too).
+// E = 16: 8 channels of each half of the head.  The pairs of a position rotation of the whole head then meet inside a
+// thread, loads and stores cover 128 contiguous bytes of a head, and shuffles and reductions are shared by four times
+// the channels (8192 tokens of 32 + 8 + 8 heads of 128, L1 and shuffles bounding both: see the table of measurements).
+// E = 4: any layout of the rotation (halves that do not fall on multiples of 8 channels, or cross the middle).
+template <int HD, int E, bool WIDE>
+__global__ void __launch_bounds__(512) kv4_append_kernel(const Kv4AppendArgs a) {
+  constexpr int LANES = HD / E;
   constexpr int HPW = 32 / LANES;                       // heads per warp
+  constexpr bool SPLIT = E == 16;
   const int lane = threadIdx.x & 31;
   const int l = lane & (LANES - 1);                     // lane within the head
-  const int e0 = 4 * l;                                 // its first channel
-  const int heads = a.heads_q + 2 * a.cache.heads;
-  const int groups = (heads + HPW - 1) / HPW;           // warps per token
-  const int64_t warp = (int64_t)blockIdx.x * AP_WARPS + (threadIdx.x >> 5);
-  const int64_t t = warp / groups;
-  if (t >= a.T) return;                                 // whole warps
-  const int head = (int)(warp - t * groups) * HPW + lane / LANES;
-  const bool live = head < heads;
-  const int kind = head < a.heads_q ? 0 : head < a.heads_q + a.cache.heads ? 1 : 2;   // query, key, value
-  const int h = kind == 0 ? head : kind == 1 ? head - a.heads_q : head - a.heads_q - a.cache.heads;
+  const int e0 = (SPLIT ? 8 : 4) * l;                   // its first channel
+  const int heads = a.cache.heads;
+  const int wq = (a.heads_q + HPW - 1) / HPW, wk = (heads + HPW - 1) / HPW;   // warps a token for queries; keys or values
+  const int64_t t = blockIdx.x;
+  int w = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (w >= wq + 2 * wk) return;                         // whole warps
+  const int kind = w < wq ? 0 : w < wq + wk ? 1 : 2;    // query, key, value
+  w -= kind == 0 ? 0 : kind == 1 ? wq : wq + wk;
+  const int h = w * HPW + lane / LANES;
+  const bool live = h < (kind == 0 ? a.heads_q : heads);
 
-  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (live) {
+  float v[E];
+  {
     const uint16_t* src = kind == 0 ? a.Q + t * a.ldq : kind == 1 ? a.K + t * a.ldk : a.V + t * a.ldv;
-    const float4 x = ap_load4(src + h * HD + e0);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    ap_load<HD, E, WIDE>(v, src + (live ? h : 0) * HD, e0);
   }
   const uint16_t* norm = kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr;
-  if (a.q_norm || a.k_norm) {
-    float s = __fadd_rn(__fadd_rn(__fmul_rn(v[0], v[0]), __fmul_rn(v[1], v[1])),
-                        __fadd_rn(__fmul_rn(v[2], v[2]), __fmul_rn(v[3], v[3])));
+  if (norm) {                                           // the same for the whole warp
+    // sum of squares, neighbours first: the thread's channels, the lanes, then the head's halves
+    float s[E];
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
-    if (live && norm) {
-      const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(s, 1.0f / HD), a.eps)));
-      const float4 w = ap_load4(norm + e0);
-      v[0] = __fmul_rn(__fmul_rn(v[0], r), w.x);
-      v[1] = __fmul_rn(__fmul_rn(v[1], r), w.y);
-      v[2] = __fmul_rn(__fmul_rn(v[2], r), w.z);
-      v[3] = __fmul_rn(__fmul_rn(v[3], r), w.w);
+    for (int c = 0; c < E; c += 2) {
+      s[c] = v[c], s[c + 1] = v[c + 1];
+      ap_mul2(s[c], s[c + 1], v[c], v[c + 1]);
+    }
+#pragma unroll
+    for (int o = 1; o < (SPLIT ? 8 : 4); o <<= 1)
+#pragma unroll
+      for (int c = 0; c < E; c += 2 * o) s[c] = __fadd_rn(s[c], s[c + o]);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+      s[0] = __fadd_rn(s[0], __shfl_xor_sync(0xffffffffu, s[0], o));
+      if constexpr (SPLIT) s[8] = __fadd_rn(s[8], __shfl_xor_sync(0xffffffffu, s[8], o));
+    }
+    if constexpr (SPLIT) s[0] = __fadd_rn(s[0], s[8]);
+    const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(s[0], 1.0f / HD), a.eps)));
+    float g[E];
+    ap_load<HD, E, WIDE>(g, norm, e0);
+#pragma unroll
+    for (int c = 0; c < E; c += 2) {
+      ap_mul2(v[c], v[c + 1], r, r);
+      ap_mul2(v[c], v[c + 1], g[c], g[c + 1]);
     }
   }
   bool bad = false;
   if (a.rope) {
     const int pos = a.positions[t];
     bad = pos < 0 || pos >= a.rope_rows;
-    const int half = a.rope_dim / 2;
-    const float* row = a.rope + (int64_t)(bad ? 0 : pos) * a.rope_dim;
-    const bool turns = live && kind < 2 && e0 < a.rope_dim;
-    if (a.interleaved) {
-      if (turns) {
-        const float2 c = *reinterpret_cast<const float2*>(row + e0 / 2);
-        const float2 s = *reinterpret_cast<const float2*>(row + half + e0 / 2);
-        const float x0 = v[0], x1 = v[1], x2 = v[2], x3 = v[3];
-        v[0] = __fsub_rn(__fmul_rn(x0, c.x), __fmul_rn(x1, s.x));
-        v[1] = __fadd_rn(__fmul_rn(x1, c.x), __fmul_rn(x0, s.x));
-        v[2] = __fsub_rn(__fmul_rn(x2, c.y), __fmul_rn(x3, s.y));
-        v[3] = __fadd_rn(__fmul_rn(x3, c.y), __fmul_rn(x2, s.y));
-      }
-    } else {
-      // the partner channels are half / 4 lanes away
-      const bool first = e0 < half;
-      const int from = lane + (first ? half / 4 : -(half / 4));
-      float o[4];
+    if (kind < 2) {
+      const int half = a.rope_dim / 2;
+      const float* row = a.rope + (int64_t)(bad ? 0 : pos) * a.rope_dim;
+      if (a.interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(0xffffffffu, v[i], from & 31);
-      if (turns) {
-        const int e = first ? e0 : e0 - half;
-        const float4 c = *reinterpret_cast<const float4*>(row + e);
-        const float4 s = *reinterpret_cast<const float4*>(row + half + e);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        for (int c = 0; c < E; c += 4) {
+          const int e = e0 + (c >= 8 ? HD / 2 + c - 8 : c);
+          if (e < a.rope_dim) {
+            const float2 cs = __ldg(reinterpret_cast<const float2*>(row + e / 2));
+            const float2 sn = __ldg(reinterpret_cast<const float2*>(row + half + e / 2));
+            const float x0 = v[c], x1 = v[c + 1], x2 = v[c + 2], x3 = v[c + 3];
+            v[c] = __fsub_rn(__fmul_rn(x0, cs.x), __fmul_rn(x1, sn.x));
+            v[c + 1] = __fadd_rn(__fmul_rn(x1, cs.x), __fmul_rn(x0, sn.x));
+            v[c + 2] = __fsub_rn(__fmul_rn(x2, cs.y), __fmul_rn(x3, sn.y));
+            v[c + 3] = __fadd_rn(__fmul_rn(x3, cs.y), __fmul_rn(x2, sn.y));
+          }
+        }
+      } else if (SPLIT && half == HD / 2) {
+        ap_turn<(SPLIT ? 8 : 0)>(v, v + (SPLIT ? 8 : 0), row + e0, row + half + e0);
+      } else {
+        // the partner channels are some lanes away (SPLIT: in the head's first half, which holds all that turn)
+        constexpr int N = SPLIT ? 8 : 4;
+        const bool first = e0 < half, turns = e0 < a.rope_dim;
+        const int from = (lane + (first ? half / N : -(half / N))) & 31;
+        float o[N];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __fmul_rn(v[i], cc[i]), q = __fmul_rn(o[i], ss[i]);
-          v[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
+        for (int c = 0; c < N; ++c) o[c] = __shfl_sync(0xffffffffu, v[c], from);
+        if (turns) {
+          if (first) {
+            ap_turn<N>(v, o, row + e0, row + half + e0);
+          } else {
+            ap_turn<N>(o, v, row + e0 - half, row + e0);
+          }
         }
       }
     }
   }
   const bool rotate = kind < 2 ? a.cache.rotate_k != 0 : a.cache.rotate_v != 0;
-  if (a.cache.rotate_k || a.cache.rotate_v) {
-    float y[4];
-    {
-      const float p0 = v[0] + v[1], p1 = v[0] - v[1], p2 = v[2] + v[3], p3 = v[2] - v[3];
-      y[0] = p0 + p2, y[1] = p1 + p3, y[2] = p0 - p2, y[3] = p1 - p3;
+  if (rotate) {
+    // Hadamard butterflies, neighbours first: within 8 (or 4) channels, across the lanes, across the head's halves
+    constexpr int N = SPLIT ? 8 : 4;
+#pragma unroll
+    for (int c = 0; c < E; c += 2) {
+      const float x = v[c], y = v[c + 1];
+      v[c] = x + y;
+      v[c + 1] = x - y;
     }
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1)
+    for (int o = 2; o < N; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float p = __shfl_xor_sync(0xffffffffu, y[i], o);
-        y[i] = (l & o) ? p - y[i] : y[i] + p;
+      for (int c = 0; c < E; c += 2)
+        if ((c & o) == 0) {
+          const uint64_t x = ptx::f2_pack(v[c], v[c + 1]), y = ptx::f2_pack(v[c + o], v[c + o + 1]);
+          ptx::f2_unpack(ptx::f2_add(x, y), v[c], v[c + 1]);
+          ptx::f2_unpack(ptx::f2_sub(x, y), v[c + o], v[c + o + 1]);
+        }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) {
+      // the upper lane of a pair keeps the difference: partner - own
+      const float sign = (l & o) ? -1.0f : 1.0f;
+#pragma unroll
+      for (int c = 0; c < E; c += 2) {
+        const uint64_t p = ptx::f2_pack(__shfl_xor_sync(0xffffffffu, v[c], o), __shfl_xor_sync(0xffffffffu, v[c + 1], o));
+        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(v[c], v[c + 1]), ptx::f2_pack(sign, sign), p), v[c], v[c + 1]);
       }
-    if (rotate) {
+    }
+    if constexpr (SPLIT) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = y[i];
+      for (int c = 0; c < 8; c += 2) {
+        const uint64_t x = ptx::f2_pack(v[c], v[c + 1]), y = ptx::f2_pack(v[c + 8], v[c + 9]);
+        ptx::f2_unpack(ptx::f2_add(x, y), v[c], v[c + 1]);
+        ptx::f2_unpack(ptx::f2_sub(x, y), v[c + 8], v[c + 9]);
+      }
     }
   }
-  float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (bad && lane == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
-  if (!live) return;
   // 1 / sqrt(hd), and that over 7
   constexpr float kNorm = HD == 128 ? (float)0.08838834764831845 : 0.125f;
   constexpr float kStep = (float)(1.0 / (7.0 * (HD == 128 ? 11.313708498984761 : 8.0)));
   if (kind == 0) {
-    if (rotate) {
+    if (!live) return;
+    const float f = rotate ? kNorm : 1.0f;
+    uint16_t* dst = a.Q_out + (t * a.heads_q + h) * (int64_t)HD + e0;
+    uint32_t y[E / 2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __fmul_rn(v[i], kNorm);
+    for (int c = 0; c < E; c += 2) {
+      ap_mul2(v[c], v[c + 1], f, f);
+      y[c / 2] = bad ? 0u : ap_bf16x2(v[c], v[c + 1]);
     }
-    if (bad) v[0] = v[1] = v[2] = v[3] = 0.0f;
-    *reinterpret_cast<uint2*>(a.Q_out + (t * a.heads_q + h) * (int64_t)HD + e0) = ap_bf16x4(v);
+    if constexpr (SPLIT) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(dst + HD / 2) = make_uint4(y[4], y[5], y[6], y[7]);
+    } else {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(y[0], y[1]);
+    }
     return;
   }
+  float m = 0.0f;
+#pragma unroll
+  for (int c = 0; c < E; c += 2) m = ptx::max3(m, fabsf(v[c]), fabsf(v[c + 1]));
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (!live) return;
   const int64_t slot = a.slots[t];
   if (slot < 0 || bad) return;
   const int64_t page = slot >> a.cache.page_shift;
@@ -164,72 +250,95 @@ __global__ void __launch_bounds__(32 * AP_WARPS) kv4_append_kernel(const Kv4Appe
     return;
   }
   const int64_t in_page = slot & ((1 << a.cache.page_shift) - 1);
-  const int64_t at = (((page * a.cache.heads + h) << a.cache.page_shift) + in_page);
+  const int64_t at = (((page * heads + h) << a.cache.page_shift) + in_page);
   const bool zero = !(m >= kKv4Tiny);
   const float inv = zero ? 0.0f : __fmul_rn(__frcp_rn(m), 7.0f);
-  uint32_t b[4];
+  uint8_t* codes = (kind == 1 ? a.cache.k_codes : a.cache.v_codes) + at * (HD / 2) + e0 / 2;
+  uint32_t packed[E / 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(__fmul_rn(v[i], inv), kRowRoundMagic)) & 15u;
-  const uint16_t packed = (uint16_t)(b[0] | (b[1] << 4) | (b[2] << 8) | (b[3] << 12));
-  uint8_t* codes = kind == 1 ? a.cache.k_codes : a.cache.v_codes;
-  *reinterpret_cast<uint16_t*>(codes + at * (HD / 2) + 2 * l) = packed;
+  for (int c = 0; c < E; c += 4) {
+    uint32_t b[4];
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      float x, y;
+      ptx::f2_unpack(ptx::f2_add(ptx::f2_mul(ptx::f2_pack(v[c + k], v[c + k + 1]), ptx::f2_pack(inv, inv)),
+                                 ptx::f2_pack(kRowRoundMagic, kRowRoundMagic)), x, y);
+      b[k] = __float_as_uint(x), b[k + 1] = __float_as_uint(y);
+    }
+    packed[c / 4] = (b[0] & 15u) | ((b[1] & 15u) << 4) | ((b[2] & 15u) << 8) | ((b[3] & 15u) << 12);
+  }
+  if constexpr (SPLIT) {
+    *reinterpret_cast<uint32_t*>(codes) = packed[0] | (packed[1] << 16);
+    *reinterpret_cast<uint32_t*>(codes + HD / 4) = packed[2] | (packed[3] << 16);
+  } else {
+    *reinterpret_cast<uint16_t*>(codes) = (uint16_t)packed[0];
+  }
   if (l == 0) {
     float* scales = kind == 1 ? a.cache.k_scales : a.cache.v_scales;
     scales[at] = zero ? 0.0f : __fmul_rn(m, rotate ? kStep : (float)(1.0 / 7.0));
   }
 }
 
-// Cached rows back as bf16(code * scale), in the cache's own basis; rows without a slot become 0.  One thread a
-// 4-byte piece (8 channels).
-__global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View c, const int64_t* __restrict__ slots, int64_t T,
+// Cached rows back as bf16(code * scale), in the cache's own basis; rows without a slot become 0.  A block a token, a
+// thread a 4-byte piece (8 channels).
+__global__ void __launch_bounds__(256) kv4_read_kernel(const Kv4View c, const int64_t* __restrict__ slots,
                                                        uint16_t* __restrict__ K_out, uint16_t* __restrict__ V_out,
                                                        unsigned int* status) {
-  const int words = c.head_dim / 8;
-  const int64_t per_token = 2 * (int64_t)c.heads * words;
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t t = i / per_token;
-  if (t >= T) return;
-  const int r = (int)(i - t * per_token);
-  const int kv = r >= c.heads * words;
-  const int h = (r - kv * c.heads * words) / words, w = r % words;
-  uint16_t* out = kv ? V_out : K_out;
-  const int64_t slot = slots[t];
+  const int64_t t = blockIdx.x;
+  const int wshift = c.head_dim == 128 ? 4 : 3;          // words a head, log2
+  const int per = c.heads << wshift;
+  const int64_t slot = __ldg(slots + t);
   const int64_t page = slot >> c.page_shift;
-  uint4 y = make_uint4(0u, 0u, 0u, 0u);
-  if (slot >= 0 && page < c.pages) {
-    const int64_t at = ((page * c.heads + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
-    const uint32_t x = reinterpret_cast<const uint32_t*>((kv ? c.v_codes : c.k_codes))[at * words + w];
-    const float s = (kv ? c.v_scales : c.k_scales)[at];
-    uint32_t o[4];
+  const bool in = slot >= 0 && page < c.pages;
+  if (slot >= 0 && !in && threadIdx.x == 0) atomicOr(status, PQ_DEV_BAD_INDEX);
+  for (int r = threadIdx.x; r < 2 * per; r += blockDim.x) {
+    const bool kv = r >= per;
+    const int p = kv ? r - per : r;
+    const int h = p >> wshift;
+    uint4 y = make_uint4(0u, 0u, 0u, 0u);
+    if (in) {
+      const int64_t at = ((page * c.heads + h) << c.page_shift) + (slot & ((1 << c.page_shift) - 1));
+      const uint32_t x = reinterpret_cast<const uint32_t*>((kv ? c.v_codes : c.k_codes))[(at << wshift) + (p & ((1 << wshift) - 1))];
+      const float s = (kv ? c.v_scales : c.k_scales)[at];
+      uint32_t o[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float lo = (float)((int)(x << (28 - 8 * k)) >> 28) * s, hi = (float)((int)(x << (24 - 8 * k)) >> 28) * s;
-      const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-      o[k] = *reinterpret_cast<const uint32_t*>(&p);
+      for (int k = 0; k < 4; ++k)
+        o[k] = ap_bf16x2((float)((int)(x << (28 - 8 * k)) >> 28) * s, (float)((int)(x << (24 - 8 * k)) >> 28) * s);
+      y = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    y = make_uint4(o[0], o[1], o[2], o[3]);
-  } else if (slot >= 0) {
-    atomicOr(status, PQ_DEV_BAD_INDEX);
+    *reinterpret_cast<uint4*>((kv ? V_out : K_out) + (t * per + p) * 8) = y;
   }
-  *reinterpret_cast<uint4*>(out + (t * c.heads + h) * (int64_t)c.head_dim + 8 * w) = y;
+}
+
+template <int HD, int E, bool WIDE>
+cudaError_t launch_append(const Kv4AppendArgs& a, cudaStream_t stream) {
+  constexpr int HPW = 32 / (HD / E);
+  const int warps = (a.heads_q + HPW - 1) / HPW + 2 * ((a.cache.heads + HPW - 1) / HPW);
+  const int rounds = (warps + 15) / 16, block = (warps + rounds - 1) / rounds;
+  kv4_append_kernel<HD, E, WIDE><<<dim3((unsigned)a.T, (unsigned)rounds), 32 * block, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t stream) {
-  const int heads = a.heads_q + 2 * a.cache.heads;
-  const int hpw = a.cache.head_dim == 128 ? 1 : 2;
-  const int64_t warps = a.T * ((heads + hpw - 1) / hpw);
-  const unsigned grid = (unsigned)((warps + AP_WARPS - 1) / AP_WARPS);
-  if (a.cache.head_dim == 128) kv4_append_kernel<32><<<grid, 32 * AP_WARPS, 0, stream>>>(a);
-  else kv4_append_kernel<16><<<grid, 32 * AP_WARPS, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int hd = a.cache.head_dim;
+  const bool wide = hd == 128;
+  // Rotations of the whole head, of 8-channel groups within its first half, or of neighbours suit 16 channels a lane.
+  if (!a.rope || a.interleaved || a.rope_dim == hd || (a.rope_dim % 16 == 0 && a.rope_dim <= hd / 2)) {
+    const bool vec = aligned16(a.Q) && aligned16(a.K) && aligned16(a.V) && a.ldq % 8 == 0 && a.ldk % 8 == 0 && a.ldv % 8 == 0 &&
+                     aligned16(a.q_norm) && aligned16(a.k_norm);
+    if (vec) return wide ? launch_append<128, 16, true>(a, stream) : launch_append<64, 16, true>(a, stream);
+    return wide ? launch_append<128, 16, false>(a, stream) : launch_append<64, 16, false>(a, stream);
+  }
+  return wide ? launch_append<128, 4, false>(a, stream) : launch_append<64, 4, false>(a, stream);
 }
 
 cudaError_t launch_kv4_read(const Kv4View& c, const int64_t* slots, int64_t T, uint16_t* K_out, uint16_t* V_out,
                             unsigned int* status, cudaStream_t stream) {
-  const int64_t n = T * 2 * c.heads * (c.head_dim / 8);
-  kv4_read_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(c, slots, T, K_out, V_out, status);
+  const int per = 2 * c.heads * (c.head_dim / 8);
+  const int threads = per >= 256 ? 256 : (per + 31) / 32 * 32;
+  kv4_read_kernel<<<(unsigned)T, threads, 0, stream>>>(c, slots, K_out, V_out, status);
   return cudaGetLastError();
 }
 
