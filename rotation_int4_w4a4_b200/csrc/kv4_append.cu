@@ -85,7 +85,7 @@ __device__ __forceinline__ void ap_turn(float* a, float* b, const float* cos, co
 // the channels (8192 tokens of 32 + 8 + 8 heads of 128, L1 and shuffles bounding both: see the table of measurements).
 // E = 4: any layout of the rotation (halves that do not fall on multiples of 8 channels, or cross the middle).
 template <int HD, int E, bool WIDE>
-__global__ void __launch_bounds__(512) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs a) {
   constexpr int LANES = HD / E;
   constexpr int HPW = 32 / LANES;                       // heads per warp
   constexpr bool SPLIT = E == 16;
@@ -95,6 +95,8 @@ __global__ void __launch_bounds__(512) kv4_append_kernel(const Kv4AppendArgs a) 
   const int heads = a.cache.heads;
   const int wq = (a.heads_q + HPW - 1) / HPW, wk = (heads + HPW - 1) / HPW;   // warps a token for queries; keys or values
   const int64_t t = blockIdx.x;
+  const int64_t slot = a.slots[t];
+  const int pos = a.rope ? a.positions[t] : 0;
   int w = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (w >= wq + 2 * wk) return;                         // whole warps
   const int kind = w < wq ? 0 : w < wq + wk ? 1 : 2;    // query, key, value
@@ -137,7 +139,6 @@ __global__ void __launch_bounds__(512) kv4_append_kernel(const Kv4AppendArgs a) 
   }
   bool bad = false;
   if (a.rope) {
-    const int pos = a.positions[t];
     bad = pos < 0 || pos >= a.rope_rows;
     if (kind < 2) {
       const int half = a.rope_dim / 2;
@@ -242,7 +243,6 @@ __global__ void __launch_bounds__(512) kv4_append_kernel(const Kv4AppendArgs a) 
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!live) return;
-  const int64_t slot = a.slots[t];
   if (slot < 0 || bad) return;
   const int64_t page = slot >> a.cache.page_shift;
   if (page >= a.cache.pages) {
