@@ -91,7 +91,7 @@ static_assert(kPairSmem <= 232448, "shared memory exceeds 227 KB");
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_pair_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const float* __restrict__ scales_A,
     const float* __restrict__ scales_W, void* __restrict__ Y, int T, int N, int steps, int m_tiles, int tiles,
-    int out_bf16, int pdl, unsigned int* status) {
+    int out_bf16, unsigned int* status) {
   extern __shared__ unsigned char smem_raw[];
   PairSmem& S = *reinterpret_cast<PairSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -125,8 +125,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_p
 
   if (warp == 0) {
     if (lane == 0) {
-      // Launched as the dependent of the quantisation: it reads the codes only once that is complete.
-      if (pdl) ptx::griddep_wait();
       const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
       int step = 0;
       bool ok = true;
@@ -176,7 +174,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_p
     }
   } else if (warp >= P_EPI_WARP0) {
     // Lane quarter warp % 4 (channels), token half of the tile.
-    if (pdl) ptx::griddep_wait();
     const int ew = warp - P_EPI_WARP0;
     const int sub = warp & 3, half = ew >> 2;
     const uint32_t acc_empty0 = ptx::mapa_shared(ptx::smem_addr(&S.acc_empty[0]), 0);
@@ -236,31 +233,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_p
 constexpr int TM = 128;                 // weight rows per tile
 constexpr int T_THREADS = 192;
 
-// NP: token columns of a tile.  The stages leave room for two CTAs per SM.
-template <int NP> struct TileGeom {
-  static constexpr int STAGES = NP == 16 ? 6 : NP == 32 ? 5 : NP == 64 ? 4 : 3;
+// NP: token columns of a tile.  DEEP: stages for one CTA per SM (about 200 KB in flight), otherwise for two.
+template <int NP, bool DEEP> struct TileGeom {
+  static constexpr int SHALLOW = NP == 16 ? 6 : NP == 32 ? 5 : NP == 64 ? 4 : 3;
+  static constexpr int STAGES = DEEP ? 2 * SHALLOW : SHALLOW;
   static constexpr uint32_t TX = (TM + NP) * KB;
   static constexpr uint32_t COLS = NP < 32 ? 32 : NP;
 };
 
-template <int NP> struct __align__(1024) TileSmem {
-  uint8_t a[TileGeom<NP>::STAGES][TM * KB];
-  uint8_t b[TileGeom<NP>::STAGES][NP * KB];
-  uint64_t full[TileGeom<NP>::STAGES], empty[TileGeom<NP>::STAGES];
+template <int NP, bool DEEP> struct __align__(1024) TileSmem {
+  uint8_t a[TileGeom<NP, DEEP>::STAGES][TM * KB];
+  uint8_t b[TileGeom<NP, DEEP>::STAGES][NP * KB];
+  uint64_t full[TileGeom<NP, DEEP>::STAGES], empty[TileGeom<NP, DEEP>::STAGES];
   uint64_t acc_full;
   uint32_t tmem_slot;
   int abort_flag;
 };
 
+// Token column c of the cluster's R partial tiles (int32 [token][128 channels] at the same offset in each), 4 channels a
+// lane.
+template <int R>
+__device__ __forceinline__ void add_ranges(int4& d, uint32_t base, int c, int lane) {
+  int4 v[R];
+#pragma unroll
+  for (int p = 0; p < R; ++p) v[p] = ptx::ld_cluster_v4(ptx::mapa_shared(base + 16u * (uint32_t)(c * (TM / 4) + lane), (uint32_t)p));
+#pragma unroll
+  for (int p = 0; p < R; ++p) d.x += v[p].x, d.y += v[p].y, d.z += v[p].z, d.w += v[p].w;
+}
+
 // Grid: x = tile * split + range (the cluster), tiles channel-fastest.
-template <int NP>
+template <int NP, bool DEEP>
 __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const float* __restrict__ scales_A,
     const float* __restrict__ scales_W, void* __restrict__ Y, int T, int N, int steps, int m_tiles, int split,
     int out_bf16, int pdl, unsigned int* status) {
-  constexpr int STAGES = TileGeom<NP>::STAGES;
+  using Geom = TileGeom<NP, DEEP>;
+  constexpr int STAGES = Geom::STAGES;
   extern __shared__ unsigned char smem_raw[];
-  TileSmem<NP>& S = *reinterpret_cast<TileSmem<NP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  TileSmem<NP, DEEP>& S = *reinterpret_cast<TileSmem<NP, DEEP>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   static_assert(sizeof(S.a) + sizeof(S.b) >= sizeof(int) * TM * NP, "partial tile overlays the stages");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = (int)blockIdx.x / split, rank = (int)blockIdx.x % split;
@@ -282,7 +292,7 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
     ptx::prefetch_tmap(&tmA);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(&S.tmem_slot, TileGeom<NP>::COLS);
+    ptx::tmem_alloc(&S.tmem_slot, Geom::COLS);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -295,7 +305,7 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
       // The first ring of weights is requested before the wait for the kernel that writes the token codes.
       const int head = min(STAGES, k1 - k0);
       for (int i = 0; i < head; ++i) {
-        ptx::mbar_arrive_expect_tx(&S.full[i], TileGeom<NP>::TX);
+        ptx::mbar_arrive_expect_tx(&S.full[i], Geom::TX);
         ptx::tma_load_2d(S.a[i], &tmW, &S.full[i], (k0 + i) * KB, m0);
       }
       if (pdl) ptx::griddep_wait();
@@ -304,7 +314,7 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
       for (int kb = k0 + head; kb < k1; ++kb, ++step) {
         const int s = step % STAGES;
         if (!wait_or_abort(&S.empty[s], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &S.abort_flag, status)) break;
-        ptx::mbar_arrive_expect_tx(&S.full[s], TileGeom<NP>::TX);
+        ptx::mbar_arrive_expect_tx(&S.full[s], Geom::TX);
         ptx::tma_load_2d(S.a[s], &tmW, &S.full[s], kb * KB, m0);
         ptx::tma_load_2d(S.b[s], &tmA, &S.full[s], kb * KB, t0);
       }
@@ -367,17 +377,39 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
   ptx::tc_fence_before();
   if (split > 1) {
     ptx::cluster_sync();                                  // every partial tile is written
-    // This CTA adds token columns rank, rank + split, ... over the cluster; a warp takes 32 channels of one.
+    // This CTA adds token columns rank, rank + split, ... over the cluster; a warp takes one column, a lane 4 channels of
+    // it, with the reads of all the cluster's tiles (and of two columns) in flight at once.
     if (pdl) ptx::griddep_wait();
     const uint32_t mine = ptx::smem_addr(S.a);
-    for (int w = warp; w < 4 * ((NP - rank + split - 1) / split); w += T_THREADS / 32) {
-      const int c = rank + split * (w >> 2), row = 32 * (w & 3) + lane;
-      const int t = t0 + c, n = m0 + row;
-      if (t < T && n < N) {
-        int d = 0;
-        for (int p = 0; p < split; ++p)
-          d += ptx::ld_cluster_s32(ptx::mapa_shared(mine + 4u * (uint32_t)(c * TM + row), (uint32_t)p));
-        store_y(Y, (int64_t)t * N + n, d, __ldg(scales_A + t), __ldg(scales_W + n), out_bf16);
+    constexpr int W = T_THREADS / 32;
+    const int n = m0 + 4 * lane;
+    float sw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sw[k] = n + k < N ? __ldg(scales_W + n + k) : 0.0f;
+    const int columns = min(NP, T - t0);
+    for (int c0 = rank + split * warp; c0 < columns; c0 += 2 * split * W) {
+      int4 d[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+      float sa[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = c0 + u * split * W;
+        if (c < columns) {
+          sa[u] = __ldg(scales_A + t0 + c);
+          if (split == 2) add_ranges<2>(d[u], mine, c, lane);
+          else if (split == 4) add_ranges<4>(d[u], mine, c, lane);
+          else add_ranges<8>(d[u], mine, c, lane);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int c = c0 + u * split * W;
+        if (c < columns) {
+          const int v[4] = {d[u].x, d[u].y, d[u].z, d[u].w};
+          const int64_t at = (int64_t)(t0 + c) * N + n;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (n + k < N) store_y(Y, at + k, v[k], sa[u], sw[k], out_bf16);
+        }
       }
     }
     ptx::cluster_sync();                                  // nobody leaves while its tile is read
@@ -386,7 +418,7 @@ __global__ void __launch_bounds__(T_THREADS) w8a8_tile_kernel(
   }
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, TileGeom<NP>::COLS);
+    ptx::tmem_dealloc(tmem, Geom::COLS);
   }
 }
 
@@ -401,14 +433,14 @@ void pdl_attribute(cudaLaunchAttribute* a) {
   a->val.programmaticStreamSerializationAllowed = 1;
 }
 
-template <int NP>
+template <int NP, bool DEEP>
 pq_status launch_tile(const CUtensorMap& tmW, const CUtensorMap& tmA, const float* scales_A, const float* scales_W,
                       void* Y, int T, int N, int steps, int m_tiles, int64_t tiles, int split, int bf16, bool pdl,
                       unsigned int* status, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(TileSmem<NP>) + 1024;
-  static_assert(2 * smem <= 232448, "two CTAs of the tile kernel share an SM");
+  constexpr size_t smem = sizeof(TileSmem<NP, DEEP>) + 1024;
+  static_assert((DEEP ? 1 : 2) * smem <= 232448, "shared memory exceeds 227 KB an SM");
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(w8a8_tile_kernel<NP>), (int)smem, done);
+  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(w8a8_tile_kernel<NP, DEEP>), (int)smem, done);
   if (e != cudaSuccess) return cuda_fail(e, "w8a8_tile_kernel attributes");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
@@ -423,7 +455,7 @@ pq_status launch_tile(const CUtensorMap& tmW, const CUtensorMap& tmA, const floa
   pdl_attribute(&attr[1]);
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_tile_kernel<NP>, tmW, tmA, scales_A, scales_W, Y, T, N, steps, m_tiles,
+  return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_tile_kernel<NP, DEEP>, tmW, tmA, scales_A, scales_W, Y, T, N, steps, m_tiles,
                                       split, bf16, pdl ? 1 : 0, status),
                    "w8a8_tile_kernel launch");
 }
@@ -455,23 +487,28 @@ pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t
     cfg.blockDim = dim3(P_THREADS, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    pdl_attribute(&attr);
-    cfg.attrs = &attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    // Never as a programmatic dependent: CTAs that fill an SM would wait there while the quantisation still needs it
+    // (8192 x 4096 x 14336: 466 us so, 423 us one after the other).
     return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_pair_kernel, tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps,
-                                        (int)pair_m, (int)pair_tiles, bf16, pdl ? 1 : 0, status),
+                                        (int)pair_m, (int)pair_tiles, bf16, status),
                      "w8a8_pair_kernel launch");
   }
   const int np = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
-  // Ranges of the reduction: as long as the CTAs still fit next to each other (two an SM) and each keeps some steps.
+  // Ranges of the reduction: as long as every CTA still has an SM of its own and keeps some steps.  (Two CTAs an SM, with
+  // half the stages each, streamed no faster, and as a dependent they waited for SMs: 64 tokens, N = D = 4096, 8 ranges:
+  // 20.7 us behind the quantisation; 4: 14.5.)
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sms && steps >= 4 * split) split *= 2;
+  while (split < 8 && tiles * split * 2 <= sms && steps >= 4 * split) split *= 2;
   pq_status st = operand_map(&tmW, codes_W, N, D, TM);
   if (st == PQ_OK) st = operand_map(&tmA, codes_A, T, D, np);
   if (st != PQ_OK) return st;
-#define PQ_TILE_CASE(NP) launch_tile<NP>(tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps, (int)m_tiles, tiles, split, bf16, pdl, status, stream)
+#define PQ_TILE_CASE(NP)                                                                                                  \
+  (tiles * split <= sms                                                                                                    \
+       ? launch_tile<NP, true>(tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps, (int)m_tiles, tiles, split, bf16, pdl, \
+                               status, stream)                                                                            \
+       : launch_tile<NP, false>(tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps, (int)m_tiles, tiles, split, bf16,   \
+                                pdl, status, stream))
   return np == 16 ? PQ_TILE_CASE(16) : np == 32 ? PQ_TILE_CASE(32) : np == 64 ? PQ_TILE_CASE(64) : PQ_TILE_CASE(128);
 #undef PQ_TILE_CASE
 }
