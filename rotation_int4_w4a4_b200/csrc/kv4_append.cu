@@ -69,11 +69,10 @@ __device__ __forceinline__ void ap_turn(float* a, float* b, const float* cos, co
     const float4 c4 = __ldg(reinterpret_cast<const float4*>(cos + c)), s4 = __ldg(reinterpret_cast<const float4*>(sin + c));
     const float cc[4] = {c4.x, c4.y, c4.z, c4.w}, ss[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      const uint64_t x = ptx::f2_pack(a[c + k], a[c + k + 1]), y = ptx::f2_pack(b[c + k], b[c + k + 1]);
-      const uint64_t co = ptx::f2_pack(cc[k], cc[k + 1]), si = ptx::f2_pack(ss[k], ss[k + 1]);
-      ptx::f2_unpack(ptx::f2_sub(ptx::f2_mul(x, co), ptx::f2_mul(y, si)), a[c + k], a[c + k + 1]);
-      ptx::f2_unpack(ptx::f2_add(ptx::f2_mul(y, co), ptx::f2_mul(x, si)), b[c + k], b[c + k + 1]);
+    for (int k = 0; k < 4; ++k) {                         // (scalar: a packed product and sum may become one packed FMA)
+      const float x = a[c + k], y = b[c + k];
+      a[c + k] = __fsub_rn(__fmul_rn(x, cc[k]), __fmul_rn(y, ss[k]));
+      b[c + k] = __fadd_rn(__fmul_rn(y, cc[k]), __fmul_rn(x, ss[k]));
     }
   }
 }
@@ -259,12 +258,7 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
   for (int c = 0; c < E; c += 4) {
     uint32_t b[4];
 #pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-      float x, y;
-      ptx::f2_unpack(ptx::f2_add(ptx::f2_mul(ptx::f2_pack(v[c + k], v[c + k + 1]), ptx::f2_pack(inv, inv)),
-                                 ptx::f2_pack(kRowRoundMagic, kRowRoundMagic)), x, y);
-      b[k] = __float_as_uint(x), b[k + 1] = __float_as_uint(y);
-    }
+    for (int k = 0; k < 4; ++k) b[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[c + k], inv), kRowRoundMagic));
     packed[c / 4] = (b[0] & 15u) | ((b[1] & 15u) << 4) | ((b[2] & 15u) << 8) | ((b[3] & 15u) << 12);
   }
   if constexpr (SPLIT) {

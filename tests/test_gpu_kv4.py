@@ -80,6 +80,63 @@ def test_append(pq, T, hq, hkv, hd, page, q_norm, k_norm, rope_dim, inter, rk, r
     pq.pq_check_status()
 
 
+def neighbours_sum(v):
+    while v.shape[-1] > 1:
+        v = v[..., 0::2] + v[..., 1::2]
+    return v
+
+
+def butterflies(y):
+    n, shape, h = y.shape[-1], y.shape, 1
+    while h < n:
+        v = y.reshape(*shape[:-1], n // (2 * h), 2, h)
+        y = torch.stack([v[..., 0, :] + v[..., 1, :], v[..., 0, :] - v[..., 1, :]], dim=-2).reshape(shape)
+        h *= 2
+    return y
+
+
+@pytest.mark.parametrize("hd,rope_dim,inter", [(128, 128, False), (128, 64, False), (128, 24, False), (128, 128, True), (64, 64, False),
+                                               (64, 32, False), (64, 48, False), (64, 32, True), (128, 0, False)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_bits(pq, hd, rope_dim, inter, norm):
+    """Codes and scales are those of the documented float32 formula, each product and sum rounded on its own, bit for bit:
+    a code next to a rounding border does not depend on how the kernel groups its arithmetic."""
+    T, hkv, hq, page = 700, 3, 6, 32
+    gen = generator(hd + rope_dim)
+    rows = torch.randn(T, (hq + 2 * hkv) * hd, generator=gen, device="cuda").to(torch.bfloat16)
+    Q, K, V = rows.split([hq * hd, hkv * hd, hkv * hd], dim=1)
+    w = (1 + 0.2 * torch.randn(hd, generator=gen, device="cuda")).to(torch.bfloat16) if norm else None
+    rope = rope_table(900, rope_dim) if rope_dim else None
+    positions = torch.randint(0, 900, (T,), generator=gen, device="cuda", dtype=torch.int32)
+    cache = pq.KV4Cache.empty(-(-T // page), hkv, page, hd)
+    slots = torch.arange(T, device="cuda")
+    Q_out = torch.empty(T, hq, hd, dtype=torch.bfloat16, device="cuda")
+    pq.pq_kv4_append(cache, Q, K, V, Q_out, positions, slots, rope=rope, q_norm=w, k_norm=w, eps=1e-5, interleaved=inter)
+
+    def formula(x, heads, turned):
+        x = x.float().reshape(T, heads, hd)
+        if turned and norm:
+            r = 1 / torch.sqrt(neighbours_sum(x * x) * (1 / hd) + 1e-5)
+            x = (x * r) * w.float()
+        if turned and rope_dim:
+            cs = rope[positions.long()][:, None, :]
+            cos, sin = cs[..., :rope_dim // 2], cs[..., rope_dim // 2:]
+            a, b = (x[..., 0:rope_dim:2], x[..., 1:rope_dim:2]) if inter else (x[..., :rope_dim // 2], x[..., rope_dim // 2:rope_dim])
+            u, v = a * cos - b * sin, b * cos + a * sin
+            head = torch.stack([u, v], dim=-1).flatten(-2) if inter else torch.cat([u, v], dim=-1)
+            x = torch.cat([head, x[..., rope_dim:]], dim=-1)
+        return butterflies(x)
+
+    assert torch.equal(Q_out, (formula(Q, hq, True) * (1 / hd ** 0.5)).to(torch.bfloat16))
+    for i, (x, turned) in ((0, (K, True)), (2, (V, False))):
+        y = formula(x, hkv, turned)
+        m = y.abs().amax(-1, keepdim=True)
+        want = torch.round(y * (m.reciprocal() * 7))
+        got, _ = unpack(cache.tensors[i][slots // page, :, slots % page], cache.tensors[i + 1][slots // page, :, slots % page])
+        assert torch.equal(got.float(), want)
+        assert torch.equal(cache.tensors[i + 1][slots // page, :, slots % page], (m * (1 / (7 * hd ** 0.5)))[..., 0])
+
+
 def test_append_zero_heads_and_bad_indices(pq):
     hd, hkv, page = 128, 2, 16
     cache = pq.KV4Cache.empty(2, hkv, page, hd)
