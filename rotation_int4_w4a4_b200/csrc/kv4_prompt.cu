@@ -164,19 +164,6 @@ __device__ __forceinline__ void fwht(float (&v)[N]) {
 // Swizzled place of 16-byte chunk c of row r in a block of 128-byte rows.
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// What a row's thread keeps of a step's tokens when some are hidden: which the row sees, and their scales.
-struct StepView {
-  const float4* ks;        // 4 tokens a vector
-  const float4* vs;
-  const uint32_t* valid;   // a bit a token
-  float c;                 // score units: |scale| log2(e) times the row's power of two
-  int tok0, row_lo, row_hi;
-  __device__ __forceinline__ bool sees(int t) const {    // token t of the step
-    const int tok = tok0 + t;
-    return ((valid[t >> 5] >> (t & 31)) & 1u) && tok >= row_lo && tok <= row_hi;
-  }
-};
-
 // Largest of 32 raw scores.
 __device__ __forceinline__ float chunk_max(const uint32_t (&r)[32]) {
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -204,61 +191,59 @@ __device__ __forceinline__ float chunk_exp(const uint32_t (&r)[32], float c, flo
   return a0 + a1;
 }
 
-// The same with hidden tokens: 16 scores in log2 units, -inf where the row does not see.
-__device__ __forceinline__ void masked_scores(const uint32_t (&r)[16], int t, const StepView& v, float (&e)[16]) {
+// Bits of the 64 tokens from `first` on that lie in [lo, hi].
+__device__ __forceinline__ uint64_t token_bits(int first, int lo, int hi) {
+  const int a = lo - first, b = hi - first;
+  const uint64_t upto = b < 0 ? 0ull : b >= 63 ? ~0ull : (2ull << b) - 1;
+  const uint64_t from = a <= 0 ? ~0ull : a > 63 ? 0ull : ~0ull << a;
+  return upto & from;
+}
+
+// 32 raw scores in log2 units, -inf where the row does not see the token (a bit each).
+__device__ __forceinline__ void chunk_mask(uint32_t (&r)[32], uint32_t seen, const float4* ks, float c) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float4 ks = v.ks[t / 4 + k];
-    const float kk[4] = {ks.x, ks.y, ks.z, ks.w};
+  for (int k = 0; k < 8; ++k) {
+    const float4 k4 = ks[k];
+    const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      e[4 * k + q] = v.sees(t + 4 * k + q) ? __uint_as_float(r[4 * k + q]) * (kk[q] * v.c) : -INFINITY;
+      r[4 * k + q] = __float_as_uint((seen >> (4 * k + q)) & 1u ? __uint_as_float(r[4 * k + q]) * (kk[q] * c) : -INFINITY);
   }
 }
 
-// Maximum of the row's 64 scores of a half step with hidden tokens (log2 units; tokens t0 .. of the step), and the
-// largest value scale seen.
-__device__ __forceinline__ float half_max_masked(uint32_t s_col, int t0, const StepView& v, float& vm) {
-  float top = -INFINITY;
+// Largest value scale of 32 tokens, among those the row sees.
+__device__ __forceinline__ float chunk_scale_max(uint32_t seen, const float4* vs) {
+  float m = 0.0f;
 #pragma unroll 1
-  for (int t = 0; t < HT; t += 16) {
-    uint32_t r[16];
-    float e[16];
-    ptx::tmem_ld32x16(s_col + t, r);
-    ptx::tmem_ld_wait(r);
-    masked_scores(r, t0 + t, v, e);
-    const float* vs = reinterpret_cast<const float*>(v.vs) + t0 + t;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      top = fmaxf(top, e[k]);
-      if (v.sees(t0 + t + k)) vm = fmaxf(vm, finite_or_0(vs[k]));
-    }
+  for (int k = 0; k < 8; ++k) {
+    const float4 v = vs[k];
+    const uint32_t b = seen >> (4 * k);
+    m = ptx::max3(m, b & 1u ? finite_or_0(v.x) : 0.0f, b & 2u ? finite_or_0(v.y) : 0.0f);
+    m = ptx::max3(m, b & 4u ? finite_or_0(v.z) : 0.0f, b & 8u ? finite_or_0(v.w) : 0.0f);
   }
-  return top;
+  return m;
 }
 
-// Their probabilities, written over scores already read; returns their sum.
-__device__ __forceinline__ float half_exp_masked(uint32_t s_col, int t0, const StepView& v, float ref) {
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int t = 0; t < HT; t += 16) {
-    uint32_t r[16], p[8];
-    float e[16];
-    ptx::tmem_ld32x16(s_col + t, r);
-    ptx::tmem_ld_wait(r);
-    masked_scores(r, t0 + t, v, e);
-    const float* vs = reinterpret_cast<const float*>(v.vs) + t0 + t;
+// 2^(s + off) of 32 masked scores, their sum, and times the value scales as 16 registers of fp16 pairs.  A
+// hidden token's value scale may be anything: select, do not multiply.
+__device__ __forceinline__ float chunk_exp_masked(const uint32_t (&r)[32], uint32_t seen, const float4* vs, float off,
+                                                  uint32_t (&p)[16]) {
+  float sum[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float x = ex2(e[k] - ref);
-      sum += x;
-      e[k] = v.sees(t0 + t + k) ? x * vs[k] : 0.0f;      // a hidden token's value scale may be anything
+  for (int k = 0; k < 8; ++k) {
+    const float4 v4 = vs[k];
+    const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
+    float y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float e = ex2(__uint_as_float(r[4 * k + q]) + off);
+      sum[q & 1] += e;
+      y[q] = (seen >> (4 * k + q)) & 1u ? e * vv[q] : 0.0f;
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) p[k] = pack_f16(e[2 * k], e[2 * k + 1]);
-    ptx::tmem_st32x8(s_col + t / 2, p);
+    p[2 * k] = pack_f16(y[0], y[1]);
+    p[2 * k + 1] = pack_f16(y[2], y[3]);
   }
-  return sum;
+  return sum[0] + sum[1];
 }
 
 // 32 output columns in channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4 (odd k: 16 times).
@@ -391,16 +376,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     }
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t s_col = lane_base + S_COL + 128 * i, o_col = lane_base + O_COL + 128 * i;
-    auto view = [&](int j) {
-      const int sc = j % SC_RING, pos = n - w.qlen + rr / group;
-      return StepView{reinterpret_cast<const float4*>(S.ks[sc]), reinterpret_cast<const float4*>(S.vs[sc]), S.valid[sc], c_row,
-                      (j0 + j) * PT, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1)};
-    };
     float m = -INFINITY, l = 0.0f;
     bool ok = i < tiles;
     for (int h = 0; h < 2 * steps && ok; ++h) {            // half steps
       const int j = h >> 1, sc = j % SC_RING, t0 = HT * (h & 1);
-      const uint32_t s_buf = s_col + HT * (h & 1);
+      const uint32_t s_buf = s_col + t0;
       if (t0 == 0) ok = pr_warp_wait(&S.sc_full[sc], (uint32_t)(j / SC_RING) & 1u, &S.abort_flag, a.status);
       ok = ok && pr_warp_wait(&S.s_full[i][h & 1], (uint32_t)j & 1u, &S.abort_flag, a.status);
       if (!ok) break;
@@ -427,15 +407,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         }
         return true;
       };
+      // The maximum is not taken first: the reference of the halves before serves until a row's probabilities outgrow
+      // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
       if (whole) {
+        bool over = m == -INFINITY;
+        uint32_t pa[16], pb[16];
         float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
         const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
         kp.x *= c_row, kp.y *= c_row;
-        // The maximum is not taken first: the reference of the steps before serves until a row's probabilities outgrow
-        // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
-        bool over = m == -INFINITY;
         float sum0, sum1;
-        uint32_t pa[16], pb[16];
         for (int pass = 0;; ++pass) {
           uint32_t xa[32], xb[32];                       // the scores of the half's two groups of 32 tokens
           ptx::tmem_ld32(s_buf, xa);
@@ -453,17 +433,41 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
         if (!ok) break;
-        ptx::tmem_st32x16(s_buf, pa);
-        ptx::tmem_st32x16(s_buf + 16, pb);
         // each sum without its values' power of two
         l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
+        ptx::tmem_st32x16(s_buf, pa);
+        ptx::tmem_st32x16(s_buf + 16, pb);
       } else {
-        float vm = 0.0f;
-        const float mx = half_max_masked(s_buf, t0, view(j), vm);
-        const float cand = mx + scale_exponent(vm);
+        const int pos = n - w.qlen + rr / group;
+        const uint64_t bits = token_bits((j0 + j) * PT + t0, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1));
+        const uint32_t sa = (uint32_t)bits & (t0 ? valid.z : valid.x), sb = (uint32_t)(bits >> 32) & (t0 ? valid.w : valid.y);
+        const float4* ks = reinterpret_cast<const float4*>(S.ks[sc]) + t0 / 4;
+        const float4* vs = reinterpret_cast<const float4*>(S.vs[sc]) + t0 / 4;
+        float top = -INFINITY, vm = 0.0f;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t seen = g ? sb : sa;
+          uint32_t x[32];
+          ptx::tmem_ld32(s_buf + 32 * g, x);
+          ptx::tmem_ld_wait(x);
+          chunk_mask(x, seen, ks + 8 * g, c_row);
+          top = fmaxf(top, chunk_max(x));
+          vm = fmaxf(vm, chunk_scale_max(seen, vs + 8 * g));
+        }
+        const float cand = top + scale_exponent(vm);
         const bool grow = cand > m + kLazy || (m == -INFINITY && cand > m);
         if (__any_sync(0xffffffffu, grow) && !(ok = raise(grow, cand))) break;
-        l += half_exp_masked(s_buf, t0, view(j), m == -INFINITY ? 0.0f : m);
+        const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+        for (int g = 0; g < 2; ++g) {
+          const uint32_t seen = g ? sb : sa;
+          uint32_t x[32], p[16];
+          ptx::tmem_ld32(s_buf + 32 * g, x);
+          ptx::tmem_ld_wait(x);
+          chunk_mask(x, seen, ks + 8 * g, c_row);
+          l += chunk_exp_masked(x, seen, vs + 8 * g, -ref, p);
+          ptx::tmem_st32x16(s_buf + 16 * g, p);          // over scores already read
+        }
       }
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
