@@ -57,7 +57,6 @@ constexpr int PR_STAGES = 2;             // key and value stages
 constexpr int SC_RING = 4;               // scale stages: a step's scales outlive its keys by at most one step
 constexpr uint64_t kPrWaitNs = 2000000000ull;
 constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i + 64 (half & 1), O_i at 256 + 128 i
-constexpr float kLazy = 8.0f;            // log2 growth of the reference that is let pass where the maximum is taken
 constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 65504) from which it is taken elsewhere
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
@@ -74,7 +73,7 @@ struct __align__(1024) PromptSmem {
   // What multiplies a token's score, and its probability: its scales, or (scales multiplied in) its group's powers of 2.
   float ks[SC_RING][PT], vs[SC_RING][PT];
   uint32_t valid[SC_RING][4];                            // which tokens exist, a bit each
-  int scaled[SC_RING];                                   // every row sees all tokens: scales are in the operands
+  int scaled[SC_RING][4];                                // the 32 tokens' scales are in the operands
   float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
@@ -147,18 +146,11 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
   return false;
 }
 
-// Unnormalised Walsh-Hadamard transform of a head in registers, Sylvester order.
-template <int N>
-__device__ __forceinline__ void fwht(float (&v)[N]) {
-#pragma unroll
-  for (int h = 1; h < N; h <<= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if ((i & h) == 0) {
-        const float x = v[i], y = v[i + h];
-        v[i] = x + y;
-        v[i + h] = x - y;
-      }
+// Pairs through one butterfly: (x + y, x - y).
+__device__ __forceinline__ void butterfly2(uint64_t& x, uint64_t& y) {
+  const uint64_t s = ptx::f2_add(x, y);
+  y = ptx::f2_sub(x, y);
+  x = s;
 }
 
 // Swizzled place of 16-byte chunk c of row r in a block of 128-byte rows.
@@ -199,54 +191,54 @@ __device__ __forceinline__ uint64_t token_bits(int first, int lo, int hi) {
   return upto & from;
 }
 
-// 32 raw scores in log2 units, -inf where the row does not see the token (a bit each).
-__device__ __forceinline__ void chunk_mask(uint32_t (&r)[32], uint32_t seen, const float4* ks, float c) {
+// The same with the scales of 32 tokens (log2 units), of which the row sees some (a bit each): the largest score and the
+// largest value scale seen so far.  What a hidden token holds is selected away, never multiplied by 0.
+__device__ __forceinline__ void chunk_tops(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* vs, float c,
+                                           float& top, float& vm) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float4 k4 = ks[k];
-    const float kk[4] = {k4.x, k4.y, k4.z, k4.w};
+    const float4 k4 = ks[k], v4 = vs[k];
+    const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      r[4 * k + q] = __float_as_uint((seen >> (4 * k + q)) & 1u ? __uint_as_float(r[4 * k + q]) * (kk[q] * c) : -INFINITY);
+      if (seen & (1u << (4 * k + q))) {
+        top = fmaxf(top, __uint_as_float(r[4 * k + q]) * (kk[q] * c));
+        vm = fmaxf(vm, finite_or_0(vv[q]));
+      }
   }
 }
 
-// Largest value scale of 32 tokens, among those the row sees.
-__device__ __forceinline__ float chunk_scale_max(uint32_t seen, const float4* vs) {
-  float m = 0.0f;
-#pragma unroll 1
-  for (int k = 0; k < 8; ++k) {
-    const float4 v = vs[k];
-    const uint32_t b = seen >> (4 * k);
-    m = ptx::max3(m, b & 1u ? finite_or_0(v.x) : 0.0f, b & 2u ? finite_or_0(v.y) : 0.0f);
-    m = ptx::max3(m, b & 4u ? finite_or_0(v.z) : 0.0f, b & 8u ? finite_or_0(v.w) : 0.0f);
-  }
-  return m;
-}
-
-// 2^(s + off) of 32 masked scores, their sum, and times the value scales as 16 registers of fp16 pairs.  A
-// hidden token's value scale may be anything: select, do not multiply.
-__device__ __forceinline__ float chunk_exp_masked(const uint32_t (&r)[32], uint32_t seen, const float4* vs, float off,
-                                                  uint32_t (&p)[16]) {
-  float sum[2] = {0.0f, 0.0f};
+// chunk_exp with the scales: probabilities times value scales in p; top: the largest magnitude of those so far.
+__device__ __forceinline__ float chunk_exp_masked(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* vs,
+                                                  float c, float off, uint32_t (&p)[16], float& top) {
+  const uint64_t c2 = ptx::f2_pack(c, c), off2 = ptx::f2_pack(off, off);
+  uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float4 v4 = vs[k];
-    const float vv[4] = {v4.x, v4.y, v4.z, v4.w};
-    float y[4];
+    const float4 k4 = ks[k], v4 = vs[k];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float e = ex2(__uint_as_float(r[4 * k + q]) + off);
-      sum[q & 1] += e;
-      y[q] = (seen >> (4 * k + q)) & 1u ? e * vv[q] : 0.0f;
+    for (int q = 0; q < 2; ++q) {
+      const int t = 4 * k + 2 * q;
+      const uint64_t f = ptx::f2_mul(q ? ptx::f2_pack(k4.z, k4.w) : ptx::f2_pack(k4.x, k4.y), c2);
+      float e0, e1, y0, y1;
+      ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(r[t]), __uint_as_float(r[t + 1])), f, off2), e0, e1);
+      const bool s0 = seen & (1u << t), s1 = seen & (2u << t);
+      e0 = s0 ? ex2(e0) : 0.0f;
+      e1 = s1 ? ex2(e1) : 0.0f;
+      sum[q] = ptx::f2_add(sum[q], ptx::f2_pack(e0, e1));
+      y0 = e0 * (s0 ? (q ? v4.z : v4.x) : 0.0f);
+      y1 = e1 * (s1 ? (q ? v4.w : v4.y) : 0.0f);
+      top = ptx::max3(top, fabsf(y0), fabsf(y1));
+      p[t / 2] = pack_f16(y0, y1);
     }
-    p[2 * k] = pack_f16(y[0], y[1]);
-    p[2 * k + 1] = pack_f16(y[2], y[3]);
   }
-  return sum[0] + sum[1];
+  float a0, a1;
+  ptx::f2_unpack(ptx::f2_add(sum[0], sum[1]), a0, a1);
+  return a0 + a1;
 }
 
-// 32 output columns in channel order: place 2k of each 8 holds channel k, 2k + 1 holds k + 4 (odd k: 16 times).
+// Columns of tensor memory hold channels in the operands' order: place 2k of each 8 channel k, 2k + 1 channel k + 4 (odd
+// k: 16 times too large on the keys' side, which the queries undo, and on the values' side, undone here).
 __device__ __forceinline__ void load_channels(float (&o)[32], uint32_t col) {
   uint32_t x[32];
   ptx::tmem_ld32(col, x);
@@ -260,17 +252,86 @@ __device__ __forceinline__ void load_channels(float (&o)[32], uint32_t col) {
       o[c + k + 4] = __uint_as_float(x[c + 2 * k + 1]) * f;
     }
 }
+
+// Unnormalised Walsh-Hadamard transform (Sylvester order) of a row's HD columns: the stages within 32 channels go back
+// to tensor memory, those across them follow 16 columns of each 32 at a time; put(c, v) takes channels c .. c + 15 of
+// the 32-channel block b.  Two columns an instruction (channels k and k + 4) but for the stage between them.
+template <int HD, typename Put>
+__device__ __forceinline__ void rotate_row(uint32_t col, Put put) {
+  constexpr int N32 = HD / 32;
+  const uint64_t up = ptx::f2_pack(kOddNibble, kOddNibble), down = ptx::f2_pack(-kOddNibble, -kOddNibble);
+#pragma unroll 1
+  for (int c = 0; c < HD; c += 32) {
+    uint32_t x[32];
+    uint64_t v[16];
+    ptx::tmem_ld32(col + c, x);
+    ptx::tmem_ld_wait(x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = ptx::f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {                    // channels k, k + 1; the odd one's factor goes in
+      const uint64_t y = v[k + 1];
+      v[k + 1] = ptx::f2_fma(y, down, v[k]);
+      v[k] = ptx::f2_fma(y, up, v[k]);
+    }
+#pragma unroll
+    for (int h = 2; h < 16; h <<= 1) {                   // channels 2, 8, 16 apart
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if ((k & h) == 0) butterfly2(v[k], v[k + h]);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {                       // 4 apart
+      float a, b;
+      ptx::f2_unpack(v[k], a, b);
+      x[2 * k] = __float_as_uint(a + b);
+      x[2 * k + 1] = __float_as_uint(a - b);
+    }
+    ptx::tmem_st32x16(col + c, reinterpret_cast<const uint32_t(&)[16]>(x[0]));
+    ptx::tmem_st32x16(col + c + 16, reinterpret_cast<const uint32_t(&)[16]>(x[16]));
+  }
+  ptx::tmem_st_wait();
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 16) {
+    uint32_t x[N32][16];
+    uint64_t v[N32][8];
+#pragma unroll
+    for (int b = 0; b < N32; ++b) ptx::tmem_ld32x16(col + 32 * b + c, x[b]);
+#pragma unroll
+    for (int b = 0; b < N32; ++b) {
+      ptx::tmem_ld_wait(x[b]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[b][k] = ptx::f2_pack(__uint_as_float(x[b][2 * k]), __uint_as_float(x[b][2 * k + 1]));
+    }
+#pragma unroll
+    for (int h = 1; h < N32; h <<= 1)
+#pragma unroll
+      for (int b = 0; b < N32; ++b)
+        if ((b & h) == 0) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) butterfly2(v[b][k], v[b + h][k]);
+        }
+#pragma unroll
+    for (int b = 0; b < N32; ++b)
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) ptx::f2_unpack(v[b][4 * g + k], y[k], y[k + 4]);
+        put(4 * b + c / 8 + g, y);
+      }
+  }
+}
 __device__ __forceinline__ uint4 bf16x8(const float* o, float f) {
   return make_uint4(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f), pack_bf16(o[4] * f, o[5] * f),
                     pack_bf16(o[6] * f, o[7] * f));
 }
 
-// Whether every row of the block sees all tokens of the step: known from the lengths alone, so producers and softmax
-// agree on it.
+// Whether every row of the block sees all of the 32 tokens from tok0 on: known from the lengths alone.
 struct Interior {
   int c_lo, c_hi, p_first, p_last, window;
   __device__ __forceinline__ bool operator()(int tok0) const {
-    return tok0 >= c_lo && tok0 + PT <= c_hi && tok0 + PT - 1 <= p_first && (window <= 0 || tok0 > p_last - window);
+    return tok0 >= c_lo && tok0 + 32 <= c_hi && tok0 + 31 <= p_first && (window <= 0 || tok0 > p_last - window);
   }
 };
 
@@ -279,7 +340,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   using Smem = PromptSmem<HD>;
   constexpr int HB = HD / 2;
   extern __shared__ unsigned char smem_raw[];
-  Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // an offset, not an address: the compiler keeps seeing shared memory
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   ptx::griddep_launch_dependents();                      // the kernel that joins chunks waits for this one
@@ -340,24 +402,47 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     const bool live = r < w.rows;
     const int rr = min(r, w.rows - 1);
     const int head = w.kvh * group + rr % group;
+    // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
+    // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
+    // its fetch.
+    constexpr int LPR = HD / 8, RPI = 32 / LPR;
+    const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
+    auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
+    // body(row of the tile, token, query head) over the warp's rows that exist
+    auto each_row = [&](auto body) {
+      int q = w.r0 + PT * i + io_row;
+      int tok = q / group, hq = q - tok * group;
+#pragma unroll 4
+      for (int k = 0; k < LPR; ++k) {
+        if (q < w.rows) body(io_row + RPI * k, (int64_t)w.q0 + tok, w.kvh * group + hq);
+        q += RPI;
+        hq += RPI;
+        while (hq >= group) hq -= group, ++tok;
+      }
+    };
     float c_row;                                         // raw scores to log2 units, but for the keys' power of two
     {
-      const uint4* src = reinterpret_cast<const uint4*>(a.Q + (int64_t)(w.q0 + rr / group) * a.ldq + head * HD);
+      each_row([&](int to, int64_t t, int hq) {
+        ptx::cp_async16(place(to, io_chunk), reinterpret_cast<const uint4*>(a.Q + t * a.ldq + hq * HD) + io_chunk, 16);
+      });
+      ptx::cp_async_wait_all();
+      __syncwarp();
       float mq = 0.0f;
 #pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
-        const uint4 x = __ldg(src + c);
+        const uint4 x = *place(row, c);
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          mq = fmaxf(mq, fmaxf(finite_or_0(__uint_as_float(y[q] << 16)), finite_or_0(__uint_as_float(y[q] & 0xFFFF0000u))));
+          mq = ptx::max3(mq, finite_or_0(__uint_as_float(y[q] << 16)), finite_or_0(__uint_as_float(y[q] & 0xFFFF0000u)));
       }
-      const float eq = scale_exponent(mq);
-      const float f = live ? (a.scale < 0.0f ? -ex2(-eq) : ex2(-eq)) : 0.0f;
+      const float eq = scale_exponent(live ? mq : 0.0f);
+      const float f = a.scale < 0.0f ? -ex2(-eq) : ex2(-eq);
       c_row = fabsf(a.scale) * kLog2e * ex2(eq);
-#pragma unroll 4
+#pragma unroll 2
       for (int c = 0; c < HD / 8; ++c) {
-        const uint4 x = __ldg(src + c);
+        uint4 x = *place(row, c);
+        if (!live) x = make_uint4(0u, 0u, 0u, 0u);
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
         float v[8];
 #pragma unroll
@@ -366,9 +451,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           v[2 * q + 1] = __uint_as_float(y[q] & 0xFFFF0000u) * f;
         }
         // channels 0 4 | 1 5 | 2 6 | 3 7; the keys' odd channels come 16 times too large
-        *reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(row, c % 8)) =
-            make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1] * kOddNibble, v[5] * kOddNibble), pack_f16(v[2], v[6]),
-                       pack_f16(v[3] * kOddNibble, v[7] * kOddNibble));
+        *place(row, c) = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1] * kOddNibble, v[5] * kOddNibble), pack_f16(v[2], v[6]),
+                                    pack_f16(v[3] * kOddNibble, v[7] * kOddNibble));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -386,7 +470,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       if (!ok) break;
       ptx::tc_fence_after();
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
-      const bool whole = (valid.x & valid.y & valid.z & valid.w) == 0xffffffffu && S.scaled[sc] != 0;
+      const uint32_t va = t0 ? valid.z : valid.x, vb = t0 ? valid.w : valid.y;
       // Raises rows' references to cand (largest score plus the exponent of the largest value scale), in the sum and in O.
       auto raise = [&](bool grow, float cand) {
         const float m_new = grow ? cand : m;
@@ -409,9 +493,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       };
       // The maximum is not taken first: the reference of the halves before serves until a row's probabilities outgrow
       // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
-      if (whole) {
+      uint32_t pa[16], pb[16];
+      if ((va & vb) == 0xffffffffu && (S.scaled[sc][2 * (h & 1)] & S.scaled[sc][2 * (h & 1) + 1]) != 0) {
         bool over = m == -INFINITY;
-        uint32_t pa[16], pb[16];
         float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
         const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
         kp.x *= c_row, kp.y *= c_row;
@@ -435,40 +519,43 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         if (!ok) break;
         // each sum without its values' power of two
         l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
-        ptx::tmem_st32x16(s_buf, pa);
-        ptx::tmem_st32x16(s_buf + 16, pb);
       } else {
         const int pos = n - w.qlen + rr / group;
         const uint64_t bits = token_bits((j0 + j) * PT + t0, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1));
-        const uint32_t sa = (uint32_t)bits & (t0 ? valid.z : valid.x), sb = (uint32_t)(bits >> 32) & (t0 ? valid.w : valid.y);
+        const uint32_t sa = (uint32_t)bits & va, sb = (uint32_t)(bits >> 32) & vb;
         const float4* ks = reinterpret_cast<const float4*>(S.ks[sc]) + t0 / 4;
         const float4* vs = reinterpret_cast<const float4*>(S.vs[sc]) + t0 / 4;
-        float top = -INFINITY, vm = 0.0f;
-#pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t seen = g ? sb : sa;
+        float sum = 0.0f;
+        bool over = m == -INFINITY && (sa | sb) != 0u;
+        for (int pass = 0;; ++pass) {
           uint32_t x[32];
-          ptx::tmem_ld32(s_buf + 32 * g, x);
-          ptx::tmem_ld_wait(x);
-          chunk_mask(x, seen, ks + 8 * g, c_row);
-          top = fmaxf(top, chunk_max(x));
-          vm = fmaxf(vm, chunk_scale_max(seen, vs + 8 * g));
-        }
-        const float cand = top + scale_exponent(vm);
-        const bool grow = cand > m + kLazy || (m == -INFINITY && cand > m);
-        if (__any_sync(0xffffffffu, grow) && !(ok = raise(grow, cand))) break;
-        const float ref = m == -INFINITY ? 0.0f : m;
+          if (__any_sync(0xffffffffu, over)) {
+            float top = -INFINITY, vm = 0.0f;
 #pragma unroll 1
-        for (int g = 0; g < 2; ++g) {
-          const uint32_t seen = g ? sb : sa;
-          uint32_t x[32], p[16];
-          ptx::tmem_ld32(s_buf + 32 * g, x);
+            for (int g = 0; g < 2; ++g) {
+              ptx::tmem_ld32(s_buf + 32 * g, x);
+              ptx::tmem_ld_wait(x);
+              chunk_tops(x, g ? sb : sa, ks + 8 * g, vs + 8 * g, c_row, top, vm);
+            }
+            const float cand = top + scale_exponent(vm);
+            if (!(ok = raise(over && cand > m, cand))) break;
+          }
+          const float ref = m == -INFINITY ? 0.0f : m;
+          float top = 0.0f;
+          ptx::tmem_ld32(s_buf, x);
           ptx::tmem_ld_wait(x);
-          chunk_mask(x, seen, ks + 8 * g, c_row);
-          l += chunk_exp_masked(x, seen, vs + 8 * g, -ref, p);
-          ptx::tmem_st32x16(s_buf + 16 * g, p);          // over scores already read
+          sum = chunk_exp_masked(x, sa, ks, vs, c_row, -ref, pa, top);
+          ptx::tmem_ld32(s_buf + 32, x);
+          ptx::tmem_ld_wait(x);
+          sum += chunk_exp_masked(x, sb, ks + 8, vs + 8, c_row, -ref, pb, top);
+          over = top > kTop;
+          if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
+        if (!ok) break;
+        l += sum;
       }
+      ptx::tmem_st32x16(s_buf, pa);
+      ptx::tmem_st32x16(s_buf + 16, pb);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       __syncwarp();
@@ -479,83 +566,50 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       if (ok && steps > 0) ok = pr_warp_wait(&S.o_full[i][1], (uint32_t)(steps - 1) & 1u, &S.abort_flag, a.status);
       ptx::tc_fence_after();
       const bool some = ok && steps > 0;
-      const int64_t token = w.q0 + rr / group;
+      // The queries' place (their products are done) takes each row's output, HD / 8 chunks of 16 bytes; rows leave from
+      // there whole.  A warp touches its own rows only.
+      auto stage = [&](int c, uint4 x) { *place(row, c) = x; };
+      auto flush = [&](auto dst_of) {                    // dst_of(token, head): where the row goes
+        __syncwarp();
+        each_row([&](int from, int64_t t, int hq) { reinterpret_cast<uint4*>(dst_of(t, hq))[io_chunk] = *place(from, io_chunk); });
+        __syncwarp();
+      };
       if (part.chunks > 1) {
-        const int64_t at = ((int64_t)w.chunk * a.T + token) * a.heads_q + head;
-        if (live) part.ml[at] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
+        const int64_t token = w.q0 + rr / group, first = (int64_t)w.chunk * a.T;
+        if (live) part.ml[(first + token) * a.heads_q + head] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
         if (some) {
 #pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            load_channels(o, o_col + c);
-            if (live) {
-              float4* dst = reinterpret_cast<float4*>(part.o + at * HD + c);
+          for (int half = 0; half < 2; ++half) {         // HD / 2 channels in float32 fill the place
+#pragma unroll 1
+            for (int c = 0; c < HD / 2; c += 32) {
+              float o[32];
+              load_channels(o, o_col + half * (HD / 2) + c);
 #pragma unroll
-              for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 8; ++k)
+                stage(c / 4 + k, make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                                            __float_as_uint(o[4 * k + 3])));
             }
+            flush([&](int64_t t, int hq) { return part.o + ((first + t) * a.heads_q + hq) * HD + half * (HD / 2); });
           }
         }
       } else {
-        uint4* dst = reinterpret_cast<uint4*>(a.O + token * a.ldo + head * HD);
-        float f = l == 0.0f ? 0.0f : 1.0f / l;
+        const float f = l == 0.0f ? 0.0f : 1.0f / l;
         if (!some) {
-          if (live)
-            for (int c = 0; c < HD / 8; ++c) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int c = 0; c < HD / 8; ++c) stage(c, make_uint4(0u, 0u, 0u, 0u));
         } else if (!a.cache.rotate_v) {
 #pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
             float o[32];
             load_channels(o, o_col + c);
-            if (live) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) dst[c / 8 + k] = bf16x8(o + 8 * k, f);
-            }
+            for (int k = 0; k < 4; ++k) stage(c / 8 + k, bf16x8(o + 8 * k, f));
           }
-        } else {
-          // x H / sqrt(head_dim): the stages within 32 channels go back to tensor memory, those across them follow 8
-          // channels of each 32 at a time
-          f *= HD == 128 ? 0.08838834764831845f : 0.125f;
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            load_channels(o, o_col + c);
-            fwht(o);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t y[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[16 * h + k]);
-              ptx::tmem_st32x16(o_col + c + 16 * h, y);
-            }
-          }
-          ptx::tmem_st_wait();
-#pragma unroll 1
-          for (int c = 0; c < 32; c += 16) {
-            constexpr int N32 = HD / 32;
-            float o[16][N32];
-#pragma unroll
-            for (int b = 0; b < N32; ++b) {
-              uint32_t x[16];
-              ptx::tmem_ld32x16(o_col + 32 * b + c, x);
-              ptx::tmem_ld_wait(x);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k][b] = __uint_as_float(x[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) fwht(o[k]);
-            if (live) {
-#pragma unroll
-              for (int b = 0; b < N32; ++b)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  float y[8];
-#pragma unroll
-                  for (int k = 0; k < 8; ++k) y[k] = o[8 * h + k][b];
-                  dst[4 * b + c / 8 + h] = bf16x8(y, f);
-                }
-            }
-          }
+        } else {                                         // x H / sqrt(head_dim)
+          const float fr = f * (HD == 128 ? 0.08838834764831845f : 0.125f);
+          rotate_row<HD>(o_col, [&](int c, const float* y) { stage(c, bf16x8(y, fr)); });
         }
+        flush([&](int64_t t, int hq) { return a.O + t * a.ldo + (int64_t)hq * HD; });
       }
       ptx::tc_fence_before();
     }
@@ -570,7 +624,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     auto locate = [&](int j) {
       const int tok = (j0 + j) * PT + t;
       at_next = -1;
-      if (tok < n && j < steps) {
+      if (tok >= c_lo && tok < c_hi && j < steps) {
         const int page = table[tok >> ps];
         if (page < 0 || page >= a.cache.pages) atomicOr(a.status, PQ_DEV_BAD_INDEX);
         else at_next = (((int64_t)page * a.cache.heads + w.kvh) << ps) + (tok & ((1 << ps) - 1));
@@ -591,19 +645,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const int s = j % PR_STAGES, sc = j % SC_RING;
       const uint32_t reuse = ((uint32_t)(j / PR_STAGES) & 1u) ^ 1u;
       if (!pr_warp_wait(&S.k_empty[s], reuse, &S.abort_flag, a.status, 0)) break;
-      const bool scaled = interior((j0 + j) * PT);
       const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
-      float km = finite_or_0(ks), vm = finite_or_0(vs);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
-        vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-      }
+      const float km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(ks))));
+      const float vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(vs))));
+      const bool scaled = interior((j0 + j) * PT + 32 * wq);
       const float ke = scale_exponent(km), ve = scale_exponent(vm);
       S.ks[sc][t] = scaled ? ex2(ke) : ks;
       S.vs[sc][t] = scaled ? ex2(ve) : vs;
       if (lane == 0) {
-        if (wq == 0) S.scaled[sc] = scaled ? 1 : 0;
+        S.scaled[sc][wq] = scaled ? 1 : 0;
         S.valid[sc][wq] = bits;
         S.k_pow[sc][wq] = ex2(ke);
         S.v_exp[sc][wq] = ve;
