@@ -408,16 +408,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     constexpr int LPR = HD / 8, RPI = 32 / LPR;
     const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
     auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
-    // body(row of the tile, token, query head) over the warp's rows that exist
+    // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
+    // group is a multiplication by its reciprocal (rows + group below 2^16).
+    const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
+    const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
     auto each_row = [&](auto body) {
-      int q = w.r0 + PT * i + io_row;
-      int tok = q / group, hq = q - tok * group;
 #pragma unroll 4
       for (int k = 0; k < LPR; ++k) {
-        if (q < w.rows) body(io_row + RPI * k, (int64_t)w.q0 + tok, w.kvh * group + hq);
-        q += RPI;
-        hq += RPI;
-        while (hq >= group) hq -= group, ++tok;
+        const int to = io_row + RPI * k, x = to + tile_off;
+        const int t = group == 1 ? x : (int)__umulhi((uint32_t)x, inv_group);
+        if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
       }
     };
     float c_row;                                         // raw scores to log2 units, but for the keys' power of two
@@ -427,32 +427,34 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       });
       ptx::cp_async_wait_all();
       __syncwarp();
-      float mq = 0.0f;
+      // largest magnitude, two channels an instruction; infinities and NaN do not count (the rare second pass)
+      uint32_t mw = 0u;
 #pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
         const uint4 x = *place(row, c);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mq = ptx::max3(mq, finite_or_0(__uint_as_float(y[q] << 16)), finite_or_0(__uint_as_float(y[q] & 0xFFFF0000u)));
+        mw = __vimax3_u16x2(mw, x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
+        mw = __vimax3_u16x2(mw, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
+      }
+      float mq = __uint_as_float(max(mw << 16, mw & 0xFFFF0000u));
+      if (!(mq < INFINITY)) {
+        mq = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < HD; ++c)
+          mq = fmaxf(mq, finite_or_0(__uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(place(row, c / 8))[c % 8] << 16)));
       }
       const float eq = scale_exponent(live ? mq : 0.0f);
-      const float f = a.scale < 0.0f ? -ex2(-eq) : ex2(-eq);
+      const float f = a.scale < 0.0f ? -ex2(-eq) : ex2(-eq), f16 = f * kOddNibble;
       c_row = fabsf(a.scale) * kLog2e * ex2(eq);
-#pragma unroll 2
+      // channels 0 4 | 1 5 | 2 6 | 3 7; the keys' odd channels come 16 times too large
+#pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
         uint4 x = *place(row, c);
         if (!live) x = make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-        float v[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          v[2 * q] = __uint_as_float(y[q] << 16) * f;
-          v[2 * q + 1] = __uint_as_float(y[q] & 0xFFFF0000u) * f;
-        }
-        // channels 0 4 | 1 5 | 2 6 | 3 7; the keys' odd channels come 16 times too large
-        *place(row, c) = make_uint4(pack_f16(v[0], v[4]), pack_f16(v[1] * kOddNibble, v[5] * kOddNibble), pack_f16(v[2], v[6]),
-                                    pack_f16(v[3] * kOddNibble, v[7] * kOddNibble));
+        auto even = [&](uint32_t lo, uint32_t hi) { return pack_f16(__uint_as_float(lo << 16) * f, __uint_as_float(hi << 16) * f); };
+        auto odd = [&](uint32_t lo, uint32_t hi) {
+          return pack_f16(__uint_as_float(lo & 0xFFFF0000u) * f16, __uint_as_float(hi & 0xFFFF0000u) * f16);
+        };
+        *place(row, c) = make_uint4(even(x.x, x.z), odd(x.x, x.z), even(x.y, x.w), odd(x.y, x.w));
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
