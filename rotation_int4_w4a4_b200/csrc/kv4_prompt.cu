@@ -95,8 +95,11 @@ __device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abo
 }
 __device__ __forceinline__ bool pr_warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status,
                                              int spins = kSpin) {
+  // the whole warp polls: an elected lane's answer would have to travel to the others first
+  for (int k = 0; k <= spins; ++k)
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
   int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = pr_wait(bar, parity, abort_flag, status, spins) ? 1 : 0;
+  if ((threadIdx.x & 31) == 0) ok = pr_wait(bar, parity, abort_flag, status, 0) ? 1 : 0;
   ok = __shfl_sync(0xffffffffu, ok, 0);
   __syncwarp();
   return ok != 0;
