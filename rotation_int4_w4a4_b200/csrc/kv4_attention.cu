@@ -45,13 +45,10 @@ constexpr int AT_TILES = AT_BLOCK / 16;
 // Query rows a key/value head and sequence from which on the tensor-core kernel of kv4_prompt.cu takes the call.
 constexpr int64_t kPromptRows = 64;
 constexpr float kRowsTop = 16384.0f;    // a product of probability and value scale from which the reference is raised (fp16: 65504)
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
-                                         const uint32_t a3, const uint32_t b0, const uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// A nibble alone in the low bits of an fp16 is n 2^-24, below the normal range (matrix instructions take those at full
+// value); four places up it is 16 times that.
+constexpr float kCodeUnit = 5.9604644775390625e-8f;      // 2^-24
+constexpr float kQueryExp = 15.0f;      // a row's queries enter below 2^15: exact down to 2^-25 of the row's largest
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                         const uint32_t a3, const uint32_t b0, const uint32_t b1) {
@@ -125,7 +122,10 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 
     // ---- query operands: B fragment of step (w, h): channels (d, d + 4), (d + 1, d + 5), d = 8 (KW t + w) + 2 h
     uint32_t qb[NT][KS][2];
-    float bq[NT][2];                     // -136 * sum of the query, for this thread's two columns
+    // For this thread's two columns: -8 * sum of the query (the codes' offset), and raw scores to log2 units, but for the
+    // keys' scales.
+    float bq[NT][2];
+    uint64_t cq[NT];
     int pos[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -139,25 +139,40 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
         for (int w = 0; w < KW; ++w) x[w][0] = x[w][1] = x[w][2] = x[w][3] = 0u;
       }
-      float sum = 0.0f;
+      float sum = 0.0f, mq = 0.0f;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          qb[nt][2 * w + h][0] = __byte_perm(x[w][h], x[w][h + 2], 0x5410);   // channels 2h, 2h + 4
-          qb[nt][2 * w + h][1] = __byte_perm(x[w][h], x[w][h + 2], 0x7632);   // channels 2h + 1, 2h + 5
-        }
+      for (int w = 0; w < KW; ++w)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          sum += __uint_as_float(x[w][k] << 16) + __uint_as_float(x[w][k] & 0xFFFF0000u);
+          mq = ptx::max3(mq, finite_or_0(__uint_as_float(x[w][k] << 16)), finite_or_0(__uint_as_float(x[w][k] & 0xFFFF0000u)));
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 1));
+      mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, 2));
+      const float eq = scale_exponent(mq), f = ex2(kQueryExp - eq);
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = __uint_as_float(x[w][k] << 16) * f;
+          v[2 * k + 1] = __uint_as_float(x[w][k] & 0xFFFF0000u) * f;
+          sum += v[2 * k] + v[2 * k + 1];
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          qb[nt][2 * w + h][0] = pack_f16(v[2 * h], v[2 * h + 4]);
+          qb[nt][2 * w + h][1] = pack_f16(v[2 * h + 1] * kOddNibble, v[2 * h + 5] * kOddNibble);
+        }
       }
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      float c2[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        bq[nt][e] = -136.0f * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        bq[nt][e] = -8.0f * kCodeUnit * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
+        c2[e] = c_log2 * ex2(__shfl_sync(0xffffffffu, eq, 4 * (2 * t + e)) + (24.0f - kQueryExp));
         pos[nt][e] = n - qlen + min(rows - 1, r0 + 8 * nt + 2 * t + e) / group;
       }
+      cq[nt] = ptx::f2_pack(c2[0], c2[1]);
     }
 
     float o[NT][KS][4];
@@ -272,20 +287,20 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         for (int w = 0; w < KW; ++w)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t a0 = biased_pair(kx[i][0][w], 8 * h), a2 = biased_pair(kx[i][0][w], 8 * h + 4);
-            const uint32_t a1 = biased_pair(kx[i][1][w], 8 * h), a3 = biased_pair(kx[i][1][w], 8 * h + 4);
+            const uint32_t x0 = kx[i][0][w] >> (8 * h), x1 = kx[i][1][w] >> (8 * h);
+            const uint32_t a0 = and_xor(x0, 0x000F000Fu, 0x00080008u), a2 = and_xor(x0, 0x00F000F0u, 0x00800080u);
+            const uint32_t a1 = and_xor(x1, 0x000F000Fu, 0x00080008u), a3 = and_xor(x1, 0x00F000F0u, 0x00800080u);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_bf16(s[i][nt], a0, a1, a2, a3, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
+              mma_f16(s[i][nt], a0, a1, a2, a3, qb[nt][2 * w + h][0], qb[nt][2 * w + h][1]);
           }
-        const float f0 = ks[i][0] * c_log2, f1 = ks[i][1] * c_log2;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[i][nt][0] *= f0;
-          s[i][nt][1] *= f0;
-          s[i][nt][2] *= f1;
-          s[i][nt][3] *= f1;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(s[i][nt][2 * h], s[i][nt][2 * h + 1]),
+                                       ptx::f2_mul(ptx::f2_pack(ks[i][h], ks[i][h]), cq[nt])),
+                           s[i][nt][2 * h], s[i][nt][2 * h + 1]);
       }
       if (!whole) {
 #pragma unroll

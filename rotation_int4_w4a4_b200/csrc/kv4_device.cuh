@@ -26,10 +26,6 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t 
   return y;
 }
 
-// Two nibbles at bits 0..3 and 16..19 of x >> s -> two bf16 values 136 + code: nibble ^ 8 is code + 8, under 0x4300
-// (128, whose last mantissa bit counts 1).
-__device__ __forceinline__ uint32_t biased_pair(uint32_t x, int s) { return and_xor(x >> s, 0x000F000Fu, 0x43084308u); }
-
 __device__ __forceinline__ uint32_t hsub2_bits(uint32_t a, uint32_t b) {
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -70,12 +66,12 @@ __device__ __forceinline__ float finite_or_0(float x) {
   return y < 3.0e38f ? y : 0.0f;
 }
 
-// An exponent e with x < 2^e (x >= 0), within -100..100; 0 for x = 0.  Scores taken relative to (largest score + e)
+// An exponent e with x < 2^e (x >= 0), within -100..126; 0 for x = 0.  Scores taken relative to (largest score + e)
 // make probability times value scale at most 1, which fp16 holds; output and sum carry the same factor, so it
 // leaves with their quotient.
 __device__ __forceinline__ float scale_exponent(float x) {
   const int e = (int)(__float_as_uint(x) >> 23) - 126;
-  return x == 0.0f ? 0.0f : (float)max(-100, min(100, e));
+  return x == 0.0f ? 0.0f : (float)max(-100, min(126, e));
 }
 
 // One query row's output from its un-normalised float32 sums: lane l of the warp holds channels E l .. E l + E - 1
