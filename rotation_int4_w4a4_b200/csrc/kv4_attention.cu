@@ -29,6 +29,7 @@
 // tokens, one block each; a second kernel joins the chunks' float32 partial results.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "internal.h"
 #include "kv4.h"
@@ -77,8 +78,42 @@ __device__ __forceinline__ void load_words(uint32_t (&x)[W], const uint8_t* p) {
   }
 }
 
+// Work cut into equal shares.  An item is one row tile of one sequence and key/value head; its length is the steps of 128
+// tokens (a block's four warps, 32 each) of its sequence.  Items lie end to end (sequence, head, row tile) and each block
+// takes the same number of steps of that line, so lengths that differ cost nothing.  A block whose share ends inside an
+// item leaves a partial result: slot 2 c + 1 of block c for an item that begins there, 2 c for one that began before.
+struct Shares {
+  float* o;       // [2 blocks][R][HD], un-normalised
+  float2* ml;     // [2 blocks][R]: reference exponent and sum
+  int4* begun;    // [blocks]: sequence, head, row tile and last block of the item in slot 2 c + 1 (sequence -1: none)
+  int blocks;     // 0: an item a block, no shares
+};
+constexpr int AT_STEP = AT_BLOCK * AT_WARPS;
+constexpr int AT_SEQS = 1024;           // sequences whose lengths a block can add up
+constexpr int AT_MIN_STEPS = 2;         // a share's least length
+constexpr int AT_LEAD = 3;              // steps that an item's beginning and end cost, ahead of its own on the line
+
+struct Span {
+  int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first cached token that any row sees
+  int steps;
+};
+__device__ __forceinline__ Span span_of(const Kv4AttnArgs& a, int b, bool report) {
+  Span s;
+  s.q0 = max(0, a.q_start[b]);
+  s.qlen = min((int)a.T, a.q_start[b + 1]) - s.q0;
+  s.n = max(0, a.seq_lens[b]);
+  const int64_t cap = (int64_t)a.table_width << a.cache.page_shift;
+  if (s.n > cap) {
+    s.n = (int)cap;
+    if (report) atomicOr(a.status, PQ_DEV_BAD_INDEX);
+  }
+  s.lo = a.window > 0 ? max(0, s.n - s.qlen - a.window + 1) : 0;
+  s.steps = max(1, (s.n + AT_STEP - 1) / AT_STEP - s.lo / AT_STEP);
+  return s;
+}
+
 template <int HD, int NT>
-__global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Partials part,
+__global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Shares shares,
                                                                 int row_tiles) {
   constexpr int R = 8 * NT;              // query rows per tile
   constexpr int KS = HD / 16;            // channel steps of the first product = channel tiles of the second
@@ -91,34 +126,101 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
   ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int b = blockIdx.z, kvh = blockIdx.y;
-  const int chunk = blockIdx.x % part.chunks;
   const int group = a.heads_q / a.cache.heads;
-  const int q0 = max(0, a.q_start[b]);
-  const int qlen = min((int)a.T, a.q_start[b + 1]) - q0;
   const int ps = a.cache.page_shift;
-  const int rows = qlen * group;
-  if (rows <= 0) return;
-  int n = max(0, a.seq_lens[b]);
-  {
-    const int64_t cap = (int64_t)a.table_width << ps;
-    if (n > cap) {
-      n = (int)cap;
-      if (threadIdx.x == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
-    }
-  }
-  const int32_t* table = a.table + b * a.table_stride;
   const float c_log2 = a.scale * kLog2e;
+  // Shares: where each sequence's items begin on the line, and this block's part of it.
+  __shared__ int64_t sm_first[AT_SEQS + 1];
+  __shared__ int64_t sm_sum[AT_WARPS];
+  __shared__ int64_t sm_share;
+  // What a block remembers of an item while it walks the tokens; two, since a warp may be done with one before the others.
+  struct Item { int64_t next; int b, kvh, rt, step0, step1, steps, q0, rows; };
+  __shared__ Item sm_item[2];
+  if (shares.blocks) {
+    const int per = (a.B + 32 * AT_WARPS - 1) / (32 * AT_WARPS), b0 = threadIdx.x * per;
+    auto length = [&](int b) {
+      if (b >= a.B) return (int64_t)0;
+      const Span s = span_of(a, b, false);
+      return s.qlen <= 0 ? (int64_t)0 : (int64_t)(AT_LEAD + s.steps) * a.cache.heads * (((int64_t)s.qlen * group + R - 1) / R);
+    };
+    int64_t mine = 0;
+    for (int k = 0; k < per; ++k) mine += length(b0 + k);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sm_sum[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < AT_WARPS; ++w) {
+      if (w < warp) upto += sm_sum[w];
+      total += sm_sum[w];
+    }
+    int64_t at = upto - mine;
+    for (int k = 0; k < per; ++k)
+      if (b0 + k < a.B) {
+        sm_first[b0 + k] = at;
+        if (per > 1) at += length(b0 + k);
+      }
+    if (threadIdx.x == 0) {
+      sm_first[a.B] = total;
+      shares.begun[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      sm_share = max((int64_t)AT_MIN_STEPS, (total + shares.blocks - 1) / shares.blocks);
+      sm_item[1].next = sm_share * blockIdx.x;
+    }
+    __syncthreads();
+  }
 
-  for (int rt = blockIdx.x / part.chunks; rt * R < rows; rt += row_tiles) {
+  for (int done = 0;; ++done) {
+    // ---- the next item, or the share's part of one
+    int b, kvh, rt, step0, step1;
+    int64_t line = 0, end = 0;
+    if (shares.blocks) {
+      line = sm_item[(done & 1) ^ 1].next;
+      end = min(sm_share * (blockIdx.x + 1), sm_first[a.B]);
+      if (line >= end) break;
+      int l = 0, h = a.B - 1;                            // the last sequence that begins at or before line
+      while (l < h) {
+        const int mid = (l + h + 1) / 2;
+        if (sm_first[mid] <= line) l = mid; else h = mid - 1;
+      }
+      b = l;
+    } else {
+      b = blockIdx.z;
+    }
+    const Span sp = span_of(a, b, threadIdx.x == 0);
+    const int qlen = sp.qlen, n = sp.n, rows = qlen * group;
+    if (shares.blocks) {
+      const int tiles = (rows + R - 1) / R, length = AT_LEAD + sp.steps;
+      const int64_t off = line - sm_first[b];
+      const int item = (int)(off / length);
+      kvh = item / tiles;
+      rt = item % tiles;
+      const int from = (int)(off - (int64_t)item * length), to = (int)min((int64_t)length, from + (end - line));
+      line += to - from;
+      step0 = max(0, from - AT_LEAD);
+      step1 = to - AT_LEAD;
+      if (step1 <= 0) break;                             // the share ends in the lead: the next block begins the item
+    } else {
+      kvh = blockIdx.y;
+      rt = blockIdx.x + done * row_tiles;
+      if ((int64_t)rt * R >= rows) break;
+      step0 = 0;
+      step1 = sp.steps;
+    }
+    if (threadIdx.x == 0) sm_item[done & 1] = Item{line, b, kvh, rt, step0, step1, sp.steps, sp.q0, rows};
+    const int32_t* table = a.table + b * a.table_stride;
     const int r0 = rt * R;
     // positions of the tile's first and last row, and the tokens the tile sees
     const int p_first = n - qlen + r0 / group, p_last = n - qlen + min(rows - 1, r0 + R - 1) / group;
     const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
     const int hi = min(n, p_last + 1);
-    // this chunk's part of [lo, hi); chunk borders are fixed multiples of chunk_len
-    const int c_lo = part.chunks > 1 ? max(lo, chunk * part.chunk_len) : lo;
-    const int c_hi = part.chunks > 1 && chunk < part.chunks - 1 ? min(hi, (chunk + 1) * part.chunk_len) : hi;
+    const int t_first = sp.lo / AT_STEP * AT_STEP;
+    const int c_lo = max(lo, t_first + step0 * AT_STEP);
+    const int c_hi = step1 == sp.steps ? hi : min(hi, t_first + step1 * AT_STEP);
 
     // ---- query operands: B fragment of step (w, h): channels (d, d + 4), (d + 1, d + 5), d = 8 (KW t + w) + 2 h
     uint32_t qb[NT][KS][2];
@@ -132,7 +234,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
       const int r = r0 + 8 * nt + g;
       uint32_t x[KW][4];
       if (r < rows) {
-        const uint16_t* src = a.Q + (int64_t)(q0 + r / group) * a.ldq + (kvh * group + r % group) * HD + 8 * KW * t;
+        const uint16_t* src = a.Q + (int64_t)(sp.q0 + r / group) * a.ldq + (kvh * group + r % group) * HD + 8 * KW * t;
 #pragma unroll
         for (int w = 0; w < KW; ++w) load_words<4>(x[w], reinterpret_cast<const uint8_t*>(src + 8 * w));
       } else {
@@ -476,7 +578,9 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         }
       }
     __syncthreads();
-    for (int r = warp; r < R && r0 + r < rows; r += AT_WARPS) {
+    const Item& it = sm_item[done & 1];
+    const bool entire = it.step0 == 0 && it.step1 == it.steps;
+    for (int r = warp; r < R && it.rt * R + r < it.rows; r += AT_WARPS) {
       constexpr int E = HD / 32;
       float mx = -INFINITY;
 #pragma unroll
@@ -492,84 +596,173 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
         for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w][r][E * lane + i], f, y[i]);
       }
-      const int64_t token = q0 + (r0 + r) / group;
-      const int head = kvh * group + (r0 + r) % group;
-      if (part.chunks == 1) {
+      const int at = it.rt * R + r;
+      const int64_t token = it.q0 + at / group;
+      const int head = it.kvh * group + at % group;
+      if (entire) {
         finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + head * HD, lane);
       } else {
-        const int64_t row = ((int64_t)chunk * a.T + token) * a.heads_q + head;
-        if (lane == 0) part.ml[row] = make_float2(mx, sum);
+        const int64_t row = (int64_t)(2 * blockIdx.x + (it.step0 == 0)) * R + r;
+        if (lane == 0) shares.ml[row] = make_float2(mx, sum);
         if (mx != -INFINITY || sum != 0.0f) {
 #pragma unroll
-          for (int i = 0; i < E; ++i) part.o[row * HD + E * lane + i] = y[i];
+          for (int i = 0; i < E; ++i) shares.o[row * HD + E * lane + i] = y[i];
         }
       }
     }
+    if (threadIdx.x == 0 && it.step0 == 0 && !entire)
+      shares.begun[blockIdx.x] = make_int4(it.b, it.kvh, it.rt, (int)((it.next + (it.steps - it.step1) - 1) / sm_share));
   }
 }
 
-// Joins the chunks of each query row, a block a row: its warps take every fourth chunk each.  Rows of tokens outside
-// every sequence stay as they were.  Launched as the programmatic dependent of the kernel that writes the chunks.
-constexpr int JN_WARPS = 4;
-template <int HD>
-__global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_kernel(const Kv4AttnArgs a, const Partials part) {
+// Joins a query row's partial results: a warp does (parts = 1), or a block, whose warps take every eighth piece each and
+// the first joins theirs.  at(k): piece k's row in ml_of and o_of.
+constexpr int JN_WARPS = 8;
+template <int HD, int parts, typename At>
+__device__ __forceinline__ void join_row(const float2* ml_of, const float* o_of, int pieces, At at, int rotate, uint16_t* dst) {
+  __shared__ float sm_o[JN_WARPS * HD];
+  __shared__ float2 sm_ml[JN_WARPS];
+  const int part = parts == 1 ? 0 : threadIdx.x >> 5;
   constexpr int E = HD / 32;
-  __shared__ float sm_o[JN_WARPS][HD];
-  __shared__ float sm_m[JN_WARPS], sm_l[JN_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x, total = a.T * a.heads_q;
-  const int64_t token = row / a.heads_q;
-  ptx::griddep_wait();
-  if (token < a.q_start[0] || token >= a.q_start[a.B]) return;   // the whole block
+  const int lane = threadIdx.x & 31;
   float mx = -INFINITY;
-  for (int c = warp + JN_WARPS * lane; c < part.chunks; c += 32 * JN_WARPS) mx = fmaxf(mx, part.ml[c * total + row].x);
+  for (int c = part + parts * lane; c < pieces; c += 32 * parts) mx = fmaxf(mx, ml_of[at(c)].x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   const float mu = mx == -INFINITY ? 0.0f : mx;
   float sum = 0.0f, y[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) y[i] = 0.0f;
-#pragma unroll 4
-  for (int c = warp; c < part.chunks; c += JN_WARPS) {
-    const float2 ml = part.ml[c * total + row];
-    const bool some = ml.x != -INFINITY || ml.y != 0.0f;     // otherwise nothing seen and no output written
-    const float f = some ? ex2(ml.x - mu) : 0.0f;
-    sum = fmaf(ml.y, f, sum);
-    float x[E];
+  for (int c0 = part; c0 < pieces; c0 += 32 * parts) {   // 32 pieces a turn: a lane takes each one's factor
+    const int mine = c0 + parts * lane;
+    float f = -1.0f;                                     // nothing seen and no output written: not to be read
+    if (mine < pieces) {
+      const float2 ml = ml_of[at(mine)];
+      if (ml.x != -INFINITY || ml.y != 0.0f) {
+        f = ex2(ml.x - mu);
+        sum = fmaf(ml.y, f, sum);
+      }
+    }
+    const int turn = min(32, (pieces - c0 + parts - 1) / parts);
+#pragma unroll 8
+    for (int k = 0; k < turn; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      float x[E];
 #pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = some ? part.o[(c * total + row) * HD + E * lane + i] : 0.0f;
+      for (int i = 0; i < E; ++i) x[i] = o_of[at(c0 + parts * k) * HD + E * lane + i];
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = fmaf(x[i], f, y[i]);
+      for (int i = 0; i < E; ++i) y[i] = fk != -1.0f ? fmaf(x[i], fk, y[i]) : y[i];
+    }
   }
 #pragma unroll
-  for (int i = 0; i < E; ++i) sm_o[warp][E * lane + i] = y[i];
-  if (lane == 0) {
-    sm_m[warp] = mx;
-    sm_l[warp] = sum;
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if constexpr (parts == 1) {
+    finish_row<HD>(y, sum, rotate, dst, lane);
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < E; ++i) sm_o[part * HD + E * lane + i] = y[i];
+  if (lane == 0) sm_ml[part] = make_float2(mx, sum);
   __syncthreads();
-  if (warp != 0) return;
+  if (part == 0) {
 #pragma unroll
-  for (int w = 1; w < JN_WARPS; ++w) mx = fmaxf(mx, sm_m[w]);
-  const float all = mx == -INFINITY ? 0.0f : mx;
-  sum = 0.0f;
+    for (int w = 1; w < parts; ++w) mx = fmaxf(mx, sm_ml[w].x);
+    const float all = mx == -INFINITY ? 0.0f : mx;
+    sum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) y[i] = 0.0f;
+    for (int i = 0; i < E; ++i) y[i] = 0.0f;
 #pragma unroll
-  for (int w = 0; w < JN_WARPS; ++w) {
-    const float f = sm_m[w] == -INFINITY ? (sm_l[w] == 0.0f ? 0.0f : 1.0f) : ex2(sm_m[w] - all);
-    sum = fmaf(sm_l[w], f, sum);
+    for (int w = 0; w < parts; ++w) {
+      const float2 ml = sm_ml[w];
+      const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - all);
+      sum = fmaf(ml.y, f, sum);
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w][E * lane + i], f, y[i]);
+      for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w * HD + E * lane + i], f, y[i]);
+    }
+    finish_row<HD>(y, sum, rotate, dst, lane);
   }
-  finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + (row - token * a.heads_q) * HD, lane);
+}
+
+// The chunks of the prompt kernel, a warp or a block a row.  Rows of tokens outside every sequence stay as they were.  Both
+// joining kernels are launched as programmatic dependents of the kernel that writes the pieces.
+template <int HD>
+__global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_kernel(const Kv4AttnArgs a, const Partials part, int warp_a_row) {
+  const int64_t total = a.T * a.heads_q;
+  const int64_t row = warp_a_row ? (int64_t)blockIdx.x * JN_WARPS + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t token = row / a.heads_q;
+  ptx::griddep_wait();
+  if (token < a.q_start[0] || token >= min((int64_t)a.q_start[a.B], a.T)) return;   // the whole block, or warp
+  auto at = [&](int k) { return k * total + row; };
+  uint16_t* dst = a.O + token * a.ldo + (row - token * a.heads_q) * HD;
+  if (warp_a_row) join_row<HD, 1>(part.ml, part.o, part.chunks, at, a.cache.rotate_v, dst);
+  else join_row<HD, JN_WARPS>(part.ml, part.o, part.chunks, at, a.cache.rotate_v, dst);
+}
+
+// The shares: blocks (x, y) look at `per` blocks' slots from x per on, for items that begin in one and go on in the next
+// ones.  Few items have many pieces: a block a row (y, y + gridDim.y ..); many have few: a warp a row.
+template <int HD, int R>
+__global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_shares_kernel(const Kv4AttnArgs a, const Shares shares, int per,
+                                                                        int warp_a_row) {
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, group = a.heads_q / a.cache.heads;
+  const int first = blockIdx.x * per, last = min(first + per, shares.blocks);
+  for (int c0 = first; c0 < last; c0 += 32) {
+    const int mine = c0 + lane;
+    uint32_t begun = __ballot_sync(0xffffffffu, mine < last && shares.begun[min(mine, last - 1)].x >= 0);
+    for (; begun; begun &= begun - 1) {
+      const int c = c0 + __ffs(begun) - 1;
+      const int4 item = shares.begun[c];                 // sequence, head, row tile, last block
+      const Span sp = span_of(a, item.x, false);
+      const int rows = min(R, sp.qlen * group - item.z * R), pieces = item.w - c + 1;
+      auto join = [&](int r, auto parts) {
+        const int at = item.z * R + r;
+        const int64_t token = sp.q0 + at / group;
+        const int head = item.y * group + at % group;
+        join_row<HD, decltype(parts)::value>(shares.ml, shares.o, pieces,
+                                             [&](int k) { return (int64_t)(2 * (c + k) + (k == 0)) * R + r; },
+                                             a.cache.rotate_v, a.O + token * a.ldo + head * HD);
+      };
+      if (warp_a_row) {
+        for (int r = blockIdx.y * JN_WARPS + (threadIdx.x >> 5); r < rows; r += gridDim.y * JN_WARPS)
+          join(r, std::integral_constant<int, 1>());
+      } else {
+        for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+          join(r, std::integral_constant<int, JN_WARPS>());
+          __syncthreads();
+        }
+      }
+    }
+  }
+}
+
+cudaError_t launch_join(const void* kernel, dim3 grid, void** args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(32 * JN_WARPS, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
 template <int HD, int NT>
-cudaError_t launch_rows(const Kv4AttnArgs& a, const Partials& part, int row_tiles, cudaStream_t stream) {
-  const dim3 grid((unsigned)(part.chunks * row_tiles), (unsigned)a.cache.heads, (unsigned)a.B);
-  kv4_rows_kernel<HD, NT><<<grid, 32 * AT_WARPS, 0, stream>>>(a, part, row_tiles);
-  return cudaGetLastError();
+cudaError_t launch_rows(const Kv4AttnArgs& a, const Shares& shares, int row_tiles, int64_t max_rows, cudaStream_t stream) {
+  const dim3 grid = shares.blocks ? dim3((unsigned)shares.blocks)
+                                  : dim3((unsigned)row_tiles, (unsigned)a.cache.heads, (unsigned)a.B);
+  kv4_rows_kernel<HD, NT><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !shares.blocks) return e;
+  // Joining blocks: a few for each item, if those are fewer than shares.
+  const int64_t items = std::max<int64_t>(1, std::min<int64_t>(4 * (int64_t)a.B * a.cache.heads * row_tiles, shares.blocks));
+  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(max_rows, 8 * NT));
+  int per = (int)((shares.blocks + items - 1) / items), warp_a_row = items == shares.blocks;
+  void* args[] = {const_cast<Kv4AttnArgs*>(&a), const_cast<Shares*>(&shares), &per, &warp_a_row};
+  return launch_join(reinterpret_cast<const void*>(kv4_join_shares_kernel<HD, 8 * NT>),
+                     dim3((unsigned)((shares.blocks + per - 1) / per), (unsigned)(warp_a_row ? (rows + JN_WARPS - 1) / JN_WARPS : rows)),
+                     args, stream);
 }
 
 }  // namespace
@@ -580,69 +773,60 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   const int sms = device_sm_count();
   const bool prompt = max_rows > kPromptRows;
   const int nt = max_rows > 8 ? 2 : 1;
-  const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
-  int64_t units, want, unit_len;
-  if (prompt) {
-    // One block an SM: chunks only where the tiles leave SMs idle, at least four steps of 128 tokens each.
-    units = kv4_prompt_tiles(a) * a.cache.heads;
-    want = sms / std::max<int64_t>(units, 1);
-    unit_len = 512;
-  } else {
-    // Three blocks an SM run at once.  Few sequences: as many chunks as make one full round of blocks (one token over
-    // 65536: 33 us, 42 with three rounds); from 8 sequences on two, since their lengths differ and short chunks even that
-    // out (16 of up to 4096: 26 us against 30); many: about three (64 of up to 8192: 92 us, 110 with one chunk each).
-    units = (int64_t)a.B * a.cache.heads * row_tiles;
-    const int64_t slots = 3 * (int64_t)sms;
-    want = units * 2 > slots ? (8 * (int64_t)sms + units - 1) / units : (a.B < 8 ? slots : 2 * slots) / units;
-    // Up to 640 tokens one block is enough: a second kernel and its workspace cost the host more than the chunks save (517
-    // tokens: 8.2 us on the device against 7.5, 10 us a call against 14).
-    unit_len = max_len <= 640 ? 640 : 256;
-  }
-  const int64_t most = (max_len + unit_len - 1) / unit_len;
-  Partials part = {};
-  part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, most), 256));
-  if (a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;    // the joining kernel takes a block a row
-  part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);
+  const bool wide = a.cache.head_dim == 128;
+  // Float32 workspace for partial results: [rows][head_dim] outputs, [rows] references and sums, then `extra` bytes.
   void* ws = nullptr;
-  cudaError_t e;
-  if (part.chunks > 1) {
-    const size_t rows = (size_t)part.chunks * a.T * a.heads_q;
-    const size_t bytes = rows * (a.cache.head_dim * sizeof(float) + sizeof(float2));
+  auto workspace = [&](size_t rows, size_t extra, float** o, float2** ml) {
+    const size_t bytes = rows * (a.cache.head_dim * sizeof(float) + sizeof(float2)) + extra;
     cudaMemPool_t pool = nullptr;
-    e = scratch_pool(&pool);
+    cudaError_t e = scratch_pool(&pool);
     if (e != cudaSuccess) return cuda_fail(e, "scratch memory pool");
     e = cudaMallocFromPoolAsync(&ws, bytes, pool, stream);
     if (e != cudaSuccess) {
       set_error("cudaMallocFromPoolAsync(%zu bytes of attention workspace): %s", bytes, cudaGetErrorString(e));
       return PQ_ERR_ALLOC;
     }
-    part.o = static_cast<float*>(ws);
-    part.ml = reinterpret_cast<float2*>(part.o + rows * a.cache.head_dim);
-  }
-  const bool wide = a.cache.head_dim == 128;
-  pq_status st;
+    *o = static_cast<float*>(ws);
+    *ml = reinterpret_cast<float2*>(*o + rows * a.cache.head_dim);
+    return PQ_OK;
+  };
+  pq_status st = PQ_OK;
   if (prompt) {
-    st = launch_kv4_prompt(a, part, stream);
+    // One block an SM: chunks only where the tiles leave SMs idle, at least four steps of 128 tokens each.
+    const int64_t want = sms / std::max<int64_t>(kv4_prompt_tiles(a) * a.cache.heads, 1);
+    Partials part = {};
+    part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, (max_len + 511) / 512), 256));
+    if (a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;  // the joining kernel takes a block a row
+    part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);
+    if (part.chunks > 1) st = workspace((size_t)part.chunks * a.T * a.heads_q, 0, &part.o, &part.ml);
+    if (st == PQ_OK) st = launch_kv4_prompt(a, part, stream);
+    if (st == PQ_OK && part.chunks > 1) {
+      int warp_a_row = part.chunks < 2 * JN_WARPS;
+      const int64_t rows = a.T * a.heads_q;
+      void* args[] = {const_cast<Kv4AttnArgs*>(&a), &part, &warp_a_row};
+      st = cuda_fail(launch_join(wide ? reinterpret_cast<const void*>(kv4_join_kernel<128>) : reinterpret_cast<const void*>(kv4_join_kernel<64>),
+                                 dim3((unsigned)(warp_a_row ? (rows + JN_WARPS - 1) / JN_WARPS : rows)), args, stream),
+                     "kv4_join_kernel launch");
+    }
   } else {
-    e = wide ? (nt == 1 ? launch_rows<128, 1>(a, part, row_tiles, stream) : launch_rows<128, 2>(a, part, row_tiles, stream))
-             : (nt == 1 ? launch_rows<64, 1>(a, part, row_tiles, stream) : launch_rows<64, 2>(a, part, row_tiles, stream));
-    st = cuda_fail(e, "kv4_rows_kernel launch");
-  }
-  if (st == PQ_OK && part.chunks > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.T * a.heads_q), 1, 1);
-    cfg.blockDim = dim3(32 * JN_WARPS, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = wide ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<128>, a, part) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<64>, a, part);
-    st = cuda_fail(e, "kv4_join_kernel launch");
+    // Up to 640 tokens one block an item is enough: a second kernel and its workspace cost the host more than the shares
+    // save (517 tokens: 8.2 us on the device against 7.5, 10 us a call against 14).  Otherwise as many shares as blocks run
+    // at once.
+    const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
+    Shares shares = {};
+    if (max_len > 640 && a.B <= AT_SEQS) {
+      shares.blocks = (nt == 1 ? 3 : 2) * sms;
+      const size_t rows = (size_t)shares.blocks * 2 * 8 * nt;
+      st = workspace(rows, shares.blocks * sizeof(int4), &shares.o, &shares.ml);
+      shares.begun = reinterpret_cast<int4*>(shares.ml + rows);
+    }
+    if (st == PQ_OK)
+      st = cuda_fail(wide ? (nt == 1 ? launch_rows<128, 1>(a, shares, row_tiles, max_rows, stream) : launch_rows<128, 2>(a, shares, row_tiles, max_rows, stream))
+                          : (nt == 1 ? launch_rows<64, 1>(a, shares, row_tiles, max_rows, stream) : launch_rows<64, 2>(a, shares, row_tiles, max_rows, stream)),
+                     "kv4_rows_kernel launch");
   }
   if (ws) {
-    e = cudaFreeAsync(ws, stream);
+    const cudaError_t e = cudaFreeAsync(ws, stream);
     if (st == PQ_OK && e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync(attention workspace)");
   }
   return st;
