@@ -269,6 +269,32 @@ def test_bounds_that_do_not_fit(pq, qs, ls, max_q, max_len):
     run_and_check(pq, make_case(pq, 8, qs, ls, 8, 2, 64, 32), max_q, max_len)
 
 
+def spread(seed, B, q, ctx, empty):
+    """(new, cached) tokens of B sequences: short ones outnumber long ones, every `empty`-th has nothing cached and every
+    seventh asks for nothing."""
+    gen = torch.Generator().manual_seed(seed)
+    ls = [0 if b % empty == 2 else int(ctx ** float(torch.rand((), generator=gen))) for b in range(B)]
+    return [0 if b % 7 == 3 else 1 + b % q for b in range(B)], ls
+
+
+@pytest.mark.parametrize("hd,hq,hkv,page,window,qs,ls", [
+    (64, 8, 2, 16, 0, *spread(1, 300, 3, 2500, 5)),
+    (128, 8, 2, 64, 700, *spread(2, 40, 4, 9000, 6)),
+    (128, 16, 1, 32, 0, *spread(3, 20, 3, 6000, 9)),
+    (64, 2, 2, 16, 0, [1] * 500, [700 if b == 123 else 0 for b in range(500)]),
+    (128, 4, 4, 16, 0, [1, 1], [30000, 1]),
+    (64, 4, 2, 16, 0, *spread(4, 1024, 1, 900, 50)),
+    (64, 4, 2, 16, 0, *spread(5, 1025, 1, 900, 50)),
+    (64, 1, 1, 16, 0, [0, 0, 1, 0], [5000, 0, 4999, 70]),
+])
+def test_many_sequences_in_equal_shares(pq, hd, hq, hkv, page, window, qs, ls):
+    """The tokens of all sequences are cut into equal shares: sequences of one share, shares of one sequence, shares that end
+    where a sequence begins; the same twice gives the same bits."""
+    case = make_case(pq, len(ls), qs, ls, hq, hkv, hd, page)
+    first = run_and_check(pq, case, max(qs), max(max(ls), 700), window=window)
+    assert torch.equal(first, run_and_check(pq, case, max(qs), max(max(ls), 700), window=window))
+
+
 @pytest.mark.parametrize("q,n", [(1, 400), (150, 400)])
 def test_padding_rows_strides_and_scale(pq, q, n):
     cache, Q, starts, lens, table = make_case(pq, 4, [q, q], [n, n + 7], 8, 2, 128, 16)
