@@ -44,7 +44,7 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_BLOCK = 32;            // tokens a warp takes at a time
 constexpr int AT_TILES = AT_BLOCK / 16;
 // Query rows a key/value head and sequence from which on the tensor-core kernel of kv4_prompt.cu takes the call.
-constexpr int64_t kPromptRows = 64;
+constexpr int64_t kPromptRows = 32;
 constexpr float kRowsTop = 16384.0f;    // a product of probability and value scale from which the reference is raised (fp16: 65504)
 // A nibble alone in the low bits of an fp16 is n 2^-24, below the normal range (matrix instructions take those at full
 // value); four places up it is 16 times that.
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
               // a hidden token's value scale may be anything: select, do not multiply
               const float w0 = whole || s0 != -INFINITY ? p0 * vs[i][h] : 0.0f;
               const float w1 = whole || s1 != -INFINITY ? p1 * vs[i][h] : 0.0f;
-              top = ptx::max3(top, w0, w1);
+              top = ptx::max3(top, fabsf(w0), fabsf(w1));
               pb[i][nt][h] = pack_f16(w0, w1);
             }
           over = top > kRowsTop;
