@@ -359,8 +359,8 @@ pq_status pq_quant_rows8(const void* X, int64_t T, int64_t D, int64_t ldx, int g
  *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense.  No scratch, one launch.
  *
  * pq_w8a8_linear — pq_quant_rows8(X, T, D, ldx, g, codes_A, scales_A) followed by pq_w8a8_gemm, in one
- *   call: the product is launched as a programmatic dependent and its first weight loads overlap the
- *   quantisation.  codes_A and scales_A are caller-owned and written.  codes_W and scales_W must be
+ *   call; up to about 40 output tiles of 256 x 256 the product is launched as a programmatic dependent and
+ *   its first weight loads overlap the quantisation.  codes_A and scales_A are caller-owned and written.  codes_W and scales_W must be
  *   complete when the call is made (written by work enqueued on `stream` before it, or earlier); Y
  *   must not overlap X, codes_A or scales_A.
  */
@@ -442,8 +442,16 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *     s_t = scale * (q . k_t),  O = softmax(s) v   (times H / sqrt(head_dim) for ROTATE_V),
  *   k_t, v_t = code * scale of the slot block_table[b][t / page_size] * page_size + t % page_size; query
  *   head h reads key/value head h / (heads_q / heads).  A row that sees nothing becomes 0.
- *   Codes enter the products exactly; scores, maxima, sums and the output run in float32; the queries
- *   are bf16 and the probabilities are rounded to bf16 for the second product.
+ *   Scores, maxima, sums and the output run in float32.  What is rounded to fewer bits:
+ *     - a probability times its value's scale, to fp16 (2^-11 of it), for the second product;
+ *     - queries, to fp16 relative to their row's largest channel: exact down to 2^-25 of it (2^-10 in calls with
+ *       more than 32 rows a sequence and key/value head), so that the codes enter the products exactly;
+ *     - in calls with more than 32 such rows, where all rows of a tile see 32 tokens: key and value codes times
+ *       their scales, to fp16 (2^-11; values twice) relative to the largest scale of the 32.
+ *   Scales may be negative.  A NaN or infinite scale, or a NaN query, reaches only the rows that see the token or
+ *   own the query; what a row must not see may hold anything and changes no bit of it.
+ *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives
+ *   the same bits.
  *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
  *   q_start     device int32 [B + 1], ascending, within 0..T.  Rows outside every sequence stay as they were.
  *   seq_lens    device int32 [B];  block_table device int32 [B][table_width].  Entries behind a
@@ -453,8 +461,9 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *               A sequence beyond them is still computed in full, only more slowly.
  *   window      0: none.
  *   O           device bf16 [T][heads_q][head_dim], row stride ldo (a multiple of 8).
- *   Scratch: when long contexts are cut over several blocks, float32 partial results of
- *   4 (head_dim + 2) bytes per row, query head and piece, from the library's stream-ordered pool.
+ *   Scratch: when contexts are cut over several blocks, float32 partial results from the library's
+ *   stream-ordered pool: at most 4 (head_dim + 2) bytes per row, query head and piece (more than 32 rows), or
+ *   32 (or 16) such rows for each block that the device runs at once (fewer; lengths above 640).
  */
 pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q, const int32_t* q_start,
                            const int32_t* seq_lens, const int32_t* block_table, int64_t table_width, int64_t B,

@@ -1,32 +1,38 @@
-// Attention over the paged 4-bit cache for a few query rows a sequence (decode; sm_100a).
+// Attention over the paged 4-bit cache for a few query rows a sequence (decode; sm_100a), and what chooses between this
+// kernel and the one for prompts.
 //
 // Per query row (token at position p, query head) and cached token t of its key/value head, t <= p (and t > p - window):
 //   s_t = scale (q . kc_t) ks_t,  P = softmax(s),  o = sum_t P_t vs_t vc_t   (then o H / sqrt(hd) for rotated values)
-// kc, vc: 4-bit codes, ks, vs: their scales.  The codes are exact in bf16, so the products run on the tensor cores on
+// kc, vc: 4-bit codes, ks, vs: their scales.  The codes are exact in fp16, so the products run on the tensor cores on
 // the codes themselves; ks multiplies the finished dot product and vs the probability, both in float32.
 //
 // The cache is read once for all query rows of a key/value head (the group's heads x the sequence's new tokens), 64
-// bytes a token for keys and as much for values, and HBM bounds the kernel, with the unpacking close behind (about 14
-// instructions a token and warp).  A warp owns blocks of 32 tokens:
+// bytes a token for keys and as much for values.  Bytes are the floor; the unpacking bounds it (about 650 instructions for
+// 32 tokens of a head of 128, issued in half of the cycles by the 12 warps an SM that the registers leave room for).
+// 256 users of 4096 tokens: 295 us, 60% of the copy's bandwidth; 64 of up to 8192: 74; one of 65536: 33.
+// A warp owns blocks of 32 tokens:
 //   - keys are the A operand (16 tokens x 16 channels), the query rows the 8-column B operand: a thread's 16-byte
 //     load of one token is its share of the A operands of all 8 channel steps, because the channels of a dot product
 //     may be taken in any order as long as the queries follow the same one (set up once).  No shared memory.
 //   - the scores come out tokens x rows and stay in the warp's registers;
 //   - probabilities go back in as B operand (movmatrix transposes 8 x 8 of them) against the values as A operand
 //     (16 channels x 16 tokens): two tokens' words are byte-permuted together, then masked.
-//   - keys become bf16, as the queries are: nibble ^ 8 under 0x4300 is 128 + (code + 8), and the offset 136 leaves
-//     with the query's sum: the accumulator starts at -136 sum(q).
+//   - keys: nibble ^ 8 = code + 8 alone in an fp16 is (code + 8) 2^-24, below the normal range but exact, and four
+//     places up 16 times that: one mask a pair of codes and one shift a word.  The offset 8 leaves with the query's sum
+//     (the accumulator starts at -8 sum(q)), the factors with the queries, which become fp16 scaled below 2^15 (exact
+//     down to 2^-25 of a row's largest) and with the scores' float32 factor.
 //   - values become fp16: nibble ^ 8 under 0x6400 is 1024 + (code + 8), and 1032 is subtracted from the operand
 //     itself, exactly, since a long sum of probabilities times 1032 would drown the result.
-//   - the loads of the next block are issued as soon as this block's registers are free; 16 warps an SM (128 registers a
-//     thread) keep 64 KB in flight.
+//   - the loads of the next block are issued as soon as this block's registers are free (168 a thread): 52 KB an SM in
+//     flight.
 // The second product takes P_t vs_t as fp16.  Both are relative to a reference (a score plus the exponent of a value
 // scale) that a row keeps until its products outgrow fp16; only then, and at first, are the block's maximum score and
 // value scale reduced over the warp.  Rounding a product costs half a step of fp16, 2^-11, an eighth of what bf16 would.
 // Sums and the output are float32.
 //
-// A block's warps join their maxima, sums and outputs through shared memory.  Long contexts are cut into chunks of
-// tokens, one block each; a second kernel joins the chunks' float32 partial results.
+// A block's warps join their maxima, sums and outputs through shared memory.  The tokens of all sequences and heads are
+// cut into equal shares, one for each block that runs at once (64 users of 0 to 8192 tokens: 74 us; chunks of fixed length,
+// of which short sequences leave some empty: 89); a second kernel joins the float32 partial results.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
@@ -43,7 +49,9 @@ namespace {
 constexpr int AT_WARPS = 4;
 constexpr int AT_BLOCK = 32;            // tokens a warp takes at a time
 constexpr int AT_TILES = AT_BLOCK / 16;
-// Query rows a key/value head and sequence from which on the tensor-core kernel of kv4_prompt.cu takes the call.
+// Up to so many query rows a key/value head and sequence this kernel takes the call, beyond them the one of kv4_prompt.cu,
+// whose tiles have 128 rows (us, this against that; 2048 tokens, 4 heads a key/value head of 128): 64 sequences of 32
+// rows 133 : 156, of 64 rows 240 : 156; 8 of 64 rows 42 : 39.  (One sequence of 64 rows over 8192: 29 : 39.)
 constexpr int64_t kPromptRows = 32;
 constexpr float kRowsTop = 16384.0f;    // a product of probability and value scale from which the reference is raised (fp16: 65504)
 // A nibble alone in the low bits of an fp16 is n 2^-24, below the normal range (matrix instructions take those at full
@@ -91,7 +99,8 @@ struct Shares {
 constexpr int AT_STEP = AT_BLOCK * AT_WARPS;
 constexpr int AT_SEQS = 1024;           // sequences whose lengths a block can add up
 constexpr int AT_MIN_STEPS = 2;         // a share's least length
-constexpr int AT_LEAD = 3;              // steps that an item's beginning and end cost, ahead of its own on the line
+// Steps that an item's beginning and end cost, ahead of its own on the line (64 users, us: 0 steps 95, 1 85, 3 69, 6 73).
+constexpr int AT_LEAD = 3;
 
 struct Span {
   int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first cached token that any row sees
@@ -436,26 +445,32 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         float sum[2];
         for (int pass = 0;; ++pass) {
           if (__any_sync(0xffffffffu, over)) {
-            // Raise the references to this block's largest score plus the exponent of the largest value scale, both over
-            // the tokens that the row sees.
+            // Raise the references of the rows that need it (not of their neighbours in the tile, whose results must not
+            // depend on them) to this block's largest score plus the exponent of the largest value scale, both over the
+            // tokens that the row sees.
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = -INFINITY, y = 0.0f;
+              float x = -INFINITY, y = 0.0f, most = 0.0f;
+              const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
 #pragma unroll
               for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float z = s[i][nt][2 * h + e];
                   x = fmaxf(x, z);
-                  if (z != -INFINITY) y = fmaxf(y, finite_or_0(vs[i][h]));
+                  if (z != -INFINITY) {
+                    y = fmaxf(y, finite_or_0(vs[i][h]));
+                    most = fmaxf(most, fabsf(ex2(z - ref) * vs[i][h]));
+                  }
                 }
 #pragma unroll
               for (int b = 4; b < 32; b <<= 1) {
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, b));
                 y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, b));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, b));
               }
-              x = fmaxf(m[nt][e], x + scale_exponent(y));
+              x = m[nt][e] == -INFINITY || most > kRowsTop ? fmaxf(m[nt][e], x + scale_exponent(y)) : m[nt][e];
               alpha[e] = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
               m[nt][e] = x;
             }
@@ -658,28 +673,28 @@ __device__ __forceinline__ void join_row(const float2* ml_of, const float* o_of,
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if constexpr (parts == 1) {
     finish_row<HD>(y, sum, rotate, dst, lane);
-    return;
-  }
+  } else {
 #pragma unroll
-  for (int i = 0; i < E; ++i) sm_o[part * HD + E * lane + i] = y[i];
-  if (lane == 0) sm_ml[part] = make_float2(mx, sum);
-  __syncthreads();
-  if (part == 0) {
+    for (int i = 0; i < E; ++i) sm_o[part * HD + E * lane + i] = y[i];
+    if (lane == 0) sm_ml[part] = make_float2(mx, sum);
+    __syncthreads();
+    if (part == 0) {
 #pragma unroll
-    for (int w = 1; w < parts; ++w) mx = fmaxf(mx, sm_ml[w].x);
-    const float all = mx == -INFINITY ? 0.0f : mx;
-    sum = 0.0f;
+      for (int w = 1; w < parts; ++w) mx = fmaxf(mx, sm_ml[w].x);
+      const float all = mx == -INFINITY ? 0.0f : mx;
+      sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) y[i] = 0.0f;
+      for (int i = 0; i < E; ++i) y[i] = 0.0f;
 #pragma unroll
-    for (int w = 0; w < parts; ++w) {
-      const float2 ml = sm_ml[w];
-      const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - all);
-      sum = fmaf(ml.y, f, sum);
+      for (int w = 0; w < parts; ++w) {
+        const float2 ml = sm_ml[w];
+        const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - all);
+        sum = fmaf(ml.y, f, sum);
 #pragma unroll
-      for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w * HD + E * lane + i], f, y[i]);
+        for (int i = 0; i < E; ++i) y[i] = fmaf(sm_o[w * HD + E * lane + i], f, y[i]);
+      }
+      finish_row<HD>(y, sum, rotate, dst, lane);
     }
-    finish_row<HD>(y, sum, rotate, dst, lane);
   }
 }
 

@@ -19,16 +19,20 @@
 //                      row's P would outgrow fp16; at the end its output row.
 //   warps 12..15       producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
-// Nothing may spill: the operands leave so little of the L1 cache that a spilled register comes back from L2.
+// No register of a half step may spill: the operands leave so little of the L1 cache that it would come back from L2 (with
+// the next half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).
+// 4096 of 8192 tokens, 32 + 8 heads of 128: 496 us, 51% of the library's bf16 rate; a half step takes 2300 cycles, of which
+// the matrix instructions need 1400 and the exponentials 1000: the chain scores -> exponentials -> P -> product -> next
+// scores bounds it, with 10% of the SMs' time idle behind the last blocks.
 //
-// Where the scales go.  A step whose 128 tokens every row of the block sees takes keys and values with their scales
+// Where the scales go.  Of 32 tokens that every row of the block sees, keys and values come with their scales
 // multiplied in, as fp16 relative to a power of two for each 32 tokens (a key: one rounding of code * scale; a value:
 // the scale's and the product's; half a step is 2^-11, an eighth of a bf16 cache's).  With the scales left to the
 // softmax, every thread would read two scales a token from shared memory, a broadcast that costs four times its bytes:
-// measured, 3800 of 6200 shared-memory cycles a step.  Steps with tokens that some row must not see (the diagonal, a
-// window's edge, the ends of a sequence) keep the bare codes, exact, and the scales in the softmax, where a hidden
-// token's can be left out whatever it holds.  Queries become fp16 relative to their row's largest channel (exact but
-// for channels below 2^-10 of it).
+// measured, 3800 of 6200 shared-memory cycles a step.  Where some row must not see a token (the diagonal, a window's
+// edge, the ends of a sequence) the 32 keep the bare codes, exact, and the scales in the softmax, where a hidden token's
+// can be left out whatever it holds: a row's result must not depend on it, not even in its last bit.
+// Queries become fp16 relative to their row's largest channel (exact but for channels below 2^-10 of it).
 // Channels sit in the operands in the order 0 4 1 5 2 6 3 7 of each 8 (the order in which nibbles come out of a word);
 // queries are staged in the same order and the output is read back through it.
 // Keys are rows of 128 bytes, K-major; values lie the same way and enter as an MN-major operand.
@@ -84,25 +88,20 @@ struct __align__(1024) PromptSmem {
   int abort_flag;
 };
 
-// spins: polls before the waiting lane sleeps between them.  Softmax and MMA issue poll (a sleeping lane comes back
+// spins: polls before the waiting warp sleeps between them.  Softmax and MMA issue poll (a sleeping warp comes back
 // late); the producers, two stages ahead, sleep: their polls would take issue slots from the others.
 constexpr int kSpin = 200;
-__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status, int spins) {
-  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, spins)) return true;
-  *abort_flag = 1;
-  atomicOr(status, PQ_DEV_TIMEOUT);
-  return false;
-}
 __device__ __forceinline__ bool pr_warp_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status,
                                              int spins = kSpin) {
-  // the whole warp polls: an elected lane's answer would have to travel to the others first
-  for (int k = 0; k <= spins; ++k)
-    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) ok = pr_wait(bar, parity, abort_flag, status, 0) ? 1 : 0;
-  ok = __shfl_sync(0xffffffffu, ok, 0);
+  // the whole warp polls: an elected lane's answer would have to travel to the others first (4096 of 8192 tokens: 533 us
+  // that way, 496 this way)
+  if (__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag, kPrWaitNs, spins))) return true;
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    atomicOr(status, PQ_DEV_TIMEOUT);
+  }
   __syncwarp();
-  return ok != 0;
+  return false;
 }
 
 // The work of a block: sequence, key/value head, first row of its 256, chunk of the context.

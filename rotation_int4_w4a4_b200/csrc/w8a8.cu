@@ -476,7 +476,9 @@ pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t
   const int bf16 = out_dtype == PQ_OUT_BF16 ? 1 : 0;
   const int64_t pair_m = (N + 2 * PM - 1) / (2 * PM), pair_tiles = pair_m * ((T + PN - 1) / PN);
   CUtensorMap tmW, tmA;
-  // The pair kernel needs enough 256 x 256 tiles to occupy most SM pairs.
+  // The pair kernel reads half the operand bytes a product but needs 256 x 256 tiles for most SM pairs (us, pair against
+  // tile): 512 tokens, N = 14336, D = 4096 (112 tiles) 39 : 53; N = 8192 (64) 24.7 : 28.7; N = 5120 (40) 28.8 : 28.7 with the
+  // quantisation; D = 14336, N = 4096 (32) 57 : 53.
   if (T > 128 && pair_tiles * 4 >= 3 * (sms / 2)) {
     if (pair_tiles >= ((int64_t)1 << 30)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
     pq_status st = operand_map(&tmW, codes_W, N, D, PM);

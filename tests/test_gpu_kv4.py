@@ -322,6 +322,21 @@ def test_hidden_poison_inside_the_sequence(pq, q, n):
         assert torch.equal(O[:q - 1], O2[:q - 1])
 
 
+@pytest.mark.parametrize("q,n", [(2, 90), (5, 333), (8, 1500), (40, 700), (200, 900)])
+def test_later_tokens_change_no_bit(pq, q, n):
+    """What the newest tokens' rows meet (scores and values that outgrow whatever their tile's rows share) does not reach
+    the rows before them, not even in the last bit."""
+    cache, Q, starts, lens, table = make_case(pq, q + n, [q], [n], 4, 2, 128, 16, poison=False)
+    O = torch.empty_like(Q)
+    pq.pq_kv4_attention(cache, Q, O, starts, lens, table, q, n)
+    page, place = int(table[0, (n - 1) // 16]), (n - 1) % 16
+    for k, v in ((3.0, 0.1), (40.0, 40.0), (0.01, 3e5), (500.0, 1e-3), (1e5, 1e5), (-7.0, -9e4)):
+        cache.tensors[1][page, :, place], cache.tensors[3][page, :, place] = k, v
+        O2 = torch.empty_like(Q)
+        pq.pq_kv4_attention(cache, Q, O2, starts, lens, table, q, n)
+        assert torch.equal(O[:q - 1], O2[:q - 1]), (k, v)
+
+
 @pytest.mark.parametrize("q", [1, 140])
 def test_bad_pages_and_lengths(pq, q):
     """A page outside the cache is skipped, a length beyond the table is cut, and both are reported."""
