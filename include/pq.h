@@ -443,24 +443,26 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *   k_t, v_t = code * scale of the slot block_table[b][t / page_size] * page_size + t % page_size; query
  *   head h reads key/value head h / (heads_q / heads).  A row that sees nothing becomes 0.
  *   Scores, maxima, sums and the output run in float32.  What is rounded to fewer bits:
- *     - a probability times its value's scale, to fp16 (2^-11 of it), for the second product;
- *     - queries, to fp16 relative to their row's largest channel: exact down to 2^-25 of it (2^-10 in calls with
- *       more than 32 rows a sequence and key/value head), so that the codes enter the products exactly;
- *     - in calls with more than 32 such rows, where all rows of a tile see 32 tokens: key and value codes times
- *       their scales, to fp16 (2^-11; values twice) relative to the largest scale of the 32.
- *   Scales may be negative.  A NaN or infinite scale, or a NaN query, reaches only the rows that see the token or
- *   own the query; what a row must not see may hold anything and changes no bit of it.
+ *     - a probability times its value's scale, to fp16, for the second product: by 2^-11 of it, or 2^-24 of the
+ *       row's largest such product if that is more (third item: of its largest probability times the largest scale);
+ *     - queries, to fp16 relative to their row's largest channel: exact down to 2^-25 of it;
+ *     - in calls with more than 32 query rows a sequence and key/value head, where all rows of a tile see 32
+ *       tokens: key and value codes times their scales, to fp16 (2^-11; values twice) relative to the largest
+ *       scale of the 32.  Codes are exact otherwise.
+ *   Scales may be negative.  A NaN or infinite scale, or a NaN query, reaches only the rows that see the token
+ *   or own the query; what a row must not see may hold anything and changes no bit of it.
  *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives
  *   the same bits.
  *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
  *   q_start     device int32 [B + 1], ascending, within 0..T.  Rows outside every sequence stay as they were.
- *   seq_lens    device int32 [B];  block_table device int32 [B][table_width].  Entries behind a
+ *   seq_lens    device int32 [B];  block_table device int32 [B][table_width], table_width pages hold at most
+ *               2^30 tokens.  Entries behind a
  *               sequence's last page are not read.  A listed page outside the cache counts as 16-token
  *               pieces that nobody sees; a length beyond table_width pages is cut to them.
  *   max_q, max_len  upper bounds of the sequences' new tokens and lengths (>= 1): they size the launch.
  *               A sequence beyond them is still computed in full, only more slowly.
  *   window      0: none.
- *   O           device bf16 [T][heads_q][head_dim], row stride ldo (a multiple of 8).
+ *   O           device bf16 [T][heads_q][head_dim], row stride ldo (a multiple of 8); may not overlap Q.
  *   Scratch: when contexts are cut over several blocks, float32 partial results from the library's
  *   stream-ordered pool: at most 4 (head_dim + 2) bytes per row, query head and piece (more than 32 rows), or
  *   32 (or 16) such rows for each block that the device runs at once (fewer; lengths above 640).

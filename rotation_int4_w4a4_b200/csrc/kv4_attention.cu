@@ -57,7 +57,6 @@ constexpr float kRowsTop = 16384.0f;    // a product of probability and value sc
 // A nibble alone in the low bits of an fp16 is n 2^-24, below the normal range (matrix instructions take those at full
 // value); four places up it is 16 times that.
 constexpr float kCodeUnit = 5.9604644775390625e-8f;      // 2^-24
-constexpr float kQueryExp = 15.0f;      // a row's queries enter below 2^15: exact down to 2^-25 of the row's largest
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                         const uint32_t a3, const uint32_t b0, const uint32_t b1) {
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     }
 
     float o[NT][KS][4];
-    float m[NT][2], l[NT][2];            // reference exponent (score maximum + scale exponent) and sum
+    float m[NT][2], l[NT][2];            // reference exponent and sum
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
@@ -446,31 +445,30 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         for (int pass = 0;; ++pass) {
           if (__any_sync(0xffffffffu, over)) {
             // Raise the references of the rows that need it (not of their neighbours in the tile, whose results must not
-            // depend on them) to this block's largest score plus the exponent of the largest value scale, both over the
-            // tokens that the row sees.
+            // depend on them) to this block's largest score plus exponent of the value scale, over the tokens that the row
+            // sees: their largest product is then 1/2 to 1.
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = -INFINITY, y = 0.0f, most = 0.0f;
+              float x = -INFINITY, most = 0.0f;
               const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
 #pragma unroll
               for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                   const float z = s[i][nt][2 * h + e];
-                  x = fmaxf(x, z);
                   if (z != -INFINITY) {
-                    y = fmaxf(y, finite_or_0(vs[i][h]));
-                    most = fmaxf(most, fabsf(ex2(z - ref) * vs[i][h]));
+                    const float p = ex2(z - ref);
+                    x = fmaxf(x, z + value_exponent(vs[i][h]));
+                    most = ptx::max3(most, fabsf(p * vs[i][h]), p * (kRowsTop / kSumTop * (4 * AT_BLOCK)));
                   }
                 }
 #pragma unroll
               for (int b = 4; b < 32; b <<= 1) {
                 x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, b));
-                y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, b));
                 most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, b));
               }
-              x = m[nt][e] == -INFINITY || most > kRowsTop ? fmaxf(m[nt][e], x + scale_exponent(y)) : m[nt][e];
+              x = m[nt][e] == -INFINITY || most > kRowsTop ? fmaxf(m[nt][e], x) : m[nt][e];
               alpha[e] = x == -INFINITY ? 1.0f : ex2(m[nt][e] - x);
               m[nt][e] = x;
             }
@@ -501,7 +499,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
               top = ptx::max3(top, fabsf(w0), fabsf(w1));
               pb[i][nt][h] = pack_f16(w0, w1);
             }
-          over = top > kRowsTop;
+          over = top > kRowsTop || fmaxf(sum[0], sum[1]) > kSumTop;
           if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
         l[nt][0] += sum[0];

@@ -74,6 +74,18 @@ __device__ __forceinline__ float scale_exponent(float x) {
   return x == 0.0f ? 0.0f : (float)max(-100, min(126, e));
 }
 
+// The same for one token's value scale, of either sign and finite or not, within -80..126: what its score is raised by for
+// the row's reference.  The lower end keeps a probability whose value is (next to) nothing below 2^80.
+__device__ __forceinline__ float value_exponent(float scale) {
+  return fmaxf(-80.0f, (float)min(126, (int)(__float_as_uint(finite_or_0(scale)) >> 23) - 126));
+}
+// A sum of probabilities from which the reference is raised although their products with the value scales are small.
+constexpr float kSumTop = 1e28f;
+
+// Queries enter the products as fp16, a row's below 2^15: exact down to 2^-25 of the row's largest channel (the odd ones
+// carry a factor of 1/16).
+constexpr float kQueryExp = 15.0f;
+
 // One query row's output from its un-normalised float32 sums: lane l of the warp holds channels E l .. E l + E - 1
 // (E = HD / 32).  Divides by the sum of the probabilities (none: 0), rotates back, stores bf16.
 template <int HD>

@@ -32,7 +32,7 @@
 // measured, 3800 of 6200 shared-memory cycles a step.  Where some row must not see a token (the diagonal, a window's
 // edge, the ends of a sequence) the 32 keep the bare codes, exact, and the scales in the softmax, where a hidden token's
 // can be left out whatever it holds: a row's result must not depend on it, not even in its last bit.
-// Queries become fp16 relative to their row's largest channel (exact but for channels below 2^-10 of it).
+// Queries become fp16 relative to their row's largest channel (exact but for channels below 2^-25 of it).
 // Channels sit in the operands in the order 0 4 1 5 2 6 3 7 of each 8 (the order in which nibbles come out of a word);
 // queries are staged in the same order and the output is read back through it.
 // Keys are rows of 128 bytes, K-major; values lie the same way and enter as an MN-major operand.
@@ -193,21 +193,20 @@ __device__ __forceinline__ uint64_t token_bits(int first, int lo, int hi) {
   return upto & from;
 }
 
-// The same with the scales of 32 tokens (log2 units), of which the row sees some (a bit each): the largest score and the
-// largest value scale seen so far.  What a hidden token holds is selected away, never multiplied by 0.
-__device__ __forceinline__ void chunk_tops(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* vs, float c,
-                                           float& top, float& vm) {
+// The same with the scales of 32 tokens (log2 units), of which the row sees some (a bit each): the largest score
+// plus exponent of the value scale.  What a hidden token holds is selected away, never multiplied by 0.
+__device__ __forceinline__ float chunk_top(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* vs, float c) {
+  float top = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float4 k4 = ks[k], v4 = vs[k];
     const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (seen & (1u << (4 * k + q))) {
-        top = fmaxf(top, __uint_as_float(r[4 * k + q]) * (kk[q] * c));
-        vm = fmaxf(vm, finite_or_0(vv[q]));
-      }
+      if (seen & (1u << (4 * k + q)))
+        top = fmaxf(top, fmaf(__uint_as_float(r[4 * k + q]), kk[q] * c, value_exponent(vv[q])));
   }
+  return top;
 }
 
 // chunk_exp with the scales: probabilities times value scales in p; top: the largest magnitude of those so far.
@@ -445,8 +444,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           mq = fmaxf(mq, finite_or_0(__uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(place(row, c / 8))[c % 8] << 16)));
       }
       const float eq = scale_exponent(live ? mq : 0.0f);
-      const float f = a.scale < 0.0f ? -ex2(-eq) : ex2(-eq), f16 = f * kOddNibble;
-      c_row = fabsf(a.scale) * kLog2e * ex2(eq);
+      const float up = ex2(kQueryExp - eq), f = a.scale < 0.0f ? -up : up, f16 = f * kOddNibble;
+      c_row = fabsf(a.scale) * kLog2e * ex2(eq - kQueryExp);
       // channels 0 4 | 1 5 | 2 6 | 3 7; the keys' odd channels come 16 times too large
 #pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
@@ -534,14 +533,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         for (int pass = 0;; ++pass) {
           uint32_t x[32];
           if (__any_sync(0xffffffffu, over)) {
-            float top = -INFINITY, vm = 0.0f;
+            float cand = -INFINITY;
 #pragma unroll 1
             for (int g = 0; g < 2; ++g) {
               ptx::tmem_ld32(s_buf + 32 * g, x);
               ptx::tmem_ld_wait(x);
-              chunk_tops(x, g ? sb : sa, ks + 8 * g, vs + 8 * g, c_row, top, vm);
+              cand = fmaxf(cand, chunk_top(x, g ? sb : sa, ks + 8 * g, vs + 8 * g, c_row));
             }
-            const float cand = top + scale_exponent(vm);
             if (!(ok = raise(over && cand > m, cand))) break;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
@@ -552,7 +550,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           ptx::tmem_ld32(s_buf + 32, x);
           ptx::tmem_ld_wait(x);
           sum += chunk_exp_masked(x, sb, ks + 8, vs + 8, c_row, -ref, pb, top);
-          over = top > kTop;
+          over = top > kTop || sum > kSumTop;
           if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
         if (!ok) break;

@@ -1,4 +1,5 @@
 // Argument checks and dispatch of the 8-bit product and of the 4-bit key/value cache.
+#include <algorithm>
 #include <cmath>
 
 #include "internal.h"
@@ -10,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxD8 = 65536;               // 2^7 * 2^7 * D stays below 2^31
 constexpr int64_t kMaxRows = (int64_t)1 << 24;  // rows of one call (keeps every grid within its limits)
+constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // tokens of a sequence (positions, and sums of two, stay within int32)
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -244,8 +246,8 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
   }
   if (B < 1 || B > 65535) { set_error("B=%lld must be in 1..65535", (long long)B); return PQ_ERR_INVALID_ARG; }
   if (T < 1 || T > kMaxRows) { set_error("T=%lld must be in 1..2^24", (long long)T); return PQ_ERR_INVALID_ARG; }
-  if (table_width < 1 || table_width * (int64_t)cache->page_size >= ((int64_t)1 << 31)) {
-    set_error("table_width=%lld pages must hold 1..2^31-1 tokens", (long long)table_width);
+  if (table_width < 1 || table_width > kMaxTokens || table_width * (int64_t)cache->page_size > kMaxTokens) {
+    set_error("table_width=%lld pages must hold 1..2^30 tokens", (long long)table_width);
     return PQ_ERR_INVALID_ARG;
   }
   if (max_q < 1 || max_len < 1 || max_len >= ((int64_t)1 << 31)) {
@@ -265,8 +267,8 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
   a.B = (int)B;
   a.T = T;
   a.scale = scale;
-  a.window = (int)window;
+  a.window = (int)std::min(window, kMaxTokens);          // a wider one hides nothing
   a.O = static_cast<uint16_t*>(O);
   a.ldo = ldo;
-  return kv4_attention_run(a, max_q, max_len, reinterpret_cast<cudaStream_t>(stream));
+  return kv4_attention_run(a, max_q, std::min(max_len, kMaxTokens), reinterpret_cast<cudaStream_t>(stream));
 }

@@ -337,6 +337,46 @@ def test_later_tokens_change_no_bit(pq, q, n):
         assert torch.equal(O[:q - 1], O2[:q - 1]), (k, v)
 
 
+def scores_of(cache, Q, table, j):
+    """Code products q . kc of cached token j with every query row, float64 [T, heads_q]."""
+    page, place = int(table[0, j // cache.page_size]), j % cache.page_size
+    code, _ = unpack(cache.tensors[0][page, :, place], torch.ones(cache.heads, device="cuda"))
+    return torch.einsum("tgrd,gd->tgr", Q.double().view(len(Q), cache.heads, -1, cache.head_dim), code.double()).flatten(1)
+
+
+@pytest.mark.parametrize("q,n,j", [(1, 300, 290), (3, 900, 700), (7, 40, 20), (140, 700, 350), (140, 300, 199)])
+def test_a_value_of_zero_with_the_highest_score(pq, q, n, j):
+    """Scores may lie further apart than float32's exponents: a token whose value is zero (scale 0) and whose score is
+    thousands above all others leaves exactly 0 in the rows that see it, and no infinite sum."""
+    cache, Q, starts, lens, table = make_case(pq, n + j, [q], [n], 8, 2, 128, 16, rv=False, poison=False)
+    cache.tensors[1][int(table[0, j // 16]), :, j % 16] = 1e4
+    cache.tensors[3][int(table[0, j // 16]), :, j % 16] = 0.0
+    O = torch.empty_like(Q)
+    pq.pq_kv4_attention(cache, Q, O, starts, lens, table, q, n)
+    assert O.isfinite().all()
+    sees = (torch.arange(q, device="cuda") >= j - (n - q))[:, None]
+    on_top = (scores_of(cache, Q, table, j) > 30) & sees     # 30 * 1e4 / sqrt(128): the others stay below 3000
+    assert on_top.any() and (O[on_top] == 0).all() and (O[~sees.expand_as(on_top)] != 0).any(-1).all()
+
+
+@pytest.mark.parametrize("q,n,j", [(1, 300, 3), (1, 2000, 1), (4, 900, 2), (8, 700, 600)])
+def test_a_large_value_that_hardly_counts(pq, q, n, j):
+    """The largest value scale belongs to a token whose probability is 0: the others keep their precision.  Both runs round
+    each product by 2^-11, so they differ by 2^-10 of the largest value at most, and by a step of bf16."""
+    cache, Q, starts, lens, table = make_case(pq, n + j, [q], [n], 8, 2, 128, 16, rv=False, poison=False)
+    page, place = int(table[0, j // 16]), j % 16
+    cache.tensors[1][page, :, place] = 1e4
+    outs = []
+    for scale in (1e6, 0.02):
+        cache.tensors[3][page, :, place] = scale
+        outs.append(torch.empty_like(Q))
+        pq.pq_kv4_attention(cache, Q, outs[-1], starts, lens, table, q, n)
+    off = scores_of(cache, Q, table, j) < -30
+    a, b = (x[off].double() for x in outs)
+    assert off.any() and b.abs().max() < 10
+    assert ((a - b).abs() <= 2.0 ** -10 * 8 * cache.tensors[3].abs().max() * (1 + 2.0 ** -8) + 2.0 ** -8 * (a.abs() + b.abs())).all()
+
+
 @pytest.mark.parametrize("q", [1, 140])
 def test_bad_pages_and_lengths(pq, q):
     """A page outside the cache is skipped, a length beyond the table is cut, and both are reported."""

@@ -117,6 +117,12 @@ def test_attention(pq, change, word):
     refused_kv(pq, "pq_kv4_attention", {}, change, "PQ_ERR_INVALID_ARG", word)
 
 
+@pytest.mark.parametrize("width", [(1 << 26) + 1, 1 << 30, 1 << 40, 1 << 62])
+def test_attention_lengths(pq, width):
+    """Pages of 16: tokens of a sequence are numbered in int32, sums of two of them too."""
+    refused_kv(pq, "pq_kv4_attention", {"page_size": 16}, {"width": width}, "PQ_ERR_INVALID_ARG", "table_width")
+
+
 # ------------------------------------------------------------------- the binding's own checks
 class FakeCuda:
     """Stands in for a CUDA tensor (never dereferenced)."""
