@@ -76,6 +76,7 @@ struct __align__(1024) PromptSmem {
   uint8_t v[PR_STAGES][KBLK][PT * 128];
   // What multiplies a token's score, and its probability: its scales, or (scales multiplied in) its group's powers of 2.
   float ks[SC_RING][PT], vs[SC_RING][PT];
+  float ve[SC_RING][PT];                                 // value_exponent of vs
   uint32_t valid[SC_RING][4];                            // which tokens exist, a bit each
   int scaled[SC_RING][4];                                // the 32 tokens' scales are in the operands
   float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
@@ -195,16 +196,15 @@ __device__ __forceinline__ uint64_t token_bits(int first, int lo, int hi) {
 
 // The same with the scales of 32 tokens (log2 units), of which the row sees some (a bit each): the largest score
 // plus exponent of the value scale.  What a hidden token holds is selected away, never multiplied by 0.
-__device__ __forceinline__ float chunk_top(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* vs, float c) {
+__device__ __forceinline__ float chunk_top(const uint32_t (&r)[32], uint32_t seen, const float4* ks, const float4* ve, float c) {
   float top = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float4 k4 = ks[k], v4 = vs[k];
+    const float4 k4 = ks[k], v4 = ve[k];
     const float kk[4] = {k4.x, k4.y, k4.z, k4.w}, vv[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      if (seen & (1u << (4 * k + q)))
-        top = fmaxf(top, fmaf(__uint_as_float(r[4 * k + q]), kk[q] * c, value_exponent(vv[q])));
+      if (seen & (1u << (4 * k + q))) top = fmaxf(top, fmaf(__uint_as_float(r[4 * k + q]), kk[q] * c, vv[q]));
   }
   return top;
 }
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
             for (int g = 0; g < 2; ++g) {
               ptx::tmem_ld32(s_buf + 32 * g, x);
               ptx::tmem_ld_wait(x);
-              cand = fmaxf(cand, chunk_top(x, g ? sb : sa, ks + 8 * g, vs + 8 * g, c_row));
+              cand = fmaxf(cand, chunk_top(x, g ? sb : sa, ks + 8 * g, reinterpret_cast<const float4*>(S.ve[sc]) + t0 / 4 + 8 * g, c_row));
             }
             if (!(ok = raise(over && cand > m, cand))) break;
           }
@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const float ke = scale_exponent(km), ve = scale_exponent(vm);
       S.ks[sc][t] = scaled ? ex2(ke) : ks;
       S.vs[sc][t] = scaled ? ex2(ve) : vs;
+      S.ve[sc][t] = scaled ? ve + 1.0f : value_exponent(vs);
       if (lane == 0) {
         S.scaled[sc][wq] = scaled ? 1 : 0;
         S.valid[sc][wq] = bits;
