@@ -811,7 +811,7 @@ pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tile
 
 int64_t kv4_prompt_tiles(const Kv4AttnArgs& a) {
   const int64_t group = a.heads_q / a.cache.heads;
-  return (a.T * group + 2 * PT - 1) / (2 * PT) + a.B;
+  return (a.T * group + (2 * PT - 1) * (int64_t)a.B) / (2 * PT);   // a sequence's last tile may hold a single row
 }
 
 pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream) {

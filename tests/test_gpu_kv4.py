@@ -445,6 +445,31 @@ def test_repeats_capture_and_streams(pq, q, n, B):
             assert torch.equal(O, w)
 
 
+@pytest.mark.parametrize("qs,ls", [([1, 1, 0, 1], [40, 3000, 0, 700]), ([2, 1], [5000, 1]), ([150, 60], [700, 900])])
+def test_replayed_with_new_lengths(pq, qs, ls):
+    """A captured call reads lengths and pages when it is replayed: the cut of the work follows them."""
+    cache, Q, starts, lens, table = make_case(pq, 77, qs, ls, 8, 2, 128, 64)
+    last, pages = lens.clone(), table.clone()
+    O = torch.zeros_like(Q)
+    lens.copy_(last.clamp_max(1))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pq.pq_kv4_attention(cache, Q, O, starts, lens, table, max(qs), max(ls))
+    for n, flip in ((last.clamp_max(1), False), (last, False), (last // 3, False), (last.flip(0).minimum(last), False), (last, True)):
+        lens.copy_(n)
+        if flip:                                             # the first two sequences trade places
+            for x in (lens, table):
+                x[:2] = x[:2].flip(0)
+        O.fill_(7)
+        graph.replay()
+        want = torch.full_like(Q, 7)
+        pq.pq_kv4_attention(cache, Q, want, starts, lens, table, max(qs), max(ls))
+        assert torch.equal(O, want)
+        exact, tol = attention64(cache, Q, starts, lens, table, 128 ** -0.5, 0, torch.full(Q.shape, 7.0, dtype=torch.float64, device="cuda"))
+        assert ((O.double() - exact).abs() <= tol).all()
+    pq.pq_check_status()
+
+
 def test_large_cache_offsets(pq):
     """Pages whose bytes lie beyond 2^31 (codes) of the cache's start."""
     hkv, hd, page = 8, 128, 256
