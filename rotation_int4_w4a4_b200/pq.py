@@ -388,15 +388,19 @@ def pq_quant_rows8(X, codes, scales, g=0, T=None, D=None, ldx=None, stream=None)
 
 
 def _rows8(X, T, D, ldx, dev, torch):
-    """Pointer, rows, channels and row stride of bf16 rows (a single row's stride says nothing: its length stands in)."""
+    """Pointer, rows, channels and row stride of bf16 rows (a single row's stride says nothing: its length stands in).
+    An ldx that is not the tensor's stride is refused: the kernels would read other rows, or past the last one."""
     if isinstance(X, int):
         return X, T, D, D if ldx is None else ldx
     if X.dim() != 2:
         raise ValueError("X: expected a 2-D tensor")
     rows, cols = X.shape
     T, D = rows if T is None else T, cols if D is None else D
+    own = X.stride(0) if rows > 1 else cols
     if ldx is None:
-        ldx = X.stride(0) if rows > 1 else cols
+        ldx = own
+    elif ldx != own and rows > 1:
+        raise ValueError(f"X: row stride {own} differs from ldx={ldx}")
     if X.dtype is not torch.bfloat16 or X.stride(1) != 1 or T > rows or D > cols or X.get_device() != dev:
         _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
         if X.get_device() != dev:
