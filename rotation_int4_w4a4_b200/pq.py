@@ -366,10 +366,11 @@ def _raw_stream(stream, dev, torch):
 
 
 def _on(x, name, kind, dtype, need, dev):
-    """:func:`_arg` and that the tensor lives on the current device (the library launches there)."""
+    """:func:`_arg` and that the tensor lives on the current device (the library launches there).  is_cuda counts beside
+    the device's index: without an initialised CUDA both the current device and a host tensor's are -1."""
     if x is None:
         return None
-    if not isinstance(x, int) and x.dtype is dtype and x.is_contiguous() and x.numel() >= need and x.get_device() == dev:
+    if not isinstance(x, int) and x.dtype is dtype and x.is_cuda and x.is_contiguous() and x.numel() >= need and x.get_device() == dev:
         return x.data_ptr()
     p = _arg(x, name, kind, need)              # names what is wrong, if it is the tensor's type, layout or size
     if not isinstance(x, int) and x.get_device() != dev:
@@ -401,7 +402,7 @@ def _rows8(X, T, D, ldx, dev, torch):
         ldx = own
     elif ldx != own and rows > 1:
         raise ValueError(f"X: row stride {own} differs from ldx={ldx}")
-    if X.dtype is not torch.bfloat16 or X.stride(1) != 1 or T > rows or D > cols or X.get_device() != dev:
+    if X.dtype is not torch.bfloat16 or not X.is_cuda or X.stride(1) != 1 or T > rows or D > cols or X.get_device() != dev:
         _arg(X, "X", "bf16", (T - 1) * ldx + D if T > 0 else 0, rows_strided=True)
         if X.get_device() != dev:
             raise ValueError(f"X: on {X.device}, but the current device is cuda:{dev}")

@@ -80,3 +80,52 @@ def test_row_strides_that_are(pq, reached, call):
     with pytest.raises(ValueError, match="X: holds"):
         call(pq, FakeCuda(wide[:1, :128]), T=1, D=256, ldx=1024)
     assert len(reached) == 4
+
+
+class Host:
+    """A CPU tensor whose address must not leave the binding."""
+
+    def __init__(self, t):
+        self._t = t
+        self.shape, self.dtype, self.is_cuda, self.device = t.shape, t.dtype, False, t.device
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    def data_ptr(self):
+        raise AssertionError("the address of a host tensor was taken")
+
+
+ROWS = {"X": ((4, 256), torch.bfloat16), "codes": ((4, 256), torch.int8), "scales": ((4,), torch.float32)}
+GEMM = {"codes_A": ((4, 256), torch.int8), "scales_A": ((4,), torch.float32), "codes_W": ((8, 256), torch.int8),
+        "scales_W": ((8,), torch.float32), "Y": ((4, 8), torch.float32)}
+LINEAR = dict([("X", ROWS["X"])], **GEMM)
+
+
+@pytest.mark.parametrize("name,spec,host", [(n, s, h) for n, s in (("pq_quant_rows8", ROWS), ("pq_w8a8_gemm", GEMM), ("pq_w8a8_linear", LINEAR))
+                                            for h in s])
+def test_host_tensors_are_refused(pq, reached, name, spec, host):
+    """One argument on the CPU, the others on the GPU; nothing has touched CUDA before."""
+    args = {k: (Host if k == host else FakeCuda)(torch.empty(shape, dtype=dtype)) for k, (shape, dtype) in spec.items()}
+    with pytest.raises(ValueError, match="expected a CUDA tensor"):
+        getattr(pq, name)(**args)
+    assert not reached
+
+
+def test_host_tensors_of_the_cache_calls_are_refused(pq, reached):
+    codes, sc = FakeCuda(torch.empty(3, 2, 16, 64, dtype=torch.uint8)), FakeCuda(torch.empty(3, 2, 16))
+    cache = pq.KV4Cache(codes, sc, codes, sc)
+    rows, i64, i32 = torch.empty(5, 256, dtype=torch.bfloat16), torch.zeros(5, dtype=torch.int64), torch.zeros(6, dtype=torch.int32)
+    good = FakeCuda(rows)
+    for Q, K, Q_out, slots in ((Host(rows), good, good, FakeCuda(i64)), (good, Host(rows), good, FakeCuda(i64)),
+                               (good, good, Host(rows), FakeCuda(i64)), (good, good, good, Host(i64))):
+        with pytest.raises(ValueError, match="expected a CUDA tensor"):
+            pq.pq_kv4_append(cache, Q, K, good, Q_out, None, slots)
+    with pytest.raises(ValueError, match="expected a CUDA tensor"):
+        pq.pq_kv4_read(cache, Host(i64), good, good)
+    table = torch.zeros(5, 4, dtype=torch.int32)
+    for starts, lens, tab in ((Host(i32), FakeCuda(i32), FakeCuda(table)), (FakeCuda(i32), Host(i32), FakeCuda(table)),
+                              (FakeCuda(i32), FakeCuda(i32), Host(table))):
+        with pytest.raises(ValueError, match="expected a CUDA tensor"):
+            pq.pq_kv4_attention(cache, good, good, starts, lens, tab, 1, 10)
+    assert not reached
