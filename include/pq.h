@@ -445,11 +445,11 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *   head h reads key/value head h / (heads_q / heads).  A row that sees nothing becomes 0.
  *   Scores, maxima, sums and the output run in float32.  What is rounded to fewer bits:
  *     - a probability times its value's scale, to fp16, for the second product: by 2^-11 of it, or 2^-24 of the
- *       row's largest such product if that is more (third item: of its largest probability times the largest scale);
+ *       row's largest such product if that is more (third item: 2^-18 of it);
  *     - queries, to fp16 relative to their row's largest channel: exact down to 2^-25 of it;
  *     - in calls with more than 32 query rows a sequence and key/value head, where all rows of a tile see 32
- *       tokens: key and value codes times their scales, to fp16 (2^-11; values twice) relative to the largest
- *       scale of the 32.  Codes are exact otherwise.
+ *       tokens whose nonzero scales lie within a factor of 64: key and value codes times their scales, to fp16
+ *       (2^-11; values twice).  Codes are exact otherwise.
  *   Scales may be negative.  A NaN or infinite scale, or a NaN query, reaches only the rows that see the token
  *   or own the query; what a row must not see may hold anything and changes no bit of it.
  *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives

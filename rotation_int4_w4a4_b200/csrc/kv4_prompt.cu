@@ -25,13 +25,14 @@
 // the matrix instructions need 1400 and the exponentials 1000: the chain scores -> exponentials -> P -> product -> next
 // scores bounds it, with 10% of the SMs' time idle behind the last blocks.
 //
-// Where the scales go.  Of 32 tokens that every row of the block sees, keys and values come with their scales
-// multiplied in, as fp16 relative to a power of two for each 32 tokens (a key: one rounding of code * scale; a value:
-// the scale's and the product's; half a step is 2^-11, an eighth of a bf16 cache's).  With the scales left to the
-// softmax, every thread would read two scales a token from shared memory, a broadcast that costs four times its bytes:
-// measured, 3800 of 6200 shared-memory cycles a step.  Where some row must not see a token (the diagonal, a window's
-// edge, the ends of a sequence) the 32 keep the bare codes, exact, and the scales in the softmax, where a hidden token's
-// can be left out whatever it holds: a row's result must not depend on it, not even in its last bit.
+// Where the scales go.  Of 32 tokens that every row of the block sees and whose scales are of a size (kScaleSpread), keys
+// and values come with their scales multiplied in, as fp16 relative to a power of two for each 32 tokens (a key: one
+// rounding of code * scale; a value: the scale's and the product's; half a step is 2^-11, an eighth of a bf16 cache's).
+// With the scales left to the softmax, every thread would read two scales a token from shared memory, a broadcast that
+// costs four times its bytes: measured, 3800 of 6200 shared-memory cycles a step.  Where scales differ by more, or some row
+// must not see a token (the diagonal, a window's edge, the ends of a sequence), the 32 keep the bare codes, exact, and the
+// scales in the softmax, where a hidden token's can be left out whatever it holds: a row's result must not depend on it,
+// not even in its last bit.
 // Queries become fp16 relative to their row's largest channel (exact but for channels below 2^-25 of it).
 // Channels sit in the operands in the order 0 4 1 5 2 6 3 7 of each 8 (the order in which nibbles come out of a word);
 // queries are staged in the same order and the output is read back through it.
@@ -62,6 +63,11 @@ constexpr int SC_RING = 4;               // scale stages: a step's scales outliv
 constexpr uint64_t kPrWaitNs = 2000000000ull;
 constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i + 64 (half & 1), O_i at 256 + 128 i
 constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 65504) from which it is taken elsewhere
+// Scales are multiplied into the operands of 32 tokens whose nonzero scales (finite ones) lie within this factor, of the keys
+// and of the values.  The reference of such a step is its largest score plus the exponent of its largest value scale, which
+// may belong to another token: the largest product is then up to 2^6 below 1 and keeps 18 of fp16's 24 places below it.
+// Within the factor every operand is a normal fp16 number (of scales above 2^-100).
+constexpr float kScaleSpread = 64.0f;
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
   return (1u << 4) | ((uint32_t)b_mn_major << 16) |
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       ptx::tc_fence_after();
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
       const uint32_t va = t0 ? valid.z : valid.x, vb = t0 ? valid.w : valid.y;
-      // Raises rows' references to cand (largest score plus the exponent of the largest value scale), in the sum and in O.
+      // Raises rows' references to cand (largest score plus exponent of a value scale), in the sum and in O.
       auto raise = [&](bool grow, float cand) {
         const float m_new = grow ? cand : m;
         const float f = m_new == -INFINITY ? 1.0f : ex2(m - m_new);
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           ptx::tmem_ld_wait(xa);
           ptx::tmem_ld_wait(xb);
           if (__any_sync(0xffffffffu, over)) {
-            const float cand = fmaxf(chunk_max(xa) * kp.x, chunk_max(xb) * kp.y) + fmaxf(v2.x, v2.y);
+            const float cand = fmaxf(fmaf(chunk_max(xa), kp.x, v2.x), fmaf(chunk_max(xb), kp.y, v2.y));
             if (!(ok = raise(over && cand > m, cand))) break;
           }
           const float ref = m == -INFINITY ? 0.0f : m;
@@ -650,7 +656,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
       const float km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(ks))));
       const float vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(vs))));
-      const bool scaled = interior((j0 + j) * PT + 32 * wq);
+      auto least = [](float x) {                         // smallest nonzero magnitude of the warp's finite scales
+        const float y = finite_or_0(x);
+        return __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(y == 0.0f ? INFINITY : y)));
+      };
+      const bool scaled = interior((j0 + j) * PT + 32 * wq) && km <= kScaleSpread * least(ks) && vm <= kScaleSpread * least(vs);
       const float ke = scale_exponent(km), ve = scale_exponent(vm);
       S.ks[sc][t] = scaled ? ex2(ke) : ks;
       S.vs[sc][t] = scaled ? ex2(ve) : vs;

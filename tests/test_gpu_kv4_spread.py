@@ -52,3 +52,22 @@ def test_few_rows(pq, hd, rv, qs, ls, hq, hkv, page, window):
 ])
 def test_many_rows(pq, hd, rv, qs, ls, hq, hkv, page, window):
     check(pq, make_case(pq, sum(ls) + hd, qs, ls, hq, hkv, hd, page, rv=rv), max(qs), max(ls), window=window)
+
+
+@pytest.mark.parametrize("rv", [False, True])
+@pytest.mark.parametrize("key", [1.0, 30.0, 1e4])
+@pytest.mark.parametrize("value", [3e-3, 8.0, 50.0, 700.0, 2.0 ** 20])
+@pytest.mark.parametrize("q,n,js", [(1, 900, [3]), (7, 700, [0, 600]), (140, 700, [3]), (140, 700, [40]), (64, 3000, [0, 1000, 2900]), (300, 400, [290])])
+def test_one_token_of_another_scale(pq, q, n, js, value, key, rv):
+    """A token whose value scale lies far above or below the others', with any share of the probability (its score is near the
+    others', or dozens or thousands above or below them), costs the other tokens nothing of their precision."""
+    cache, Q, starts, lens, table = make_case(pq, n + q, [q], [n], 8, 2, 128, 16, rv=rv, poison=False)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(q)
+    for i in (1, 3):                                      # the others' scales: within a factor of 2
+        cache.tensors[i].copy_(torch.rand(cache.tensors[i].shape, generator=gen, device="cuda") * 0.05 + 0.05)
+    for j in js:
+        page, place = int(table[0, j // 16]), j % 16
+        cache.tensors[1][page, :, place] *= key
+        cache.tensors[3][page, :, place] *= value
+    check(pq, (cache, Q, starts, lens, table), q, n)
