@@ -457,9 +457,9 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
  *   q_start     device int32 [B + 1], ascending, within 0..T.  Rows outside every sequence stay as they were.
  *   seq_lens    device int32 [B];  block_table device int32 [B][table_width], table_width pages hold at most
- *               2^30 tokens.  Entries behind a
- *               sequence's last page are not read.  A listed page outside the cache counts as 16-token
- *               pieces that nobody sees; a length beyond table_width pages is cut to them.
+ *               2^30 tokens.  Entries behind a sequence's last page, and those in front of the first page that a
+ *               window leaves to its new tokens, may hold anything.  A listed page outside the cache counts as
+ *               16-token pieces that nobody sees; a length beyond table_width pages is cut to them.
  *   max_q, max_len  upper bounds of the sequences' new tokens and lengths (>= 1): they size the launch.
  *               A sequence beyond them is still computed in full, only more slowly.
  *   window      0: none.

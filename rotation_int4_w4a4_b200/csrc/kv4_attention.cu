@@ -309,12 +309,13 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) page_of[i] = tok0 + 16 * i < n ? __ldg(table + ((tok0 + 16 * i) >> ps)) : 0;
     };
+    // Pieces in front of what the tile sees (a window's older pages may be anyone's by now) are not looked at.
     auto locate = [&](int tok0) {
-      all = tok0 + AT_BLOCK <= n;
+      all = tok0 + AT_BLOCK <= n && tok0 + 16 > c_lo;
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
         const int tok = tok0 + 16 * i;
-        int k = min(16, n - tok);
+        int k = tok + 16 > c_lo ? min(16, n - tok) : 0;
         uint32_t at = 0;
         if (k > 0) {
           const int page = page_of[i];

@@ -1,0 +1,29 @@
+"""Pages of a sequence that a sliding window has left behind, and lengths and starts at the ends of their types."""
+import pytest
+import torch
+
+from tests.test_gpu_kv4 import make_case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pq():
+    from rotation_int4_w4a4_b200 import pq as _pq
+    return _pq
+
+
+@pytest.mark.parametrize("page", [16, 32, 64])
+@pytest.mark.parametrize("q,n,max_len", [(1, 300, 300), (1, 3000, 3000), (3, 777, 777), (64, 900, 900), (300, 1000, 1000)])
+def test_pages_before_the_window_are_not_looked_at(pq, q, n, max_len, page):
+    """A server takes back the pages that no new token's window reaches; their places in the table say nothing any more."""
+    cache, Q, starts, lens, table = make_case(pq, n, [q], [n], 8, 2, 128, page, poison=False)
+    for window in (1, 7, 16, 17, 40, 60, 100, 200, 255):
+        want, O = torch.empty_like(Q), torch.empty_like(Q)
+        pq.pq_kv4_attention(cache, Q, want, starts, lens, table, q, max_len, window=window)
+        freed = table.clone()
+        freed[0, :max(0, n - q - window + 1) // page] = -1
+        pq.pq_check_status()
+        pq.pq_kv4_attention(cache, Q, O, starts, lens, freed, q, max_len, window=window)
+        pq.pq_check_status()
+        assert torch.equal(O, want)
