@@ -341,9 +341,10 @@ pq_status pq_w4a4_gemm_launch_count_g(int64_t T, int64_t N, int64_t D, int g, in
  * pq_quant_rows8 — rows of bf16 to signed 8-bit codes, activations and weights alike:
  *   y = x H_g / sqrt(g) per block of g channels (g = 64, 128, 256; g = 0: y = x), scales[t] =
  *   max|y[t]| / 127 over the whole row, codes = RNE(y / scale) in -127..127.  A row whose maximum is
- *   below 1e-36 counts as zero (scale 0, codes 0).  H is symmetric, so rotated activations against
+ *   below 1e-36 counts as zero (scale 0, codes 0); one with a NaN or an infinity (after the rotation too) gets
+ *   scale NaN and codes 0, so that all that is made of it is NaN.  H is symmetric, so rotated activations against
  *   weights rotated with the same g leave the product unchanged before quantisation.
- *   X       device bf16 [T][ldx] (first D columns used), ldx >= D, ldx % 8 == 0; finite.
+ *   X       device bf16 [T][ldx] (first D columns used), ldx >= D, ldx % 8 == 0.
  *   D       16..65536, a multiple of 16 and of g.  T >= 1.
  *   codes   device int8 [T][D];  scales device float32 [T] (both dense, 16-byte aligned).
  */
@@ -355,7 +356,8 @@ pq_status pq_quant_rows8(const void* X, int64_t T, int64_t D, int64_t ldx, int g
  *   exact in int32 for any codes in -128..127 (D <= 65536: |d| <= 2^30); then converted to float32
  *   (one rounding above 2^24), multiplied with the two scales in float32 and stored.
  *   codes_A int8 [T][D], scales_A float32 [T], codes_W int8 [N][D], scales_W float32 [N]: device, dense.
- *   T, N >= 1 (any N; no multiple is asked), D 16..65536 and a multiple of 16.  Scales must be finite.
+ *   T, N >= 1 (any N; no multiple is asked), D 16..65536 and a multiple of 16.  A scale that is
+ *   not finite reaches its own row or column only.
  *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense.  No scratch, one launch.
  *
  * pq_w8a8_linear — pq_quant_rows8(X, T, D, ldx, g, codes_A, scales_A) followed by pq_w8a8_gemm, in one

@@ -1,6 +1,6 @@
 // Rows of bf16 -> signed 8-bit codes with one symmetric scale a row (sm_100a):
 //   y = x H_g / sqrt(g) per block of g channels (g = 64, 128 or 256; g = 0: y = x),
-//   scale = max|y| / 127, codes = RNE(y / scale) in -127..127.
+//   scale = max|y| / 127, codes = RNE(y / scale) in -127..127; scale NaN and codes 0 if max|y| is infinite or NaN.
 // The row scale of the RRS page's set-up (per-token activation quantisation) at 8 bits (ParoQuant
 // page §4.1 keeps in 8 bits what 4 bits lose); weights take the same pass, one scale an output channel.
 //
@@ -108,10 +108,18 @@ __global__ void __launch_bounds__(1024) quant_rows8_kernel(const uint16_t* __res
               for (int i = 0; i < 8; i += 2) butterfly(v[u + s] + i, v[u + s + h] + i);
             }
     }
+    // NaN stays in the maximum: a row that holds one must not come out as numbers
+    float m2 = 0.0f;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) m = fmaxf(m, row_absmax<8>(v[s]));
+    for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int i = 0; i < 8; i += 4) {
+        m = ptx::max3_nan(m, fabsf(v[s][i]), fabsf(v[s][i + 1]));
+        m2 = ptx::max3_nan(m2, fabsf(v[s][i + 2]), fabsf(v[s][i + 3]));
+      }
+    m = ptx::max_nan(m, m2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (tpr > 32) {                                        // the same for the whole block
       // two buffers: a round's maxima are read before the round after next overwrites them
       float* buf = red[round & 1];
@@ -119,17 +127,20 @@ __global__ void __launch_bounds__(1024) quant_rows8_kernel(const uint16_t* __res
       __syncthreads();
       m = lane < tpr / 32 ? buf[sub * (tpr / 32) + lane] : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
     if (!live) continue;
-    const bool zero = !(m >= kQ8Tiny);
-    const float inv = zero ? 0.0f : 127.0f / m;
-    if (t == 0) scales[row] = zero ? 0.0f : m * scale_mult;
+    const float inv = m >= kQ8Tiny && m < INFINITY ? 127.0f / m : 0.0f;
+    if (t == 0) scales[row] = inv != 0.0f ? m * scale_mult : m < kQ8Tiny ? 0.0f : NAN;
     uint2* dst = reinterpret_cast<uint2*>(codes + row * D);
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       const int c = piece(s);
       if (c >= pieces) continue;
+      if (inv == 0.0f) {
+        dst[c] = make_uint2(0u, 0u);
+        continue;
+      }
       uint32_t b[8];                                        // codes in the low bytes (1.5 * 2^23 added)
 #pragma unroll
       for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(fmaf(v[s][i], inv, kRowRoundMagic));
