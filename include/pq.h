@@ -410,8 +410,9 @@ typedef struct pq_kv4_cache {
  *   rotated caches: y = x H / sqrt(head_dim)  (queries and keys: ROTATE_K; values: ROTATE_V)
  *   queries: Q_out = bf16(y).   Keys, values: scale = max|y| / 7, codes = RNE(y / scale), into the slot
  *   (a head whose maximum is below 1e-36 counts as zero: scale 0, codes 0).
- *   All in float32, each product and sum rounded on its own; nothing but Q_out is rounded to bf16.  Inputs
- *   finite: a NaN or infinite channel spoils its head (and the slot's codes and scale of that head) only.
+ *   All in float32, each product and sum rounded on its own; nothing but Q_out is rounded to bf16.  A NaN or
+ *   infinite channel spoils its head only: a query's Q_out is not finite there, a key or value head whose maximum is
+ *   NaN or infinite gets scale NaN and codes 0, so that what attends to it is NaN.
  *   Q, K, V     device bf16 [T][heads_q | heads | heads][head_dim], row strides ldq, ldk, ldv (elements,
  *               multiples of 4; 8-byte aligned): columns of one projection's output will do.
  *   heads_q     a multiple of cache->heads.

@@ -5,7 +5,7 @@
 //      or (2i, 2i + 1): (a, b) -> (a cos - b sin, b cos + a sin)              (if a table is given)
 //   3. y = x H / sqrt(hd)                                                     (if the cache is rotated)
 //   4. queries: bf16(y).  Keys, values: scale = max|y| / 7, code = RNE(y / scale), two codes a byte, into the
-//      token's slot of the paged cache.
+//      token's slot of the paged cache (a maximum that is infinite or NaN: scale NaN, codes 0).
 // (OSTQuant page: Hadamard on Q and K after the position rotation, one rotation per head for V; RRS page,
 // set-up of the experiments: the cache quantised in groups of 128, here the head.)
 //
@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
   }
   float m = 0.0f;
 #pragma unroll
-  for (int c = 0; c < E; c += 2) m = ptx::max3(m, fabsf(v[c]), fabsf(v[c + 1]));
+  for (int c = 0; c < E; c += 2) m = ptx::max3_nan(m, fabsf(v[c]), fabsf(v[c + 1]));
 #pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 1; o < LANES; o <<= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!live) return;
   if (slot < 0 || bad) return;
   const int64_t page = slot >> a.cache.page_shift;
@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
   }
   const int64_t in_page = slot & ((1 << a.cache.page_shift) - 1);
   const int64_t at = (((page * heads + h) << a.cache.page_shift) + in_page);
-  const bool zero = !(m >= kKv4Tiny);
-  const float inv = zero ? 0.0f : __fmul_rn(__frcp_rn(m), 7.0f);
+  const bool some = m >= kKv4Tiny && m < INFINITY;
+  const float inv = some ? __fmul_rn(__frcp_rn(m), 7.0f) : 0.0f;
   uint8_t* codes = (kind == 1 ? a.cache.k_codes : a.cache.v_codes) + at * (HD / 2) + e0 / 2;
   uint32_t packed[E / 4];
 #pragma unroll
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
     uint32_t b[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) b[k] = __float_as_uint(__fadd_rn(__fmul_rn(v[c + k], inv), kRowRoundMagic));
-    packed[c / 4] = (b[0] & 15u) | ((b[1] & 15u) << 4) | ((b[2] & 15u) << 8) | ((b[3] & 15u) << 12);
+    packed[c / 4] = some ? (b[0] & 15u) | ((b[1] & 15u) << 4) | ((b[2] & 15u) << 8) | ((b[3] & 15u) << 12) : 0u;
   }
   if constexpr (SPLIT) {
     *reinterpret_cast<uint32_t*>(codes) = packed[0] | (packed[1] << 16);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
   }
   if (l == 0) {
     float* scales = kind == 1 ? a.cache.k_scales : a.cache.v_scales;
-    scales[at] = zero ? 0.0f : __fmul_rn(m, rotate ? kStep : (float)(1.0 / 7.0));
+    scales[at] = some ? __fmul_rn(m, rotate ? kStep : (float)(1.0 / 7.0)) : m < kKv4Tiny ? 0.0f : NAN;
   }
 }
 
