@@ -458,7 +458,8 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives
  *   the same bits.
  *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
- *   q_start     device int32 [B + 1], ascending, within 0..T.  Rows outside every sequence stay as they were.
+ *   q_start     device int32 [B + 1], ascending, within 0..T (an entry outside counts as the nearer end).  Rows
+ *               outside every sequence stay as they were.
  *   seq_lens    device int32 [B];  block_table device int32 [B][table_width], table_width pages hold at most
  *               2^30 tokens.  Entries behind a sequence's last page, and those in front of the first page that a
  *               window leaves to its new tokens, may hold anything.  A listed page outside the cache counts as

@@ -107,8 +107,7 @@ struct Span {
 };
 __device__ __forceinline__ Span span_of(const Kv4AttnArgs& a, int b, bool report) {
   Span s;
-  s.q0 = max(0, a.q_start[b]);
-  s.qlen = min((int)a.T, a.q_start[b + 1]) - s.q0;
+  new_tokens(a.q_start, (int)a.T, b, s.q0, s.qlen);
   s.n = max(0, a.seq_lens[b]);
   const int64_t cap = (int64_t)a.table_width << a.cache.page_shift;
   if (s.n > cap) {

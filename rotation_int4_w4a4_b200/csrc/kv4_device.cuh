@@ -19,6 +19,12 @@ struct Partials {
   int chunk_len;  // tokens of a chunk
 };
 
+// Sequence b's new tokens, the first and how many: rows of the call, whatever q_start holds.
+__device__ __forceinline__ void new_tokens(const int32_t* q_start, int T, int b, int& q0, int& qlen) {
+  q0 = min(max(q_start[b], 0), T);
+  qlen = max(0, min(max(q_start[b + 1], 0), T) - q0);
+}
+
 // (x & mask) ^ flip in one instruction (of two constants the compiler would make two).
 __device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
   uint32_t y;

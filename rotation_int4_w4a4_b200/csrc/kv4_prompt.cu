@@ -129,10 +129,7 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     int q0 = 0, qlen = 0;
-    if (b < a.B) {
-      q0 = max(0, a.q_start[b]);
-      qlen = max(0, min((int)a.T, a.q_start[b + 1]) - q0);
-    }
+    if (b < a.B) new_tokens(a.q_start, (int)a.T, b, q0, qlen);
     const int tiles = (qlen * group + 2 * PT - 1) / (2 * PT);
     int upto = tiles;
 #pragma unroll

@@ -1,4 +1,4 @@
-"""Pages of a sequence that a sliding window has left behind, and lengths and starts at the ends of their types."""
+"""Pages of a sequence that a sliding window has left behind, and starts and bounds at the ends of their types."""
 import pytest
 import torch
 
@@ -27,3 +27,18 @@ def test_pages_before_the_window_are_not_looked_at(pq, q, n, max_len, page):
         pq.pq_kv4_attention(cache, Q, O, starts, lens, freed, q, max_len, window=window)
         pq.pq_check_status()
         assert torch.equal(O, want)
+
+
+@pytest.mark.parametrize("q,n", [(5, 300), (5, 2000), (200, 900)])
+@pytest.mark.parametrize("ends", [(2 ** 31 - 1, -2 ** 31), (-2 ** 31, -1), (2 ** 31 - 2, 2 ** 31 - 1), (-7, None), (0, 2 ** 31 - 1)])
+def test_starts_outside_the_rows(pq, q, n, ends):
+    """An entry of q_start outside 0..T counts as the nearer end: no row beyond Q is read or written."""
+    cache, Q, starts, lens, table = make_case(pq, n, [q], [n], 8, 2, 128, 16, poison=False)
+    want, O = torch.full_like(Q, 11.0), torch.full_like(Q, 11.0)
+    first, last = (min(max(q if x is None else x, 0), q) for x in ends)
+    if last > first:
+        pq.pq_kv4_attention(cache, Q, want, starts, lens, table, q, n)
+    ends = torch.tensor([q if x is None else x for x in ends], dtype=torch.int32, device="cuda")
+    pq.pq_kv4_attention(cache, Q, O, ends, lens, table, q, n)
+    assert torch.equal(O, want)
+    pq.pq_check_status()
