@@ -250,7 +250,7 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
     set_error("table_width=%lld pages must hold 1..2^30 tokens", (long long)table_width);
     return PQ_ERR_INVALID_ARG;
   }
-  if (max_q < 1 || max_len < 1 || max_len >= ((int64_t)1 << 31)) {
+  if (max_q < 1 || max_len < 1) {
     set_error("max_q=%lld and max_len=%lld must be >= 1", (long long)max_q, (long long)max_len);
     return PQ_ERR_INVALID_ARG;
   }
@@ -270,5 +270,6 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
   a.window = (int)std::min(window, kMaxTokens);          // a wider one hides nothing
   a.O = static_cast<uint16_t*>(O);
   a.ldo = ldo;
-  return kv4_attention_run(a, max_q, std::min(max_len, kMaxTokens), reinterpret_cast<cudaStream_t>(stream));
+  // Bounds beyond what a call can hold say no more than that (and would wrap when multiplied with the heads).
+  return kv4_attention_run(a, std::min(max_q, kMaxRows), std::min(max_len, kMaxTokens), reinterpret_cast<cudaStream_t>(stream));
 }

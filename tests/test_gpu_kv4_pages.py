@@ -42,3 +42,15 @@ def test_starts_outside_the_rows(pq, q, n, ends):
     pq.pq_kv4_attention(cache, Q, O, ends, lens, table, q, n)
     assert torch.equal(O, want)
     pq.pq_check_status()
+
+
+@pytest.mark.parametrize("q,n", [(1, 300), (1, 2000), (70, 900)])
+@pytest.mark.parametrize("max_q,max_len", [(2 ** 62, 2 ** 31), (2 ** 63 - 1, 2 ** 63 - 1), (2 ** 33, 2 ** 40), (1 << 24, 1 << 30)])
+def test_bounds_as_large_as_their_type(pq, q, n, max_q, max_len):
+    """Upper bounds that bound nothing: as many query rows and tokens as there can be."""
+    cache, Q, starts, lens, table = make_case(pq, n, [q], [n], 8, 2, 128, 16, poison=False)
+    want, O = torch.empty_like(Q), torch.empty_like(Q)
+    pq.pq_kv4_attention(cache, Q, want, starts, lens, table, 1 << 20, 1 << 30)
+    pq.pq_kv4_attention(cache, Q, O, starts, lens, table, max_q, max_len)
+    assert torch.equal(O, want)
+    pq.pq_check_status()
