@@ -451,8 +451,8 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *       row's largest such product if that is more (third item: 2^-18 of it);
  *     - queries, to fp16 relative to their row's largest channel: exact down to 2^-25 of it;
  *     - in calls with more than 32 query rows a sequence and key/value head, where all rows of a tile see 32
- *       tokens whose nonzero scales lie within a factor of 64: key and value codes times their scales, to fp16
- *       (2^-11; values twice).  Codes are exact otherwise.
+ *       tokens whose key scales (0 aside) lie within a factor of 64, and so their value scales: key and value codes
+ *       times their scales, to fp16 (2^-11; values twice).  Codes are exact otherwise.
  *   Scales may be negative.  A NaN or infinite scale, or a NaN query, reaches only the rows that see the token
  *   or own the query; what a row must not see may hold anything and changes no bit of it.
  *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives

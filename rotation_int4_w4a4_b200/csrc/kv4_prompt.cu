@@ -63,10 +63,10 @@ constexpr int SC_RING = 4;               // scale stages: a step's scales outliv
 constexpr uint64_t kPrWaitNs = 2000000000ull;
 constexpr uint32_t S_COL = 0, O_COL = 256;               // tensor memory: S_i at 128 i + 64 (half & 1), O_i at 256 + 128 i
 constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 65504) from which it is taken elsewhere
-// Scales are multiplied into the operands of 32 tokens whose nonzero scales (finite ones) lie within this factor, of the keys
-// and of the values.  The reference of such a step is its largest score plus the exponent of its largest value scale, which
-// may belong to another token: the largest product is then up to 2^6 below 1 and keeps 18 of fp16's 24 places below it.
-// Within the factor every operand is a normal fp16 number (of scales above 2^-100).
+// Scales are multiplied into the operands of 32 tokens whose key scales (0 aside) lie within this factor, and their value
+// scales (0 counts: such a token's score must not set the reference).  The reference of such a step is its largest score plus
+// the exponent of its largest value scale, which may belong to another token: the largest product is then up to 2^6 below 1
+// and keeps 18 of fp16's 24 places below it.  Within the factor every operand is a normal fp16 number (of scales above 2^-100).
 constexpr float kScaleSpread = 64.0f;
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
@@ -653,11 +653,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const uint32_t bits = __ballot_sync(0xffffffffu, at >= 0);
       const float km = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(ks))));
       const float vm = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(finite_or_0(vs))));
-      auto least = [](float x) {                         // smallest nonzero magnitude of the warp's finite scales
-        const float y = finite_or_0(x);
-        return __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(y == 0.0f ? INFINITY : y)));
-      };
-      const bool scaled = interior((j0 + j) * PT + 32 * wq) && km <= kScaleSpread * least(ks) && vm <= kScaleSpread * least(vs);
+      const float k1 = finite_or_0(ks);
+      const float k_least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(k1 == 0.0f ? INFINITY : k1)));
+      const float v_least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(finite_or_0(vs))));
+      const bool scaled = interior((j0 + j) * PT + 32 * wq) && km <= kScaleSpread * k_least && vm < kScaleSpread * v_least;
       const float ke = scale_exponent(km), ve = scale_exponent(vm);
       S.ks[sc][t] = scaled ? ex2(ke) : ks;
       S.vs[sc][t] = scaled ? ex2(ve) : vs;

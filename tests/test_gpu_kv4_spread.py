@@ -71,3 +71,16 @@ def test_one_token_of_another_scale(pq, q, n, js, value, key, rv):
         cache.tensors[1][page, :, place] *= key
         cache.tensors[3][page, :, place] *= value
     check(pq, (cache, Q, starts, lens, table), q, n)
+
+
+@pytest.mark.parametrize("rv", [False, True])
+@pytest.mark.parametrize("q,n,j0,step", [(1, 900, 3, 40), (140, 700, 3, 1000), (140, 700, 5, 97), (300, 1500, 0, 33), (64, 500, 0, 1)])
+def test_values_of_zero(pq, q, n, j0, step, rv):
+    """Tokens whose value is zero (scale 0) may take all of a row's probability but e^-40: the little that the other tokens
+    leave comes out as precisely as any output.  step 1: more than half of the tokens, whole blocks of 32 among them."""
+    cache, Q, starts, lens, table = make_case(pq, n + q, [q], [n], 8, 2, 128, 16, rv=rv, poison=False)
+    for j in range(j0, n if step > 1 else n * 2 // 3, step):
+        page, place = int(table[0, j // 16]), j % 16
+        cache.tensors[1][page, :, place] = 0.8
+        cache.tensors[3][page, :, place] = 0.0
+    check(pq, (cache, Q, starts, lens, table), q, n)
