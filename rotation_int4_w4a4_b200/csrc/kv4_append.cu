@@ -23,6 +23,7 @@
 
 #include "internal.h"
 #include "kv4.h"
+#include "nan_max.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -239,9 +240,9 @@ __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs 
   }
   float m = 0.0f;
 #pragma unroll
-  for (int c = 0; c < E; c += 2) m = ptx::max3_nan(m, fabsf(v[c]), fabsf(v[c + 1]));
+  for (int c = 0; c < E; c += 2) m = max3_nan(m, fabsf(v[c]), fabsf(v[c + 1]));
 #pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = 1; o < LANES; o <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (!live) return;
   if (slot < 0 || bad) return;
   const int64_t page = slot >> a.cache.page_shift;

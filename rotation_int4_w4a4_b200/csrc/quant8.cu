@@ -16,6 +16,7 @@
 #include <cstdint>
 
 #include "internal.h"
+#include "nan_max.cuh"
 #include "ptx.cuh"
 #include "rows.cuh"
 
@@ -114,12 +115,12 @@ __global__ void __launch_bounds__(1024) quant_rows8_kernel(const uint16_t* __res
     for (int s = 0; s < SLOTS; ++s)
 #pragma unroll
       for (int i = 0; i < 8; i += 4) {
-        m = ptx::max3_nan(m, fabsf(v[s][i]), fabsf(v[s][i + 1]));
-        m2 = ptx::max3_nan(m2, fabsf(v[s][i + 2]), fabsf(v[s][i + 3]));
+        m = max3_nan(m, fabsf(v[s][i]), fabsf(v[s][i + 1]));
+        m2 = max3_nan(m2, fabsf(v[s][i + 2]), fabsf(v[s][i + 3]));
       }
-    m = ptx::max_nan(m, m2);
+    m = max_nan(m, m2);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (tpr > 32) {                                        // the same for the whole block
       // two buffers: a round's maxima are read before the round after next overwrites them
       float* buf = red[round & 1];
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(1024) quant_rows8_kernel(const uint16_t* __res
       __syncthreads();
       m = lane < tpr / 32 ? buf[sub * (tpr / 32) + lane] : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = ptx::max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
     }
     if (!live) continue;
     const float inv = m >= kQ8Tiny && m < INFINITY ? 127.0f / m : 0.0f;
