@@ -308,13 +308,13 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) page_of[i] = tok0 + 16 * i < n ? __ldg(table + ((tok0 + 16 * i) >> ps)) : 0;
     };
-    // Pieces in front of what the tile sees (a window's older pages may be anyone's by now) are not looked at.
-    auto locate = [&](int tok0) {
-      all = tok0 + AT_BLOCK <= n && tok0 + 16 > c_lo;
+    // Pieces in front of token `from` are not looked at: a window's older pages may be anyone's by now.
+    auto locate = [&](int tok0, int from) {
+      all = tok0 + AT_BLOCK <= n && tok0 + 16 > from;
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
         const int tok = tok0 + 16 * i;
-        int k = tok + 16 > c_lo ? min(16, n - tok) : 0;
+        int k = tok + 16 > from ? min(16, n - tok) : 0;
         uint32_t at = 0;
         if (k > 0) {
           const int page = page_of[i];
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     const int first = (c_lo & ~(AT_BLOCK - 1)) + AT_BLOCK * warp;
     if (first < c_hi) {
       look_up(first);
-      locate(first);
+      locate(first, c_lo);
       load_k();
       load_v(vx, vs);
       look_up(first + AT_BLOCK * AT_WARPS);
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
       uint32_t vn[AT_TILES][4][VW];
       float vsn[AT_TILES][2];
       if (next < c_hi) {
-        locate(next);
+        locate(next, next);
         load_k();
         load_v(vn, vsn);
         look_up(next + AT_BLOCK * AT_WARPS);
