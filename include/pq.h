@@ -361,10 +361,10 @@ pq_status pq_quant_rows8(const void* X, int64_t T, int64_t D, int64_t ldx, int g
  *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense.  No scratch, one launch.
  *
  * pq_w8a8_linear — pq_quant_rows8(X, T, D, ldx, g, codes_A, scales_A) followed by pq_w8a8_gemm, in one
- *   call; up to about 40 output tiles of 256 x 256 the product is launched as a programmatic dependent and
- *   its first weight loads overlap the quantisation.  codes_A and scales_A are caller-owned and written.  codes_W and scales_W must be
- *   complete when the call is made (written by work enqueued on `stream` before it, or earlier); Y
- *   must not overlap X, codes_A or scales_A.
+ *   call.  With T <= 128, or fewer output tiles of 256 x 256 than three quarters of the device's pairs of SMs, the
+ *   product is launched as a programmatic dependent and its first weight loads overlap the quantisation.  codes_A
+ *   and scales_A are caller-owned and written.  codes_W and scales_W must be complete when the call is made
+ *   (written by work enqueued on `stream` before it, or earlier); Y must not overlap X, codes_A or scales_A.
  */
 pq_status pq_w8a8_gemm(const int8_t* codes_A, const float* scales_A, const int8_t* codes_W, const float* scales_W,
                        int64_t T, int64_t N, int64_t D, void* Y, pq_out_dtype out_dtype, void* stream);
@@ -457,6 +457,9 @@ pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots, int64_t T
  *   or own the query; what a row must not see may hold anything and changes no bit of it.
  *   How far a call's other sequences cut a row's tokens into pieces may change its last bits; the same call gives
  *   the same bits.
+ *   max_q chooses one kernel for the whole call: beyond 32 query rows a key/value head, a sequence of one token takes
+ *   a block of 256 rows like any other.  Steps of single tokens and chunks of prompts are faster as two calls (63
+ *   tokens over up to 8192 and a chunk of 512 over 4096, 32 + 8 heads of 128: 323 us in one, 88 and 60 apart).
  *   Q           device bf16 [T][heads_q][head_dim], row stride ldq (a multiple of 8), as Q_out above.
  *   q_start     device int32 [B + 1], ascending, within 0..T (an entry outside counts as the nearer end).  Rows
  *               outside every sequence stay as they were.

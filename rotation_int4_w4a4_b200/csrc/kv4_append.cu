@@ -83,7 +83,7 @@ __device__ __forceinline__ void ap_turn(float* a, float* b, const float* cos, co
 // E = 16: 8 channels of each half of the head.  The pairs of a position rotation of the whole head then meet inside a
 // thread, loads and stores cover 128 contiguous bytes of a head, and shuffles and reductions are shared by four times
 // the channels (8192 tokens of 32 + 8 + 8 heads of 128: 66 us, 3.0 TB/s of the copy's 6.55, the L1 pipe that carries loads,
-// stores and shuffles bounding it; 95 us with 4 channels a lane everywhere).
+// stores and shuffles bounding it, 24 bytes of spills a thread among them; 95 us with 4 channels a lane everywhere).
 // E = 4: any layout of the rotation (halves that do not fall on multiples of 8 channels, or cross the middle).
 template <int HD, int E, bool WIDE>
 __global__ void __launch_bounds__(512, 3) kv4_append_kernel(const Kv4AppendArgs a) {

@@ -7,9 +7,10 @@
 // the codes themselves; ks multiplies the finished dot product and vs the probability, both in float32.
 //
 // The cache is read once for all query rows of a key/value head (the group's heads x the sequence's new tokens), 64
-// bytes a token for keys and as much for values.  Bytes are the floor; the unpacking bounds it (about 650 instructions for
-// 32 tokens of a head of 128: ALU pipe 58%, issue 56%; the same time with all pages in L2, and with 16 warps an SM).
-// 256 users of 4096 tokens: 295 us, 60% of the copy's bandwidth; 64 of up to 8192: 74; one of 65536: 33.
+// bytes a token for keys and as much for values.  Bytes are the floor.  Above it lie the instructions (about 650 for 32
+// tokens of a head of 128), but no pipe is full: ALU 58%, issue 55%, DRAM 47%; a quarter of a warp's time is fixed latencies,
+// a fifth its own issue, an eighth each memory, a busy pipe and other warps' turns.  The same time with all pages in L2, and
+// with 16 warps an SM.  256 users of 4096 tokens: 287 us, 61% of the copy's bandwidth; 64 of up to 8192: 74; one of 65536: 33.
 // A warp owns blocks of 32 tokens:
 //   - keys are the A operand (16 tokens x 16 channels), the query rows the 8-column B operand: a thread's 16-byte
 //     load of one token is its share of the A operands of all 8 channel steps, because the channels of a dot product
@@ -50,8 +51,10 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_BLOCK = 32;            // tokens a warp takes at a time
 constexpr int AT_TILES = AT_BLOCK / 16;
 // Up to so many query rows a key/value head and sequence this kernel takes the call, beyond them the one of kv4_prompt.cu,
-// whose tiles have 128 rows (us, this against that; 2048 tokens, 4 heads a key/value head of 128): 64 sequences of 32
-// rows 133 : 156, of 64 rows 240 : 156; 8 of 64 rows 42 : 39.  (One sequence of 64 rows over 8192: 29 : 39.)
+// whose tiles have 128 rows (us, this against that; 8 key/value heads of 128, the same for 1, 4 and 8 heads of queries on
+// each).  64 sequences over 2048 tokens: 32 rows 137 : 162, 48 rows 192 : 162.  16 over 300: 32 rows 14 : 18, 48 rows 25 : 18.
+// Where that kernel's tiles are few it comes later: 8 over 2048, 64 rows 42 : 51, 96 rows 56 : 37; one over 8192, 64 rows
+// 29 : 29; one over 1024, 96 rows 19 : 24.
 constexpr int64_t kPromptRows = 32;
 constexpr float kRowsTop = 16384.0f;    // a product of probability and value scale from which the reference is raised (fp16: 65504)
 // A nibble alone in the low bits of an fp16 is n 2^-24, below the normal range (matrix instructions take those at full
@@ -825,9 +828,11 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
                      "kv4_join_kernel launch");
     }
   } else {
-    // Up to 640 tokens one block an item is enough: a second kernel and its workspace cost the host more than the shares
-    // save (517 tokens: 8.2 us on the device against 7.5, 10 us a call against 14).  Otherwise as many shares as blocks run
-    // at once.
+    // Up to 640 tokens one block an item, otherwise as many shares as blocks run at once: a second kernel and its workspace
+    // cost more than shares of short sequences save (us on the device, one block against shares; 8 key/value heads of 128).
+    // One sequence: 512 tokens 8.8 : 14.8, 1024 12.3 : 13.8, 1536 15.7 : 12.4, 2048 19.4 : 12.5.  64 of up to: 512 tokens
+    // 15.3 : 21.0, 1024 24.5 : 27.1, 2048 35.5 : 35.2.  (A host that launches call by call sees 3 to 6 us more between them.)
+    // The sides meet between 1000 and 2000 tokens, so calls from 641 to there take up to 5 us longer than they need.
     const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
     Shares shares = {};
     if (max_len > 640 && a.B <= AT_SEQS) {

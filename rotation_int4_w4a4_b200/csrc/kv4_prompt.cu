@@ -19,9 +19,10 @@
 //                      row's P would outgrow fp16; at the end its output row.
 //   warps 12..15       producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
-// No register of a half step may spill: the operands leave so little of the L1 cache that it would come back from L2 (with
-// the next half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).
-// 4096 of 8192 tokens, 32 + 8 heads of 128: 496 us, 51% of the library's bf16 rate; a half step takes 2300 cycles, of which
+// Spills in a half step cost much: the operands leave so little of the L1 cache that they come back from L2 (with the next
+// half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).  The compiler reports 40 bytes of stores and 84 of
+// loads (heads of 64: 28 and 56); which code they belong to is not known.
+// 4096 of 8192 tokens, 32 + 8 heads of 128: 505 us, 51% of the library's bf16 rate; a half step takes 2300 cycles, of which
 // the matrix instructions need 1400 and the exponentials 1000: the chain scores -> exponentials -> P -> product -> next
 // scores bounds it, with 10% of the SMs' time idle behind the last blocks.
 //

@@ -183,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) w8a8_p
       const int n = (u % m_tiles) * 2 * PM + PM * rank + 32 * sub + lane;       // this thread's channel
       const int t0 = (u / m_tiles) * PN + P_EPI_COLS * half;
       const float sw = n < N ? __ldg(scales_W + n) : 0.0f;
-      // The token scales of this half (its four warps write and read their own copy of 32 each).
+      // The token scales of this half, 4 a lane; the epilogue shuffles them out.
       float sa_l[P_EPI_COLS / 32];
 #pragma unroll
       for (int i = 0; i < P_EPI_COLS / 32; ++i) sa_l[i] = t0 + 32 * i + lane < T ? __ldg(scales_A + t0 + 32 * i + lane) : 0.0f;
@@ -492,8 +492,9 @@ pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t
     cfg.blockDim = dim3(P_THREADS, 1, 1);
     cfg.dynamicSmemBytes = kPairSmem;
     cfg.stream = stream;
-    // Never as a programmatic dependent: CTAs that fill an SM would wait there while the quantisation still needs it
-    // (8192 x 4096 x 14336: 466 us so, 423 us one after the other).
+    // Not a programmatic dependent: its CTAs fill an SM and would wait there for the quantisation, with nothing to load
+    // meanwhile but the first weights (measured with a plain wait at the start, in a graph, so against one after the other:
+    // 8192 x 4096 x 14336 413 : 416 us, 4096 x 4096 x 4096 105 : 106, 512 x 14336 x 4096 40 : 41).
     return cuda_fail(cudaLaunchKernelEx(&cfg, w8a8_pair_kernel, tmW, tmA, scales_A, scales_W, Y, (int)T, (int)N, steps,
                                         (int)pair_m, (int)pair_tiles, bf16, status),
                      "w8a8_pair_kernel launch");
