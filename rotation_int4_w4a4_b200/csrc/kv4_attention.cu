@@ -795,8 +795,14 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   auto workspace = [&](size_t rows, size_t extra, float** o, float2** ml) {
     const size_t bytes = rows * (a.cache.head_dim * sizeof(float) + sizeof(float2)) + extra;
     cudaMemPool_t pool = nullptr;
-    cudaError_t e = scratch_pool(&pool);
+    // A device's first call makes the pool, which a thread that captures may do in relaxed mode only (it is no work on a stream).
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return cuda_fail(e, "capture mode");
+    e = scratch_pool(&pool);
+    const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return cuda_fail(e, "scratch memory pool");
+    if (back != cudaSuccess) return cuda_fail(back, "capture mode");
     e = cudaMallocFromPoolAsync(&ws, bytes, pool, stream);
     if (e != cudaSuccess) {
       set_error("cudaMallocFromPoolAsync(%zu bytes of attention workspace): %s", bytes, cudaGetErrorString(e));
