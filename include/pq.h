@@ -340,7 +340,8 @@ pq_status pq_w4a4_gemm_launch_count_g(int64_t T, int64_t N, int64_t D, int g, in
  *
  * pq_quant_rows8 — rows of bf16 to signed 8-bit codes, activations and weights alike:
  *   y = x H_g / sqrt(g) per block of g channels (g = 64, 128, 256; g = 0: y = x), scales[t] =
- *   max|y[t]| / 127 over the whole row, codes = RNE(y / scale) in -127..127.  A row whose maximum is
+ *   max|y[t]| / 127 over the whole row, codes = RNE(y / scale) in -127..127 (in float32, as y * (127 / max): a
+ *   quotient a few units in the last place from a half-integer may go either way).  A row whose maximum is
  *   below 1e-36 counts as zero (scale 0, codes 0); one with a NaN or an infinity (after the rotation too) gets
  *   scale NaN and codes 0, so that all that is made of it is NaN.  H is symmetric, so rotated activations against
  *   weights rotated with the same g leave the product unchanged before quantisation.
