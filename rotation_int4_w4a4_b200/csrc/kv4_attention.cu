@@ -837,7 +837,7 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     // Up to 640 tokens one block an item, otherwise as many shares as blocks run at once: a second kernel and its workspace
     // cost more than shares of short sequences save (us on the device, one block against shares; 8 key/value heads of 128).
     // One sequence: 512 tokens 8.8 : 14.8, 1024 12.3 : 13.8, 1536 15.7 : 12.4, 2048 19.4 : 12.5.  64 of up to: 512 tokens
-    // 15.3 : 21.0, 1024 24.5 : 27.1, 2048 35.5 : 35.2.  (A host that launches call by call sees 3 to 6 us more between them.)
+    // 15.3 : 21.0, 1024 24.5 : 27.1, 2048 35.5 : 35.2.  (Call by call the host adds 1 to 2 us to the shares.)
     // The sides meet between 1000 and 2000 tokens, so calls from 641 to there take up to 5 us longer than they need.
     const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
     Shares shares = {};

@@ -68,6 +68,7 @@ constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 
 // scales (0 counts: such a token's score must not set the reference).  The reference of such a step is its largest score plus
 // the exponent of its largest value scale, which may belong to another token: the largest product is then up to 2^6 below 1
 // and keeps 18 of fp16's 24 places below it.  Within the factor every operand is a normal fp16 number (of scales above 2^-100).
+// 4096 of 8192 tokens: 478 us with every step so, 482 where the first 64 tokens differ by more, 696 where all do.
 constexpr float kScaleSpread = 64.0f;
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
