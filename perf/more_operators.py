@@ -153,18 +153,18 @@ def _prepare_fp4(case, seed):
     T, N, D, fmt = case["T"], case["N"], case["D"], case["fmt"]
     x = _normal(gen, T, D)
     x[:, torch.randperm(D, generator=gen, device=DEV)[:8]] *= 30.0   # outlier channels, as activations have them
-    st = {"X": x.to(torch.bfloat16), "scale_A": 1.0, "scale_W": 1.0}
+    st = {"X": x.to(torch.bfloat16), "factor_A": 1.0, "factor_W": 1.0}
     w = _normal(gen, N, D) * 0.02
     if fmt == "nv":                                  # factors of the tensors, as a calibration leaves them
-        st["scale_A"] = float(torch.tensor(128.0 / (6 * 448), dtype=torch.float32))
-        st["scale_W"] = float(torch.tensor(0.12 / (6 * 448), dtype=torch.float32))
+        st["factor_A"] = float(torch.tensor(128.0 / (6 * 448), dtype=torch.float32))
+        st["factor_W"] = float(torch.tensor(0.12 / (6 * 448), dtype=torch.float32))
     if case["quantised"]:
-        st["codes_A"], s = _quantise(st["X"].float(), fmt, 1.0, st["scale_A"])
+        st["codes_A"], s = _quantise(st["X"].float(), fmt, 1.0, st["factor_A"])
         st["scales_A"] = _place_scales(s)
     else:                                            # written by the call
         st["codes_A"] = torch.empty(T, D // 2, dtype=torch.uint8, device=DEV)
         st["scales_A"] = torch.empty(_scale_bytes(T, D // BLOCK[fmt]), dtype=torch.uint8, device=DEV)
-    st["codes_W"], s = _quantise(w, fmt, 1.0, st["scale_W"])
+    st["codes_W"], s = _quantise(w, fmt, 1.0, st["factor_W"])
     st["scales_W"] = _place_scales(s)
     st["Y"] = torch.empty(T, N, dtype=torch.bfloat16 if case["out"] == "bf16" else torch.float32, device=DEV)
     return st
@@ -268,10 +268,10 @@ def _plain_fp4(st):
         y = st["X"].float()
         if g:
             y = _hadamard_tree(y.reshape(T, -1, g)).reshape(T, D)
-        codes, s = _quantise(y, fmt, 1 / math.sqrt(g) if g else 1.0, st["scale_A"])
+        codes, s = _quantise(y, fmt, 1 / math.sqrt(g) if g else 1.0, st["factor_A"])
         a = _values(codes, _place_scales(s), fmt, T, D, torch.float32)
     w = _values(st["codes_W"], st["scales_W"], fmt, N, D, torch.float32)
-    return ((a @ w.t()) * (st["scale_A"] * st["scale_W"])).to(st["Y"].dtype)
+    return ((a @ w.t()) * (st["factor_A"] * st["factor_W"])).to(st["Y"].dtype)
 
 
 def _cached(st, kv, b):
@@ -338,10 +338,10 @@ def _own_run(st):
     if c["op"] == "fp4":
         if c["quantised"]:
             pq.pq_fp4_gemm(st["codes_A"], st["scales_A"], st["codes_W"], st["scales_W"], st["Y"], fmt=c["fmt"],
-                           alpha=st["scale_A"] * st["scale_W"])
+                           alpha=st["factor_A"] * st["factor_W"])
         else:
             pq.pq_fp4_linear(st["X"], st["codes_A"], st["scales_A"], st["codes_W"], st["scales_W"], st["Y"], fmt=c["fmt"],
-                             g=c["g"], scale_A=st["scale_A"], scale_W=st["scale_W"])
+                             g=c["g"], factor_A=st["factor_A"], factor_W=st["factor_W"])
         return st["Y"]
     pq.pq_kv4_attention_masked(_own_cache(st, pq), st["Q"], st["O"], st["q_start"], st["seq_lens"], st["table"],
                                max_q=st["max_q"], max_len=st["max_len"], scale=1 / math.sqrt(c["hd"]), window=c["window"],
@@ -411,9 +411,9 @@ def _exact_fp4(st):
         a = st["X"].double()
         if c["g"]:
             a = (a.reshape(-1, c["g"]) @ _hadamard_matrix(c["g"])).reshape(T, D)
-        a = _exact_rows(a, fmt, st["scale_A"])
+        a = _exact_rows(a, fmt, st["factor_A"])
     w = _values(st["codes_W"], st["scales_W"], fmt, N, D, torch.float64)
-    return (a @ w.t()) * (st["scale_A"] * st["scale_W"])
+    return (a @ w.t()) * (st["factor_A"] * st["factor_W"])
 
 
 def _exact_attention(st):
