@@ -38,29 +38,29 @@ def _attend(name, op, B, q, ctx, ragged, hq, hkv, hd, page, window, sinks, rotat
 def listed():
     return [
         # One token through a 4096 x 4096 projection: generation for one user, where latency counts.
-        _fp4("fp4 linear, 1 token", 1, 4096, 4096, 128, "nv", "bf16", False),
+        _fp4("fp4 linear 1 token", 1, 4096, 4096, 128, "nv", "bf16", False),
         # A decode batch through the up projection of the LLaMA-3-8B shape.
-        _fp4("fp4 linear, 64 tokens", 64, 14336, 4096, 128, "mx", "bf16", False),
+        _fp4("fp4 linear 64 tokens", 64, 14336, 4096, 128, "mx", "bf16", False),
         # Odd sizes: a short prompt, a head of 1003 outputs, a reduction that fills no whole tile.
-        _fp4("fp4 product, odd sizes", 391, 1003, 4192, 0, "nv", "f32", True),
+        _fp4("fp4 product odd sizes", 391, 1003, 4192, 0, "nv", "f32", True),
         # A prompt of 2048 tokens through the query projection of the LLaMA-3-8B shape.
-        _fp4("fp4 linear, 2048 tokens", 2048, 4096, 4096, 64, "mx", "bf16", False),
+        _fp4("fp4 linear 2048 tokens", 2048, 4096, 4096, 64, "mx", "bf16", False),
         # The down projection of the LLaMA-3-8B shape over a long prompt.
-        _fp4("fp4 linear, down projection", 8192, 4096, 14336, 128, "nv", "bf16", False),
+        _fp4("fp4 linear down projection", 8192, 4096, 14336, 128, "nv", "bf16", False),
         # One user, a short context, a tree of 8 drafted tokens: the smallest verification step.
-        _attend("tree, 8 drafts over 1029", "tree", 1, 8, 1029, False, 32, 8, 128, 64, 0, 0, True),
+        _attend("tree 8 drafts over 1029", "tree", 1, 8, 1029, False, 32, 8, 128, 64, 0, 0, True),
         # A verification step of 16 users over ragged contexts, some of them empty, with trees of up to 61 drafts.
-        _attend("tree, 16 users, 61 drafts", "tree", 16, 61, 8192, True, 32, 8, 128, 64, 0, 0, True),
+        _attend("tree 16 users 61 drafts", "tree", 16, 61, 8192, True, 32, 8, 128, 64, 0, 0, True),
         # Heads of 64 in groups of 7, trees under a window with sinks.
-        _attend("tree, window and sinks", "tree", 5, 25, 2999, True, 14, 2, 64, 16, 512, 4, False),
+        _attend("tree window and sinks", "tree", 5, 25, 2999, True, 14, 2, 64, 16, 512, 4, False),
         # One user, a long conversation through a window with sinks: the smallest step of that kind.
-        _attend("sinks, 1 token over 65536", "sinks", 1, 1, 65536, False, 32, 8, 128, 64, 4096, 4, True),
+        _attend("sinks 1 token over 65536", "sinks", 1, 1, 65536, False, 32, 8, 128, 64, 4096, 4, True),
         # A decode batch over ragged contexts, some of them empty.
-        _attend("sinks, 64 users, ragged", "sinks", 64, 1, 8192, True, 32, 8, 128, 64, 1024, 100, True),
+        _attend("sinks 64 users ragged", "sinks", 64, 1, 8192, True, 32, 8, 128, 64, 1024, 100, True),
         # Ragged chunks of prompts over earlier context, heads of 64 in groups of 7.
-        _attend("sinks, ragged chunks", "sinks", 6, 801, 2999, True, 14, 2, 64, 16, 700, 5, False),
+        _attend("sinks ragged chunks", "sinks", 6, 801, 2999, True, 14, 2, 64, 16, 700, 5, False),
         # The second half of a prompt of 8192 tokens.
-        _attend("sinks, 4096 of 8192 tokens", "sinks", 1, 4096, 8192, False, 32, 8, 128, 64, 2048, 16, True),
+        _attend("sinks 4096 of 8192 tokens", "sinks", 1, 4096, 8192, False, 32, 8, 128, 64, 2048, 16, True),
     ]
 
 
