@@ -374,6 +374,56 @@ pq_status pq_w8a8_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g
                          void* stream);
 
 /*
+ * 4-bit floating point with one scale a block of channels ("microscaled"): codes are E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives), two a byte, the even channel in the low nibble; the tensor cores multiply codes and scales.
+ *   PQ_FP4_MX  blocks of 32 channels, scales E8M0 (2^(byte - 127); 255 is NaN).
+ *   PQ_FP4_NV  blocks of 16 channels, scales E4M3 (up to 448; 127 is NaN), and one factor a tensor outside them.
+ * Scales lie in pieces of 512 bytes, each 128 rows x 4 blocks: the byte of row r and block b is at
+ *   ((r / 128) * pieces + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4,   pieces = ceil(ceil(D / block) / 4),
+ * which is how tensor memory takes them.  pq_fp4_scale_bytes gives a buffer's size.  Bytes of rows past the last may hold
+ * anything; blocks past the last, in a row's last four bytes, are written as 0 by pq_quant_fp4 (and must not be NaN).
+ *
+ * pq_quant_fp4 — rows of bf16 to codes and scales, activations and weights alike:
+ *   y = x H_g / sqrt(g) per block of g channels (g = 64, 128, 256; g = 0: y = x), m = max|y| over a block of channels,
+ *   MX: scale = 2^(floor(log2 m) - 2) (the shared exponent of the OCP microscaling formats, version 1.0), codes =
+ *       E2M1(y / scale); blocks with m < 2^-100 count as zero.
+ *   NV: scale = E4M3(m / (6 factor)), codes = E2M1(y / (scale factor)); a block whose scale rounds to 0 gets codes 0, and
+ *       scales stop at 448: with factor = max|y| / (6 * 448) over the tensor (or a calibrated bound) nothing is cut off.
+ *   E2M1 and E4M3 round to nearest, ties to even; magnitudes above 6 become 6.  In float32, as y * (1 / scale): a quotient a
+ *   few units in the last place from a border may go either way.  A block with a NaN or an infinity (after the rotation
+ *   too) gets scale NaN and codes 0, so that all that is made of it is NaN.
+ *   X       device bf16 [T][ldx] (first D columns used), ldx >= D, ldx % 8 == 0.
+ *   D       32..65536, a multiple of 32 and of g.  T 1..2^24.
+ *   factor  NV: 2^-100..2^100.  MX: ignored.
+ *   codes   device uint8 [T][D / 2], dense;  scales device, as above.  All 16-byte aligned; no overlap.
+ *
+ * pq_fp4_gemm — Y[t][n] = alpha * sum_b sa[t][b] sw[n][b] sum_(k in block b) qa[t][k] qw[n][k], products exact, summed in
+ *   float32 by the tensor cores (in ranges of the reduction that are added in float32 in their order), multiplied with alpha
+ *   in float32 and stored.  alpha: any finite number; NV: the product of the two tensors' factors belongs into it.
+ *   codes_A [T][D / 2], codes_W [N][D / 2], scales_A, scales_W as written by pq_quant_fp4 with the same format.  T, N in
+ *   1..2^24 (no multiple is asked), D as above.  A NaN scale reaches its own row or column only.  The same call gives the
+ *   same bits.
+ *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense, 16-byte aligned.  No scratch, one launch.
+ *
+ * pq_fp4_linear — pq_quant_fp4(X, T, D, ldx, g, format, factor_A, codes_A, scales_A) followed by pq_fp4_gemm with alpha =
+ *   factor_A * factor_W (NV; MX: 1), in one call.  codes_A and scales_A are caller-owned and written.  With few output
+ *   tiles the product is launched as a programmatic dependent and its first weight loads overlap the quantisation:
+ *   codes_W and scales_W must be complete when the call is made (written by work enqueued on `stream` before it, or
+ *   earlier); Y must not overlap X, codes_A or scales_A.
+ */
+typedef enum { PQ_FP4_MX = 0, PQ_FP4_NV = 1 } pq_fp4_format;
+/* Bytes of the scales of `rows` rows of D channels (host only; 0 for sizes or a format that the calls refuse). */
+int64_t pq_fp4_scale_bytes(int64_t rows, int64_t D, pq_fp4_format format);
+pq_status pq_quant_fp4(const void* X, int64_t T, int64_t D, int64_t ldx, int g, pq_fp4_format format, float factor,
+                       uint8_t* codes, uint8_t* scales, void* stream);
+pq_status pq_fp4_gemm(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W,
+                      int64_t T, int64_t N, int64_t D, pq_fp4_format format, float alpha, void* Y,
+                      pq_out_dtype out_dtype, void* stream);
+pq_status pq_fp4_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g, pq_fp4_format format, float factor_A,
+                        uint8_t* codes_A, uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W,
+                        float factor_W, int64_t N, void* Y, pq_out_dtype out_dtype, void* stream);
+
+/*
  * The cache of keys and values in 4 bits (RRS page, set-up of the experiments: the cache quantised in
  * groups of 128, here one group per head), in pages:
  *   k_codes, v_codes    device uint8 [pages][heads][page_size][head_dim / 2], nibbles as everywhere.

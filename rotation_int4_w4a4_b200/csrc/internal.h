@@ -212,6 +212,13 @@ cudaError_t launch_quant_rows8(const void* X, int64_t rows, int D, int64_t ldx, 
 pq_status w8a8_launch(const int8_t* codes_A, const float* scales_A, const int8_t* codes_W, const float* scales_W,
                       int64_t T, int64_t N, int64_t D, void* Y, pq_out_dtype out_dtype, cudaStream_t stream,
                       bool pdl);
+// E2M1 codes with one scale a block of channels (quant_fp4.cu; nv: blocks of 16, otherwise 32) and their product (fp4.cu);
+// pdl as above.
+cudaError_t launch_quant_fp4(const void* X, int64_t rows, int D, int64_t ldx, int g, bool nv, float factor, uint8_t* codes,
+                             uint8_t* scales, cudaStream_t stream);
+pq_status fp4_launch(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W,
+                     int64_t T, int64_t N, int64_t D, bool nv, float alpha, void* Y, pq_out_dtype out_dtype,
+                     cudaStream_t stream, bool pdl);
 // Launches the bounded-wait diagnostic (a wait that cannot complete, limited to limit_ns).
 pq_status gemm_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream);
 // Device address of the GEMM's status word on the current device.

@@ -1,4 +1,4 @@
-// Argument checks and dispatch of the 8-bit product and of the 4-bit key/value cache.
+// Argument checks and dispatch of the 8-bit and 4-bit floating-point products and of the 4-bit key/value cache.
 #include <algorithm>
 #include <cmath>
 
@@ -53,6 +53,60 @@ pq_status check_gemm8(const int8_t* codes_A, const float* scales_A, const int8_t
     return PQ_ERR_INVALID_ARG;
   }
   if (out_dtype != PQ_OUT_F32 && out_dtype != PQ_OUT_BF16) { set_error("bad out_dtype"); return PQ_ERR_INVALID_ARG; }
+  if (!aligned16(codes_A) || !aligned16(scales_A) || !aligned16(codes_W) || !aligned16(scales_W) || !aligned16(Y)) {
+    set_error("device pointers must be 16-byte aligned");
+    return PQ_ERR_INVALID_ARG;
+  }
+  return PQ_OK;
+}
+
+pq_status check_fp4(int64_t T, int64_t D, pq_fp4_format format) {
+  if (format != PQ_FP4_MX && format != PQ_FP4_NV) { set_error("bad format %d", (int)format); return PQ_ERR_INVALID_ARG; }
+  if (T < 1 || T > kMaxRows) { set_error("T=%lld must be in 1..2^24", (long long)T); return PQ_ERR_INVALID_ARG; }
+  if (D < 32 || D > kMaxD8 || D % 32 != 0) {
+    set_error("D=%lld must be in 32..65536 and a multiple of 32", (long long)D);
+    return PQ_ERR_INVALID_ARG;
+  }
+  return PQ_OK;
+}
+
+pq_status check_quant_fp4(const void* X, int64_t T, int64_t D, int64_t ldx, int g, pq_fp4_format format, float factor,
+                          const uint8_t* codes, const uint8_t* scales) {
+  if (!X || !codes || !scales) { set_error("X, codes and scales must be non-NULL"); return PQ_ERR_INVALID_ARG; }
+  if (g != 0 && g != 64 && g != 128 && g != 256) {
+    set_error("g=%d: rows are rotated in blocks of 64, 128 or 256 (or not, g = 0)", g);
+    return PQ_ERR_UNSUPPORTED;
+  }
+  const pq_status st = check_fp4(T, D, format);
+  if (st != PQ_OK) return st;
+  if (g && D % g != 0) { set_error("D=%lld must be a multiple of g=%d", (long long)D, g); return PQ_ERR_INVALID_ARG; }
+  if (ldx < D || ldx % 8 != 0) {
+    set_error("ldx=%lld must be >= D=%lld and a multiple of 8", (long long)ldx, (long long)D);
+    return PQ_ERR_INVALID_ARG;
+  }
+  if (format == PQ_FP4_NV && !(factor >= 0x1p-100f && factor <= 0x1p100f)) {
+    set_error("factor=%g must be in 2^-100..2^100", (double)factor);
+    return PQ_ERR_INVALID_ARG;
+  }
+  if (!aligned16(X) || !aligned16(codes) || !aligned16(scales)) {
+    set_error("device pointers must be 16-byte aligned");
+    return PQ_ERR_INVALID_ARG;
+  }
+  return PQ_OK;
+}
+
+pq_status check_gemm_fp4(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W,
+                         int64_t T, int64_t N, int64_t D, pq_fp4_format format, float alpha, const void* Y,
+                         pq_out_dtype out_dtype) {
+  if (!codes_A || !scales_A || !codes_W || !scales_W || !Y) {
+    set_error("all tensor pointers must be non-NULL");
+    return PQ_ERR_INVALID_ARG;
+  }
+  const pq_status st = check_fp4(T, D, format);
+  if (st != PQ_OK) return st;
+  if (N < 1 || N > kMaxRows) { set_error("N=%lld must be in 1..2^24", (long long)N); return PQ_ERR_INVALID_ARG; }
+  if (out_dtype != PQ_OUT_F32 && out_dtype != PQ_OUT_BF16) { set_error("bad out_dtype"); return PQ_ERR_INVALID_ARG; }
+  if (!std::isfinite(alpha)) { set_error("alpha must be finite"); return PQ_ERR_INVALID_ARG; }
   if (!aligned16(codes_A) || !aligned16(scales_A) || !aligned16(codes_W) || !aligned16(scales_W) || !aligned16(Y)) {
     set_error("device pointers must be 16-byte aligned");
     return PQ_ERR_INVALID_ARG;
@@ -147,6 +201,51 @@ extern "C" pq_status pq_w8a8_linear(const void* X, int64_t T, int64_t D, int64_t
   st = cuda_fail(launch_quant_rows8(X, T, (int)D, ldx, g, codes_A, scales_A, s), "pq_w8a8_linear quantisation launch");
   if (st != PQ_OK) return st;
   return w8a8_launch(codes_A, scales_A, codes_W, scales_W, T, N, D, Y, out_dtype, s, /*pdl=*/true);
+}
+
+extern "C" int64_t pq_fp4_scale_bytes(int64_t rows, int64_t D, pq_fp4_format format) {
+  clear_error();
+  if (check_fp4(rows, D, format) != PQ_OK) return 0;
+  const int64_t span = format == PQ_FP4_NV ? 64 : 128;   // channels of four blocks
+  return (rows + 127) / 128 * ((D + span - 1) / span) * 512;
+}
+
+extern "C" pq_status pq_quant_fp4(const void* X, int64_t T, int64_t D, int64_t ldx, int g, pq_fp4_format format,
+                                  float factor, uint8_t* codes, uint8_t* scales, void* stream) {
+  clear_error();
+  const pq_status st = check_quant_fp4(X, T, D, ldx, g, format, factor, codes, scales);
+  if (st != PQ_OK) return st;
+  return cuda_fail(launch_quant_fp4(X, T, (int)D, ldx, g, format == PQ_FP4_NV, factor, codes, scales,
+                                    reinterpret_cast<cudaStream_t>(stream)),
+                   "pq_quant_fp4 launch");
+}
+
+extern "C" pq_status pq_fp4_gemm(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W,
+                                 const uint8_t* scales_W, int64_t T, int64_t N, int64_t D, pq_fp4_format format,
+                                 float alpha, void* Y, pq_out_dtype out_dtype, void* stream) {
+  clear_error();
+  const pq_status st = check_gemm_fp4(codes_A, scales_A, codes_W, scales_W, T, N, D, format, alpha, Y, out_dtype);
+  if (st != PQ_OK) return st;
+  return fp4_launch(codes_A, scales_A, codes_W, scales_W, T, N, D, format == PQ_FP4_NV, alpha, Y, out_dtype,
+                    reinterpret_cast<cudaStream_t>(stream), /*pdl=*/false);
+}
+
+extern "C" pq_status pq_fp4_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g, pq_fp4_format format,
+                                   float factor_A, uint8_t* codes_A, uint8_t* scales_A, const uint8_t* codes_W,
+                                   const uint8_t* scales_W, float factor_W, int64_t N, void* Y, pq_out_dtype out_dtype,
+                                   void* stream) {
+  clear_error();
+  pq_status st = check_quant_fp4(X, T, D, ldx, g, format, factor_A, codes_A, scales_A);
+  if (st != PQ_OK) return st;
+  const float alpha = format == PQ_FP4_NV ? factor_A * factor_W : 1.0f;
+  st = check_gemm_fp4(codes_A, scales_A, codes_W, scales_W, T, N, D, format, alpha, Y, out_dtype);
+  if (st != PQ_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = cuda_fail(launch_quant_fp4(X, T, (int)D, ldx, g, format == PQ_FP4_NV, factor_A, codes_A, scales_A, s),
+                 "pq_fp4_linear quantisation launch");
+  if (st != PQ_OK) return st;
+  return fp4_launch(codes_A, scales_A, codes_W, scales_W, T, N, D, format == PQ_FP4_NV, alpha, Y, out_dtype, s,
+                    /*pdl=*/true);
 }
 
 extern "C" pq_status pq_kv4_append(const pq_kv4_cache* cache, const void* Q, int64_t ldq, const void* K, int64_t ldk,

@@ -319,6 +319,42 @@ __device__ __forceinline__ void umma_s8_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// Instruction descriptor for block-scaled E2M1 operands (kind::mxf4nvf4, kind::mxf4), both K-major, float32 accumulator: A/B
+// formats bits 7-9 / 10-11 (1 = E2M1), scale type bit 23 (0 = E4M3, 1 = E8M0), N/8 at bit 17, M/128 at bit 27, and which
+// bytes of a scale word the instruction takes (sf: 0, or 2 for the second pair of two) at bits 4-5 (B) and 29-30 (A).
+__host__ __device__ constexpr uint32_t idesc_e2m1(bool e8m0, int M, int N, int sf) {
+  return ((uint32_t)sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) |
+         ((uint32_t)(M >> 7) << 27) | ((uint32_t)sf << 29);
+}
+
+// D (+)= (A * scale_A) (B * scale_B)^T on E2M1 operands, 64 codes along K; a_scale, b_scale: tensor-memory columns of
+// scale words (rows = lanes, 32 rows a column, in all four lane quarters).  NV: a word holds four E4M3 scales of 16 codes;
+// otherwise two pairs of E8M0 scales of 32 codes.  PAIR: M = 256 over a CTA pair.
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void umma_e2m1(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
+                                          uint32_t b_scale, uint32_t accumulate) {
+#define PQ_UMMA_E2M1(GROUP, KIND)                                                            \
+  asm volatile(                                                                              \
+      "{\n\t.reg .pred p;\n\t"                                                               \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                            \
+      "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem), \
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(accumulate)      \
+      : "memory")
+  if constexpr (NV && PAIR) PQ_UMMA_E2M1("2", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (NV) PQ_UMMA_E2M1("1", "mxf4nvf4.block_scale.scale_vec::4X");
+  else if constexpr (PAIR) PQ_UMMA_E2M1("2", "mxf4.block_scale.scale_vec::2X");
+  else PQ_UMMA_E2M1("1", "mxf4.block_scale.scale_vec::2X");
+#undef PQ_UMMA_E2M1
+}
+
+// 512 bytes of shared memory, 32 rows of 16, to 4 columns of tensor memory, the same in all four lane quarters (PAIR: in
+// both CTAs of the pair, each from its own shared memory at the same offset).
+template <bool PAIR>
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR) asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  else asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
 // Once all earlier pair MMAs of this thread have completed, arrive once on the mbarrier at
 // `bar`'s shared-memory offset in every CTA of the cluster whose rank bit is set in cta_mask.
 __device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint16_t cta_mask) {
@@ -448,6 +484,16 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr) {
   d |= (uint64_t)(1024 >> 4) << 32;
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// Rows of 16 bytes one after the other, without a swizzle: groups of 8 rows 128 bytes apart (stride offset).
+__device__ __forceinline__ uint64_t smem_desc_rows16(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
   return d;
 }
 

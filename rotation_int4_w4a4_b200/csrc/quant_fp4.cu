@@ -1,0 +1,241 @@
+// Rows of bf16 -> E2M1 codes with one scale a block of channels (sm_100a):
+//   y = x H_g / sqrt(g) per block of g channels (g = 64, 128 or 256; g = 0: y = x), then per block of
+//   mx: 32 channels, scale = 2^(floor(log2 max|y|) - 2), codes = E2M1(y / scale)
+//   nv: 16 channels, scale = E4M3(max|y| / (6 factor)), codes = E2M1(y / (scale factor))
+// and the scales in the order in which the product's tensor memory takes them (pieces of 128 rows x 4 blocks).
+//
+// A block of channels needs nothing from the rest of its row, so the kernel streams: 2 bytes an element in, 0.5 and a
+// scale's share out, HBM its floor.  What stands in the way is the rotation.  Here a warp takes 16 rows and 4 of the
+// log2(g) butterfly stages are one matrix instruction (m16n8k16, bf16 x +-1, exact products, float32 sums): lane t of
+// a row's four holds 16 consecutive channels of every 64, of which the matrix turns index bits 0, 1 (within 4 channels)
+// and 4, 5 (the lane), the operands' order being free; bits 2, 3, 6 and 7 are additions within the thread.  No value
+// crosses lanes but a block's maximum (mx: one shuffle) and the scale bytes of a word.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "internal.h"
+#include "nan_max.cuh"
+#include "ptx.cuh"
+#include "rows.cuh"
+
+namespace pq {
+namespace {
+
+constexpr int QF_WARPS = 8;
+constexpr int QF_ROWS = 16;                 // rows a warp takes
+// mx: blocks whose maximum is below this count as zero, so that 1 / scale stays a normal float32.
+constexpr float kTinyBlock = 7.888609052210118e-31f;     // 2^-100
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Eight float32 -> eight E2M1 codes (nearest, ties to even, +-6 at most), the first in the lowest nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t r;
+  asm("{ .reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d}; }"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Scale byte of a block from its largest magnitude, and what its channels are multiplied with (0: codes 0).  unit: the
+// rotation's 1 / sqrt(g); nv: top = unit / (6 factor) and unit is unit / factor.
+template <bool NV>
+__device__ __forceinline__ uint32_t block_scale(float m, float unit, float top, float& f) {
+  f = 0.0f;
+  if constexpr (NV) {
+    if (!(m < INFINITY)) return 0x7Fu;                   // E4M3's NaN
+    uint16_t b;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(b) : "f"(m * top));
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
+    const float s = __low2float(*reinterpret_cast<const __half2*>(&h));
+    if (s > 0.0f) f = unit / s;
+    return b & 0xFFu;
+  } else {
+    m *= unit;
+    if (!(m < INFINITY)) return 0xFFu;                   // E8M0's NaN
+    if (m < kTinyBlock) return 0u;
+    const uint32_t e = __float_as_uint(m) >> 23;         // scale 2^(e - 129), its byte e - 2
+    f = unit * __uint_as_float((256u - e) << 23);
+    return e - 2u;
+  }
+}
+
+// G: 0, 64, 128 or 256.  A warp's unit is 16 rows x 128 channels (G = 256: 256).
+template <int G, bool NV>
+__global__ void __launch_bounds__(32 * QF_WARPS) quant_fp4_kernel(const uint16_t* __restrict__ X, int64_t rows, int64_t ldx,
+                                                                  int D, int units, int64_t col_blocks, int row_warps,
+                                                                  float unit, float top, uint8_t* __restrict__ codes,
+                                                                  uint8_t* __restrict__ scales) {
+  constexpr int NS = G == 256 ? 4 : 2;                   // spans of 64 channels
+  ptx::griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int64_t block_row = (int64_t)blockIdx.x / col_blocks;
+  const int u = (int)((int64_t)blockIdx.x % col_blocks) * (QF_WARPS / row_warps) + warp / row_warps;
+  const int64_t r0 = (block_row * row_warps + warp % row_warps) * QF_ROWS;
+  if (u >= units || r0 >= rows) return;                  // whole warps
+  const int c0 = u * 64 * NS + 16 * t;                   // the thread's channels: c0 + 64 s .. + 15
+
+  uint4 x[NS][2][2];
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t r = r0 + g + 8 * h;
+      const bool in = r < rows && c0 + 64 * s < D;
+      const uint4* src = reinterpret_cast<const uint4*>(X + r * ldx + c0 + 64 * s);
+      x[s][h][0] = in ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+      x[s][h][1] = in ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
+    }
+
+  float v[2][NS][16];
+  if constexpr (G == 0) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        row_bf16x8(x[s][h][0], v[h][s]);
+        row_bf16x8(x[s][h][1], v[h][s] + 8);
+      }
+  } else {
+    // The +-1 matrix: row k <-> index bits (k & 1, k >> 3, lane (k >> 1) & 3), column n of half nn <-> (n & 1, nn, n >> 1).
+    uint32_t b[2][2];
+#pragma unroll
+    for (int nn = 0; nn < 2; ++nn)
+#pragma unroll
+      for (int hi = 0; hi < 2; ++hi) {
+        const int col = (g & 1) | (nn << 1) | ((g >> 1) << 2);
+        b[nn][hi] = 0x3F803F80u | ((__popc(((hi << 1) | (t << 2)) & col) & 1) << 15) |
+                    ((uint32_t)(__popc((1 | (hi << 1) | (t << 2)) & col) & 1) << 31);
+      }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint32_t w0[8] = {x[s][0][0].x, x[s][0][0].y, x[s][0][0].z, x[s][0][0].w,
+                              x[s][0][1].x, x[s][0][1].y, x[s][0][1].z, x[s][0][1].w};
+      const uint32_t w1[8] = {x[s][1][0].x, x[s][1][0].y, x[s][1][0].z, x[s][1][0].w,
+                              x[s][1][1].x, x[s][1][1].y, x[s][1][1].z, x[s][1][1].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int nn = 0; nn < 2; ++nn) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma_bf16(c, w0[2 * j], w1[2 * j], w0[2 * j + 1], w1[2 * j + 1], b[nn][0], b[nn][1]);
+          v[0][s][4 * j + 2 * nn] = c[0], v[0][s][4 * j + 2 * nn + 1] = c[1];
+          v[1][s][4 * j + 2 * nn] = c[2], v[1][s][4 * j + 2 * nn + 1] = c[3];
+        }
+    }
+    // Index bits 2 and 3 within the span, 6 and 7 across spans; two neighbours an instruction.
+    auto turn = [](float* a, float* c) {
+      const uint64_t p = ptx::f2_pack(a[0], a[1]), q = ptx::f2_pack(c[0], c[1]);
+      ptx::f2_unpack(ptx::f2_add(p, q), a[0], a[1]);
+      ptx::f2_unpack(ptx::f2_sub(p, q), c[0], c[1]);
+    };
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int d = 4; d < 16; d <<= 1)
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            if ((i & d) == 0) turn(v[h][s] + i, v[h][s] + i + d);
+#pragma unroll
+      for (int d = 1; d < G / 64; d <<= 1)
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          if ((s & d) == 0) {
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) turn(v[h][s] + i, v[h][s + d] + i);
+          }
+    }
+  }
+
+  const int pieces = NV ? (D + 63) / 64 : (D + 127) / 128;   // scale words a row
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = r0 + g + 8 * h;
+    uint32_t word[NV ? NS : NS / 2];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      float* y = v[h][s];
+      float m = max3_nan(fabsf(y[0]), fabsf(y[1]), fabsf(y[2])), m2 = max3_nan(fabsf(y[3]), fabsf(y[4]), fabsf(y[5]));
+      m = max3_nan(m, fabsf(y[6]), fabsf(y[7]));
+      m2 = max3_nan(m2, fabsf(y[8]), fabsf(y[9]));
+      m = max3_nan(m, fabsf(y[10]), fabsf(y[11]));
+      m2 = max3_nan(m2, fabsf(y[12]), fabsf(y[13]));
+      m = max_nan(max3_nan(m, fabsf(y[14]), fabsf(y[15])), m2);
+      if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      float f;
+      const uint32_t byte = block_scale<NV>(m, unit, top, f);
+      if constexpr (NV) {
+        word[s] = byte << (8 * t);
+      } else {
+        const uint32_t mine = byte << (16 * (s & 1) + 8 * (t >> 1));
+        if (s & 1) word[s / 2] |= mine;
+        else word[s / 2] = mine;
+      }
+      // a value times 0 is not 0 if it is infinite or NaN
+#pragma unroll
+      for (int i = 0; i < 16; ++i) y[i] = f != 0.0f ? y[i] * f : 0.0f;
+      if (r < rows && c0 + 64 * s < D)
+        *reinterpret_cast<uint2*>(codes + r * (D / 2) + (c0 + 64 * s) / 2) = make_uint2(e2m1x8(y), e2m1x8(y + 8));
+    }
+    uint8_t* place = scales + ((r >> 7) * pieces) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+#pragma unroll
+    for (int k = 0; k < (NV ? NS : NS / 2); ++k) {
+      if constexpr (NV) word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 1);
+      word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 2);
+      const int piece = u * (NV ? NS : NS / 2) + k;
+      if (t == 0 && r < rows && piece < pieces) *reinterpret_cast<uint32_t*>(place + (int64_t)piece * 512) = word[k];
+    }
+  }
+}
+
+template <int G, bool NV>
+cudaError_t launch_fp4(const void* X, int64_t rows, int D, int64_t ldx, float factor, uint8_t* codes, uint8_t* scales,
+                       cudaStream_t stream) {
+  constexpr int width = G == 256 ? 256 : 128;
+  const int units = (D + width - 1) / width;
+  const int64_t tiles = (rows + QF_ROWS - 1) / QF_ROWS;
+  int row_warps = 1;                                     // few rows: a block's warps take other channels instead
+  while (row_warps < QF_WARPS && row_warps < tiles) row_warps *= 2;
+  const int64_t col_blocks = (units + QF_WARPS / row_warps - 1) / (QF_WARPS / row_warps);
+  const int64_t blocks = col_blocks * ((tiles + row_warps - 1) / row_warps);
+  if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const double turn = G == 0 ? 1.0 : 1.0 / std::sqrt((double)G);
+  const float unit = (float)(NV ? turn / (double)factor : turn), top = (float)(turn / (6.0 * (double)factor));
+  quant_fp4_kernel<G, NV><<<(unsigned)blocks, 32 * QF_WARPS, 0, stream>>>(static_cast<const uint16_t*>(X), rows, ldx, D, units,
+                                                                          col_blocks, row_warps, unit, top, codes, scales);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quant_fp4(const void* X, int64_t rows, int D, int64_t ldx, int g, bool nv, float factor, uint8_t* codes,
+                             uint8_t* scales, cudaStream_t stream) {
+#define PQ_CASE(G) (nv ? launch_fp4<G, true>(X, rows, D, ldx, factor, codes, scales, stream) \
+                       : launch_fp4<G, false>(X, rows, D, ldx, factor, codes, scales, stream))
+  switch (g) {
+    case 64: return PQ_CASE(64);
+    case 128: return PQ_CASE(128);
+    case 256: return PQ_CASE(256);
+    default: return PQ_CASE(0);
+  }
+#undef PQ_CASE
+}
+
+}  // namespace pq

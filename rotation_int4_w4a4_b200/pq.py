@@ -24,6 +24,8 @@ PQ_FLAG_SMOOTH_AFTER_ROTATE = 0x1
 PQ_NO_PAIR = 0xFF
 PQ_KV4_ROTATE_K, PQ_KV4_ROTATE_V = 0x1, 0x2
 PQ_KV4_INTERLEAVED = 0x1
+PQ_FP4_MX, PQ_FP4_NV = range(2)
+FP4_FORMATS = {"mx": PQ_FP4_MX, "nv": PQ_FP4_NV}
 KINDS = {"hadamard": PQ_HADAMARD, "givens": PQ_GIVENS, "smooth_hadamard": PQ_SMOOTH_HADAMARD}
 
 # Every symbol the header declares.
@@ -32,6 +34,7 @@ EXPORTS = ("pq_select_pairs", "pq_make_plan", "pq_destroy_plan", "pq_transform_q
            "pq_w4a4_gemm_launch_count_g", "pq_w4a4_linear", "pq_make_plan_outliers",
            "pq_rrs_prepare", "pq_rrs_transform_quant", "pq_rrs_pack_weights", "pq_rrs_gemm",
            "pq_quant_rows8", "pq_w8a8_gemm", "pq_w8a8_linear",
+           "pq_fp4_scale_bytes", "pq_quant_fp4", "pq_fp4_gemm", "pq_fp4_linear",
            "pq_kv4_append", "pq_kv4_read", "pq_kv4_attention",
            "pq_check_status",
            "pq_selftest_wait_timeout", "pq_status_string", "pq_last_error")
@@ -75,6 +78,14 @@ lib.pq_w8a8_gemm.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _i32, _v
 lib.pq_w8a8_gemm.restype = _i32
 lib.pq_w8a8_linear.argtypes = [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp]
 lib.pq_w8a8_linear.restype = _i32
+lib.pq_fp4_scale_bytes.argtypes = [_i64, _i64, _i32]
+lib.pq_fp4_scale_bytes.restype = _i64
+lib.pq_quant_fp4.argtypes = [_vp, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp]
+lib.pq_quant_fp4.restype = _i32
+lib.pq_fp4_gemm.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _f32, _vp, _i32, _vp]
+lib.pq_fp4_gemm.restype = _i32
+lib.pq_fp4_linear.argtypes = [_vp, _i64, _i64, _i64, _i32, _i32, _f32, _vp, _vp, _vp, _vp, _f32, _i64, _vp, _i32, _vp]
+lib.pq_fp4_linear.restype = _i32
 
 
 class _KV4Struct(_c.Structure):
@@ -443,6 +454,82 @@ def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=No
     out, ca, sa, cw, sw, y = _gemm8_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, out_dtype, dev, torch)
     _check(lib.pq_w8a8_linear(xp, T, D, ldx, g, ca, sa, cw, sw, N, y, out, _raw_stream(stream, dev, torch)),
            "pq_w8a8_linear")
+
+
+def _fp4_format(fmt):
+    if fmt not in FP4_FORMATS:
+        raise ValueError(f"fmt={fmt!r}: expected 'mx' (blocks of 32, power-of-two scales) or 'nv' (blocks of 16, E4M3 scales)")
+    return FP4_FORMATS[fmt]
+
+
+def _fp4_bytes(rows, D, form):
+    """Bytes of a tensor's scales (sizes the calls refuse give a small number: the library names what is wrong)."""
+    span = 64 if form == PQ_FP4_NV else 128
+    return -(-rows // 128) * -(-D // span) * 512
+
+
+def pq_fp4_scale_bytes(rows: int, D: int, fmt: str = "nv") -> int:
+    """Size of the scale buffer (uint8) of `rows` rows of D channels."""
+    n = lib.pq_fp4_scale_bytes(rows, D, _fp4_format(fmt))
+    if n == 0:
+        raise ValueError(f"pq_fp4_scale_bytes: {lib.pq_last_error().decode(errors='replace')}")
+    return n
+
+
+def pq_quant_fp4(X, codes, scales, fmt="nv", g=0, factor=1.0, T=None, D=None, ldx=None, stream=None) -> None:
+    """X bf16 [T, ldx] -> E2M1 codes uint8 [T, D / 2] and one scale a block of channels, uint8 of :func:`pq_fp4_scale_bytes`
+    (fmt "mx": blocks of 32, "nv": of 16, times factor); rows rotated in blocks of g channels by a Hadamard matrix first
+    (g = 0: not)."""
+    dev, torch = _here()
+    form = _fp4_format(fmt)
+    xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
+    u8 = torch.uint8
+    _check(lib.pq_quant_fp4(xp, T, D, ldx, g, form, factor, _on(codes, "codes", "u8", u8, T * D // 2, dev),
+                            _on(scales, "scales", "u8", u8, _fp4_bytes(T, D, form), dev), _raw_stream(stream, dev, torch)),
+           "pq_quant_fp4")
+
+
+def _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch):
+    if not isinstance(Y, int):
+        y_kind = PQ_OUT_BF16 if Y.dtype == torch.bfloat16 else PQ_OUT_F32
+        if out_dtype is None:
+            out_dtype = y_kind
+        elif out_dtype != y_kind:
+            raise ValueError(f"Y: dtype {Y.dtype} does not match out_dtype={out_dtype}")
+    elif out_dtype is None:
+        out_dtype = PQ_OUT_F32
+    u8 = torch.uint8
+    return (out_dtype, _on(codes_A, "codes_A", "u8", u8, T * D // 2, dev),
+            _on(scales_A, "scales_A", "u8", u8, _fp4_bytes(T, D, form), dev),
+            _on(codes_W, "codes_W", "u8", u8, N * D // 2, dev),
+            _on(scales_W, "scales_W", "u8", u8, _fp4_bytes(N, D, form), dev),
+            _on(Y, "Y", "y", torch.bfloat16 if out_dtype == PQ_OUT_BF16 else torch.float32, T * N, dev))
+
+
+def pq_fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", alpha=1.0, T=None, N=None, D=None, out_dtype=None,
+                stream=None) -> None:
+    """Y [T, N] = alpha times the product of the numbers that E2M1 codes and their block scales stand for (codes uint8
+    [T, D / 2] and [N, D / 2]; fmt "nv": alpha holds the two tensors' factors)."""
+    dev, torch = _here()
+    form = _fp4_format(fmt)
+    T = codes_A.shape[0] if T is None else T
+    N = codes_W.shape[0] if N is None else N
+    D = codes_A.shape[1] * 2 if D is None else D
+    out, ca, sa, cw, sw, y = _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch)
+    _check(lib.pq_fp4_gemm(ca, sa, cw, sw, T, N, D, form, alpha, y, out, _raw_stream(stream, dev, torch)), "pq_fp4_gemm")
+
+
+def pq_fp4_linear(X, codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", g=0, factor_A=1.0, factor_W=1.0, T=None, N=None,
+                  D=None, ldx=None, out_dtype=None, stream=None) -> None:
+    """:func:`pq_quant_fp4` of X into codes_A / scales_A and :func:`pq_fp4_gemm` into Y, one call (fmt "nv": alpha =
+    factor_A * factor_W)."""
+    dev, torch = _here()
+    form = _fp4_format(fmt)
+    xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
+    N = codes_W.shape[0] if N is None else N
+    out, ca, sa, cw, sw, y = _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch)
+    _check(lib.pq_fp4_linear(xp, T, D, ldx, g, form, factor_A, ca, sa, cw, sw, factor_W, N, y, out,
+                             _raw_stream(stream, dev, torch)), "pq_fp4_linear")
 
 
 class KV4Cache:
