@@ -15,6 +15,15 @@
 //   time.
 //   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue; warps 2..5: epilogue.
 //
+// fp4_pair_kernel (many output tiles): persistent, one CTA per SM, clusters of two CTAs that share every MMA (cta_group::2,
+//   M256 N256 K64).  Here tokens are operand A and weights B, so that a thread of the epilogue has 16 channels of one token
+//   side by side and stores them whole.  Scales of 256 columns are wanted in both CTAs, those of 128 rows in each its own.
+//   Tensor memory holds two accumulators of 256 columns only if they share some (96 with nv, 64 with mx): the scales take
+//   the rest.  The epilogue reads the shared columns first and hands them over, and the next tile's reduction runs under
+//   what is left of it.
+//   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue (even CTA); warps 4..11: epilogue, two a lane
+//   quarter.
+//
 // Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains what it has in flight, meets
 // its cluster, frees tensor memory and returns.
 #include <cuda.h>
@@ -62,6 +71,244 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ void store_y(void* Y, int64_t idx, float y, int out_bf16) {
   if (out_bf16) static_cast<__nv_bfloat16*>(Y)[idx] = __float2bfloat16_rn(y);
   else static_cast<float*>(Y)[idx] = y;
+}
+
+// ------------------------------------------------------------------------------------ pair kernel
+constexpr int PM = 128;                 // tokens per CTA
+constexpr int PN = 256;                 // channels per tile
+constexpr int PN_HALF = PN / 2;         // channels each CTA stages
+constexpr int P_STAGES = 5;
+constexpr int P_THREADS = 384;
+constexpr int P_EPI_WARP0 = 4;
+
+template <bool NV> struct PairGeom {
+  static constexpr int SF = kPieces<NV> * PIECE;                        // scale bytes of 128 rows a step
+  static constexpr uint32_t TX = 2 * ((PM + PN_HALF) * KB + 3 * SF);    // both CTAs' bytes, on the even CTA's barrier
+  static constexpr int SHARED = NV ? 96 : 64;                           // columns that the two accumulators share
+  static constexpr uint32_t ACC1 = PN - SHARED;                         // the second one's first column
+  static constexpr uint32_t SF_COL = ACC1 + PN;                         // two buffers of scales, a step's each
+  static constexpr uint32_t SF_COLS = kPieces<NV> * 12;                 // of them 4 a piece for A, then 8 for B
+  static_assert(SF_COL + 2 * SF_COLS <= 512, "tensor memory");
+  static_assert(SHARED % 32 == 0 && (PN - SHARED) % 32 == 0, "two warps share the columns, 16 at a time");
+};
+
+template <bool NV> struct __align__(1024) PairSmem {
+  uint8_t a[P_STAGES][PM * KB];
+  uint8_t b[P_STAGES][PN_HALF * KB];
+  uint8_t sa[P_STAGES][PairGeom<NV>::SF];
+  uint8_t sb[P_STAGES][2][PairGeom<NV>::SF];
+  float out[8][32][17];                 // outputs on their way to rows that cannot be stored 16 bytes at a time
+  uint64_t full[P_STAGES], empty[P_STAGES];
+  uint64_t acc_full, acc_empty;         // a phase a tile
+  uint64_t mma_done, pair_done;
+  uint32_t tmem_slot;
+  int abort_flag;
+};
+
+// Tiles in strips of P_STRIP tiles of tokens, channel tiles within a strip: the tiles that run at once read few operands.
+constexpr int P_STRIP = 8;
+__device__ __forceinline__ void tile_place(int u, int m_tiles, int n_tiles, int& m, int& n) {
+  const int strip = u / (P_STRIP * n_tiles), in = u % (P_STRIP * n_tiles);
+  const int height = min(P_STRIP, m_tiles - strip * P_STRIP);
+  m = strip * P_STRIP + in % height;
+  n = in / height;
+}
+
+template <bool NV>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(
+    const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSW,
+    const __grid_constant__ CUtensorMap tmSA, float alpha, void* __restrict__ Y, int T, int N, int steps, int codes64,
+    int pieces, int m_tiles, int n_tiles, int out_bf16, unsigned int* status) {
+  using Geom = PairGeom<NV>;
+  extern __shared__ unsigned char smem_raw[];
+  PairSmem<NV>& S = *reinterpret_cast<PairSmem<NV>*>(smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+  const int first = (int)(blockIdx.x >> 1), stride = (int)(gridDim.x >> 1);
+  const int tiles = m_tiles * n_tiles;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < P_STAGES; ++s) {
+      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.empty[s], 1);
+    }
+    ptx::mbar_init(&S.acc_full, 1);
+    ptx::mbar_init(&S.acc_empty, 2 * 8);                   // both CTAs' epilogue warps
+    ptx::mbar_init(&S.mma_done, 1);
+    ptx::mbar_init(&S.pair_done, 1);
+    S.abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmW);
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmSW);
+    ptx::prefetch_tmap(&tmSA);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(&S.tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = S.tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
+      int step = 0;
+      bool ok = true;
+      for (int u = first; u < tiles && ok; u += stride) {
+        int m, n;
+        tile_place(u, m_tiles, n_tiles, m, n);
+        const int m0 = m * 2 * PM + PM * rank, n0 = n * PN;
+        const int sa0 = (m0 / 128) * pieces * 2, sb0 = (n0 / 128) * pieces * 2;
+        for (int kb = 0; kb < steps; ++kb, ++step) {
+          const int s = step % P_STAGES, sk = kb * kPieces<NV> * 2;
+          if (!wait_or_abort(&S.empty[s], ((uint32_t)(step / P_STAGES) & 1u) ^ 1u, &S.abort_flag, status)) { ok = false; break; }
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[s], Geom::TX);
+          ptx::tma_load_2d_pair(S.a[s], &tmA, full0 + 8u * s, kb * KB, m0);
+          ptx::tma_load_2d_pair(S.b[s], &tmW, full0 + 8u * s, kb * KB, n0 + PN_HALF * rank);
+          ptx::tma_load_2d_pair(S.sa[s], &tmSA, full0 + 8u * s, 0, sa0 + sk);
+          ptx::tma_load_2d_pair(S.sb[s][0], &tmSW, full0 + 8u * s, 0, sb0 + sk);
+          ptx::tma_load_2d_pair(S.sb[s][1], &tmSW, full0 + 8u * s, 0, sb0 + 2 * pieces + sk);
+        }
+      }
+      // Every load issued has landed and every release aimed at this CTA has arrived before it may exit.
+      const int j0 = step > P_STAGES ? step - P_STAGES : 0;
+      if (rank == 0)
+        for (int j = j0; j < step; ++j) drain_wait(&S.full[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
+      for (int j = j0; j < step; ++j) drain_wait(&S.empty[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, 2 * PM, PN, 0), id1 = ptx::idesc_e2m1(!NV, 2 * PM, PN, NV ? 0 : 2);
+      int step = 0, tile = 0;
+      bool ok = true;
+      for (int u = first; u < tiles && ok; u += stride, ++tile) {
+        if (tile > 0 && !wait_or_abort(&S.acc_empty, (uint32_t)(tile - 1) & 1u, &S.abort_flag, status)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + (tile & 1 ? Geom::ACC1 : 0u);
+        for (int kb = 0; kb < steps; ++kb, ++step) {
+          const int s = step % P_STAGES;
+          // The buffer of scales: the products that read it two steps ago are done.
+          if (step >= 2 && !wait_or_abort(&S.empty[(step - 2) % P_STAGES], (uint32_t)((step - 2) / P_STAGES) & 1u, &S.abort_flag, status)) { ok = false; break; }
+          if (!wait_or_abort(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)(step & 1) * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
+          const uint32_t a0 = ptx::smem_addr(S.a[s]), b0 = ptx::smem_addr(S.b[s]);
+          const uint32_t sa_smem = ptx::smem_addr(S.sa[s]), sb_smem = ptx::smem_addr(S.sb[s]);
+          const int live = min(4, codes64 - 4 * kb);      // 64-code products that are not all padding
+#pragma unroll
+          for (int p = 0; p < kPieces<NV>; ++p) {
+            ptx::tmem_copy_scales<true>(sa + 4 * p, ptx::smem_desc_rows16(sa_smem + PIECE * p));
+            ptx::tmem_copy_scales<true>(sb + 8 * p, ptx::smem_desc_rows16(sb_smem + PIECE * p));
+            ptx::tmem_copy_scales<true>(sb + 8 * p + 4, ptx::smem_desc_rows16(sb_smem + Geom::SF + PIECE * p));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int p = NV ? k : k / 2;
+            if (k < live)
+              ptx::umma_e2m1<NV, true>(d, ptx::smem_desc_sw128(a0 + 32 * k), ptx::smem_desc_sw128(b0 + 32 * k), k & 1 ? id1 : id0,
+                                       sa + 4 * p, sb + 8 * p, kb > 0 || k > 0 ? 1u : 0u);
+          }
+          ptx::umma_commit_pair(&S.empty[s], 0x3);
+        }
+        if (!ok) break;
+        ptx::umma_commit_pair(&S.acc_full, 0x3);
+      }
+      ptx::umma_commit_pair(&S.mma_done, 0x1);
+      drain_wait(&S.mma_done, 0);
+      if (tile > 0) drain_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u);
+    }
+  } else if (warp >= P_EPI_WARP0) {
+    // Lane quarter warp % 4 (tokens), half of the columns (channels): of the shared ones and of the others.
+    const int ew = warp - P_EPI_WARP0, sub = warp & 3, half = ew >> 2;
+    const uint32_t acc_empty0 = ptx::mapa_shared(ptx::smem_addr(&S.acc_empty), 0);
+    const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
+    // 16 bytes at a time where every row of Y begins on 16 bytes.
+    const bool wide = out_bf16 ? N % 8 == 0 : N % 4 == 0;
+    int tile = 0;
+    for (int u = first; u < tiles; u += stride, ++tile) {
+      int m, n;
+      tile_place(u, m_tiles, n_tiles, m, n);
+      const int row0 = m * 2 * PM + PM * rank + 32 * sub, n0 = n * PN;
+      const uint32_t acc = lanes + (tile & 1 ? Geom::ACC1 : 0u);
+      // columns of the tile: the shared ones are the first accumulator's last and the second's first
+      const int shared0 = tile & 1 ? 0 : (int)Geom::ACC1, rest0 = tile & 1 ? Geom::SHARED : 0;
+      auto put = [&](const uint32_t* r, int c) {           // 16 channels from n0 + c of this lane's token
+        const int t = row0 + lane, ch = n0 + c;
+        if (wide && ch + 16 <= N) {
+          if (t < T && out_bf16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const __nv_bfloat162 p = __floats2bfloat162_rn(alpha * __uint_as_float(r[2 * i]), alpha * __uint_as_float(r[2 * i + 1]));
+              w[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(Y) + (int64_t)t * N + ch);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          } else if (t < T) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(Y) + (int64_t)t * N + ch);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_float4(alpha * __uint_as_float(r[4 * i]), alpha * __uint_as_float(r[4 * i + 1]),
+                                   alpha * __uint_as_float(r[4 * i + 2]), alpha * __uint_as_float(r[4 * i + 3]));
+          }
+        } else if (ch < N) {                               // the whole warp: two tokens at a time, a lane a channel
+          float (*out)[17] = S.out[ew];
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) out[lane][i] = alpha * __uint_as_float(r[i]);
+          __syncwarp();
+#pragma unroll 4
+          for (int i = 0; i < 16; ++i) {
+            const int tt = row0 + 2 * i + (lane >> 4), cc = ch + (lane & 15);
+            if (tt < T && cc < N) store_y(Y, (int64_t)tt * N + cc, out[2 * i + (lane >> 4)][lane & 15], out_bf16);
+          }
+        }
+      };
+      if (!warp_wait_or_abort(&S.acc_full, (uint32_t)tile & 1u, &S.abort_flag, status)) break;
+      ptx::tc_fence_after();
+      constexpr int SH = Geom::SHARED / 32;                // chunks of 16 shared columns a warp takes
+      const int s0 = shared0 + half * (Geom::SHARED / 2);
+      uint32_t r[SH][16];
+#pragma unroll
+      for (int c = 0; c < SH; ++c) ptx::tmem_ld32x16(acc + s0 + 16 * c, r[c]);
+#pragma unroll
+      for (int c = 0; c < SH; ++c) ptx::tmem_ld_wait(r[c]);
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_remote(acc_empty0);
+#pragma unroll
+      for (int c = 0; c < SH; ++c) put(r[c], s0 + 16 * c);
+      constexpr int REST = (PN - Geom::SHARED) / 2;
+      const int o0 = rest0 + half * REST;
+#pragma unroll 1
+      for (int c = 0; c < REST; c += 16) {
+        uint32_t x[16];
+        __syncwarp();
+        ptx::tmem_ld32x16(acc + o0 + c, x);
+        ptx::tmem_ld_wait(x);
+        put(x, o0 + c);
+      }
+    }
+  }
+
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves while its peer may still arrive on its barriers or read its tiles.
+  if (threadIdx.x == 0) {
+    ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(&S.pair_done), (uint32_t)rank ^ 1u));
+    int never = 0;
+    if (!ptx::mbar_wait_bounded_cl(&S.pair_done, 0, &never, kWaitNs)) atomicOr(status, PQ_DEV_TIMEOUT);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
 }
 
 // ------------------------------------------------------------------------------------ tile kernel
@@ -335,9 +582,34 @@ pq_status launch_tile(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int64_t t
 }
 
 template <bool NV>
+pq_status launch_pair(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, int sms) {
+  constexpr size_t smem = sizeof(PairSmem<NV>) + 1024;
+  static_assert(smem <= 232448, "shared memory exceeds 227 KB");
+  static std::atomic<bool> done[kMaxDevices];
+  const cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(fp4_pair_kernel<NV>), (int)smem, done);
+  if (e != cudaSuccess) return cuda_fail(e, "fp4_pair_kernel attributes");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>((int64_t)m_tiles * n_tiles, sms / 2)), 1, 1);
+  cfg.blockDim = dim3(P_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_pair_kernel<NV>, m.w, m.a, m.sw, m.sa, c.alpha, c.Y, c.T, c.N, c.steps, c.codes64,
+                                      c.pieces, m_tiles, n_tiles, c.bf16, c.status),
+                   "fp4_pair_kernel launch");
+}
+
+template <bool NV>
 pq_status run(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t T,
               int64_t N, int64_t D, Fp4Call c) {
   const int sms = device_sm_count();
+  const int64_t pair_m = (T + 2 * PM - 1) / (2 * PM), pair_n = (N + PN - 1) / PN;
+  if (T > 128 && pair_m * pair_n * 4 >= 3 * (sms / 2)) {
+    if (pair_m * pair_n >= ((int64_t)1 << 30)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
+    Fp4Maps m;
+    const pq_status st = make_maps(&m, codes_A, scales_A, codes_W, scales_W, T, N, D, c.pieces, kPieces<NV>, PM);
+    if (st != PQ_OK) return st;
+    return launch_pair<NV>(m, c, (int)pair_m, (int)pair_n, sms);
+  }
   const int np = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
   const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
   if (tiles >= ((int64_t)1 << 31)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }

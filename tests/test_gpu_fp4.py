@@ -178,7 +178,8 @@ def _codes(rows, D, fmt, seed, lo, hi):
 
 
 SIZES = [(1, 1, 32), (1, 128, 64), (2, 7, 96), (5, 300, 256), (16, 129, 288), (17, 128, 512), (33, 1003, 1056), (64, 256, 4096),
-         (65, 96, 2048), (128, 512, 320), (129, 130, 736), (257, 1003, 4192), (300, 2500, 544), (1, 4096, 4096), (700, 5000, 1312)]
+         (65, 96, 2048), (128, 512, 320), (129, 130, 736), (257, 1003, 4192), (300, 2500, 544), (1, 4096, 4096), (700, 5000, 1312),
+         (513, 5003, 288), (2000, 2056, 800), (4100, 1300, 64)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
