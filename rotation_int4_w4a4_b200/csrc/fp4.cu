@@ -62,6 +62,19 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parit
   return ok != 0;
 }
 
+// Every lane polls: for the warp that issues to the tensor cores, whose operands then stay in uniform registers (an elected
+// lane issues; from one lane's own branch each instruction takes about 80 cycles to get its operands there, and 16 a step
+// are 1300 cycles where the products take 512).
+__device__ __forceinline__ bool issue_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
+  if (__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, 100))) return true;
+  if ((threadIdx.x & 31) == 0) {
+    *abort_flag = 1;
+    atomicOr(status, PQ_DEV_TIMEOUT);
+  }
+  __syncwarp();
+  return false;
+}
+
 // While draining: bounded in time only.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   int never = 0;
@@ -180,45 +193,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
       for (int j = j0; j < step; ++j) drain_wait(&S.empty[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, 2 * PM, PN, 0), id1 = ptx::idesc_e2m1(!NV, 2 * PM, PN, NV ? 0 : 2);
+      // Descriptors of the first stage; an offset of b bytes adds b / 16 to the address field.
+      const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(S.a[0])), db = ptx::smem_desc_sw128(ptx::smem_addr(S.b[0]));
+      const uint64_t dsa = ptx::smem_desc_rows16(ptx::smem_addr(S.sa[0])), dsb = ptx::smem_desc_rows16(ptx::smem_addr(S.sb[0]));
       int step = 0, tile = 0;
       bool ok = true;
       for (int u = first; u < tiles && ok; u += stride, ++tile) {
-        if (tile > 0 && !wait_or_abort(&S.acc_empty, (uint32_t)(tile - 1) & 1u, &S.abort_flag, status)) { ok = false; break; }
+        if (tile > 0 && !(ok = issue_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u, &S.abort_flag, status))) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + (tile & 1 ? Geom::ACC1 : 0u);
         for (int kb = 0; kb < steps; ++kb, ++step) {
           const int s = step % P_STAGES;
           // The buffer of scales: the products that read it two steps ago are done.
-          if (step >= 2 && !wait_or_abort(&S.empty[(step - 2) % P_STAGES], (uint32_t)((step - 2) / P_STAGES) & 1u, &S.abort_flag, status)) { ok = false; break; }
-          if (!wait_or_abort(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status)) { ok = false; break; }
+          if (step >= 2 && !(ok = issue_wait(&S.empty[(step - 2) % P_STAGES], (uint32_t)((step - 2) / P_STAGES) & 1u, &S.abort_flag, status))) break;
+          if (!(ok = issue_wait(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status))) break;
           ptx::tc_fence_after();
           const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)(step & 1) * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
-          const uint32_t a0 = ptx::smem_addr(S.a[s]), b0 = ptx::smem_addr(S.b[s]);
-          const uint32_t sa_smem = ptx::smem_addr(S.sa[s]), sb_smem = ptx::smem_addr(S.sb[s]);
+          const uint64_t a0 = da + (uint64_t)(s * (PM * KB / 16)), b0 = db + (uint64_t)(s * (PN_HALF * KB / 16));
+          const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (2 * Geom::SF / 16));
           const int live = min(4, codes64 - 4 * kb);      // 64-code products that are not all padding
+          if (ptx::elect_one()) {
 #pragma unroll
-          for (int p = 0; p < kPieces<NV>; ++p) {
-            ptx::tmem_copy_scales<true>(sa + 4 * p, ptx::smem_desc_rows16(sa_smem + PIECE * p));
-            ptx::tmem_copy_scales<true>(sb + 8 * p, ptx::smem_desc_rows16(sb_smem + PIECE * p));
-            ptx::tmem_copy_scales<true>(sb + 8 * p + 4, ptx::smem_desc_rows16(sb_smem + Geom::SF + PIECE * p));
-          }
+            for (int p = 0; p < kPieces<NV>; ++p) {
+              ptx::tmem_copy_scales<true>(sa + 4 * p, sa0 + PIECE / 16 * p);
+              ptx::tmem_copy_scales<true>(sb + 8 * p, sb0 + PIECE / 16 * p);
+              ptx::tmem_copy_scales<true>(sb + 8 * p + 4, sb0 + (Geom::SF + PIECE * p) / 16);
+            }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int p = NV ? k : k / 2;
-            if (k < live)
-              ptx::umma_e2m1<NV, true>(d, ptx::smem_desc_sw128(a0 + 32 * k), ptx::smem_desc_sw128(b0 + 32 * k), k & 1 ? id1 : id0,
-                                       sa + 4 * p, sb + 8 * p, kb > 0 || k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k) {
+              const int p = NV ? k : k / 2;
+              if (k < live)
+                ptx::umma_e2m1<NV, true>(d, a0 + 2 * k, b0 + 2 * k, k & 1 ? id1 : id0, sa + 4 * p, sb + 8 * p,
+                                         kb > 0 || k > 0 ? 1u : 0u);
+            }
+            ptx::umma_commit_pair(&S.empty[s], 0x3);
           }
-          ptx::umma_commit_pair(&S.empty[s], 0x3);
+          __syncwarp();
         }
         if (!ok) break;
-        ptx::umma_commit_pair(&S.acc_full, 0x3);
+        if (ptx::elect_one()) ptx::umma_commit_pair(&S.acc_full, 0x3);
+        __syncwarp();
       }
-      ptx::umma_commit_pair(&S.mma_done, 0x1);
-      drain_wait(&S.mma_done, 0);
-      if (tile > 0) drain_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u);
+      if (ptx::elect_one()) ptx::umma_commit_pair(&S.mma_done, 0x1);
+      __syncwarp();
+      if (lane == 0) {
+        drain_wait(&S.mma_done, 0);
+        if (tile > 0) drain_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u);
+      }
     }
   } else if (warp >= P_EPI_WARP0) {
     // Lane quarter warp % 4 (tokens), half of the columns (channels): of the shared ones and of the others.
@@ -428,32 +451,37 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      for (int kb = k0, step = 0; kb < k1; ++kb, ++step) {
-        const int s = step % STAGES;
-        if (!wait_or_abort(&S.full[s], (uint32_t)(step / STAGES) & 1u, &S.abort_flag, status)) break;
-        ptx::tc_fence_after();
-        const uint32_t sa = tmem + NP + (uint32_t)s * Geom::STAGE_COLS, sb = sa + 4 * kPieces<NV>;
-        const int live = min(4, codes64 - 4 * kb);        // 64-code products that are not all padding
+    constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, TM, NP, 0), id1 = ptx::idesc_e2m1(!NV, TM, NP, NV ? 0 : 2);
+    const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(S.a[0])), db = ptx::smem_desc_sw128(ptx::smem_addr(S.b[0]));
+    const uint64_t dsa = ptx::smem_desc_rows16(ptx::smem_addr(S.sa[0])), dsb = ptx::smem_desc_rows16(ptx::smem_addr(S.sb[0]));
+    for (int kb = k0, step = 0; kb < k1; ++kb, ++step) {
+      const int s = step % STAGES;
+      if (!issue_wait(&S.full[s], (uint32_t)(step / STAGES) & 1u, &S.abort_flag, status)) break;
+      ptx::tc_fence_after();
+      const uint32_t sa = tmem + NP + (uint32_t)s * Geom::STAGE_COLS, sb = sa + 4 * kPieces<NV>;
+      const uint64_t a0 = da + (uint64_t)(s * (TM * KB / 16)), b0 = db + (uint64_t)(s * (NP * KB / 16));
+      const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (Geom::SF / 16));
+      const int live = min(4, codes64 - 4 * kb);          // 64-code products that are not all padding
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int p = 0; p < kPieces<NV>; ++p) {
-          ptx::tmem_copy_scales<false>(sa + 4 * p, ptx::smem_desc_rows16(ptx::smem_addr(S.sa[s]) + PIECE * p));
-          ptx::tmem_copy_scales<false>(sb + 4 * p, ptx::smem_desc_rows16(ptx::smem_addr(S.sb[s]) + PIECE * p));
+          ptx::tmem_copy_scales<false>(sa + 4 * p, sa0 + PIECE / 16 * p);
+          ptx::tmem_copy_scales<false>(sb + 4 * p, sb0 + PIECE / 16 * p);
         }
-        const uint32_t a0 = ptx::smem_addr(S.a[s]), b0 = ptx::smem_addr(S.b[s]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, TM, NP, 0), id1 = ptx::idesc_e2m1(!NV, TM, NP, NV ? 0 : 2);
           const uint32_t col = 4 * (NV ? k : k / 2);
           if (k < live)
-            ptx::umma_e2m1<NV, false>(tmem, ptx::smem_desc_sw128(a0 + 32 * k), ptx::smem_desc_sw128(b0 + 32 * k),
-                                      k & 1 ? id1 : id0, sa + col, sb + col, step > 0 || k > 0 ? 1u : 0u);
+            ptx::umma_e2m1<NV, false>(tmem, a0 + 2 * k, b0 + 2 * k, k & 1 ? id1 : id0, sa + col, sb + col,
+                                      step > 0 || k > 0 ? 1u : 0u);
         }
         ptx::umma_commit(&S.empty[s]);
       }
-      ptx::umma_commit(&S.acc_full);
-      drain_wait(&S.acc_full, 0);
+      __syncwarp();
     }
+    if (ptx::elect_one()) ptx::umma_commit(&S.acc_full);
+    __syncwarp();
+    if (lane == 0) drain_wait(&S.acc_full, 0);
   } else {
     if (pdl) ptx::griddep_wait();                         // Y may still be read by what ran before
     const int sub = warp & 3;
