@@ -18,8 +18,7 @@
 // fp4_pair_kernel (many output tiles): persistent, one CTA per SM, clusters of two CTAs that share every MMA (cta_group::2,
 //   M256 N256 K64).  Here tokens are operand A and weights B, so that a thread of the epilogue has 16 channels of one token
 //   side by side and stores them whole.  Scales of 256 columns are wanted in both CTAs, those of 128 rows in each its own.
-//   Tensor memory holds two accumulators of 256 columns only if they share some (96 with nv, 64 with mx): the scales take
-//   the rest.  The epilogue reads the shared columns first and hands them over, and the next tile's reduction runs under
+//   Tensor memory holds two accumulators of 256 columns only if they share some (128): the scales take the rest.  The epilogue reads the shared columns first and hands them over, and the next tile's reduction runs under
 //   what is left of it.
 //   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue (even CTA); warps 4..11: epilogue, two a lane
 //   quarter.
@@ -97,20 +96,18 @@ constexpr int P_EPI_WARP0 = 4;
 template <bool NV> struct PairGeom {
   static constexpr int SF = kPieces<NV> * PIECE;                        // scale bytes of 128 rows a step
   static constexpr uint32_t TX = 2 * ((PM + PN_HALF) * KB + 3 * SF);    // both CTAs' bytes, on the even CTA's barrier
-  static constexpr int SHARED = NV ? 96 : 64;                           // columns that the two accumulators share
-  static constexpr uint32_t ACC1 = PN - SHARED;                         // the second one's first column
-  static constexpr uint32_t SF_COL = ACC1 + PN;                         // two buffers of scales, a step's each
+  static constexpr uint32_t ACC1 = PN / 2;                              // the second accumulator's first column
+  static constexpr uint32_t SF_COL = ACC1 + PN;                         // buffers of scales, a step's each
   static constexpr uint32_t SF_COLS = kPieces<NV> * 12;                 // of them 4 a piece for A, then 8 for B
-  static_assert(SF_COL + 2 * SF_COLS <= 512, "tensor memory");
-  static_assert(SHARED % 32 == 0 && (PN - SHARED) % 32 == 0, "two warps share the columns, 16 at a time");
+  static constexpr int SF_BUFS = 128 / SF_COLS;
 };
 
 template <bool NV> struct __align__(1024) PairSmem {
   uint8_t a[P_STAGES][PM * KB];
   uint8_t b[P_STAGES][PN_HALF * KB];
+  uint8_t out[8][32 * 128];             // an epilogue warp's outputs on their way to memory: 32 tokens x 128 bytes, swizzled
   uint8_t sa[P_STAGES][PairGeom<NV>::SF];
   uint8_t sb[P_STAGES][2][PairGeom<NV>::SF];
-  float out[8][32][17];                 // outputs on their way to rows that cannot be stored 16 bytes at a time
   uint64_t full[P_STAGES], empty[P_STAGES];
   uint64_t acc_full, acc_empty;         // a phase a tile
   uint64_t mma_done, pair_done;
@@ -130,8 +127,8 @@ __device__ __forceinline__ void tile_place(int u, int m_tiles, int n_tiles, int&
 template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSW,
-    const __grid_constant__ CUtensorMap tmSA, float alpha, void* __restrict__ Y, int T, int N, int steps, int codes64,
-    int pieces, int m_tiles, int n_tiles, int out_bf16, unsigned int* status) {
+    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmY, float alpha, void* __restrict__ Y, int T,
+    int N, int steps, int codes64, int pieces, int m_tiles, int n_tiles, int out_bf16, int bulk, unsigned int* status) {
   using Geom = PairGeom<NV>;
   extern __shared__ unsigned char smem_raw[];
   PairSmem<NV>& S = *reinterpret_cast<PairSmem<NV>*>(smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u));
@@ -155,6 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmSW);
     ptx::prefetch_tmap(&tmSA);
+    ptx::prefetch_tmap(&tmY);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(&S.tmem_slot, 512);
@@ -206,11 +204,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
         const uint32_t d = tmem + (tile & 1 ? Geom::ACC1 : 0u);
         for (int kb = 0; kb < steps; ++kb, ++step) {
           const int s = step % P_STAGES;
-          // The buffer of scales: the products that read it two steps ago are done.
-          if (step >= 2 && !(ok = issue_wait(&S.empty[(step - 2) % P_STAGES], (uint32_t)((step - 2) / P_STAGES) & 1u, &S.abort_flag, status))) break;
+          // The buffer of scales: the products that last read it are done.
+          const int prev = step - Geom::SF_BUFS;
+          if (prev >= 0 && !(ok = issue_wait(&S.empty[prev % P_STAGES], (uint32_t)(prev / P_STAGES) & 1u, &S.abort_flag, status))) break;
           if (!(ok = issue_wait(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status))) break;
           ptx::tc_fence_after();
-          const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)(step & 1) * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
+          const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)(step % Geom::SF_BUFS) * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
           const uint64_t a0 = da + (uint64_t)(s * (PM * KB / 16)), b0 = db + (uint64_t)(s * (PN_HALF * KB / 16));
           const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (2 * Geom::SF / 16));
           const int live = min(4, codes64 - 4 * kb);      // 64-code products that are not all padding
@@ -244,78 +243,89 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
       }
     }
   } else if (warp >= P_EPI_WARP0) {
-    // Lane quarter warp % 4 (tokens), half of the columns (channels): of the shared ones and of the others.
+    // Lane quarter warp % 4 (tokens); 64 of the columns that the accumulators share, then 64 of the others.  Outputs leave by
+    // TMA, through 4 KB of shared memory a warp (stored from the registers, a token a lane, they took 32 cycles an
+    // instruction).
     const int ew = warp - P_EPI_WARP0, sub = warp & 3, half = ew >> 2;
     const uint32_t acc_empty0 = ptx::mapa_shared(ptx::smem_addr(&S.acc_empty), 0);
     const uint32_t lanes = tmem + ((uint32_t)(32 * sub) << 16);
-    // 16 bytes at a time where every row of Y begins on 16 bytes.
-    const bool wide = out_bf16 ? N % 8 == 0 : N % 4 == 0;
+    uint8_t* const out = S.out[ew];
+    const uint32_t line = ptx::smem_addr(out) + 128u * lane, turn = (uint32_t)(lane & 7);
     int tile = 0;
     for (int u = first; u < tiles; u += stride, ++tile) {
       int m, n;
       tile_place(u, m_tiles, n_tiles, m, n);
       const int row0 = m * 2 * PM + PM * rank + 32 * sub, n0 = n * PN;
       const uint32_t acc = lanes + (tile & 1 ? Geom::ACC1 : 0u);
-      // columns of the tile: the shared ones are the first accumulator's last and the second's first
-      const int shared0 = tile & 1 ? 0 : (int)Geom::ACC1, rest0 = tile & 1 ? Geom::SHARED : 0;
-      auto put = [&](const uint32_t* r, int c) {           // 16 channels from n0 + c of this lane's token
-        const int t = row0 + lane, ch = n0 + c;
-        if (wide && ch + 16 <= N) {
-          if (t < T && out_bf16) {
-            uint32_t w[8];
+      auto put = [&](const uint32_t* r, int ch) {          // 64 channels from ch of this lane's token
+        if (row0 >= T || ch >= N) return;                  // the whole warp
+        if (bulk) {
+          // bf16: one box of 64 channels; float32: two of 32
+          for (int b = 0; b < (out_bf16 ? 1 : 2); ++b) {
+            if (ch + 32 * b >= N) break;
+            if (lane == 0) ptx::bulk_wait_read();          // the box before has left
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const __nv_bfloat162 p = __floats2bfloat162_rn(alpha * __uint_as_float(r[2 * i]), alpha * __uint_as_float(r[2 * i + 1]));
-              w[i] = *reinterpret_cast<const uint32_t*>(&p);
+            for (int c = 0; c < 8; ++c) {                  // 16 bytes
+              uint32_t w[4];
+              if (out_bf16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 p = __floats2bfloat162_rn(alpha * __uint_as_float(r[8 * c + 2 * i]), alpha * __uint_as_float(r[8 * c + 2 * i + 1]));
+                  w[i] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(alpha * __uint_as_float(b ? r[32 + 4 * c + i] : r[4 * c + i]));
+              }
+              ptx::sts_v4(line + ((c ^ turn) << 4), w[0], w[1], w[2], w[3]);
             }
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(Y) + (int64_t)t * N + ch);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          } else if (t < T) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(Y) + (int64_t)t * N + ch);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_float4(alpha * __uint_as_float(r[4 * i]), alpha * __uint_as_float(r[4 * i + 1]),
-                                   alpha * __uint_as_float(r[4 * i + 2]), alpha * __uint_as_float(r[4 * i + 3]));
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              ptx::tma_store_2d(&tmY, out, ch + 32 * b, row0);
+              ptx::bulk_commit();
+            }
+            __syncwarp();
           }
-        } else if (ch < N) {                               // the whole warp: two tokens at a time, a lane a channel
-          float (*out)[17] = S.out[ew];
-          __syncwarp();
+        } else {                                           // rows of Y that begin anywhere: 16 channels of two tokens at a time
+          float (*f)[17] = reinterpret_cast<float(*)[17]>(out);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[lane][i] = alpha * __uint_as_float(r[i]);
-          __syncwarp();
+          for (int q = 0; q < 4; ++q) {
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[lane][i] = alpha * __uint_as_float(r[16 * q + i]);
+            __syncwarp();
 #pragma unroll 4
-          for (int i = 0; i < 16; ++i) {
-            const int tt = row0 + 2 * i + (lane >> 4), cc = ch + (lane & 15);
-            if (tt < T && cc < N) store_y(Y, (int64_t)tt * N + cc, out[2 * i + (lane >> 4)][lane & 15], out_bf16);
+            for (int i = 0; i < 16; ++i) {
+              const int tt = row0 + 2 * i + (lane >> 4), cc = ch + 16 * q + (lane & 15);
+              if (tt < T && cc < N) store_y(Y, (int64_t)tt * N + cc, f[2 * i + (lane >> 4)][lane & 15], out_bf16);
+            }
           }
+          __syncwarp();
         }
       };
       if (!warp_wait_or_abort(&S.acc_full, (uint32_t)tile & 1u, &S.abort_flag, status)) break;
       ptx::tc_fence_after();
-      constexpr int SH = Geom::SHARED / 32;                // chunks of 16 shared columns a warp takes
-      const int s0 = shared0 + half * (Geom::SHARED / 2);
-      uint32_t r[SH][16];
-#pragma unroll
-      for (int c = 0; c < SH; ++c) ptx::tmem_ld32x16(acc + s0 + 16 * c, r[c]);
-#pragma unroll
-      for (int c = 0; c < SH; ++c) ptx::tmem_ld_wait(r[c]);
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_remote(acc_empty0);
-#pragma unroll
-      for (int c = 0; c < SH; ++c) put(r[c], s0 + 16 * c);
-      constexpr int REST = (PN - Geom::SHARED) / 2;
-      const int o0 = rest0 + half * REST;
 #pragma unroll 1
-      for (int c = 0; c < REST; c += 16) {
-        uint32_t x[16];
+      for (int part = 0; part < 2; ++part) {
+        // columns of the tile: the shared ones are the first accumulator's last 128 and the second's first
+        const int col = (part == (tile & 1) ? PN / 2 : 0) + 64 * half;
+        uint32_t r[64];
+        ptx::tmem_ld32(acc + col, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+        ptx::tmem_ld32(acc + col + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+        ptx::tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(r[0]));
+        ptx::tmem_ld_wait(reinterpret_cast<uint32_t(&)[32]>(r[32]));
+        if (part == 0) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_remote(acc_empty0);
+        }
+        put(r, n0 + col);
         __syncwarp();
-        ptx::tmem_ld32x16(acc + o0 + c, x);
-        ptx::tmem_ld_wait(x);
-        put(x, o0 + c);
       }
     }
+    if (lane == 0) ptx::bulk_wait();                       // every box is in memory
   }
 
   __syncwarp();
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
 
 // ----------------------------------------------------------------------------------------- launch
 struct Fp4Maps {
-  CUtensorMap w, a, sw, sa;
+  CUtensorMap w, a, sw, sa, y;
 };
 
 pq_status make_maps(Fp4Maps* m, const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W,
@@ -610,7 +620,14 @@ pq_status launch_tile(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int64_t t
 }
 
 template <bool NV>
-pq_status launch_pair(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, int sms) {
+pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, int sms) {
+  // Rows of Y that begin on 16 bytes leave by TMA.
+  const bool bulk = c.N % (c.bf16 ? 8 : 4) == 0;
+  m.y = m.a;
+  if (bulk) {
+    const cudaError_t e = make_out_tile_map(&m.y, c.Y, c.T, c.N, c.bf16 != 0);
+    if (e != cudaSuccess) return cuda_fail(e, "output tensor map");
+  }
   constexpr size_t smem = sizeof(PairSmem<NV>) + 1024;
   static_assert(smem <= 232448, "shared memory exceeds 227 KB");
   static std::atomic<bool> done[kMaxDevices];
@@ -621,8 +638,8 @@ pq_status launch_pair(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_til
   cfg.blockDim = dim3(P_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
-  return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_pair_kernel<NV>, m.w, m.a, m.sw, m.sa, c.alpha, c.Y, c.T, c.N, c.steps, c.codes64,
-                                      c.pieces, m_tiles, n_tiles, c.bf16, c.status),
+  return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_pair_kernel<NV>, m.w, m.a, m.sw, m.sa, m.y, c.alpha, c.Y, c.T, c.N, c.steps, c.codes64,
+                                      c.pieces, m_tiles, n_tiles, c.bf16, bulk ? 1 : 0, c.status),
                    "fp4_pair_kernel launch");
 }
 
