@@ -27,6 +27,7 @@ namespace {
 
 constexpr int QF_WARPS = 8;
 constexpr int QF_ROWS = 16;                 // rows a warp takes
+constexpr int PIECE = 512;                  // bytes of a piece of scales
 // mx: blocks whose maximum is below this count as zero, so that 1 / scale stays a normal float32.
 constexpr float kTinyBlock = 7.888609052210118e-31f;     // 2^-100
 
@@ -75,132 +76,155 @@ __device__ __forceinline__ uint32_t block_scale(float m, float unit, float top, 
   }
 }
 
-// G: 0, 64, 128 or 256.  A warp's unit is 16 rows x 128 channels (G = 256: 256).
+// 16 channels (32 bytes) of a row: one load where they begin on 32 bytes, otherwise two.
+__device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* p, bool in, bool aligned32) {
+  if (!in) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0u;
+  } else if (aligned32) {
+    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+        : "l"(p));
+  } else {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+
+// G: 0, 64, 128 or 256.  A warp's unit is 16 rows x 128 channels (G = 256: 256); a block's warps take row_warps units one
+// below the other and QF_WARPS / row_warps side by side.  Blocks go through the units in turn, the loads of the next one
+// under the arithmetic of this one.
 template <int G, bool NV>
-__global__ void __launch_bounds__(32 * QF_WARPS) quant_fp4_kernel(const uint16_t* __restrict__ X, int64_t rows, int64_t ldx,
-                                                                  int D, int units, int64_t col_blocks, int row_warps,
-                                                                  float unit, float top, uint8_t* __restrict__ codes,
-                                                                  uint8_t* __restrict__ scales) {
+__global__ void __launch_bounds__(32 * QF_WARPS, G == 256 ? 1 : 2) quant_fp4_kernel(
+    const uint16_t* __restrict__ X, int rows, int64_t ldx, int D, int units, int col_blocks, int blocks, int row_warps,
+    int aligned32, float unit, float top, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   constexpr int NS = G == 256 ? 4 : 2;                   // spans of 64 channels
   ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int64_t block_row = (int64_t)blockIdx.x / col_blocks;
-  const int u = (int)((int64_t)blockIdx.x % col_blocks) * (QF_WARPS / row_warps) + warp / row_warps;
-  const int64_t r0 = (block_row * row_warps + warp % row_warps) * QF_ROWS;
-  if (u >= units || r0 >= rows) return;                  // whole warps
-  const int c0 = u * 64 * NS + 16 * t;                   // the thread's channels: c0 + 64 s .. + 15
+  const int row_warp = warp % row_warps, col_warp = warp / row_warps, col_warps = QF_WARPS / row_warps;
+  const int pieces = NV ? (D + 63) / 64 : (D + 127) / 128;   // scale words a row
 
-  uint4 x[NS][2][2];
+  // The +-1 matrix: row k <-> index bits (k & 1, k >> 3, lane (k >> 1) & 3), column n of half nn <-> (n & 1, nn, n >> 1).
+  uint32_t b[2][2];
 #pragma unroll
-  for (int s = 0; s < NS; ++s)
+  for (int nn = 0; nn < 2; ++nn)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t r = r0 + g + 8 * h;
-      const bool in = r < rows && c0 + 64 * s < D;
-      const uint4* src = reinterpret_cast<const uint4*>(X + r * ldx + c0 + 64 * s);
-      x[s][h][0] = in ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-      x[s][h][1] = in ? __ldg(src + 1) : make_uint4(0u, 0u, 0u, 0u);
+    for (int hi = 0; hi < 2; ++hi) {
+      const int col = (g & 1) | (nn << 1) | ((g >> 1) << 2);
+      b[nn][hi] = 0x3F803F80u | ((__popc(((hi << 1) | (t << 2)) & col) & 1) << 15) |
+                  ((uint32_t)(__popc((1 | (hi << 1) | (t << 2)) & col) & 1) << 31);
     }
 
-  float v[2][NS][16];
-  if constexpr (G == 0) {
+  uint32_t x[NS][2][8];
+  int br = (int)blockIdx.x / col_blocks, bc = (int)blockIdx.x % col_blocks;
+  const int step_r = (int)gridDim.x / col_blocks, step_c = (int)gridDim.x % col_blocks;
+  auto load = [&]() {                                    // this thread's channels: c0 + 64 s .. + 15
+    const int r0 = (br * row_warps + row_warp) * QF_ROWS, c0 = (bc * col_warps + col_warp) * 64 * NS + 16 * t;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        row_bf16x8(x[s][h][0], v[h][s]);
-        row_bf16x8(x[s][h][1], v[h][s] + 8);
+        const int r = r0 + g + 8 * h;
+        load16(x[s][h], X + (int64_t)r * ldx + c0 + 64 * s, r < rows && c0 + 64 * s < D, aligned32 != 0);
       }
-  } else {
-    // The +-1 matrix: row k <-> index bits (k & 1, k >> 3, lane (k >> 1) & 3), column n of half nn <-> (n & 1, nn, n >> 1).
-    uint32_t b[2][2];
-#pragma unroll
-    for (int nn = 0; nn < 2; ++nn)
-#pragma unroll
-      for (int hi = 0; hi < 2; ++hi) {
-        const int col = (g & 1) | (nn << 1) | ((g >> 1) << 2);
-        b[nn][hi] = 0x3F803F80u | ((__popc(((hi << 1) | (t << 2)) & col) & 1) << 15) |
-                    ((uint32_t)(__popc((1 | (hi << 1) | (t << 2)) & col) & 1) << 31);
-      }
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const uint32_t w0[8] = {x[s][0][0].x, x[s][0][0].y, x[s][0][0].z, x[s][0][0].w,
-                              x[s][0][1].x, x[s][0][1].y, x[s][0][1].z, x[s][0][1].w};
-      const uint32_t w1[8] = {x[s][1][0].x, x[s][1][0].y, x[s][1][0].z, x[s][1][0].w,
-                              x[s][1][1].x, x[s][1][1].y, x[s][1][1].z, x[s][1][1].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int nn = 0; nn < 2; ++nn) {
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma_bf16(c, w0[2 * j], w1[2 * j], w0[2 * j + 1], w1[2 * j + 1], b[nn][0], b[nn][1]);
-          v[0][s][4 * j + 2 * nn] = c[0], v[0][s][4 * j + 2 * nn + 1] = c[1];
-          v[1][s][4 * j + 2 * nn] = c[2], v[1][s][4 * j + 2 * nn + 1] = c[3];
-        }
-    }
-    // Index bits 2 and 3 within the span, 6 and 7 across spans; two neighbours an instruction.
-    auto turn = [](float* a, float* c) {
-      const uint64_t p = ptx::f2_pack(a[0], a[1]), q = ptx::f2_pack(c[0], c[1]);
-      ptx::f2_unpack(ptx::f2_add(p, q), a[0], a[1]);
-      ptx::f2_unpack(ptx::f2_sub(p, q), c[0], c[1]);
-    };
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  };
+  load();
+  for (int at = blockIdx.x; at < blocks; at += gridDim.x) {
+    const int u = bc * col_warps + col_warp, r0 = (br * row_warps + row_warp) * QF_ROWS;
+    const int c0 = u * 64 * NS + 16 * t;
+    float v[2][NS][16];
+    if constexpr (G == 0) {
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int d = 4; d < 16; d <<= 1)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 16; i += 2)
-            if ((i & d) == 0) turn(v[h][s] + i, v[h][s] + i + d);
+          for (int i = 0; i < 8; ++i) {
+            v[h][s][2 * i] = __uint_as_float(x[s][h][i] << 16);
+            v[h][s][2 * i + 1] = __uint_as_float(x[s][h][i] & 0xFFFF0000u);
+          }
+    } else {
 #pragma unroll
-      for (int d = 1; d < G / 64; d <<= 1)
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          if ((s & d) == 0) {
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) turn(v[h][s] + i, v[h][s + d] + i);
+          for (int nn = 0; nn < 2; ++nn) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma_bf16(c, x[s][0][2 * j], x[s][1][2 * j], x[s][0][2 * j + 1], x[s][1][2 * j + 1], b[nn][0], b[nn][1]);
+            v[0][s][4 * j + 2 * nn] = c[0], v[0][s][4 * j + 2 * nn + 1] = c[1];
+            v[1][s][4 * j + 2 * nn] = c[2], v[1][s][4 * j + 2 * nn + 1] = c[3];
           }
     }
-  }
-
-  const int pieces = NV ? (D + 63) / 64 : (D + 127) / 128;   // scale words a row
+    br += step_r, bc += step_c;
+    if (bc >= col_blocks) bc -= col_blocks, ++br;
+    if (at + (int)gridDim.x < blocks) load();
+    if constexpr (G != 0) {
+      // Index bits 2 and 3 within the span, 6 and 7 across spans; two neighbours an instruction.
+      auto turn = [](float* a, float* c) {
+        const uint64_t p = ptx::f2_pack(a[0], a[1]), q = ptx::f2_pack(c[0], c[1]);
+        ptx::f2_unpack(ptx::f2_add(p, q), a[0], a[1]);
+        ptx::f2_unpack(ptx::f2_sub(p, q), c[0], c[1]);
+      };
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t r = r0 + g + 8 * h;
-    uint32_t word[NV ? NS : NS / 2];
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      float* y = v[h][s];
-      float m = max3_nan(fabsf(y[0]), fabsf(y[1]), fabsf(y[2])), m2 = max3_nan(fabsf(y[3]), fabsf(y[4]), fabsf(y[5]));
-      m = max3_nan(m, fabsf(y[6]), fabsf(y[7]));
-      m2 = max3_nan(m2, fabsf(y[8]), fabsf(y[9]));
-      m = max3_nan(m, fabsf(y[10]), fabsf(y[11]));
-      m2 = max3_nan(m2, fabsf(y[12]), fabsf(y[13]));
-      m = max_nan(max3_nan(m, fabsf(y[14]), fabsf(y[15])), m2);
-      if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-      float f;
-      const uint32_t byte = block_scale<NV>(m, unit, top, f);
-      if constexpr (NV) {
-        word[s] = byte << (8 * t);
-      } else {
-        const uint32_t mine = byte << (16 * (s & 1) + 8 * (t >> 1));
-        if (s & 1) word[s / 2] |= mine;
-        else word[s / 2] = mine;
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int d = 4; d < 16; d <<= 1)
+#pragma unroll
+            for (int i = 0; i < 16; i += 2)
+              if ((i & d) == 0) turn(v[h][s] + i, v[h][s] + i + d);
+#pragma unroll
+        for (int d = 1; d < G / 64; d <<= 1)
+#pragma unroll
+          for (int s = 0; s < NS; ++s)
+            if ((s & d) == 0) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) turn(v[h][s] + i, v[h][s + d] + i);
+            }
       }
-      // a value times 0 is not 0 if it is infinite or NaN
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = f != 0.0f ? y[i] * f : 0.0f;
-      if (r < rows && c0 + 64 * s < D)
-        *reinterpret_cast<uint2*>(codes + r * (D / 2) + (c0 + 64 * s) / 2) = make_uint2(e2m1x8(y), e2m1x8(y + 8));
     }
-    uint8_t* place = scales + ((r >> 7) * pieces) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 #pragma unroll
-    for (int k = 0; k < (NV ? NS : NS / 2); ++k) {
-      if constexpr (NV) word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 1);
-      word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 2);
-      const int piece = u * (NV ? NS : NS / 2) + k;
-      if (t == 0 && r < rows && piece < pieces) *reinterpret_cast<uint32_t*>(place + (int64_t)piece * 512) = word[k];
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + g + 8 * h;
+      const bool live = r < rows;
+      uint8_t* const row_codes = codes + (int64_t)r * (D / 2);
+      uint32_t word[NV ? NS : NS / 2];
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        float* y = v[h][s];
+        float m = max3_nan(fabsf(y[0]), fabsf(y[1]), fabsf(y[2])), m2 = max3_nan(fabsf(y[3]), fabsf(y[4]), fabsf(y[5]));
+        m = max3_nan(m, fabsf(y[6]), fabsf(y[7]));
+        m2 = max3_nan(m2, fabsf(y[8]), fabsf(y[9]));
+        m = max3_nan(m, fabsf(y[10]), fabsf(y[11]));
+        m2 = max3_nan(m2, fabsf(y[12]), fabsf(y[13]));
+        m = max_nan(max3_nan(m, fabsf(y[14]), fabsf(y[15])), m2);
+        if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        float f;
+        const uint32_t byte = block_scale<NV>(m, unit, top, f);
+        if constexpr (NV) {
+          word[s] = byte << (8 * t);
+        } else {
+          const uint32_t mine = byte << (16 * (s & 1) + 8 * (t >> 1));
+          if (s & 1) word[s / 2] |= mine;
+          else word[s / 2] = mine;
+        }
+        const uint64_t f2 = ptx::f2_pack(f, f);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(y[i], y[i + 1]), f2), y[i], y[i + 1]);
+        // times 0 an infinity or a NaN is not 0: the codes are chosen, not computed
+        const uint2 q = f != 0.0f ? make_uint2(e2m1x8(y), e2m1x8(y + 8)) : make_uint2(0u, 0u);
+        if (live && c0 + 64 * s < D) *reinterpret_cast<uint2*>(row_codes + (c0 + 64 * s) / 2) = q;
+      }
+      uint8_t* const place = scales + (int64_t)(r >> 7) * pieces * PIECE + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+#pragma unroll
+      for (int k = 0; k < (NV ? NS : NS / 2); ++k) {
+        if constexpr (NV) word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 1);
+        word[k] |= __shfl_xor_sync(0xffffffffu, word[k], 2);
+        const int piece = u * (NV ? NS : NS / 2) + k;
+        if (t == 0 && live && piece < pieces) *reinterpret_cast<uint32_t*>(place + (int64_t)piece * PIECE) = word[k];
+      }
     }
   }
 }
@@ -210,16 +234,19 @@ cudaError_t launch_fp4(const void* X, int64_t rows, int D, int64_t ldx, float fa
                        cudaStream_t stream) {
   constexpr int width = G == 256 ? 256 : 128;
   const int units = (D + width - 1) / width;
-  const int64_t tiles = (rows + QF_ROWS - 1) / QF_ROWS;
+  const int tiles = (int)((rows + QF_ROWS - 1) / QF_ROWS);
   int row_warps = 1;                                     // few rows: a block's warps take other channels instead
   while (row_warps < QF_WARPS && row_warps < tiles) row_warps *= 2;
-  const int64_t col_blocks = (units + QF_WARPS / row_warps - 1) / (QF_WARPS / row_warps);
-  const int64_t blocks = col_blocks * ((tiles + row_warps - 1) / row_warps);
-  if (blocks >= ((int64_t)1 << 31)) return cudaErrorInvalidConfiguration;
+  const int col_blocks = (units + QF_WARPS / row_warps - 1) / (QF_WARPS / row_warps);
+  const int64_t blocks = (int64_t)col_blocks * ((tiles + row_warps - 1) / row_warps);
+  if (blocks >= ((int64_t)1 << 30)) return cudaErrorInvalidConfiguration;
+  const int fit = device_sm_count() * (G == 256 ? 1 : 2);
+  const int aligned32 = (reinterpret_cast<uintptr_t>(X) & 31) == 0 && ldx % 16 == 0;
   const double turn = G == 0 ? 1.0 : 1.0 / std::sqrt((double)G);
   const float unit = (float)(NV ? turn / (double)factor : turn), top = (float)(turn / (6.0 * (double)factor));
-  quant_fp4_kernel<G, NV><<<(unsigned)blocks, 32 * QF_WARPS, 0, stream>>>(static_cast<const uint16_t*>(X), rows, ldx, D, units,
-                                                                          col_blocks, row_warps, unit, top, codes, scales);
+  quant_fp4_kernel<G, NV><<<(unsigned)std::min<int64_t>(blocks, fit), 32 * QF_WARPS, 0, stream>>>(
+      static_cast<const uint16_t*>(X), (int)rows, ldx, D, units, col_blocks, (int)blocks, row_warps, aligned32, unit, top, codes,
+      scales);
   return cudaGetLastError();
 }
 
