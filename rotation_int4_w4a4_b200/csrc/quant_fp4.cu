@@ -64,7 +64,7 @@ __device__ __forceinline__ uint32_t block_scale(float m, float unit, float top, 
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
     const float s = __low2float(*reinterpret_cast<const __half2*>(&h));
-    if (s > 0.0f) f = unit / s;
+    if (s > 0.0f) f = __fdividef(unit, s);
     return b & 0xFFu;
   } else {
     m *= unit;
