@@ -45,7 +45,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 template <bool NV> constexpr int kPieces = NV ? 4 : 2;
 
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
-  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs)) return true;
+  if (ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, 100)) return true;
   *abort_flag = 1;
   atomicOr(status, PQ_DEV_TIMEOUT);
   return false;
@@ -164,18 +164,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
   const uint32_t tmem = S.tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
-      int step = 0;
-      bool ok = true;
-      for (int u = first; u < tiles && ok; u += stride) {
-        int m, n;
-        tile_place(u, m_tiles, n_tiles, m, n);
-        const int m0 = m * 2 * PM + PM * rank, n0 = n * PN;
-        const int sa0 = (m0 / 128) * pieces * 2, sb0 = (n0 / 128) * pieces * 2;
-        for (int kb = 0; kb < steps; ++kb, ++step) {
-          const int s = step % P_STAGES, sk = kb * kPieces<NV> * 2;
-          if (!wait_or_abort(&S.empty[s], ((uint32_t)(step / P_STAGES) & 1u) ^ 1u, &S.abort_flag, status)) { ok = false; break; }
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
+    int step = 0;
+    bool ok = true;
+    for (int u = first; u < tiles && ok; u += stride) {
+      int m, n;
+      tile_place(u, m_tiles, n_tiles, m, n);
+      const int m0 = m * 2 * PM + PM * rank, n0 = n * PN;
+      const int sa0 = (m0 / 128) * pieces * 2, sb0 = (n0 / 128) * pieces * 2;
+      for (int kb = 0; kb < steps; ++kb, ++step) {
+        const int s = step % P_STAGES, sk = kb * kPieces<NV> * 2;
+        if (!(ok = issue_wait(&S.empty[s], ((uint32_t)(step / P_STAGES) & 1u) ^ 1u, &S.abort_flag, status))) break;
+        if (ptx::elect_one()) {
           if (rank == 0) ptx::mbar_arrive_expect_tx(&S.full[s], Geom::TX);
           ptx::tma_load_2d_pair(S.a[s], &tmA, full0 + 8u * s, kb * KB, m0);
           ptx::tma_load_2d_pair(S.b[s], &tmW, full0 + 8u * s, kb * KB, n0 + PN_HALF * rank);
@@ -183,8 +183,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
           ptx::tma_load_2d_pair(S.sb[s][0], &tmSW, full0 + 8u * s, 0, sb0 + sk);
           ptx::tma_load_2d_pair(S.sb[s][1], &tmSW, full0 + 8u * s, 0, sb0 + 2 * pieces + sk);
         }
+        __syncwarp();
       }
-      // Every load issued has landed and every release aimed at this CTA has arrived before it may exit.
+    }
+    // Every load issued has landed and every release aimed at this CTA has arrived before it may exit.
+    if (lane == 0) {
       const int j0 = step > P_STAGES ? step - P_STAGES : 0;
       if (rank == 0)
         for (int j = j0; j < step; ++j) drain_wait(&S.full[j % P_STAGES], (uint32_t)(j / P_STAGES) & 1u);
@@ -196,24 +199,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
       // Descriptors of the first stage; an offset of b bytes adds b / 16 to the address field.
       const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(S.a[0])), db = ptx::smem_desc_sw128(ptx::smem_addr(S.b[0]));
       const uint64_t dsa = ptx::smem_desc_rows16(ptx::smem_addr(S.sa[0])), dsb = ptx::smem_desc_rows16(ptx::smem_addr(S.sb[0]));
-      int step = 0, tile = 0;
-      bool ok = true;
-      for (int u = first; u < tiles && ok; u += stride, ++tile) {
-        if (tile > 0 && !(ok = issue_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u, &S.abort_flag, status))) break;
-        ptx::tc_fence_after();
-        const uint32_t d = tmem + (tile & 1 ? Geom::ACC1 : 0u);
-        for (int kb = 0; kb < steps; ++kb, ++step) {
-          const int s = step % P_STAGES;
-          // The buffer of scales: the products that last read it are done.
-          const int prev = step - Geom::SF_BUFS;
-          if (prev >= 0 && !(ok = issue_wait(&S.empty[prev % P_STAGES], (uint32_t)(prev / P_STAGES) & 1u, &S.abort_flag, status))) break;
-          if (!(ok = issue_wait(&S.full[s], (uint32_t)(step / P_STAGES) & 1u, &S.abort_flag, status))) break;
+      // One elected lane for the whole walk.
+      if (ptx::elect_one()) {
+        int tile = 0, s = 0, b = 0;                        // stage and buffer of scales of the step
+        uint32_t turn = 0;                                 // how often the ring has gone round, its low bit
+        int ps = 0;                                        // stage and turn of the step that last read the buffer
+        uint32_t pturn = 0;
+        int step = 0;
+        bool ok = true;
+        for (int u = first; u < tiles && ok; u += stride, ++tile) {
+          if (tile > 0 && !(ok = wait_or_abort(&S.acc_empty, (uint32_t)(tile - 1) & 1u, &S.abort_flag, status))) break;
           ptx::tc_fence_after();
-          const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)(step % Geom::SF_BUFS) * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
-          const uint64_t a0 = da + (uint64_t)(s * (PM * KB / 16)), b0 = db + (uint64_t)(s * (PN_HALF * KB / 16));
-          const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (2 * Geom::SF / 16));
-          const int live = min(4, codes64 - 4 * kb);      // 64-code products that are not all padding
-          if (ptx::elect_one()) {
+          const uint32_t d = tmem + (tile & 1 ? Geom::ACC1 : 0u);
+          for (int kb = 0; kb < steps; ++kb, ++step) {
+            if (Geom::SF_BUFS < P_STAGES) {                // otherwise the stage's own round trip says so
+              if (step >= Geom::SF_BUFS) {
+                if (!(ok = wait_or_abort(&S.empty[ps], pturn, &S.abort_flag, status))) break;
+                if (++ps == P_STAGES) ps = 0, pturn ^= 1u;
+              }
+            }
+            if (!(ok = wait_or_abort(&S.full[s], turn, &S.abort_flag, status))) break;
+            ptx::tc_fence_after();
+            const uint32_t sa = tmem + Geom::SF_COL + (uint32_t)b * Geom::SF_COLS, sb = sa + 4 * kPieces<NV>;
+            const uint64_t a0 = da + (uint64_t)(s * (PM * KB / 16)), b0 = db + (uint64_t)(s * (PN_HALF * KB / 16));
+            const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (2 * Geom::SF / 16));
+            const int live = min(4, codes64 - 4 * kb);     // 64-code products that are not all padding
 #pragma unroll
             for (int p = 0; p < kPieces<NV>; ++p) {
               ptx::tmem_copy_scales<true>(sa + 4 * p, sa0 + PIECE / 16 * p);
@@ -228,19 +238,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
                                          kb > 0 || k > 0 ? 1u : 0u);
             }
             ptx::umma_commit_pair(&S.empty[s], 0x3);
+            if (++s == P_STAGES) s = 0, turn ^= 1u;
+            if (++b == Geom::SF_BUFS) b = 0;
           }
-          __syncwarp();
+          if (!ok) break;
+          ptx::umma_commit_pair(&S.acc_full, 0x3);
         }
-        if (!ok) break;
-        if (ptx::elect_one()) ptx::umma_commit_pair(&S.acc_full, 0x3);
-        __syncwarp();
-      }
-      if (ptx::elect_one()) ptx::umma_commit_pair(&S.mma_done, 0x1);
-      __syncwarp();
-      if (lane == 0) {
+        ptx::umma_commit_pair(&S.mma_done, 0x1);
         drain_wait(&S.mma_done, 0);
         if (tile > 0) drain_wait(&S.acc_empty, (uint32_t)(tile - 1) & 1u);
       }
+      __syncwarp();
     }
   } else if (warp >= P_EPI_WARP0) {
     // Lane quarter warp % 4 (tokens); 64 of the columns that the accumulators share, then 64 of the others.  Outputs leave by
