@@ -23,6 +23,12 @@
 //   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue (even CTA); warps 4..11: epilogue, two a lane
 //   quarter.
 //
+// Issue bounds the pair kernel before the tensor cores do: a step is 12 scale copies, 4 products and a commit.  From a branch
+// on the lane's number they took 1660 cycles (8192 x 4096 x 14336: 361 us; operands move to uniform registers one by one),
+// from an elected lane with a warp's waits 800 (178 us), with the elected lane walking the steps alone 660 (167 us); the
+// four products take 550.  A warp of its own for the copies costs more in barriers than it saves (185 us), and copies a half
+// step ahead of their products twice as much (326 us: they wait for the products before them).
+//
 // Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains what it has in flight, meets
 // its cluster, frees tensor memory and returns.
 #include <cuda.h>
@@ -61,9 +67,7 @@ __device__ __forceinline__ bool warp_wait_or_abort(uint64_t* bar, uint32_t parit
   return ok != 0;
 }
 
-// Every lane polls: for the warp that issues to the tensor cores, whose operands then stay in uniform registers (an elected
-// lane issues; from one lane's own branch each instruction takes about 80 cycles to get its operands there, and 16 a step
-// are 1300 cycles where the products take 512).
+// Every lane polls, and an elected one acts: its operands stay in uniform registers.
 __device__ __forceinline__ bool issue_wait(uint64_t* bar, uint32_t parity, int* abort_flag, unsigned int* status) {
   if (__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, abort_flag, kWaitNs, 100))) return true;
   if ((threadIdx.x & 31) == 0) {
@@ -469,18 +473,20 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
       }
     }
   } else if (warp == 1) {
-    constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, TM, NP, 0), id1 = ptx::idesc_e2m1(!NV, TM, NP, NV ? 0 : 2);
-    const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(S.a[0])), db = ptx::smem_desc_sw128(ptx::smem_addr(S.b[0]));
-    const uint64_t dsa = ptx::smem_desc_rows16(ptx::smem_addr(S.sa[0])), dsb = ptx::smem_desc_rows16(ptx::smem_addr(S.sb[0]));
-    for (int kb = k0, step = 0; kb < k1; ++kb, ++step) {
-      const int s = step % STAGES;
-      if (!issue_wait(&S.full[s], (uint32_t)(step / STAGES) & 1u, &S.abort_flag, status)) break;
-      ptx::tc_fence_after();
-      const uint32_t sa = tmem + NP + (uint32_t)s * Geom::STAGE_COLS, sb = sa + 4 * kPieces<NV>;
-      const uint64_t a0 = da + (uint64_t)(s * (TM * KB / 16)), b0 = db + (uint64_t)(s * (NP * KB / 16));
-      const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (Geom::SF / 16));
-      const int live = min(4, codes64 - 4 * kb);          // 64-code products that are not all padding
-      if (ptx::elect_one()) {
+    // One elected lane for the whole walk.
+    if (ptx::elect_one()) {
+      constexpr uint32_t id0 = ptx::idesc_e2m1(!NV, TM, NP, 0), id1 = ptx::idesc_e2m1(!NV, TM, NP, NV ? 0 : 2);
+      const uint64_t da = ptx::smem_desc_sw128(ptx::smem_addr(S.a[0])), db = ptx::smem_desc_sw128(ptx::smem_addr(S.b[0]));
+      const uint64_t dsa = ptx::smem_desc_rows16(ptx::smem_addr(S.sa[0])), dsb = ptx::smem_desc_rows16(ptx::smem_addr(S.sb[0]));
+      int s = 0;
+      uint32_t turn = 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!wait_or_abort(&S.full[s], turn, &S.abort_flag, status)) break;
+        ptx::tc_fence_after();
+        const uint32_t sa = tmem + NP + (uint32_t)s * Geom::STAGE_COLS, sb = sa + 4 * kPieces<NV>;
+        const uint64_t a0 = da + (uint64_t)(s * (TM * KB / 16)), b0 = db + (uint64_t)(s * (NP * KB / 16));
+        const uint64_t sa0 = dsa + (uint64_t)(s * (Geom::SF / 16)), sb0 = dsb + (uint64_t)(s * (Geom::SF / 16));
+        const int live = min(4, codes64 - 4 * kb);        // 64-code products that are not all padding
 #pragma unroll
         for (int p = 0; p < kPieces<NV>; ++p) {
           ptx::tmem_copy_scales<false>(sa + 4 * p, sa0 + PIECE / 16 * p);
@@ -491,15 +497,15 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
           const uint32_t col = 4 * (NV ? k : k / 2);
           if (k < live)
             ptx::umma_e2m1<NV, false>(tmem, a0 + 2 * k, b0 + 2 * k, k & 1 ? id1 : id0, sa + col, sb + col,
-                                      step > 0 || k > 0 ? 1u : 0u);
+                                      kb > k0 || k > 0 ? 1u : 0u);
         }
         ptx::umma_commit(&S.empty[s]);
+        if (++s == STAGES) s = 0, turn ^= 1u;
       }
-      __syncwarp();
+      ptx::umma_commit(&S.acc_full);
+      drain_wait(&S.acc_full, 0);
     }
-    if (ptx::elect_one()) ptx::umma_commit(&S.acc_full);
     __syncwarp();
-    if (lane == 0) drain_wait(&S.acc_full, 0);
   } else {
     if (pdl) ptx::griddep_wait();                         // Y may still be read by what ran before
     const int sub = warp & 3;
