@@ -532,6 +532,27 @@ pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq
                            int64_t ldo, void* stream);
 
 /*
+ * pq_kv4_attention_masked — the same with two masks that serving needs, each or both:
+ *   sinks       with a window, the first `sinks` cached tokens stay visible: a row at position p sees the tokens t <= p with
+ *               t > p - window or t < sinks (attention sinks).  Without a window nothing is hidden and sinks says nothing.
+ *   tree        drafted tokens: the new ones of a sequence form a tree instead of a line.  Device uint32 [T][tree_words] or
+ *               NULL: bit j % 32 of word j / 32 of a row says whether it sees its sequence's new token j (its ancestors and
+ *               itself, as a rule; any set will do, and what it holds is all the row sees of the new tokens).  Bits of tokens
+ *               that the sequence does not have are ignored, new tokens behind the last word are seen by nobody.  Of the
+ *               tokens in front of the new ones a row sees all, or with a window those that a row at position
+ *               p = (those tokens) + max(bits, 1) - 1 sees: a drafted token's position is its depth, whatever slot it lies
+ *               in (append it with that position; once a branch is accepted, append its tokens again to their own slots).
+ *   tree_words  1..1024.
+ *   A row that sees nothing becomes 0.  Pages whose tokens lie all behind the sinks and in front of every row's window are not
+ *   looked at, nor are their entries in block_table followed.  Everything else, roundings and scratch included, is as told
+ *   for pq_kv4_attention; a call without sinks and tree is that call.
+ */
+pq_status pq_kv4_attention_masked(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q, const int32_t* q_start,
+                                  const int32_t* seq_lens, const int32_t* block_table, int64_t table_width, int64_t B,
+                                  int64_t T, int64_t max_q, int64_t max_len, float scale, int64_t window, int64_t sinks,
+                                  const uint32_t* tree, int64_t tree_words, void* O, int64_t ldo, void* stream);
+
+/*
  * pq_check_status — synchronises `stream`, then reads and clears the device status words
  * (the plan's, if plan != NULL, and the GEMM's).  Returns PQ_ERR_TIMEOUT if a bounded
  * device-side wait gave up since the last check (the affected output is incomplete),

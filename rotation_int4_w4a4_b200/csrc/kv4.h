@@ -54,6 +54,9 @@ struct Kv4AttnArgs {
   int64_t T;
   float scale;
   int window;                  // 0: none
+  int sinks;                   // first tokens that a window does not hide (0 without a window)
+  const uint32_t* tree;        // [T][tree_words]: which of its sequence's new tokens a row sees; NULL: those up to itself
+  int tree_words;
   uint16_t* O;
   int64_t ldo;
   unsigned int* status;
@@ -66,6 +69,8 @@ cudaError_t launch_kv4_read(const Kv4View& c, const int64_t* slots, int64_t T, u
 struct Partials;
 int64_t kv4_prompt_tiles(const Kv4AttnArgs& a);
 pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream);
+// Calls with sinks or a tree take instances of the kernels of their own.
+inline bool kv4_masked(const Kv4AttnArgs& a) { return a.sinks > 0 || a.tree != nullptr; }
 pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream);
 
 }  // namespace pq

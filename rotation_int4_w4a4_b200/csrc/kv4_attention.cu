@@ -105,9 +105,11 @@ constexpr int AT_MIN_STEPS = 2;         // a share's least length
 constexpr int AT_LEAD = 3;
 
 struct Span {
-  int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first cached token that any row sees
+  int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first token that any row's window holds
   int steps;
+  int sink_steps;                       // MASKED: steps with sinks in front of the window's; the walk skips what lies between
 };
+template <bool MASKED>
 __device__ __forceinline__ Span span_of(const Kv4AttnArgs& a, int b, bool report) {
   Span s;
   new_tokens(a.q_start, (int)a.T, b, s.q0, s.qlen);
@@ -119,10 +121,16 @@ __device__ __forceinline__ Span span_of(const Kv4AttnArgs& a, int b, bool report
   }
   s.lo = a.window > 0 ? max(0, s.n - s.qlen - a.window + 1) : 0;
   s.steps = max(1, (s.n + AT_STEP - 1) / AT_STEP - s.lo / AT_STEP);
+  s.sink_steps = 0;
+  if constexpr (MASKED) {
+    s.sink_steps = min((min(a.sinks, s.n) + AT_STEP - 1) / AT_STEP, s.lo / AT_STEP);
+    s.steps += s.sink_steps;
+  }
   return s;
 }
 
-template <int HD, int NT>
+// MASKED: with sinks, or a tree of drafted tokens.
+template <int HD, int NT, bool MASKED>
 __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Shares shares,
                                                                 int row_tiles) {
   constexpr int R = 8 * NT;              // query rows per tile
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     const int per = (a.B + 32 * AT_WARPS - 1) / (32 * AT_WARPS), b0 = threadIdx.x * per;
     auto length = [&](int b) {
       if (b >= a.B) return (int64_t)0;
-      const Span s = span_of(a, b, false);
+      const Span s = span_of<MASKED>(a, b, false);
       return s.qlen <= 0 ? (int64_t)0 : (int64_t)(AT_LEAD + s.steps) * a.cache.heads * (((int64_t)s.qlen * group + R - 1) / R);
     };
     int64_t mine = 0;
@@ -201,7 +209,7 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     } else {
       b = blockIdx.z;
     }
-    const Span sp = span_of(a, b, threadIdx.x == 0);
+    const Span sp = span_of<MASKED>(a, b, threadIdx.x == 0);
     const int qlen = sp.qlen, n = sp.n, rows = qlen * group;
     if (shares.blocks) {
       const int tiles = (rows + R - 1) / R, length = AT_LEAD + sp.steps;
@@ -225,12 +233,17 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     const int32_t* table = a.table + b * a.table_stride;
     const int r0 = rt * R;
     // positions of the tile's first and last row, and the tokens the tile sees
-    const int p_first = n - qlen + r0 / group, p_last = n - qlen + min(rows - 1, r0 + R - 1) / group;
-    const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
-    const int hi = min(n, p_last + 1);
+    int p_first = n - qlen + r0 / group, p_last = n - qlen + min(rows - 1, r0 + R - 1) / group;
+    int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+    int hi = min(n, p_last + 1);
+    const bool tree = MASKED && a.tree != nullptr;
+    if (tree) lo = sp.lo, hi = n, p_first = n - qlen - 1, p_last = n - 1;   // every row sees up to p_first; none is behind p_last
     const int t_first = sp.lo / AT_STEP * AT_STEP;
-    const int c_lo = max(lo, t_first + step0 * AT_STEP);
-    const int c_hi = step1 == sp.steps ? hi : min(hi, t_first + step1 * AT_STEP);
+    // MASKED walks steps, not tokens: those of the sinks, then those from t_first on.
+    const int c_lo = MASKED ? step0 * AT_STEP : max(lo, t_first + step0 * AT_STEP);
+    const int c_hi = MASKED ? step1 * AT_STEP : step1 == sp.steps ? hi : min(hi, t_first + step1 * AT_STEP);
+    const int sink_end = sp.sink_steps * AT_STEP, gap = t_first - sink_end;
+    auto token_of = [&](int at) { return MASKED ? at + (at >= sink_end ? gap : 0) : at; };
 
     // ---- query operands: B fragment of step (w, h): channels (d, d + 4), (d + 1, d + 5), d = 8 (KW t + w) + 2 h
     uint32_t qb[NT][KS][2];
@@ -283,6 +296,10 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         bq[nt][e] = -8.0f * kCodeUnit * __shfl_sync(0xffffffffu, sum, 4 * (2 * t + e));
         c2[e] = c_log2 * ex2(__shfl_sync(0xffffffffu, eq, 4 * (2 * t + e)) + (24.0f - kQueryExp));
         pos[nt][e] = n - qlen + min(rows - 1, r0 + 8 * nt + 2 * t + e) / group;
+        if (tree && a.window > 0) {
+          const int row = pos[nt][e] - (n - qlen);
+          pos[nt][e] = n - qlen + tree_depth(a.tree + (int64_t)(sp.q0 + row) * a.tree_words, a.tree_words, qlen);
+        }
       }
       cq[nt] = ptx::f2_pack(c2[0], c2[1]);
     }
@@ -313,11 +330,12 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     };
     // Pieces in front of token `from` are not looked at: a window's older pages may be anyone's by now.
     auto locate = [&](int tok0, int from) {
-      all = tok0 + AT_BLOCK <= n && tok0 + 16 > from;
+      // MASKED: of the sinks and from lo on
+      all = tok0 + AT_BLOCK <= n && (tok0 + 16 > from || (MASKED && tok0 + 16 < a.sinks));
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
         const int tok = tok0 + 16 * i;
-        int k = tok + 16 > from ? min(16, n - tok) : 0;
+        int k = tok + 16 > from || (MASKED && tok < a.sinks) ? min(16, n - tok) : 0;
         uint32_t at = 0;
         if (k > 0) {
           const int page = page_of[i];
@@ -381,16 +399,20 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
     };
 
     const int first = (c_lo & ~(AT_BLOCK - 1)) + AT_BLOCK * warp;
-    if (first < c_hi) {
-      look_up(first);
-      locate(first, c_lo);
+    auto inside = [&](int at) { return at < c_hi && (!MASKED || token_of(at) < hi); };
+    if (inside(first)) {
+      look_up(token_of(first));
+      locate(token_of(first), MASKED ? lo : c_lo);
       load_k();
       load_v(vx, vs);
-      look_up(first + AT_BLOCK * AT_WARPS);
+      look_up(token_of(first + AT_BLOCK * AT_WARPS));
     }
-    for (int tok0 = first; tok0 < c_hi; tok0 += AT_BLOCK * AT_WARPS) {
-      const bool whole = all && tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
-                         (a.window <= 0 || tok0 > p_last - a.window);
+    for (int at = first; inside(at); at += AT_BLOCK * AT_WARPS) {
+      const int tok0 = token_of(at);
+      const bool whole = MASKED ? all && tok0 + AT_BLOCK <= hi && tok0 + AT_BLOCK - 1 <= p_first &&
+                                      (a.window <= 0 || tok0 > p_last - a.window || tok0 + AT_BLOCK <= a.sinks)
+                                : all && tok0 >= c_lo && tok0 + AT_BLOCK <= c_hi && tok0 + AT_BLOCK - 1 <= p_first &&
+                                      (a.window <= 0 || tok0 > p_last - a.window);
       float s[AT_TILES][NT][4];
 #pragma unroll
       for (int i = 0; i < AT_TILES; ++i) {
@@ -421,24 +443,32 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int tok = tok0 + 16 * i + 8 * h + g;
-            const bool in = 8 * h + g < lim[i] && tok >= c_lo && tok < c_hi;
+            const bool in = 8 * h + g < lim[i] && (MASKED ? tok < hi : tok >= c_lo && tok < c_hi);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!(in && tok <= pos[nt][e] && (a.window <= 0 || tok > pos[nt][e] - a.window)))
-                  s[i][nt][2 * h + e] = -INFINITY;
+              for (int e = 0; e < 2; ++e) {
+                bool sees = in && (a.window <= 0 || tok > pos[nt][e] - a.window || (MASKED && tok < a.sinks));
+                if (!tree) {
+                  sees = sees && tok <= pos[nt][e];
+                } else if (tok >= n - qlen) {            // a new token: the row's list says
+                  const int row = min(rows - 1, r0 + 8 * nt + 2 * t + e) / group, j = tok - (n - qlen);
+                  sees = in && j < 32 * a.tree_words &&
+                         ((__ldg(a.tree + (int64_t)(sp.q0 + row) * a.tree_words + (j >> 5)) >> (j & 31)) & 1u);
+                }
+                if (!sees) s[i][nt][2 * h + e] = -INFINITY;
+              }
           }
       }
       // the next block's keys and values
-      const int next = tok0 + AT_BLOCK * AT_WARPS;
+      const int next = at + AT_BLOCK * AT_WARPS;
       uint32_t vn[AT_TILES][4][VW];
       float vsn[AT_TILES][2];
-      if (next < c_hi) {
-        locate(next, next);
+      if (inside(next)) {
+        locate(token_of(next), MASKED ? lo : next);
         load_k();
         load_v(vn, vsn);
-        look_up(next + AT_BLOCK * AT_WARPS);
+        look_up(token_of(next + AT_BLOCK * AT_WARPS));
       }
       uint32_t pb[AT_TILES][NT][2];
 #pragma unroll
@@ -728,7 +758,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_shares_kernel(const Kv
     for (; begun; begun &= begun - 1) {
       const int c = c0 + __ffs(begun) - 1;
       const int4 item = shares.begun[c];                 // sequence, head, row tile, last block
-      const Span sp = span_of(a, item.x, false);
+      const Span sp = span_of<false>(a, item.x, false);   // where its rows are
       const int rows = min(R, sp.qlen * group - item.z * R), pieces = item.w - c + 1;
       auto join = [&](int r, auto parts) {
         const int at = item.z * R + r;
@@ -768,7 +798,8 @@ template <int HD, int NT>
 cudaError_t launch_rows(const Kv4AttnArgs& a, const Shares& shares, int row_tiles, int64_t max_rows, cudaStream_t stream) {
   const dim3 grid = shares.blocks ? dim3((unsigned)shares.blocks)
                                   : dim3((unsigned)row_tiles, (unsigned)a.cache.heads, (unsigned)a.B);
-  kv4_rows_kernel<HD, NT><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
+  if (kv4_masked(a)) kv4_rows_kernel<HD, NT, true><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
+  else kv4_rows_kernel<HD, NT, false><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !shares.blocks) return e;
   // Joining blocks: a few for each item, if those are fewer than shares.
@@ -784,6 +815,8 @@ cudaError_t launch_rows(const Kv4AttnArgs& a, const Shares& shares, int row_tile
 }  // namespace
 
 pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream) {
+  // What a masked call walks of a sequence: its window and its sinks, in steps of 128.
+  if (kv4_masked(a) && a.window > 0) max_len = std::min<int64_t>(max_len, (int64_t)a.window + max_q + a.sinks + 256);
   const int group = a.heads_q / a.cache.heads;
   const int64_t max_rows = max_q * group;
   const int sms = device_sm_count();

@@ -25,6 +25,24 @@ __device__ __forceinline__ void new_tokens(const int32_t* q_start, int T, int b,
   qlen = max(0, min(max(q_start[b + 1], 0), T) - q0);
 }
 
+// The row's part of a tree: bits j0 .. j0 + 63 of its list, 0 outside it (j0 may be negative).
+__device__ __forceinline__ uint64_t tree_bits(const uint32_t* list, int words, int j0) {
+  const int k = j0 >> 5;                                 // floor
+  uint32_t w[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) w[i] = k + i >= 0 && k + i < words ? __ldg(list + k + i) : 0u;
+  const uint32_t lo = __funnelshift_r(w[0], w[1], j0 & 31), hi = __funnelshift_r(w[1], w[2], j0 & 31);
+  return (uint64_t)hi << 32 | lo;
+}
+
+// How far behind the first of `qlen` new tokens a drafted one lies: its list holds its ancestors and itself (an empty one: 0).
+__device__ __forceinline__ int tree_depth(const uint32_t* list, int words, int qlen) {
+  int n = 0;
+  for (int w = 0; w < words && 32 * w < qlen; ++w)
+    n += __popc(__ldg(list + w) & (qlen - 32 * w >= 32 ? 0xffffffffu : (1u << (qlen - 32 * w)) - 1));
+  return max(n, 1) - 1;
+}
+
 // (x & mask) ^ flip in one instruction (of two constants the compiler would make two).
 __device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
   uint32_t y;

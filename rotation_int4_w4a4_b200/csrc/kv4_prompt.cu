@@ -335,13 +335,15 @@ __device__ __forceinline__ uint4 bf16x8(const float* o, float f) {
 
 // Whether every row of the block sees all of the 32 tokens from tok0 on: known from the lengths alone.
 struct Interior {
-  int c_lo, c_hi, p_first, p_last, window;
+  int c_lo, c_hi, p_first, p_last, window, sinks;
   __device__ __forceinline__ bool operator()(int tok0) const {
-    return tok0 >= c_lo && tok0 + 32 <= c_hi && tok0 + 31 <= p_first && (window <= 0 || tok0 > p_last - window);
+    return tok0 >= c_lo && tok0 + 32 <= c_hi && tok0 + 31 <= p_first &&
+           (window <= 0 || tok0 > p_last - window || tok0 + 32 <= sinks);
   }
 };
 
-template <int HD>
+// MASKED: with sinks, or a tree of drafted tokens.
+template <int HD, bool MASKED>
 __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4AttnArgs a, const Partials part) {
   using Smem = PromptSmem<HD>;
   constexpr int HB = HD / 2;
@@ -361,15 +363,34 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     if (threadIdx.x == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
   }
   const int last_row = min(w.rows, w.r0 + 2 * PT) - 1;
-  const int p_first = n - w.qlen + w.r0 / group, p_last = n - w.qlen + last_row / group;
-  const int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
-  const int hi = min(n, p_last + 1);
-  const int c_lo = part.chunks > 1 ? max(lo, w.chunk * part.chunk_len) : lo;
-  const int c_hi = part.chunks > 1 && w.chunk < part.chunks - 1 ? min(hi, (w.chunk + 1) * part.chunk_len) : hi;
-  const int j0 = c_lo / PT;
-  const int steps = c_hi > c_lo ? (c_hi + PT - 1) / PT - j0 : 0;
+  int p_first = n - w.qlen + w.r0 / group, p_last = n - w.qlen + last_row / group;
+  int lo = a.window > 0 ? max(0, p_first - a.window + 1) : 0;
+  int hi = min(n, p_last + 1);
+  const int old = n - w.qlen;                            // tokens in front of the new ones
+  const bool tree = MASKED && a.tree != nullptr;
+  if (tree) {                                            // every row sees up to p_first; none is behind p_last
+    lo = a.window > 0 ? max(0, old - a.window + 1) : 0;
+    hi = n, p_first = old - 1, p_last = n - 1;
+  }
+  int c_lo, c_hi, j0, steps, sink_steps = 0, gap = 0;
+  if constexpr (MASKED) {
+    // The walk: steps with sinks, then those from lo on; a chunk takes its part of it.  Step j begins at token
+    // (j0 + j) PT, behind the sinks' steps gap tokens later.
+    sink_steps = min((min(a.sinks, hi) + PT - 1) / PT, lo / PT);
+    gap = (lo / PT - sink_steps) * PT;
+    const int all = sink_steps + max(0, (hi + PT - 1) / PT - lo / PT), per = part.chunk_len / PT;
+    j0 = part.chunks > 1 ? w.chunk * per : 0;
+    steps = max(0, (part.chunks > 1 && w.chunk < part.chunks - 1 ? min(all, j0 + per) : all) - j0);
+    c_lo = 0, c_hi = hi;
+  } else {
+    c_lo = part.chunks > 1 ? max(lo, w.chunk * part.chunk_len) : lo;
+    c_hi = part.chunks > 1 && w.chunk < part.chunks - 1 ? min(hi, (w.chunk + 1) * part.chunk_len) : hi;
+    j0 = c_lo / PT;
+    steps = c_hi > c_lo ? (c_hi + PT - 1) / PT - j0 : 0;
+  }
+  auto first_of = [&](int j) { return (j0 + j) * PT + (MASKED && j0 + j >= sink_steps ? gap : 0); };
   const int tiles = w.rows - w.r0 > PT ? 2 : 1;          // row tiles that hold rows
-  const Interior interior{c_lo, c_hi, p_first, p_last, a.window};
+  const Interior interior{c_lo, c_hi, p_first, p_last, a.window, MASKED ? a.sinks : 0};
 
   if (threadIdx.x == 32) {
     ptx::mbar_init(&S.q_full, 8);
@@ -528,8 +549,21 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         // each sum without its values' power of two
         l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
       } else {
-        const int pos = n - w.qlen + rr / group;
-        const uint64_t bits = token_bits((j0 + j) * PT + t0, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1));
+        int pos = n - w.qlen + rr / group;
+        uint64_t bits;
+        if constexpr (MASKED) {
+          const int first = first_of(j) + t0;
+          const uint32_t* list = tree ? a.tree + (int64_t)(w.q0 + rr / group) * a.tree_words : nullptr;
+          if (tree && a.window > 0) pos = old + tree_depth(list, a.tree_words, w.qlen);
+          const int last = tree ? old - 1 : min(pos, c_hi - 1);
+          bits = token_bits(first, a.window > 0 ? max(pos - a.window + 1, 0) : 0, last) | token_bits(first, 0, min(a.sinks - 1, last));
+          if (tree && first + HT > old) {
+            const uint64_t mine = tree_bits(list, a.tree_words, first - old);
+            bits |= first >= old ? mine : mine & (~0ull << (old - first));
+          }
+        } else {
+          bits = token_bits(first_of(j) + t0, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1));
+        }
         const uint32_t sa = (uint32_t)bits & va, sb = (uint32_t)(bits >> 32) & vb;
         const float4* ks = reinterpret_cast<const float4*>(S.ks[sc]) + t0 / 4;
         const float4* vs = reinterpret_cast<const float4*>(S.vs[sc]) + t0 / 4;
@@ -629,9 +663,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     float ks, vs;
     int64_t at = -1, at_next = -1;                       // cache row of the token (-1: none), one step ahead
     auto locate = [&](int j) {
-      const int tok = (j0 + j) * PT + t;
+      const int tok = first_of(j) + t;
       at_next = -1;
-      if (tok >= c_lo && tok < c_hi && j < steps) {
+      if (tok >= c_lo && tok < c_hi && j < steps && (!MASKED || tok >= lo || tok < a.sinks)) {
         const int page = table[tok >> ps];
         if (page < 0 || page >= a.cache.pages) atomicOr(a.status, PQ_DEV_BAD_INDEX);
         else at_next = (((int64_t)page * a.cache.heads + w.kvh) << ps) + (tok & ((1 << ps) - 1));
@@ -658,7 +692,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const float k1 = finite_or_0(ks);
       const float k_least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(k1 == 0.0f ? INFINITY : k1)));
       const float v_least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(finite_or_0(vs))));
-      const bool scaled = interior((j0 + j) * PT + 32 * wq) && km <= kScaleSpread * k_least && vm < kScaleSpread * v_least;
+      const bool scaled = interior(first_of(j) + 32 * wq) && km <= kScaleSpread * k_least && vm < kScaleSpread * v_least;
       const float ke = scale_exponent(km), ve = scale_exponent(vm);
       S.ks[sc][t] = scaled ? ex2(ke) : ks;
       S.vs[sc][t] = scaled ? ex2(ve) : vs;
@@ -802,16 +836,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   }
 }
 
-template <int HD>
+template <int HD, bool MASKED>
 pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tiles, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PromptSmem<HD>) + 1024;
   static_assert(smem <= 232448, "shared memory exceeds 227 KB");
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(kv4_prompt_kernel<HD>), (int)smem, done);
+  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(kv4_prompt_kernel<HD, MASKED>), (int)smem, done);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_prompt_kernel attributes");
   const int64_t grid = tiles * a.cache.heads * part.chunks;
   if (grid >= ((int64_t)1 << 31)) { set_error("too many query tiles for one call"); return PQ_ERR_INVALID_ARG; }
-  kv4_prompt_kernel<HD><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);
+  kv4_prompt_kernel<HD, MASKED><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);
   return cuda_fail(cudaGetLastError(), "kv4_prompt_kernel launch");
 }
 
@@ -824,7 +858,9 @@ int64_t kv4_prompt_tiles(const Kv4AttnArgs& a) {
 
 pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream) {
   const int64_t tiles = kv4_prompt_tiles(a);
-  return a.cache.head_dim == 128 ? launch_prompt<128>(a, part, tiles, stream) : launch_prompt<64>(a, part, tiles, stream);
+  if (kv4_masked(a))
+    return a.cache.head_dim == 128 ? launch_prompt<128, true>(a, part, tiles, stream) : launch_prompt<64, true>(a, part, tiles, stream);
+  return a.cache.head_dim == 128 ? launch_prompt<128, false>(a, part, tiles, stream) : launch_prompt<64, false>(a, part, tiles, stream);
 }
 
 }  // namespace pq

@@ -326,10 +326,14 @@ extern "C" pq_status pq_kv4_read(const pq_kv4_cache* cache, const int64_t* slots
                    "pq_kv4_read launch");
 }
 
-extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q,
-                                      const int32_t* q_start, const int32_t* seq_lens, const int32_t* block_table,
-                                      int64_t table_width, int64_t B, int64_t T, int64_t max_q, int64_t max_len,
-                                      float scale, int64_t window, void* O, int64_t ldo, void* stream) {
+namespace {
+
+constexpr int64_t kMaxTreeWords = 1024;          // lists of 32768 new tokens
+
+pq_status attention_call(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q, const int32_t* q_start,
+                         const int32_t* seq_lens, const int32_t* block_table, int64_t table_width, int64_t B, int64_t T,
+                         int64_t max_q, int64_t max_len, float scale, int64_t window, int64_t sinks, const uint32_t* tree,
+                         int64_t tree_words, void* O, int64_t ldo, void* stream) {
   clear_error();
   Kv4AttnArgs a = {};
   pq_status st = check_cache(cache, &a.cache);
@@ -354,6 +358,11 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
     return PQ_ERR_INVALID_ARG;
   }
   if (window < 0 || window >= ((int64_t)1 << 31)) { set_error("window=%lld must be in 0..2^31-1", (long long)window); return PQ_ERR_INVALID_ARG; }
+  if (sinks < 0 || sinks >= ((int64_t)1 << 31)) { set_error("sinks=%lld must be in 0..2^31-1", (long long)sinks); return PQ_ERR_INVALID_ARG; }
+  if (tree && (!aligned(tree, 4) || tree_words < 1 || tree_words > kMaxTreeWords)) {
+    set_error("a tree needs 4-byte alignment and tree_words=%lld in 1..%lld", (long long)tree_words, (long long)kMaxTreeWords);
+    return PQ_ERR_INVALID_ARG;
+  }
   if (!std::isfinite(scale)) { set_error("scale must be finite"); return PQ_ERR_INVALID_ARG; }
   const cudaError_t e = gemm_status_address(&a.status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
@@ -367,8 +376,30 @@ extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, 
   a.T = T;
   a.scale = scale;
   a.window = (int)std::min(window, kMaxTokens);          // a wider one hides nothing
+  a.sinks = window > 0 ? (int)std::min(sinks, kMaxTokens) : 0;
+  a.tree = tree;
+  a.tree_words = tree ? (int)tree_words : 0;
   a.O = static_cast<uint16_t*>(O);
   a.ldo = ldo;
   // Bounds beyond what a call can hold say no more than that (and would wrap when multiplied with the heads).
   return kv4_attention_run(a, std::min(max_q, kMaxRows), std::min(max_len, kMaxTokens), reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q,
+                                      const int32_t* q_start, const int32_t* seq_lens, const int32_t* block_table,
+                                      int64_t table_width, int64_t B, int64_t T, int64_t max_q, int64_t max_len,
+                                      float scale, int64_t window, void* O, int64_t ldo, void* stream) {
+  return attention_call(cache, Q, ldq, heads_q, q_start, seq_lens, block_table, table_width, B, T, max_q, max_len, scale, window,
+                        /*sinks=*/0, /*tree=*/nullptr, /*tree_words=*/0, O, ldo, stream);
+}
+
+extern "C" pq_status pq_kv4_attention_masked(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q,
+                                             const int32_t* q_start, const int32_t* seq_lens, const int32_t* block_table,
+                                             int64_t table_width, int64_t B, int64_t T, int64_t max_q, int64_t max_len,
+                                             float scale, int64_t window, int64_t sinks, const uint32_t* tree,
+                                             int64_t tree_words, void* O, int64_t ldo, void* stream) {
+  return attention_call(cache, Q, ldq, heads_q, q_start, seq_lens, block_table, table_width, B, T, max_q, max_len, scale, window,
+                        sinks, tree, tree_words, O, ldo, stream);
 }

@@ -35,7 +35,7 @@ EXPORTS = ("pq_select_pairs", "pq_make_plan", "pq_destroy_plan", "pq_transform_q
            "pq_rrs_prepare", "pq_rrs_transform_quant", "pq_rrs_pack_weights", "pq_rrs_gemm",
            "pq_quant_rows8", "pq_w8a8_gemm", "pq_w8a8_linear",
            "pq_fp4_scale_bytes", "pq_quant_fp4", "pq_fp4_gemm", "pq_fp4_linear",
-           "pq_kv4_append", "pq_kv4_read", "pq_kv4_attention",
+           "pq_kv4_append", "pq_kv4_read", "pq_kv4_attention", "pq_kv4_attention_masked",
            "pq_check_status",
            "pq_selftest_wait_timeout", "pq_status_string", "pq_last_error")
 
@@ -101,6 +101,9 @@ lib.pq_kv4_read.restype = _i32
 lib.pq_kv4_attention.argtypes = [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _i64, _vp,
                                  _i64, _vp]
 lib.pq_kv4_attention.restype = _i32
+lib.pq_kv4_attention_masked.argtypes = [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _i64, _i64,
+                                        _vp, _i64, _vp, _i64, _vp]
+lib.pq_kv4_attention_masked.restype = _i32
 lib.pq_selftest_wait_timeout.argtypes = [_u64, _vp]
 lib.pq_selftest_wait_timeout.restype = _i32
 lib.pq_check_status.argtypes = [_vp, _vp]
@@ -662,6 +665,32 @@ def pq_kv4_attention(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_
                                 _on(block_table, "block_table", "i32", i32, B * width, dev), width, B, T, max_q, max_len,
                                 hd ** -0.5 if scale is None else scale, window, op, ldo, _raw_stream(stream, dev, torch)),
            "pq_kv4_attention")
+
+
+def pq_kv4_attention_masked(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_q, max_len, scale=None, window=0, sinks=0,
+                            tree=None, stream=None) -> None:
+    """:func:`pq_kv4_attention` with sinks (under a window the first `sinks` tokens stay visible) and a tree of drafted tokens
+    (int32 [T, words]: bit j of a row's words, the lowest first, says that it sees its sequence's new token j)."""
+    dev, torch = _here()
+    T, hd = Q.shape[0], cache.head_dim
+    wq = _query_width(Q, hd)
+    qp, ldq = _rows_of(Q, "Q", wq, T, dev, torch)
+    op, ldo = _rows_of(O, "O", wq, T, dev, torch)
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected [sequences, pages]")
+    B, width = block_table.shape
+    i32 = torch.int32
+    words = 0
+    if tree is not None:
+        if tree.dim() != 2 or tree.shape[0] != T:
+            raise ValueError(f"tree: expected [{T}, words]")
+        words = tree.shape[1]
+    _check(lib.pq_kv4_attention_masked(cache.on(dev), qp, ldq, wq // hd, _on(q_start, "q_start", "i32", i32, B + 1, dev),
+                                       _on(seq_lens, "seq_lens", "i32", i32, B, dev),
+                                       _on(block_table, "block_table", "i32", i32, B * width, dev), width, B, T, max_q,
+                                       max_len, hd ** -0.5 if scale is None else scale, window, sinks,
+                                       _on(tree, "tree", "i32", i32, T * words, dev), words, op, ldo,
+                                       _raw_stream(stream, dev, torch)), "pq_kv4_attention_masked")
 
 
 def pq_w4a4_gemm_launch_count_g(T: int, N: int, D: int, g: int) -> int:
