@@ -437,27 +437,46 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
                                        ptx::f2_mul(ptx::f2_pack(ks[i][h], ks[i][h]), cq[nt])),
                            s[i][nt][2 * h], s[i][nt][2 * h + 1]);
       }
-      if (!whole) {
+      if (MASKED && !whole) {
+        // The tokens of the block that each of the thread's rows sees, a bit each: of the tokens in front of the new ones, and of
+        // the new ones up to the row or by its list.
+        const int old = n - qlen;
+        uint32_t exist = 0u;
+#pragma unroll
+        for (int i = 0; i < AT_TILES; ++i) exist |= ((1u << max(0, lim[i])) - 1) << (16 * i);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int last = tree ? old - 1 : min(pos[nt][e], hi - 1);
+            uint32_t sees = token_bits32(tok0, a.window > 0 ? max(0, pos[nt][e] - a.window + 1) : 0, last) |
+                            token_bits32(tok0, 0, min(a.sinks - 1, last));
+            if (tree && tok0 + AT_BLOCK > old) {
+              const int row = min(rows - 1, r0 + 8 * nt + 2 * t + e) / group;
+              const uint32_t mine = (uint32_t)tree_bits(a.tree + (int64_t)(sp.q0 + row) * a.tree_words, a.tree_words, tok0 - old);
+              sees |= tok0 >= old ? mine : mine & (~0u << (old - tok0));
+            }
+            sees = (sees & exist) >> g;
+#pragma unroll
+            for (int i = 0; i < AT_TILES; ++i)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (!((sees >> (16 * i + 8 * h)) & 1u)) s[i][nt][2 * h + e] = -INFINITY;
+          }
+      }
+      if (!MASKED && !whole) {
 #pragma unroll
         for (int i = 0; i < AT_TILES; ++i)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int tok = tok0 + 16 * i + 8 * h + g;
-            const bool in = 8 * h + g < lim[i] && (MASKED ? tok < hi : tok >= c_lo && tok < c_hi);
+            const bool in = 8 * h + g < lim[i] && tok >= c_lo && tok < c_hi;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                bool sees = in && (a.window <= 0 || tok > pos[nt][e] - a.window || (MASKED && tok < a.sinks));
-                if (!tree) {
-                  sees = sees && tok <= pos[nt][e];
-                } else if (tok >= n - qlen) {            // a new token: the row's list says
-                  const int row = min(rows - 1, r0 + 8 * nt + 2 * t + e) / group, j = tok - (n - qlen);
-                  sees = in && j < 32 * a.tree_words &&
-                         ((__ldg(a.tree + (int64_t)(sp.q0 + row) * a.tree_words + (j >> 5)) >> (j & 31)) & 1u);
-                }
-                if (!sees) s[i][nt][2 * h + e] = -INFINITY;
-              }
+              for (int e = 0; e < 2; ++e)
+                if (!(in && tok <= pos[nt][e] && (a.window <= 0 || tok > pos[nt][e] - a.window)))
+                  s[i][nt][2 * h + e] = -INFINITY;
           }
       }
       // the next block's keys and values

@@ -25,6 +25,14 @@ __device__ __forceinline__ void new_tokens(const int32_t* q_start, int T, int b,
   qlen = max(0, min(max(q_start[b + 1], 0), T) - q0);
 }
 
+// Bits of the 32 tokens from `first` on that lie in [lo, hi].
+__device__ __forceinline__ uint32_t token_bits32(int first, int lo, int hi) {
+  const int a = lo - first, b = hi - first;
+  const uint32_t upto = b < 0 ? 0u : b >= 31 ? ~0u : (2u << b) - 1;
+  const uint32_t from = a <= 0 ? ~0u : a > 31 ? 0u : ~0u << a;
+  return upto & from;
+}
+
 // The row's part of a tree: bits j0 .. j0 + 63 of its list, 0 outside it (j0 may be negative).
 __device__ __forceinline__ uint64_t tree_bits(const uint32_t* list, int words, int j0) {
   const int k = j0 >> 5;                                 // floor
