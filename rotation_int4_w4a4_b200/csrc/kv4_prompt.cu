@@ -374,13 +374,21 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   }
   int c_lo, c_hi, j0, steps, sink_steps = 0, gap = 0;
   if constexpr (MASKED) {
-    // The walk: steps with sinks, then those from lo on; a chunk takes its part of it.  Step j begins at token
-    // (j0 + j) PT, behind the sinks' steps gap tokens later.
+    // The walk: steps with sinks, then those from lo on.  Step j begins at token (j0 + j) PT, behind the sinks' steps gap
+    // tokens later.  It is cut into as many equal parts as it has chunk lengths; a block behind the last has nothing to do.
     sink_steps = min((min(a.sinks, hi) + PT - 1) / PT, lo / PT);
     gap = (lo / PT - sink_steps) * PT;
-    const int all = sink_steps + max(0, (hi + PT - 1) / PT - lo / PT), per = part.chunk_len / PT;
-    j0 = part.chunks > 1 ? w.chunk * per : 0;
-    steps = max(0, (part.chunks > 1 && w.chunk < part.chunks - 1 ? min(all, j0 + per) : all) - j0);
+    const int all = sink_steps + max(0, (hi + PT - 1) / PT - lo / PT);
+    const int parts = part.chunks > 1 ? min(part.chunks, max(1, (all * PT + part.chunk_len - 1) / part.chunk_len)) : 1;
+    if (w.chunk >= parts) {
+      const int r = w.r0 + threadIdx.x;
+      if (threadIdx.x < 2 * PT && r < w.rows)
+        part.ml[((int64_t)w.chunk * a.T + w.q0 + r / group) * a.heads_q + w.kvh * group + r % group] = make_float2(-INFINITY, 0.0f);
+      return;
+    }
+    const int per = (all + parts - 1) / parts;
+    j0 = min(all, w.chunk * per);
+    steps = min(all, j0 + per) - j0;
     c_lo = 0, c_hi = hi;
   } else {
     c_lo = part.chunks > 1 ? max(lo, w.chunk * part.chunk_len) : lo;
