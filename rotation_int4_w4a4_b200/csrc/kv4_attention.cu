@@ -103,6 +103,7 @@ constexpr int AT_SEQS = 1024;           // sequences whose lengths a block can a
 constexpr int AT_MIN_STEPS = 2;         // a share's least length
 // Steps that an item's beginning and end cost, ahead of its own on the line (64 users, us: 0 steps 95, 1 85, 3 69, 6 73).
 constexpr int AT_LEAD = 3;
+constexpr int AT_CLUSTER = 8;           // blocks of a cluster that shares an item at most
 
 struct Span {
   int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first token that any row's window holds
@@ -132,7 +133,7 @@ __device__ __forceinline__ Span span_of(const Kv4AttnArgs& a, int b, bool report
 // MASKED: with sinks, or a tree of drafted tokens.
 template <int HD, int NT, bool MASKED>
 __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kernel(const Kv4AttnArgs a, const Shares shares,
-                                                                int row_tiles) {
+                                                                int row_tiles, int cluster) {
   constexpr int R = 8 * NT;              // query rows per tile
   constexpr int KS = HD / 16;            // channel steps of the first product = channel tiles of the second
   constexpr int KW = HD / 32;            // words of a token's key a thread holds
@@ -146,6 +147,8 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
   const int g = lane >> 2, t = lane & 3;
   const int group = a.heads_q / a.cache.heads;
   const int ps = a.cache.page_shift;
+  // MASKED: an item may be cut over the blocks of a cluster, which join their results over its shared memory.
+  const int rank = MASKED && cluster > 1 ? (int)ptx::cluster_ctarank() : 0;
   const float c_log2 = a.scale * kLog2e;
   // Shares: where each sequence's items begin on the line, and this block's part of it.
   __shared__ int64_t sm_first[AT_SEQS + 1];
@@ -224,10 +227,15 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
       if (step1 <= 0) break;                             // the share ends in the lead: the next block begins the item
     } else {
       kvh = blockIdx.y;
-      rt = blockIdx.x + done * row_tiles;
-      if ((int64_t)rt * R >= rows) break;
+      rt = (MASKED && cluster > 1 ? blockIdx.x / cluster : blockIdx.x) + done * row_tiles;
+      if ((int64_t)rt * R >= rows) break;                // the whole cluster agrees
       step0 = 0;
       step1 = sp.steps;
+      if (MASKED && cluster > 1) {
+        const int per = (sp.steps + cluster - 1) / cluster;
+        step0 = min(sp.steps, rank * per);
+        step1 = min(sp.steps, step0 + per);
+      }
     }
     if (threadIdx.x == 0) sm_item[done & 1] = Item{line, b, kvh, rt, step0, step1, sp.steps, sp.q0, rows};
     const int32_t* table = a.table + b * a.table_stride;
@@ -664,7 +672,12 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
       const int at = it.rt * R + r;
       const int64_t token = it.q0 + at / group;
       const int head = it.kvh * group + at % group;
-      if (entire) {
+      if (MASKED && cluster > 1) {                       // the block's result, in place of its first warp's
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < E; ++i) sm_o[0][r][E * lane + i] = y[i];
+        if (lane == 0) sm_m[0][r] = mx, sm_l[0][r] = sum;
+      } else if (entire) {
         finish_row<HD>(y, sum, a.cache.rotate_v, a.O + token * a.ldo + head * HD, lane);
       } else {
         const int64_t row = (int64_t)(2 * blockIdx.x + (it.step0 == 0)) * R + r;
@@ -675,7 +688,43 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
         }
       }
     }
-    if (threadIdx.x == 0 && it.step0 == 0 && !entire)
+    if (MASKED && cluster > 1) {
+      ptx::cluster_sync();                               // every block's rows are in its shared memory
+      constexpr int E = HD / 32;
+      for (int r = rank + cluster * warp; r < R && it.rt * R + r < it.rows; r += cluster * AT_WARPS) {
+        const uint32_t m_at = ptx::smem_addr(&sm_m[0][r]), l_at = ptx::smem_addr(&sm_l[0][r]), o_at = ptx::smem_addr(&sm_o[0][r][E * lane]);
+        float mb = -INFINITY, lb = 0.0f;                 // a block a lane
+        if (lane < cluster) {
+          mb = ptx::ld_cluster_f32(ptx::mapa_shared(m_at, (uint32_t)lane));
+          lb = ptx::ld_cluster_f32(ptx::mapa_shared(l_at, (uint32_t)lane));
+        }
+        float v[AT_CLUSTER][E];
+#pragma unroll
+        for (int c = 0; c < AT_CLUSTER; ++c)
+#pragma unroll
+          for (int i = 0; i < E; ++i) v[c][i] = c < cluster ? ptx::ld_cluster_f32(ptx::mapa_shared(o_at, (uint32_t)c) + 4 * i) : 0.0f;
+        float mx = mb;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mu = mx == -INFINITY ? 0.0f : mx;
+        // a block that saw nothing counts for nothing; one whose scores are all NaN keeps its NaN
+        const float f = mb == -INFINITY ? (lb == 0.0f ? 0.0f : 1.0f) : ex2(mb - mu);
+        float sum = 0.0f, y[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < AT_CLUSTER; ++c) {
+          const float fc = __shfl_sync(0xffffffffu, f, c);
+          sum = fmaf(__shfl_sync(0xffffffffu, lb, c), fc, sum);
+#pragma unroll
+          for (int i = 0; i < E; ++i) y[i] = fmaf(v[c][i], fc, y[i]);
+        }
+        const int at = it.rt * R + r;
+        finish_row<HD>(y, sum, a.cache.rotate_v, a.O + (it.q0 + at / group) * a.ldo + (it.kvh * group + at % group) * HD, lane);
+      }
+      ptx::cluster_sync();                               // nobody leaves, or goes on, while its rows are read
+    }
+    if (threadIdx.x == 0 && it.step0 == 0 && !entire && !(MASKED && cluster > 1))
       shares.begun[blockIdx.x] = make_int4(it.b, it.kvh, it.rt, (int)((it.next + (it.steps - it.step1) - 1) / sm_share));
   }
 }
@@ -814,11 +863,25 @@ cudaError_t launch_join(const void* kernel, dim3 grid, void** args, cudaStream_t
 }
 
 template <int HD, int NT>
-cudaError_t launch_rows(const Kv4AttnArgs& a, const Shares& shares, int row_tiles, int64_t max_rows, cudaStream_t stream) {
+cudaError_t launch_rows(const Kv4AttnArgs& a, const Shares& shares, int row_tiles, int64_t max_rows, int cluster,
+                        cudaStream_t stream) {
   const dim3 grid = shares.blocks ? dim3((unsigned)shares.blocks)
-                                  : dim3((unsigned)row_tiles, (unsigned)a.cache.heads, (unsigned)a.B);
-  if (kv4_masked(a)) kv4_rows_kernel<HD, NT, true><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
-  else kv4_rows_kernel<HD, NT, false><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles);
+                                  : dim3((unsigned)(row_tiles * cluster), (unsigned)a.cache.heads, (unsigned)a.B);
+  if (cluster > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(32 * AT_WARPS, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv4_rows_kernel<HD, NT, true>, a, shares, row_tiles, cluster);
+  }
+  if (kv4_masked(a)) kv4_rows_kernel<HD, NT, true><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles, 1);
+  else kv4_rows_kernel<HD, NT, false><<<grid, 32 * AT_WARPS, 0, stream>>>(a, shares, row_tiles, 1);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !shares.blocks) return e;
   // Joining blocks: a few for each item, if those are fewer than shares.
@@ -840,7 +903,13 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   const int64_t max_rows = max_q * group;
   const int sms = device_sm_count();
   const bool prompt = max_rows > kPromptRows;
-  const int nt = max_rows > 8 ? 2 : 1;
+  const int64_t walk = (max_len + AT_STEP - 1) / AT_STEP;
+  // Tiles of 8 rows or 16.  Masked calls that leave blocks idle keep to 8, whose blocks are quicker (us, 8 against 16; 8
+  // key/value heads of 128, 32 rows each).  One sequence over 1029 tokens 11.4 : 14.9, 8100 19.5 : 20.2; two over 2048 14.2 :
+  // 16.2, 4300 23.3 : 20.6; four over 1029 14.9 : 17.2, 2048 19.2 : 19.2, 3000 25.6 : 22.1; 16 over 130 17.2 : 12.7.
+  const int64_t eights = a.B * a.cache.heads * ((max_rows + 7) / 8);
+  const bool narrow = kv4_masked(a) && 2 * eights <= 3 * sms && eights * walk <= 2048;
+  const int nt = max_rows > 8 && !narrow ? 2 : 1;
   const bool wide = a.cache.head_dim == 128;
   // Float32 workspace for partial results: [rows][head_dim] outputs, [rows] references and sums, then `extra` bytes.
   void* ws = nullptr;
@@ -903,15 +972,25 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     // The sides meet between 1000 and 2000 tokens, so calls from 641 to there take up to 5 us longer than they need.
     const int row_tiles = (int)std::min<int64_t>((max_rows + 8 * nt - 1) / (8 * nt), 4096);
     Shares shares = {};
-    if (max_len > 640 && a.B <= AT_SEQS) {
+    // Masked calls of few items cut each over a cluster, whose blocks join over its shared memory, as long as all run at once:
+    // no second kernel, no workspace (us, cluster against uncut or shares; 8 key/value heads of 128, one sequence, 8 rows each).
+    // 260 tokens 9.0 : 8.5, 400 8.3 : 9.6, 1029 9.0 : 13.9, 3000 10.7 : 12.8, 4300 12.2 : 12.5, 6000 13.3 : 12.9.  Equal shares
+    // use blocks that a cluster leaves idle: worth it from about 4 steps a block that they save.
+    int cluster = 1;
+    if (kv4_masked(a) && walk >= 4) {
+      const int64_t items = (int64_t)a.B * a.cache.heads * row_tiles, fit = (nt == 1 ? 3 : 2) * (int64_t)sms;
+      while (cluster < AT_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= fit) cluster *= 2;
+      if (walk > 8 * cluster || walk * (fit - items * cluster) > 4 * cluster * fit) cluster = 1;
+    }
+    if (cluster == 1 && max_len > 640 && a.B <= AT_SEQS) {
       shares.blocks = (nt == 1 ? 3 : 2) * sms;
       const size_t rows = (size_t)shares.blocks * 2 * 8 * nt;
       st = workspace(rows, shares.blocks * sizeof(int4), &shares.o, &shares.ml);
       shares.begun = reinterpret_cast<int4*>(shares.ml + rows);
     }
     if (st == PQ_OK)
-      st = cuda_fail(wide ? (nt == 1 ? launch_rows<128, 1>(a, shares, row_tiles, max_rows, stream) : launch_rows<128, 2>(a, shares, row_tiles, max_rows, stream))
-                          : (nt == 1 ? launch_rows<64, 1>(a, shares, row_tiles, max_rows, stream) : launch_rows<64, 2>(a, shares, row_tiles, max_rows, stream)),
+      st = cuda_fail(wide ? (nt == 1 ? launch_rows<128, 1>(a, shares, row_tiles, max_rows, cluster, stream) : launch_rows<128, 2>(a, shares, row_tiles, max_rows, cluster, stream))
+                          : (nt == 1 ? launch_rows<64, 1>(a, shares, row_tiles, max_rows, cluster, stream) : launch_rows<64, 2>(a, shares, row_tiles, max_rows, cluster, stream)),
                      "kv4_rows_kernel launch");
   }
   if (ws) {

@@ -157,6 +157,12 @@ __device__ __forceinline__ int4 ld_cluster_v4(uint32_t cluster_addr) {
   return v;
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
 // Every thread of every CTA of the cluster (hardware barrier, like __syncthreads).
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
