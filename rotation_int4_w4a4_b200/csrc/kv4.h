@@ -69,6 +69,7 @@ cudaError_t launch_kv4_read(const Kv4View& c, const int64_t* slots, int64_t T, u
 struct Partials;
 int64_t kv4_prompt_tiles(const Kv4AttnArgs& a);
 pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream);
+constexpr int KV4_CLUSTER = 8;           // blocks of a cluster that shares an item at most
 // Calls with sinks or a tree take instances of the kernels of their own.
 inline bool kv4_masked(const Kv4AttnArgs& a) { return a.sinks > 0 || a.tree != nullptr; }
 pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len, cudaStream_t stream);

@@ -103,7 +103,6 @@ constexpr int AT_SEQS = 1024;           // sequences whose lengths a block can a
 constexpr int AT_MIN_STEPS = 2;         // a share's least length
 // Steps that an item's beginning and end cost, ahead of its own on the line (64 users, us: 0 steps 95, 1 85, 3 69, 6 73).
 constexpr int AT_LEAD = 3;
-constexpr int AT_CLUSTER = 8;           // blocks of a cluster that shares an item at most
 
 struct Span {
   int q0, qlen, n, lo;                  // first token, new tokens, cached tokens, first token that any row's window holds
@@ -698,11 +697,9 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
           mb = ptx::ld_cluster_f32(ptx::mapa_shared(m_at, (uint32_t)lane));
           lb = ptx::ld_cluster_f32(ptx::mapa_shared(l_at, (uint32_t)lane));
         }
-        float v[AT_CLUSTER][E];
+        float v[KV4_CLUSTER][E];
 #pragma unroll
-        for (int c = 0; c < AT_CLUSTER; ++c)
-#pragma unroll
-          for (int i = 0; i < E; ++i) v[c][i] = c < cluster ? ptx::ld_cluster_f32(ptx::mapa_shared(o_at, (uint32_t)c) + 4 * i) : 0.0f;
+        for (int c = 0; c < KV4_CLUSTER; ++c) ptx::ld_cluster<E>(v[c], ptx::mapa_shared(o_at, (uint32_t)min(c, cluster - 1)));
         float mx = mb;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -713,7 +710,8 @@ __global__ void __launch_bounds__(32 * AT_WARPS, NT == 1 ? 3 : 2) kv4_rows_kerne
 #pragma unroll
         for (int i = 0; i < E; ++i) y[i] = 0.0f;
 #pragma unroll
-        for (int c = 0; c < AT_CLUSTER; ++c) {
+        for (int c = 0; c < KV4_CLUSTER; ++c) {
+          if (c >= cluster) break;
           const float fc = __shfl_sync(0xffffffffu, f, c);
           sum = fmaf(__shfl_sync(0xffffffffu, lb, c), fc, sum);
 #pragma unroll
@@ -951,12 +949,20 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
       const int64_t steps = (max_len + 127) / 128, share = std::max<int64_t>(16, tiles * a.cache.heads * steps / (2 * sms));
       if (a.B > 1 && steps >= 32) part.chunks = std::max<int>(part.chunks, (int)std::min<int64_t>((steps + share - 1) / share, 16));
       if (steps <= 8) part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(want, steps));
+      // Few tiles: the chunks of a tile as a cluster, which joins them over its shared memory, where all clusters run at once (a
+      // GPC holds two of eight) and a block has no more than 28 rows to join (us, cluster against two kernels; 8 key/value heads
+      // of 128).  64 rows over 400 tokens 15.7 : 19.4, 2048 15.5 : 21.7; 128 over 2048 20.4 : 21.4; 256 over 1029 20.5 : 20.4; 256
+      // over 400, in two, 26.7 : 17.8.  The host saves 4 us of a second launch and the workspace.
+      const int64_t c = std::min<int64_t>(std::min<int64_t>(3 * sms / 4 / (tiles * a.cache.heads), steps), KV4_CLUSTER);
+      const int64_t rows = std::min<int64_t>(max_rows, 256);
+      if (c > 1 && (rows <= 28 * c || c == KV4_CLUSTER) && (steps + c - 1) / c <= (steps + part.chunks - 1) / part.chunks + 2)
+        part.chunks = (int)c, part.cluster = 1;
     }
-    if (a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;  // the joining kernel takes a block a row
+    if (!part.cluster && a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;  // the joining kernel takes a block a row
     part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);
-    if (part.chunks > 1) st = workspace((size_t)part.chunks * a.T * a.heads_q, 0, &part.o, &part.ml);
+    if (part.chunks > 1 && !part.cluster) st = workspace((size_t)part.chunks * a.T * a.heads_q, 0, &part.o, &part.ml);
     if (st == PQ_OK) st = launch_kv4_prompt(a, part, stream);
-    if (st == PQ_OK && part.chunks > 1) {
+    if (st == PQ_OK && part.chunks > 1 && !part.cluster) {
       int warp_a_row = part.chunks < 2 * JN_WARPS;
       const int64_t rows = a.T * a.heads_q;
       void* args[] = {const_cast<Kv4AttnArgs*>(&a), &part, &warp_a_row};
@@ -979,7 +985,7 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     int cluster = 1;
     if (kv4_masked(a) && walk >= 4) {
       const int64_t items = (int64_t)a.B * a.cache.heads * row_tiles, fit = (nt == 1 ? 3 : 2) * (int64_t)sms;
-      while (cluster < AT_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= fit) cluster *= 2;
+      while (cluster < KV4_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= fit) cluster *= 2;
       if (walk > 8 * cluster || walk * (fit - items * cluster) > 4 * cluster * fit) cluster = 1;
     }
     if (cluster == 1 && max_len > 640 && a.B <= AT_SEQS) {

@@ -17,6 +17,7 @@ struct Partials {
   float2* ml;     // [chunk][T * heads_q]
   int chunks;     // 1: no partials, the output is written directly
   int chunk_len;  // tokens of a chunk
+  int cluster;    // masked calls: a tile's chunks are a cluster, which joins them over its shared memory (o and ml are not used)
 };
 
 // Sequence b's new tokens, the first and how many: rows of the call, whatever q_start holds.

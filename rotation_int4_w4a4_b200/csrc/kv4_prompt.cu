@@ -45,6 +45,7 @@
 // Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains, frees tensor memory and
 // returns.
 #include <algorithm>
+#include <cstddef>
 #include <cstdint>
 
 #include "internal.h"
@@ -88,6 +89,7 @@ struct __align__(1024) PromptSmem {
   uint32_t valid[SC_RING][4];                            // which tokens exist, a bit each
   int scaled[SC_RING][4];                                // the 32 tokens' scales are in the operands
   float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
+  float2 ml[2 * PT];                                     // cluster: each row's reference and sum
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
   uint64_t sc_full[SC_RING];
@@ -128,6 +130,10 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
   const int rest = (int)(blockIdx.x % (heads * part.chunks));
   w.kvh = rest % heads;
   w.chunk = rest / heads;
+  if (part.cluster) {                                    // the chunks side by side
+    w.kvh = rest / part.chunks;
+    w.chunk = rest % part.chunks;
+  }
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
     int q0 = 0, qlen = 0;
@@ -380,7 +386,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     gap = (lo / PT - sink_steps) * PT;
     const int all = sink_steps + max(0, (hi + PT - 1) / PT - lo / PT);
     const int parts = part.chunks > 1 ? min(part.chunks, max(1, (all * PT + part.chunk_len - 1) / part.chunk_len)) : 1;
-    if (w.chunk >= parts) {
+    if (w.chunk >= parts && !part.cluster) {
       const int r = w.r0 + threadIdx.x;
       if (threadIdx.x < 2 * PT && r < w.rows)
         part.ml[((int64_t)w.chunk * a.T + w.q0 + r / group) * a.heads_q + w.kvh * group + r % group] = make_float2(-INFINITY, 0.0f);
@@ -623,7 +629,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         each_row([&](int from, int64_t t, int hq) { reinterpret_cast<uint4*>(dst_of(t, hq))[io_chunk] = *place(from, io_chunk); });
         __syncwarp();
       };
-      if (part.chunks > 1) {
+      if (MASKED && part.cluster) {                      // joined below, when every product has been made
+        S.ml[PT * i + row] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
+      } else if (part.chunks > 1) {
         const int64_t token = w.q0 + rr / group, first = (int64_t)w.chunk * a.T;
         if (live) part.ml[(first + token) * a.heads_q + head] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
         if (some) {
@@ -838,6 +846,70 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
+  if (MASKED && part.cluster) {
+    // A chunk's rows, float32 and un-normalised, go where its keys and values were (256 rows x head_dim x 4 bytes are just
+    // that), 16-byte pieces swizzled by the row; then each block joins every part.chunks-th row of the cluster.
+    static_assert(sizeof(S.k) + sizeof(S.v) == 2 * PT * HD * 4 && offsetof(Smem, v) == offsetof(Smem, k) + sizeof(S.k), "the rows' place");
+    uint8_t* const rows_at = S.k[0][0];
+    if (warp >= PR_SOFT0 && warp < PR_PROD0) {
+      ptx::tc_fence_after();
+      const int i = (warp - PR_SOFT0) >> 2, row = PT * i + (warp & 3) * 32 + lane;
+      const float2 ml = S.ml[row];
+      if (i < tiles && steps > 0) {
+        const uint32_t o_col = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + O_COL + 128 * i;
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          load_channels(o, o_col + c);
+          if (ml.x != -INFINITY || ml.y != 0.0f) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(rows_at + row * (HD * 4) + (((c / 4 + k) ^ (row & 7)) << 4)) =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+          __syncwarp();
+        }
+      }
+      ptx::tc_fence_before();
+    }
+    ptx::cluster_sync();
+    constexpr int E = HD / 32;
+    const int mine = (int)ptx::cluster_ctarank();
+#pragma unroll 1
+    for (int row = mine + part.chunks * warp; row < 2 * PT && w.r0 + row < w.rows; row += part.chunks * (PR_THREADS / 32)) {
+      float2 ml = make_float2(-INFINITY, 0.0f);          // a chunk a lane
+      if (lane < part.chunks) {
+        const uint32_t at = ptx::mapa_shared(ptx::smem_addr(&S.ml[row]), (uint32_t)lane);
+        ml = make_float2(ptx::ld_cluster_f32(at), ptx::ld_cluster_f32(at + 4));
+      }
+      // the row's pieces of all chunks, in flight together
+      const uint32_t at = ptx::smem_addr(rows_at) + row * (HD * 4) + (((lane * E / 4) ^ (row & 7)) << 4) + (lane * E % 4) * 4;
+      float v[KV4_CLUSTER][E];
+#pragma unroll
+      for (int c = 0; c < KV4_CLUSTER; ++c) ptx::ld_cluster<E>(v[c], ptx::mapa_shared(at, (uint32_t)min(c, part.chunks - 1)));
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float mu = mx == -INFINITY ? 0.0f : mx;
+      // a chunk that saw nothing counts for nothing (its rows were not written); one whose scores are all NaN keeps its NaN
+      const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? -1.0f : 1.0f) : ex2(ml.x - mu);
+      float sum = 0.0f, y[E];
+#pragma unroll
+      for (int i = 0; i < E; ++i) y[i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < KV4_CLUSTER; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, c), lc = __shfl_sync(0xffffffffu, ml.y, c);
+        if (fc != -1.0f) {
+          sum = fmaf(lc, fc, sum);
+#pragma unroll
+          for (int i = 0; i < E; ++i) y[i] = fmaf(v[c][i], fc, y[i]);
+        }
+      }
+      const int r = w.r0 + row;
+      finish_row<HD>(y, sum, a.cache.rotate_v, a.O + (int64_t)(w.q0 + r / group) * a.ldo + (w.kvh * group + r % group) * HD, lane);
+    }
+    ptx::cluster_sync();                                 // nobody leaves while its rows are read
+  }
   if (warp == 0) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, 512);
@@ -853,6 +925,20 @@ pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tile
   if (e != cudaSuccess) return cuda_fail(e, "kv4_prompt_kernel attributes");
   const int64_t grid = tiles * a.cache.heads * part.chunks;
   if (grid >= ((int64_t)1 << 31)) { set_error("too many query tiles for one call"); return PQ_ERR_INVALID_ARG; }
+  if (part.cluster) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid, 1, 1);
+    cfg.blockDim = dim3(PR_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)part.chunks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_fail(cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<HD, MASKED>, a, part), "kv4_prompt_kernel launch");
+  }
   kv4_prompt_kernel<HD, MASKED><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);
   return cuda_fail(cudaGetLastError(), "kv4_prompt_kernel launch");
 }
