@@ -988,7 +988,12 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
       while (cluster < KV4_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= fit) cluster *= 2;
       if (walk > 8 * cluster || walk * (fit - items * cluster) > 4 * cluster * fit) cluster = 1;
     }
-    if (cluster == 1 && max_len > 640 && a.B <= AT_SEQS) {
+    // Under a window walks differ little: a block an item, as long as all run at once and none is long (us, uncut against shares;
+    // 8 key/value heads, windows of 512, 1024, 2048 and 4096).  32 sequences 14.8 : 20.2, 20.9 : 25.5, 35.7 : 35.9, 61.9 : 54.4; 48 of
+    // them 17.7 : 24.1, 26.0 : 32.5, 42.3 : 47.4, 71.9 : 73.2; 64, more than run at once, 29.9 : 30.4, 45.1 : 39.2, 71.4 : 59.0.
+    const bool uncut = kv4_masked(a) && a.window > 0 && walk <= 20 &&
+                       (int64_t)a.B * a.cache.heads * row_tiles <= (nt == 1 ? 3 : 2) * (int64_t)sms;
+    if (cluster == 1 && !uncut && max_len > 640 && a.B <= AT_SEQS) {
       shares.blocks = (nt == 1 ? 3 : 2) * sms;
       const size_t rows = (size_t)shares.blocks * 2 * 8 * nt;
       st = workspace(rows, shares.blocks * sizeof(int4), &shares.o, &shares.ml);

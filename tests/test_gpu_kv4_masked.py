@@ -237,6 +237,23 @@ def test_many_sequences_in_equal_shares(pq, hd, hq, hkv, page, window, sinks, qs
     check(pq, case, max(qs), max(ls), window=window, sinks=sinks, trees=trees_of(qs, 3))
 
 
+@pytest.mark.parametrize("hd,hq,hkv,page,rv,window,sinks,tree,qs,ls", [
+    (128, 32, 8, 64, True, 0, 0, True, [500], [8000]), (64, 14, 2, 16, False, 0, 0, True, [300, 0, 77, 640, 2], [9000, 0, 5000, 9100, 2]),
+    (128, 32, 8, 32, True, 4000, 7, False, [1000], [6000]), (128, 16, 4, 64, False, 300, 130, False, [5000], [5003]),
+    (64, 8, 8, 128, True, 1000, 4, False, [3000, 100, 2000, 1], [5000, 100, 4100, 3000]), (128, 24, 8, 16, True, 2500, 20, True, [300, 200, 280], [5000, 9000, 700]),
+])
+def test_many_tiles(pq, hd, hq, hkv, page, rv, window, sinks, tree, qs, ls):
+    """Calls of many tiles, cut into parts by their lengths; the same bits each time."""
+    case = make_case(pq, sum(ls), qs, ls, hq, hkv, hd, page, rv=rv)
+    trees = trees_of(qs, 5, 0.9) if tree else None
+    O = check(pq, case, max(qs), max(ls), window=window, sinks=sinks, trees=trees)
+    lists = pack(trees, -(-max(qs) // 32)).cuda() if tree else None
+    for _ in range(3):
+        again = torch.empty_like(O)
+        pq.pq_kv4_attention_masked(case[0], case[1], again, *case[2:], max(qs), max(ls), window=window, sinks=sinks, tree=lists)
+        assert torch.equal(O, again)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_a_verification_step(pq, fmt):
     """A layer's step with drafted tokens: 4-bit projections, append at the drafts' depths, attention of the tree under a window
