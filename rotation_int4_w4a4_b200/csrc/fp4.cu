@@ -132,7 +132,7 @@ template <bool NV>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pair_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSW,
     const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmY, float alpha, void* __restrict__ Y, int T,
-    int N, int steps, int codes64, int pieces, int m_tiles, int n_tiles, int out_bf16, int bulk, unsigned int* status) {
+    int N, int steps, int codes64, int pieces, int m_tiles, int n_tiles, int out_bf16, int bulk, int pdl, unsigned int* status) {
   using Geom = PairGeom<NV>;
   extern __shared__ unsigned char smem_raw[];
   PairSmem<NV>& S = *reinterpret_cast<PairSmem<NV>*>(smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u));
@@ -169,6 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
 
   if (warp == 0) {
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(&S.full[0]), 0);
+    if (pdl) ptx::griddep_wait();                          // for the kernel that writes the token codes
     int step = 0;
     bool ok = true;
     for (int u = first; u < tiles && ok; u += stride) {
@@ -652,8 +653,13 @@ pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, in
   cfg.blockDim = dim3(P_THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = c.stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = c.pdl ? 1 : 0;
   return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_pair_kernel<NV>, m.w, m.a, m.sw, m.sa, m.y, c.alpha, c.Y, c.T, c.N, c.steps, c.codes64,
-                                      c.pieces, m_tiles, n_tiles, c.bf16, bulk ? 1 : 0, c.status),
+                                      c.pieces, m_tiles, n_tiles, c.bf16, bulk ? 1 : 0, c.pdl ? 1 : 0, c.status),
                    "fp4_pair_kernel launch");
 }
 
