@@ -52,27 +52,33 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
   return r;
 }
 
-// Scale byte of a block from its largest magnitude, and what its channels are multiplied with (0: codes 0).  unit: the
-// rotation's 1 / sqrt(g); nv: top = unit / (6 factor) and unit is unit / factor.
+// Scale bytes of two blocks from their largest magnitudes (the second's in the high byte), and what their channels are
+// multiplied with (0: codes 0).  unit: the rotation's 1 / sqrt(g); nv: top = unit / (6 factor) and unit is unit / factor.
+// The conversions run on the unit that makes the codes, the busiest one, so two blocks share them.
 template <bool NV>
-__device__ __forceinline__ uint32_t block_scale(float m, float unit, float top, float& f) {
-  f = 0.0f;
+__device__ __forceinline__ uint32_t block_scales(float m0, float m1, float unit, float top, float& f0, float& f1) {
   if constexpr (NV) {
-    if (!(m < INFINITY)) return 0x7Fu;                   // E4M3's NaN
     uint16_t b;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %1;" : "=h"(b) : "f"(m * top));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(m1 * top), "f"(m0 * top));
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(b));
-    const float s = __low2float(*reinterpret_cast<const __half2*>(&h));
-    if (s > 0.0f) f = __fdividef(unit, s);
-    return b & 0xFFu;
+    const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const bool ok0 = m0 < INFINITY, ok1 = m1 < INFINITY;   // otherwise E4M3's NaN
+    f0 = ok0 && s.x > 0.0f ? __fdividef(unit, s.x) : 0.0f;
+    f1 = ok1 && s.y > 0.0f ? __fdividef(unit, s.y) : 0.0f;
+    return (ok0 ? b & 0xFFu : 0x7Fu) | (ok1 ? b & 0xFF00u : 0x7F00u);
   } else {
-    m *= unit;
-    if (!(m < INFINITY)) return 0xFFu;                   // E8M0's NaN
-    if (m < kTinyBlock) return 0u;
-    const uint32_t e = __float_as_uint(m) >> 23;         // scale 2^(e - 129), its byte e - 2
-    f = unit * __uint_as_float((256u - e) << 23);
-    return e - 2u;
+    uint32_t bytes = 0u;
+    auto one = [&](float m, float& f, int shift) {
+      m *= unit;
+      const uint32_t e = __float_as_uint(m) >> 23;       // scale 2^(e - 129), its byte e - 2
+      const bool fine = m >= kTinyBlock && m < INFINITY;
+      f = fine ? unit * __uint_as_float((256u - e) << 23) : 0.0f;
+      bytes |= (fine ? e - 2u : m < kTinyBlock ? 0u : 0xFFu) << shift;   // E8M0's NaN
+    };
+    one(m0, f0, 0);
+    one(m1, f1, 8);
+    return bytes;
   }
 }
 
@@ -192,30 +198,38 @@ __global__ void __launch_bounds__(32 * QF_WARPS, G == 256 ? 1 : 2) quant_fp4_ker
       uint8_t* const row_codes = codes + (int64_t)r * (D / 2);
       uint32_t word[NV ? NS : NS / 2];
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        float* y = v[h][s];
-        float m = max3_nan(fabsf(y[0]), fabsf(y[1]), fabsf(y[2])), m2 = max3_nan(fabsf(y[3]), fabsf(y[4]), fabsf(y[5]));
-        m = max3_nan(m, fabsf(y[6]), fabsf(y[7]));
-        m2 = max3_nan(m2, fabsf(y[8]), fabsf(y[9]));
-        m = max3_nan(m, fabsf(y[10]), fabsf(y[11]));
-        m2 = max3_nan(m2, fabsf(y[12]), fabsf(y[13]));
-        m = max_nan(max3_nan(m, fabsf(y[14]), fabsf(y[15])), m2);
-        if constexpr (!NV) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        float f;
-        const uint32_t byte = block_scale<NV>(m, unit, top, f);
-        if constexpr (NV) {
-          word[s] = byte << (8 * t);
-        } else {
-          const uint32_t mine = byte << (16 * (s & 1) + 8 * (t >> 1));
-          if (s & 1) word[s / 2] |= mine;
-          else word[s / 2] = mine;
-        }
-        const uint64_t f2 = ptx::f2_pack(f, f);
+      for (int s2 = 0; s2 < NS; s2 += 2) {
+        float m[2], f[2];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(y[i], y[i + 1]), f2), y[i], y[i + 1]);
-        // times 0 an infinity or a NaN is not 0: the codes are chosen, not computed
-        const uint2 q = f != 0.0f ? make_uint2(e2m1x8(y), e2m1x8(y + 8)) : make_uint2(0u, 0u);
-        if (live && c0 + 64 * s < D) *reinterpret_cast<uint2*>(row_codes + (c0 + 64 * s) / 2) = q;
+        for (int k = 0; k < 2; ++k) {
+          const float* y = v[h][s2 + k];
+          float a = max3_nan(fabsf(y[0]), fabsf(y[1]), fabsf(y[2])), b = max3_nan(fabsf(y[3]), fabsf(y[4]), fabsf(y[5]));
+          a = max3_nan(a, fabsf(y[6]), fabsf(y[7]));
+          b = max3_nan(b, fabsf(y[8]), fabsf(y[9]));
+          a = max3_nan(a, fabsf(y[10]), fabsf(y[11]));
+          b = max3_nan(b, fabsf(y[12]), fabsf(y[13]));
+          m[k] = max_nan(max3_nan(a, fabsf(y[14]), fabsf(y[15])), b);
+          if constexpr (!NV) m[k] = max_nan(m[k], __shfl_xor_sync(0xffffffffu, m[k], 1));
+        }
+        const uint32_t bytes = block_scales<NV>(m[0], m[1], unit, top, f[0], f[1]);
+        if constexpr (NV) {
+          word[s2] = (bytes & 0xFFu) << (8 * t);
+          word[s2 + 1] = (bytes >> 8) << (8 * t);
+        } else {                                         // the first span's two blocks, then the second's
+          word[s2 / 2] = ((bytes & 0xFFu) | (bytes & 0xFF00u) << 8) << (8 * (t >> 1));
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int s = s2 + k;
+          float* y = v[h][s];
+          const uint64_t f2 = ptx::f2_pack(f[k], f[k]);
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) ptx::f2_unpack(ptx::f2_mul(ptx::f2_pack(y[i], y[i + 1]), f2), y[i], y[i + 1]);
+          // times 0 an infinity or a NaN is not 0: the codes are chosen, not computed
+          const uint32_t keep = f[k] != 0.0f ? 0xffffffffu : 0u;
+          const uint2 q = make_uint2(e2m1x8(y) & keep, e2m1x8(y + 8) & keep);
+          if (live && c0 + 64 * s < D) *reinterpret_cast<uint2*>(row_codes + (c0 + 64 * s) / 2) = q;
+        }
       }
       uint8_t* const place = scales + (int64_t)(r >> 7) * pieces * PIECE + (r & 31) * 16 + ((r >> 5) & 3) * 4;
 #pragma unroll
