@@ -22,7 +22,7 @@ LIB = os.path.join(LIBDIR, "libpq.so")
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["pq_host.cpp", "transform.cu", "smooth_rows.cu", "rotate_mma.cu", "gemm.cu", "gemm_small.cu", "gemv.cu", "rrs.cu", "rows_small.cu", "gemm_static_scratch.cu",
            "ops_host.cpp", "quant8.cu", "w8a8.cu", "quant_fp4.cu", "fp4.cu", "kv4_append.cu", "kv4_attention.cu", "kv4_prompt.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh", "quant_fp4.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
                      "-I" + os.path.join(ROOT, "include")]

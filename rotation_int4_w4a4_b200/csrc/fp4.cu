@@ -39,12 +39,13 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "quant_fp4.cuh"
 
 namespace pq {
 namespace {
 
 constexpr int KB = 128;                 // bytes of a K step a row = a swizzle row: 256 codes
-constexpr int PIECE = 512;              // bytes of a piece of scales
+constexpr int PIECE = QF_PIECE;         // bytes of a piece of scales
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Scale pieces of 128 rows in a K step.
@@ -400,13 +401,27 @@ __device__ __forceinline__ void add_ranges(float (&d)[4], uint32_t base, int c, 
   }
 }
 
+// The quantisation that a product of up to 16 tokens does itself: rows of bf16 in, codes and scales out as well.
+struct Fp4Fuse {
+  const uint16_t* X;
+  int64_t ldx;
+  int D, aligned32;
+  Fp4Scaling sc;
+  uint8_t *codes, *scales;
+};
+
 // Grid: x = tile * split + range (the cluster), tiles channel-fastest.  tmSW, tmSA: the scale pieces as rows of 256 bytes;
 // pieces: 512-byte pieces of 128 rows of a tensor.  codes64: 64-code products of the whole reduction.
-template <int NP, bool NV, bool DEEP>
+// G >= 0 (NP = 16): the tokens come as bf16 rows, which the epilogue's warps rotate in blocks of G and quantise into the
+// operand's place while the weights are on their way, every tile for itself (a range of 1024 channels is 8 units for 4
+// warps); the first tile's blocks write the codes and scales out too.
+template <int NP, bool NV, bool DEEP, int G>
 __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
     const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmSW,
-    const __grid_constant__ CUtensorMap tmSA, float alpha, void* __restrict__ Y, int T, int N, int steps, int codes64,
-    int pieces, int m_tiles, int split, int out_bf16, int pdl, unsigned int* status) {
+    const __grid_constant__ CUtensorMap tmSA, const Fp4Fuse fuse, float alpha, void* __restrict__ Y, int T, int N, int steps,
+    int codes64, int pieces, int m_tiles, int split, int out_bf16, int pdl, unsigned int* status) {
+  constexpr bool FUSED = G >= 0;
+  constexpr int UNITS = G == 256 ? 1 : 2;                 // units of quantisation a step, a warp each
   using Geom = TileGeom<NP, NV, DEEP>;
   constexpr int STAGES = Geom::STAGES;
   extern __shared__ unsigned char smem_raw[];
@@ -421,7 +436,7 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(&S.full[s], 1);
+      ptx::mbar_init(&S.full[s], FUSED ? 1 + UNITS : 1);
       ptx::mbar_init(&S.empty[s], 1);
     }
     ptx::mbar_init(&S.acc_full, 1);
@@ -430,9 +445,11 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
   }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tmW);
-    ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmSW);
-    ptx::prefetch_tmap(&tmSA);
+    if (!FUSED) {
+      ptx::prefetch_tmap(&tmA);
+      ptx::prefetch_tmap(&tmSA);
+    }
   }
   if (warp == 1) {
     ptx::tmem_alloc(&S.tmem_slot, Geom::COLS);
@@ -447,11 +464,12 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
     if (lane == 0) {
       const int sw0 = (m0 / 128) * pieces * 2, sa0 = (t0 / 128) * pieces * 2;
       auto weights = [&](int s, int kb) {
-        ptx::mbar_arrive_expect_tx(&S.full[s], Geom::TX);
+        ptx::mbar_arrive_expect_tx(&S.full[s], FUSED ? TM * KB + Geom::SF : Geom::TX);
         ptx::tma_load_2d(S.a[s], &tmW, &S.full[s], kb * KB, m0);
         ptx::tma_load_2d(S.sa[s], &tmSW, &S.full[s], 0, sw0 + kb * kPieces<NV> * 2);
       };
       auto tokens = [&](int s, int kb) {
+        if (FUSED) return;
         ptx::tma_load_2d(S.b[s], &tmA, &S.full[s], kb * KB, t0);
         ptx::tma_load_2d(S.sb[s], &tmSA, &S.full[s], 0, sa0 + kb * kPieces<NV> * 2);
       };
@@ -508,6 +526,42 @@ __global__ void __launch_bounds__(T_THREADS) fp4_tile_kernel(
     }
     __syncwarp();
   } else {
+    if constexpr (FUSED) {
+      using Unit = Fp4Unit<G, NV>;
+      constexpr int WIDTH = 64 * Unit::SPANS;
+      const int g = lane >> 2, t = lane & 3;
+      uint32_t b[2][2];
+      Unit::signs(b);
+      Unit x;
+      // unit i of the range: half i % UNITS of step i / UNITS; the four warps take them in turn
+      const int units = (k1 - k0) * UNITS;
+      auto load = [&](int i) { x.load(fuse.X, fuse.ldx, T, fuse.D, 0, (k0 * UNITS + i) * WIDTH, fuse.aligned32 != 0); };
+      const int i0 = warp - 2;
+      if (i0 < units) load(i0);
+      for (int i = i0; i < units; i += 4) {
+        const int step = i / UNITS, half = i % UNITS, s = step % STAGES, u = k0 * UNITS + i;
+        float v[2][Unit::SPANS][16];
+        x.rotate(b, v);
+        if (i + 4 < units) load(i + 4);
+        if (step >= STAGES && !warp_wait_or_abort(&S.empty[s], ((uint32_t)(step / STAGES) & 1u) ^ 1u, &S.abort_flag, status)) break;
+        const bool out = m0 == 0;
+        Unit::quantise(
+            v, fuse.sc,
+            [&](int h, int sp, uint2 q) {                 // 16 codes, half of a 16-byte piece of the swizzled row
+              const int r = g + 8 * h, c = u * WIDTH + 64 * sp + 16 * t, piece = 2 * (half * Unit::SPANS + sp) + (t >> 1);
+              *reinterpret_cast<uint2*>(S.b[s] + r * KB + ((piece ^ (r & 7)) << 4) + (t & 1) * 8) = q;
+              if (out && r < T && c < fuse.D) *reinterpret_cast<uint2*>(fuse.codes + (int64_t)r * (fuse.D / 2) + c / 2) = q;
+            },
+            [&](int h, int k, uint32_t word) {
+              const int r = g + 8 * h, piece = half * Unit::WORDS + k, at = u * Unit::WORDS + k;
+              if (t == 0) *reinterpret_cast<uint32_t*>(S.sb[s] + piece * PIECE + r * 16) = word;
+              if (t == 0 && out && r < T && at < pieces) *reinterpret_cast<uint32_t*>(fuse.scales + at * PIECE + r * 16) = word;
+            });
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&S.full[s]);
+      }
+    }
     if (pdl) ptx::griddep_wait();                         // Y may still be read by what ran before
     const int sub = warp & 3;
     const int n = m0 + 32 * sub + lane;
@@ -588,13 +642,18 @@ struct Fp4Maps {
 };
 
 pq_status make_maps(Fp4Maps* m, const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W,
-                    const uint8_t* scales_W, int64_t T, int64_t N, int64_t D, int64_t pieces, int pieces_step, int a_rows) {
+                    const uint8_t* scales_W, int64_t T, int64_t N, int64_t D, int64_t pieces, int pieces_step, int a_rows,
+                    bool weights_only = false) {
   const auto scale_map = [&](CUtensorMap* map, const uint8_t* base, int64_t rows) {
     return make_u8_tile_map(map, base, (rows + 127) / 128 * pieces * 2, 256, 256, 2 * pieces_step, /*swizzle128=*/false);
   };
   cudaError_t e = make_u8_tile_map(&m->w, codes_W, N, D / 2, KB, TM, /*swizzle128=*/true);
-  if (e == cudaSuccess) e = make_u8_tile_map(&m->a, codes_A, T, D / 2, KB, a_rows, /*swizzle128=*/true);
   if (e == cudaSuccess) e = scale_map(&m->sw, scales_W, N);
+  if (weights_only) {
+    m->a = m->w, m->sa = m->sw;         // not used
+    return cuda_fail(e, "4-bit operand tensor map");
+  }
+  if (e == cudaSuccess) e = make_u8_tile_map(&m->a, codes_A, T, D / 2, KB, a_rows, /*swizzle128=*/true);
   if (e == cudaSuccess) e = scale_map(&m->sa, scales_A, T);
   return cuda_fail(e, "4-bit operand tensor map");
 }
@@ -606,14 +665,16 @@ struct Fp4Call {
   bool pdl;
   unsigned int* status;
   cudaStream_t stream;
+  int g;                                // -1: the token codes are in hand
+  Fp4Fuse fuse;
 };
 
-template <int NP, bool NV, bool DEEP>
+template <int NP, bool NV, bool DEEP, int G = -1>
 pq_status launch_tile(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int64_t tiles, int split) {
   constexpr size_t smem = sizeof(TileSmem<NP, NV, DEEP>) + 1024;
   static_assert((DEEP ? 1 : 2) * smem <= 232448, "shared memory exceeds 227 KB an SM");
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(fp4_tile_kernel<NP, NV, DEEP>), (int)smem, done);
+  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(fp4_tile_kernel<NP, NV, DEEP, G>), (int)smem, done);
   if (e != cudaSuccess) return cuda_fail(e, "fp4_tile_kernel attributes");
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
@@ -629,8 +690,8 @@ pq_status launch_tile(const Fp4Maps& m, const Fp4Call& c, int m_tiles, int64_t t
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = c.pdl ? 2 : 1;
-  return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_tile_kernel<NP, NV, DEEP>, m.w, m.a, m.sw, m.sa, c.alpha, c.Y, c.T, c.N, c.steps,
-                                      c.codes64, c.pieces, m_tiles, split, c.bf16, c.pdl ? 1 : 0, c.status),
+  return cuda_fail(cudaLaunchKernelEx(&cfg, fp4_tile_kernel<NP, NV, DEEP, G>, m.w, m.a, m.sw, m.sa, c.fuse, c.alpha, c.Y, c.T, c.N,
+                                      c.steps, c.codes64, c.pieces, m_tiles, split, c.bf16, c.pdl ? 1 : 0, c.status),
                    "fp4_tile_kernel launch");
 }
 
@@ -663,6 +724,18 @@ pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, in
                    "fp4_pair_kernel launch");
 }
 
+int tile_tokens(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+// K steps of the tile kernel's reduction, and the ranges it is cut into: as long as every CTA still has an SM of its own and
+// keeps some steps.
+int fp4_ranges(int64_t T, int64_t N, int64_t D, int* split) {
+  const int np = tile_tokens(T), sms = device_sm_count(), steps = (int)((D + 2 * KB - 1) / (2 * KB));
+  const int64_t tiles = (N + TM - 1) / TM * ((T + np - 1) / np);
+  *split = 1;
+  while (*split < 8 && tiles * *split * 2 <= sms && steps >= 4 * *split) *split *= 2;
+  return steps;
+}
+
 template <bool NV>
 pq_status run(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t T,
               int64_t N, int64_t D, Fp4Call c) {
@@ -675,15 +748,21 @@ pq_status run(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* co
     if (st != PQ_OK) return st;
     return launch_pair<NV>(m, c, (int)pair_m, (int)pair_n, sms);
   }
-  const int np = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const int np = tile_tokens(T);
   const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
   if (tiles >= ((int64_t)1 << 31)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
-  // Ranges of the reduction: as long as every CTA still has an SM of its own and keeps some steps.
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= sms && c.steps >= 4 * split) split *= 2;
+  fp4_ranges(T, N, D, &split);
   Fp4Maps m;
-  const pq_status st = make_maps(&m, codes_A, scales_A, codes_W, scales_W, T, N, D, c.pieces, kPieces<NV>, np);
+  const pq_status st = make_maps(&m, codes_A, scales_A, codes_W, scales_W, T, N, D, c.pieces, kPieces<NV>, np, c.g >= 0);
   if (st != PQ_OK) return st;
+  if (c.g >= 0) {
+#define PQ_FUSED_CASE(G)                                                                     \
+  (tiles * split <= sms ? launch_tile<16, NV, true, G>(m, c, (int)m_tiles, tiles, split) \
+                        : launch_tile<16, NV, false, G>(m, c, (int)m_tiles, tiles, split))
+    return c.g == 0 ? PQ_FUSED_CASE(0) : c.g == 64 ? PQ_FUSED_CASE(64) : c.g == 128 ? PQ_FUSED_CASE(128) : PQ_FUSED_CASE(256);
+#undef PQ_FUSED_CASE
+  }
 #define PQ_TILE_CASE(NP)                                                                   \
   (tiles * split <= sms ? launch_tile<NP, NV, true>(m, c, (int)m_tiles, tiles, split) \
                         : launch_tile<NP, NV, false>(m, c, (int)m_tiles, tiles, split))
@@ -700,7 +779,32 @@ pq_status fp4_launch(const uint8_t* codes_A, const uint8_t* scales_A, const uint
   const cudaError_t e = gemm_status_address(&status);
   if (e != cudaSuccess) return cuda_fail(e, "status word");
   const Fp4Call c = {alpha, Y, (int)T, (int)N, (int)((D + 2 * KB - 1) / (2 * KB)), (int)((D + 63) / 64),
-                     (int)(nv ? (D + 63) / 64 : (D + 127) / 128), out_dtype == PQ_OUT_BF16 ? 1 : 0, pdl, status, stream};
+                     (int)(nv ? (D + 63) / 64 : (D + 127) / 128), out_dtype == PQ_OUT_BF16 ? 1 : 0, pdl, status, stream, -1, {}};
+  return nv ? run<true>(codes_A, scales_A, codes_W, scales_W, T, N, D, c)
+            : run<false>(codes_A, scales_A, codes_W, scales_W, T, N, D, c);
+}
+
+pq_status fp4_linear_launch(const void* X, int64_t T, int64_t D, int64_t ldx, int g, bool nv, float factor, uint8_t* codes_A,
+                            uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t N, float alpha, void* Y,
+                            pq_out_dtype out_dtype, cudaStream_t stream) {
+  // Up to 16 tokens one kernel does both, where no block has more than 4 steps of them to quantise (us on the device, one kernel
+  // against two; one token).  4096 x 4096, 4 steps a block: 6.7 : 6.3, and 3 less of the host for the second launch; 14336 x
+  // 4096, 16 steps: 12.9 : 8.8; 4096 x 14336, 14 steps: 13.9 : 10.3.
+  int split = 1;
+  const int steps = fp4_ranges(T, N, D, &split);
+  if (T > kFp4FusedT || steps > 4 * split) {
+    const pq_status st = cuda_fail(launch_quant_fp4(X, T, (int)D, ldx, g, nv, factor, codes_A, scales_A, stream),
+                                   "pq_fp4_linear quantisation launch");
+    if (st != PQ_OK) return st;
+    return fp4_launch(codes_A, scales_A, codes_W, scales_W, T, N, D, nv, alpha, Y, out_dtype, stream, /*pdl=*/true);
+  }
+  unsigned int* status = nullptr;
+  const cudaError_t e = gemm_status_address(&status);
+  if (e != cudaSuccess) return cuda_fail(e, "status word");
+  const int aligned32 = (reinterpret_cast<uintptr_t>(X) & 31) == 0 && ldx % 16 == 0;
+  const Fp4Call c = {alpha, Y, (int)T, (int)N, (int)((D + 2 * KB - 1) / (2 * KB)), (int)((D + 63) / 64),
+                     (int)(nv ? (D + 63) / 64 : (D + 127) / 128), out_dtype == PQ_OUT_BF16 ? 1 : 0, /*pdl=*/false, status, stream, g,
+                     {static_cast<const uint16_t*>(X), ldx, (int)D, aligned32, Fp4Scaling::of(g, nv, factor), codes_A, scales_A}};
   return nv ? run<true>(codes_A, scales_A, codes_W, scales_W, T, N, D, c)
             : run<false>(codes_A, scales_A, codes_W, scales_W, T, N, D, c);
 }

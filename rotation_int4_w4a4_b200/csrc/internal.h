@@ -222,6 +222,11 @@ cudaError_t launch_quant_fp4(const void* X, int64_t rows, int D, int64_t ldx, in
 pq_status fp4_launch(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W,
                      int64_t T, int64_t N, int64_t D, bool nv, float alpha, void* Y, pq_out_dtype out_dtype,
                      cudaStream_t stream, bool pdl);
+// Both: one kernel for up to kFp4FusedT tokens, otherwise one after the other.
+constexpr int64_t kFp4FusedT = 16;
+pq_status fp4_linear_launch(const void* X, int64_t T, int64_t D, int64_t ldx, int g, bool nv, float factor, uint8_t* codes_A,
+                            uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t N, float alpha, void* Y,
+                            pq_out_dtype out_dtype, cudaStream_t stream);
 // Launches the bounded-wait diagnostic (a wait that cannot complete, limited to limit_ns).
 pq_status gemm_wait_timeout_selftest(uint64_t limit_ns, cudaStream_t stream);
 // Device address of the GEMM's status word on the current device.

@@ -240,12 +240,8 @@ extern "C" pq_status pq_fp4_linear(const void* X, int64_t T, int64_t D, int64_t 
   const float alpha = format == PQ_FP4_NV ? factor_A * factor_W : 1.0f;
   st = check_gemm_fp4(codes_A, scales_A, codes_W, scales_W, T, N, D, format, alpha, Y, out_dtype);
   if (st != PQ_OK) return st;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = cuda_fail(launch_quant_fp4(X, T, (int)D, ldx, g, format == PQ_FP4_NV, factor_A, codes_A, scales_A, s),
-                 "pq_fp4_linear quantisation launch");
-  if (st != PQ_OK) return st;
-  return fp4_launch(codes_A, scales_A, codes_W, scales_W, T, N, D, format == PQ_FP4_NV, alpha, Y, out_dtype, s,
-                    /*pdl=*/true);
+  return fp4_linear_launch(X, T, D, ldx, g, format == PQ_FP4_NV, factor_A, codes_A, scales_A, codes_W, scales_W, N, alpha, Y,
+                           out_dtype, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" pq_status pq_kv4_append(const pq_kv4_cache* cache, const void* Q, int64_t ldq, const void* K, int64_t ldk,

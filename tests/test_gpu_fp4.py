@@ -244,7 +244,9 @@ def test_a_nan_scale_stays_in_its_row(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
-@pytest.mark.parametrize("T,N,D,g", [(1, 4096, 4096, 128), (40, 257, 768, 256), (129, 1003, 1056, 0), (600, 4200, 2048, 64)])
+@pytest.mark.parametrize("T,N,D,g", [(1, 4096, 4096, 128), (40, 257, 768, 256), (129, 1003, 1056, 0), (600, 4200, 2048, 64),
+                                     (2, 100, 32, 0), (3, 1, 64, 64), (16, 130, 288, 0), (5, 2000, 1280, 256), (7, 20000, 8192, 128),
+                                     (16, 40000, 1024, 256), (1, 300, 65536, 64), (9, 5000, 480, 0), (17, 700, 640, 128)])
 def test_linear_is_quantisation_and_product(fmt, T, N, D, g):
     import torch
     from rotation_int4_w4a4_b200 import pq
