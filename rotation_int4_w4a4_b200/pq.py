@@ -460,14 +460,15 @@ def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=No
 
 
 def _fp4_format(fmt):
-    if fmt not in FP4_FORMATS:
+    form = FP4_FORMATS.get(fmt)
+    if form is None:
         raise ValueError(f"fmt={fmt!r}: expected 'mx' (blocks of 32, power-of-two scales) or 'nv' (blocks of 16, E4M3 scales)")
-    return FP4_FORMATS[fmt]
+    return form
 
 
 def _fp4_bytes(rows, D, form):
     """Bytes of a tensor's scales (sizes the calls refuse give a small number: the library names what is wrong)."""
-    span = 64 if form == PQ_FP4_NV else 128
+    span = 64 if form else 128
     return -(-rows // 128) * -(-D // span) * 512
 
 
@@ -493,20 +494,20 @@ def pq_quant_fp4(X, codes, scales, fmt="nv", g=0, factor=1.0, T=None, D=None, ld
 
 
 def _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch):
+    y_type = torch.bfloat16 if out_dtype == PQ_OUT_BF16 else torch.float32
     if not isinstance(Y, int):
-        y_kind = PQ_OUT_BF16 if Y.dtype == torch.bfloat16 else PQ_OUT_F32
+        y_kind = PQ_OUT_BF16 if Y.dtype is torch.bfloat16 else PQ_OUT_F32
         if out_dtype is None:
-            out_dtype = y_kind
+            out_dtype, y_type = y_kind, torch.bfloat16 if y_kind == PQ_OUT_BF16 else torch.float32
         elif out_dtype != y_kind:
             raise ValueError(f"Y: dtype {Y.dtype} does not match out_dtype={out_dtype}")
     elif out_dtype is None:
         out_dtype = PQ_OUT_F32
-    u8 = torch.uint8
-    return (out_dtype, _on(codes_A, "codes_A", "u8", u8, T * D // 2, dev),
+    u8, half = torch.uint8, D // 2
+    return (out_dtype, _on(codes_A, "codes_A", "u8", u8, T * half, dev),
             _on(scales_A, "scales_A", "u8", u8, _fp4_bytes(T, D, form), dev),
-            _on(codes_W, "codes_W", "u8", u8, N * D // 2, dev),
-            _on(scales_W, "scales_W", "u8", u8, _fp4_bytes(N, D, form), dev),
-            _on(Y, "Y", "y", torch.bfloat16 if out_dtype == PQ_OUT_BF16 else torch.float32, T * N, dev))
+            _on(codes_W, "codes_W", "u8", u8, N * half, dev),
+            _on(scales_W, "scales_W", "u8", u8, _fp4_bytes(N, D, form), dev), _on(Y, "Y", "y", y_type, T * N, dev))
 
 
 def pq_fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", alpha=1.0, T=None, N=None, D=None, out_dtype=None,
