@@ -581,6 +581,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         const uint32_t sa = (uint32_t)bits & va, sb = (uint32_t)(bits >> 32) & vb;
         const float4* ks = reinterpret_cast<const float4*>(S.ks[sc]) + t0 / 4;
         const float4* vs = reinterpret_cast<const float4*>(S.vs[sc]) + t0 / 4;
+        // 32 tokens that none of the warp's rows sees cost nothing: in front of a window, behind the diagonal, past the sinks.
+        const bool some_a = __any_sync(0xffffffffu, sa != 0u), some_b = __any_sync(0xffffffffu, sb != 0u);
         float sum = 0.0f;
         bool over = m == -INFINITY && (sa | sb) != 0u;
         for (int pass = 0;; ++pass) {
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           if (__any_sync(0xffffffffu, over)) {
             float cand = -INFINITY;
 #pragma unroll 1
-            for (int g = 0; g < 2; ++g) {
+            for (int g = some_a ? 0 : 1; g < (some_b ? 2 : 1); ++g) {
               ptx::tmem_ld32(s_buf + 32 * g, x);
               ptx::tmem_ld_wait(x);
               cand = fmaxf(cand, chunk_top(x, g ? sb : sa, ks + 8 * g, reinterpret_cast<const float4*>(S.ve[sc]) + t0 / 4 + 8 * g, c_row));
@@ -597,12 +599,23 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
           }
           const float ref = m == -INFINITY ? 0.0f : m;
           float top = 0.0f;
-          ptx::tmem_ld32(s_buf, x);
-          ptx::tmem_ld_wait(x);
-          sum = chunk_exp_masked(x, sa, ks, vs, c_row, -ref, pa, top);
-          ptx::tmem_ld32(s_buf + 32, x);
-          ptx::tmem_ld_wait(x);
-          sum += chunk_exp_masked(x, sb, ks + 8, vs + 8, c_row, -ref, pb, top);
+          sum = 0.0f;
+          if (some_a) {
+            ptx::tmem_ld32(s_buf, x);
+            ptx::tmem_ld_wait(x);
+            sum = chunk_exp_masked(x, sa, ks, vs, c_row, -ref, pa, top);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pa[k] = 0u;
+          }
+          if (some_b) {
+            ptx::tmem_ld32(s_buf + 32, x);
+            ptx::tmem_ld_wait(x);
+            sum += chunk_exp_masked(x, sb, ks + 8, vs + 8, c_row, -ref, pb, top);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pb[k] = 0u;
+          }
           over = top > kTop || sum > kSumTop;
           if (pass == 1 || !__any_sync(0xffffffffu, over)) break;
         }
