@@ -136,8 +136,11 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
   }
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const int b = b0 + lane;
-    int q0 = 0, qlen = 0;
-    if (b < a.B) new_tokens(a.q_start, (int)a.T, b, q0, qlen);
+    int q0 = 0, qlen = 0, n = 0;
+    if (b < a.B) {
+      n = a.seq_lens[b];                                 // on its way beside the starts
+      new_tokens(a.q_start, (int)a.T, b, q0, qlen);
+    }
     const int tiles = (qlen * group + 2 * PT - 1) / (2 * PT);
     int upto = tiles;
 #pragma unroll
@@ -153,6 +156,7 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
       w.qlen = __shfl_sync(0xffffffffu, qlen, src);
       w.r0 = (__shfl_sync(0xffffffffu, upto, src) - 1 - tile) * 2 * PT;
       w.rows = w.qlen * group;
+      w.n = max(0, __shfl_sync(0xffffffffu, n, src));
       return true;
     }
     tile -= __shfl_sync(0xffffffffu, upto, 31);
@@ -363,7 +367,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   if (!find_work(a, part, w)) return;                    // the whole block agrees
   const int group = a.heads_q / a.cache.heads;
   const int ps = a.cache.page_shift;
-  int n = max(0, a.seq_lens[w.b]);
+  int n = w.n;
   if (n > (int64_t)a.table_width << ps) {
     n = (int)((int64_t)a.table_width << ps);
     if (threadIdx.x == 0) atomicOr(a.status, PQ_DEV_BAD_INDEX);
@@ -406,6 +410,36 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   const int tiles = w.rows - w.r0 > PT ? 2 : 1;          // row tiles that hold rows
   const Interior interior{c_lo, c_hi, p_first, p_last, a.window, MASKED ? a.sinks : 0};
 
+      // ---- of the softmax warps: their rows, whose queries are requested before the block sets itself up
+  const int i = (warp - PR_SOFT0) >> 2;                  // row tile
+      const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
+      const int r = w.r0 + PT * i + row;
+      const bool live = r < w.rows;
+      const int rr = min(r, w.rows - 1);
+      const int head = w.kvh * group + rr % group;
+      // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
+      // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
+      // its fetch.
+      constexpr int LPR = HD / 8, RPI = 32 / LPR;
+      const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
+      auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
+      // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
+      // group is a multiplication by its reciprocal (rows + group below 2^16).
+      const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
+      const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
+      auto each_row = [&](auto body) {
+#pragma unroll 4
+        for (int k = 0; k < LPR; ++k) {
+          const int to = io_row + RPI * k, x = to + tile_off;
+          const int t = group == 1 ? x : (int)__umulhi((uint32_t)x, inv_group);
+          if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
+        }
+      };
+  if (warp >= PR_SOFT0 && warp < PR_PROD0)
+    each_row([&](int to, int64_t t, int hq) {
+      ptx::cp_async16(place(to, io_chunk), reinterpret_cast<const uint4*>(a.Q + t * a.ldq + hq * HD) + io_chunk, 16);
+    });
+
   if (threadIdx.x == 32) {
     ptx::mbar_init(&S.q_full, 8);
     for (int s = 0; s < PR_STAGES; ++s) {
@@ -437,35 +471,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
 
   if (warp >= PR_SOFT0 && warp < PR_PROD0) {
     // ------------------------------------------------------------------------------- softmax
-    const int i = (warp - PR_SOFT0) >> 2;                // row tile
-    const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
-    const int r = w.r0 + PT * i + row;
-    const bool live = r < w.rows;
-    const int rr = min(r, w.rows - 1);
-    const int head = w.kvh * group + rr % group;
-    // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
-    // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
-    // its fetch.
-    constexpr int LPR = HD / 8, RPI = 32 / LPR;
-    const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
-    auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
-    // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
-    // group is a multiplication by its reciprocal (rows + group below 2^16).
-    const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
-    const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
-    auto each_row = [&](auto body) {
-#pragma unroll 4
-      for (int k = 0; k < LPR; ++k) {
-        const int to = io_row + RPI * k, x = to + tile_off;
-        const int t = group == 1 ? x : (int)__umulhi((uint32_t)x, inv_group);
-        if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
-      }
-    };
     float c_row;                                         // raw scores to log2 units, but for the keys' power of two
     {
-      each_row([&](int to, int64_t t, int hq) {
-        ptx::cp_async16(place(to, io_chunk), reinterpret_cast<const uint4*>(a.Q + t * a.ldq + hq * HD) + io_chunk, 16);
-      });
       ptx::cp_async_wait_all();
       __syncwarp();
       // largest magnitude, two channels an instruction; infinities and NaN do not count (the rare second pass)
