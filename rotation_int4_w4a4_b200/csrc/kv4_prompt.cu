@@ -516,11 +516,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       const int j = h >> 1, sc = j % SC_RING, t0 = HT * (h & 1);
       const uint32_t s_buf = s_col + t0;
       if (t0 == 0) ok = pr_warp_wait(&S.sc_full[sc], (uint32_t)(j / SC_RING) & 1u, &S.abort_flag, a.status);
-      ok = ok && pr_warp_wait(&S.s_full[i][h & 1], (uint32_t)j & 1u, &S.abort_flag, a.status);
       if (!ok) break;
-      ptx::tc_fence_after();
+      // what the half's tokens bring, read while the scores are still on their way
       const uint4 valid = *reinterpret_cast<const uint4*>(S.valid[sc]);
+      const int2 scaled = *reinterpret_cast<const int2*>(&S.scaled[sc][2 * (h & 1)]);
+      float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
+      const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
       const uint32_t va = t0 ? valid.z : valid.x, vb = t0 ? valid.w : valid.y;
+      if (!(ok = pr_warp_wait(&S.s_full[i][h & 1], (uint32_t)j & 1u, &S.abort_flag, a.status))) break;
+      ptx::tc_fence_after();
       // Raises rows' references to cand (largest score plus exponent of a value scale), in the sum and in O.
       auto raise = [&](bool grow, float cand) {
         const float m_new = grow ? cand : m;
@@ -544,10 +548,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       // The maximum is not taken first: the reference of the halves before serves until a row's probabilities outgrow
       // it, and only then (and at first) is the maximum found, the reference raised and the half done again.
       uint32_t pa[16], pb[16];
-      if ((va & vb) == 0xffffffffu && (S.scaled[sc][2 * (h & 1)] & S.scaled[sc][2 * (h & 1) + 1]) != 0) {
+      if ((va & vb) == 0xffffffffu && (scaled.x & scaled.y) != 0) {
         bool over = m == -INFINITY;
-        float2 kp = *reinterpret_cast<const float2*>(&S.k_pow[sc][2 * (h & 1)]);
-        const float2 v2 = *reinterpret_cast<const float2*>(&S.v_exp[sc][2 * (h & 1)]);
         kp.x *= c_row, kp.y *= c_row;
         float sum0, sum1;
         for (int pass = 0;; ++pass) {
