@@ -4,15 +4,18 @@
 
 Objects go to ``_build/`` at the repository root; the shared library to
 ``rotation_int4_w4a4_b200/_lib/libpq.so``.  The CUDA runtime is linked statically, so the
-library depends only on the driver (``libcuda``) at run time.
+library depends only on the driver (``libcuda``) at run time.  Beside it lies ``_pqcall.so``, the
+Python module through which pq.py makes its quickest calls, compiled against the installed torch.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -23,6 +26,8 @@ OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["pq_host.cpp", "transform.cu", "smooth_rows.cu", "rotate_mma.cu", "gemm.cu", "gemm_small.cu", "gemv.cu", "rrs.cu", "rows_small.cu", "gemm_static_scratch.cu",
            "ops_host.cpp", "quant8.cu", "w8a8.cu", "quant_fp4.cu", "fp4.cu", "kv4_append.cu", "kv4_attention.cu", "kv4_prompt.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh", "quant_fp4.cuh"]
+CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
+CALL_LIB = os.path.join(LIBDIR, "_pqcall.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
                      "-I" + os.path.join(ROOT, "include")]
@@ -42,6 +47,19 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _call_command() -> list[str]:
+    """The compiler's command for _pqcall.so (torch is found, not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("torch is not installed: _pqcall.so reads its tensors")
+    torch = list(spec.submodule_search_locations)[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"] + ["-isystem" + d for d in include] +
+            [CALL_SOURCE, "-o", CALL_LIB, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
@@ -55,12 +73,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + hdrs):
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc()] + NVCC_FLAGS + extra + ["-c", s, "-o", o])
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        for cmd, res in zip(jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), jobs)):
+    call = [_call_command()] if force or _stale(CALL_LIB, [CALL_SOURCE, hdrs[-1]]) else []
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        for cmd, res in zip(call + jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), call + jobs)):
             if verbose or res.returncode != 0:
                 sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
             if res.returncode != 0:
-                raise RuntimeError(f"nvcc failed for {cmd[-3]}")
+                raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB] + objs + ["-cudart", "static"]
         res = subprocess.run(cmd, capture_output=True, text=True)

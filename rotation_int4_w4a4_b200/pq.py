@@ -459,6 +459,26 @@ def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=No
            "pq_w8a8_linear")
 
 
+_call = None
+
+
+def _caller():
+    """The compiled module behind the quickest calls (csrc/binding.cpp), loaded at the first of them: it needs torch."""
+    global _call
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries have to be there first)
+    path = os.path.join(os.path.dirname(_LIB_PATH), "_pqcall.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_pqcall.so is not built ({path}); run python -m rotation_int4_w4a4_b200.build")
+    loader = importlib.machinery.ExtensionFileLoader("_pqcall", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pqcall", loader))
+    module.bind(*(_c.cast(f, _vp).value for f in (lib.pq_quant_fp4, lib.pq_fp4_gemm, lib.pq_fp4_linear, lib.pq_kv4_attention_masked)))
+    _call = module
+    return module
+
+
 def _fp4_format(fmt):
     form = FP4_FORMATS.get(fmt)
     if form is None:
@@ -484,6 +504,10 @@ def pq_quant_fp4(X, codes, scales, fmt="nv", g=0, factor=1.0, T=None, D=None, ld
     """X bf16 [T, ldx] -> E2M1 codes uint8 [T, D / 2] and one scale a block of channels, uint8 of :func:`pq_fp4_scale_bytes`
     (fmt "mx": blocks of 32, "nv": of 16, times factor); rows rotated in blocks of g channels by a Hadamard matrix first
     (g = 0: not)."""
+    if T is None and D is None and ldx is None and stream is None:
+        st = (_call or _caller()).quant_fp4(X, codes, scales, fmt, g, factor)
+        if st >= 0:                            # -1: something is not as it should be, and is named below
+            return _check(st, "pq_quant_fp4")
     dev, torch = _here()
     form = _fp4_format(fmt)
     xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
@@ -514,6 +538,10 @@ def pq_fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", alpha=1.0, T=
                 stream=None) -> None:
     """Y [T, N] = alpha times the product of the numbers that E2M1 codes and their block scales stand for (codes uint8
     [T, D / 2] and [N, D / 2]; fmt "nv": alpha holds the two tensors' factors)."""
+    if T is None and N is None and D is None and out_dtype is None and stream is None:
+        st = (_call or _caller()).fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt, alpha)
+        if st >= 0:
+            return _check(st, "pq_fp4_gemm")
     dev, torch = _here()
     form = _fp4_format(fmt)
     T = codes_A.shape[0] if T is None else T
@@ -527,6 +555,10 @@ def pq_fp4_linear(X, codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", g=0, fac
                   D=None, ldx=None, out_dtype=None, stream=None) -> None:
     """:func:`pq_quant_fp4` of X into codes_A / scales_A and :func:`pq_fp4_gemm` into Y, one call (fmt "nv": alpha =
     factor_A * factor_W)."""
+    if T is None and N is None and D is None and ldx is None and out_dtype is None and stream is None:
+        st = (_call or _caller()).fp4_linear(X, codes_A, scales_A, codes_W, scales_W, Y, fmt, g, factor_A, factor_W)
+        if st >= 0:
+            return _check(st, "pq_fp4_linear")
     dev, torch = _here()
     form = _fp4_format(fmt)
     xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
@@ -672,6 +704,11 @@ def pq_kv4_attention_masked(cache: KV4Cache, Q, O, q_start, seq_lens, block_tabl
                             tree=None, stream=None) -> None:
     """:func:`pq_kv4_attention` with sinks (under a window the first `sinks` tokens stay visible) and a tree of drafted tokens
     (int32 [T, words]: bit j of a row's words, the lowest first, says that it sees its sequence's new token j)."""
+    if stream is None:
+        st = (_call or _caller()).attention_masked(cache.handle, cache.device, Q, O, q_start, seq_lens, block_table, max_q, max_len,
+                                                   scale, window, sinks, tree)
+        if st >= 0:
+            return _check(st, "pq_kv4_attention_masked")
     dev, torch = _here()
     T, hd = Q.shape[0], cache.head_dim
     wq = _query_width(Q, hd)
