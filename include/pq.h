@@ -406,10 +406,10 @@ pq_status pq_w8a8_linear(const void* X, int64_t T, int64_t D, int64_t ldx, int g
  *   Y device [T][N] float32 or bf16 (RNE of the float32 result), dense, 16-byte aligned.  No scratch, one launch.
  *
  * pq_fp4_linear — pq_quant_fp4(X, T, D, ldx, g, format, factor_A, codes_A, scales_A) followed by pq_fp4_gemm with alpha =
- *   factor_A * factor_W (NV; MX: 1), in one call.  codes_A and scales_A are caller-owned and written.  With few output
- *   tiles the product is launched as a programmatic dependent and its first weight loads overlap the quantisation:
- *   codes_W and scales_W must be complete when the call is made (written by work enqueued on `stream` before it, or
- *   earlier); Y must not overlap X, codes_A or scales_A.
+ *   factor_A * factor_W (NV: a normal float32, or factor_W 0; MX: 1), in one call, the same bits.  codes_A and scales_A are
+ *   caller-owned and written.  Up to 16 tokens may be one kernel; otherwise the product is launched as a programmatic
+ *   dependent whose first weight loads may overlap the quantisation: codes_W and scales_W must be complete when the call is
+ *   made (written by work enqueued on `stream` before it, or earlier); Y must not overlap X, codes_A or scales_A.
  */
 typedef enum { PQ_FP4_MX = 0, PQ_FP4_NV = 1 } pq_fp4_format;
 /* Bytes of the scales of `rows` rows of D channels (host only; 0 for sizes or a format that the calls refuse). */

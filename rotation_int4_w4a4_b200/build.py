@@ -47,11 +47,11 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _call_command() -> list[str]:
-    """The compiler's command for _pqcall.so (torch is found, not imported)."""
+def _call_command() -> list[str] | None:
+    """The compiler's command for _pqcall.so (torch is found, not imported), None without torch: the library needs none."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("torch is not installed: _pqcall.so reads its tensors")
+        return None
     torch = list(spec.submodule_search_locations)[0]
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
@@ -74,6 +74,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc()] + NVCC_FLAGS + extra + ["-c", s, "-o", o])
     call = [_call_command()] if force or _stale(CALL_LIB, [CALL_SOURCE, hdrs[-1]]) else []
+    if call == [None]:
+        sys.stderr.write("torch is not installed: _pqcall.so, which reads its tensors, is left out\n")
+        call = []
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         for cmd, res in zip(call + jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), call + jobs)):
             if verbose or res.returncode != 0:

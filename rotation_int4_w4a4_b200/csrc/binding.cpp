@@ -30,9 +30,9 @@ PyObject* not_taken() {
 
 const at::Tensor* tensor(PyObject* o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
-// A tensor of the current device and of this type.
+// A tensor of the current device and of this type, with memory and strides (sparse ones have none).
 bool here(const at::Tensor* x, at::ScalarType type, int dev) {
-  return x && x->defined() && x->is_cuda() && x->get_device() == dev && x->scalar_type() == type;
+  return x && x->defined() && x->layout() == at::kStrided && x->is_cuda() && x->get_device() == dev && x->scalar_type() == type;
 }
 
 // A dense one of at least `need` elements.
@@ -46,6 +46,8 @@ bool integer(PyObject* o, int64_t* v) {
   *v = PyLong_AsLongLong(o);
   return !(*v == -1 && PyErr_Occurred());
 }
+
+bool int32(PyObject* o, int64_t* v) { return integer(o, v) && *v == (int32_t)*v; }
 
 bool number(PyObject* o, double* v) {
   if (!PyFloat_Check(o) && !PyLong_Check(o)) return false;   // no tensor: reading one would wait for the device
@@ -95,6 +97,16 @@ int device() {
 }
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
+// Tensors without memory (fake ones, functional ones) throw when asked for it, and no exception may leave a C entry.
+template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
+PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return F(a, n);
+  } catch (...) {
+    return not_taken();
+  }
+}
+
 template <typename F>
 PyObject* call(F f) {
   pq_status st;
@@ -105,14 +117,14 @@ PyObject* call(F f) {
 }
 
 // quant_fp4(X, codes, scales, fmt, g, factor)
-PyObject* py_quant_fp4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* py_quant_fp4(PyObject* const* a, Py_ssize_t n) {
   if (n != 6) return not_taken();
   const int dev = device();
   Rows X;
   pq_fp4_format f;
   int64_t g;
   double factor;
-  if (dev < 0 || !rows_of(a[0], dev, &X) || tensor(a[0])->dim() != 2 || !format_of(a[3], &f) || !integer(a[4], &g) ||
+  if (dev < 0 || !rows_of(a[0], dev, &X) || tensor(a[0])->dim() != 2 || !format_of(a[3], &f) || !int32(a[4], &g) ||
       !number(a[5], &factor))
     return not_taken();
   void* codes = dense(a[1], at::kByte, X.T * X.D / 2, dev);
@@ -133,6 +145,7 @@ struct Product {
 bool product(PyObject* const* a, int64_t T, int64_t D, pq_fp4_format f, int dev, Product* p) {
   const at::Tensor *w = tensor(a[2]), *y = tensor(a[4]);
   if (!w || !w->defined() || w->dim() < 1 || !y || !y->defined()) return false;
+  if (w->dim() == 2 && w->size(1) != D / 2) return false;
   if (y->scalar_type() != at::kBFloat16 && y->scalar_type() != at::kFloat) return false;
   p->N = w->size(0);
   p->out = y->scalar_type() == at::kBFloat16 ? PQ_OUT_BF16 : PQ_OUT_F32;
@@ -145,7 +158,7 @@ bool product(PyObject* const* a, int64_t T, int64_t D, pq_fp4_format f, int dev,
 }
 
 // fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt, alpha)
-PyObject* py_fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* py_fp4_gemm(PyObject* const* a, Py_ssize_t n) {
   if (n != 7) return not_taken();
   const int dev = device();
   pq_fp4_format f;
@@ -163,7 +176,7 @@ PyObject* py_fp4_gemm(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // fp4_linear(X, codes_A, scales_A, codes_W, scales_W, Y, fmt, g, factor_A, factor_W)
-PyObject* py_fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* py_fp4_linear(PyObject* const* a, Py_ssize_t n) {
   if (n != 10) return not_taken();
   const int dev = device();
   Rows X;
@@ -171,7 +184,7 @@ PyObject* py_fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int64_t g;
   double fa, fw;
   Product p;
-  if (dev < 0 || !rows_of(a[0], dev, &X) || tensor(a[0])->dim() != 2 || !format_of(a[6], &f) || !integer(a[7], &g) ||
+  if (dev < 0 || !rows_of(a[0], dev, &X) || tensor(a[0])->dim() != 2 || !format_of(a[6], &f) || !int32(a[7], &g) ||
       !number(a[8], &fa) || !number(a[9], &fw) || !product(a + 1, X.T, X.D, f, dev, &p))
     return not_taken();
   void* stream = stream_of(dev);
@@ -182,7 +195,7 @@ PyObject* py_fp4_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // attention_masked(cache handle, cache device, Q, O, q_start, seq_lens, block_table, max_q, max_len, scale, window, sinks, tree)
-PyObject* py_attention_masked(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* py_attention_masked(PyObject* const* a, Py_ssize_t n) {
   if (n != 13) return not_taken();
   const int dev = device();
   int64_t handle, on, max_q, max_len, window, sinks;
@@ -219,7 +232,7 @@ PyObject* py_attention_masked(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // bind(addresses of pq_quant_fp4, pq_fp4_gemm, pq_fp4_linear, pq_kv4_attention_masked)
-PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* py_bind(PyObject* const* a, Py_ssize_t n) {
   int64_t v[4];
   for (Py_ssize_t i = 0; i < 4; ++i)
     if (n != 4 || !integer(a[i], &v[i])) {
@@ -233,7 +246,7 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
-#define PQ_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(py_##name)), METH_FASTCALL, nullptr}
+#define PQ_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(entry<py_##name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PQ_METHOD(bind), PQ_METHOD(quant_fp4), PQ_METHOD(fp4_gemm), PQ_METHOD(fp4_linear),
                          PQ_METHOD(attention_masked), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pqcall", "Calls of libpq with tensors read in place.", -1, methods,

@@ -1,5 +1,6 @@
 // Argument checks and dispatch of the 8-bit and 4-bit floating-point products and of the 4-bit key/value cache.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "internal.h"
@@ -238,6 +239,10 @@ extern "C" pq_status pq_fp4_linear(const void* X, int64_t T, int64_t D, int64_t 
   pq_status st = check_quant_fp4(X, T, D, ldx, g, format, factor_A, codes_A, scales_A);
   if (st != PQ_OK) return st;
   const float alpha = format == PQ_FP4_NV ? factor_A * factor_W : 1.0f;
+  if (format == PQ_FP4_NV && factor_W != 0.0f && std::fabs(alpha) < FLT_MIN) {
+    set_error("factor_A * factor_W = %g * %g is below float32's normal numbers", (double)factor_A, (double)factor_W);
+    return PQ_ERR_INVALID_ARG;
+  }
   st = check_gemm_fp4(codes_A, scales_A, codes_W, scales_W, T, N, D, format, alpha, Y, out_dtype);
   if (st != PQ_OK) return st;
   return fp4_linear_launch(X, T, D, ldx, g, format == PQ_FP4_NV, factor_A, codes_A, scales_A, codes_W, scales_W, N, alpha, Y,

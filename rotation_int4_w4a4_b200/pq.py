@@ -486,6 +486,19 @@ def _fp4_format(fmt):
     return form
 
 
+def _fp4_group(g):
+    """g as a C int holds it: the library says which are rotations."""
+    if isinstance(g, int) and not -2 ** 31 <= g < 2 ** 31:
+        raise ValueError(f"g={g}: expected 0, 64, 128 or 256")
+    return g
+
+
+def _fp4_width(codes_W, D, given):
+    """Weights wider than the activations are a mistake, unless the caller has named D (narrower ones hold too little)."""
+    if given is None and not isinstance(codes_W, int) and codes_W.dim() == 2 and codes_W.shape[1] * 2 > D:
+        raise ValueError(f"codes_W: rows of {codes_W.shape[1]} bytes, expected {D // 2}")
+
+
 def _fp4_bytes(rows, D, form):
     """Bytes of a tensor's scales (sizes the calls refuse give a small number: the library names what is wrong)."""
     span = 64 if form else 128
@@ -512,7 +525,7 @@ def pq_quant_fp4(X, codes, scales, fmt="nv", g=0, factor=1.0, T=None, D=None, ld
     form = _fp4_format(fmt)
     xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
     u8 = torch.uint8
-    _check(lib.pq_quant_fp4(xp, T, D, ldx, g, form, factor, _on(codes, "codes", "u8", u8, T * D // 2, dev),
+    _check(lib.pq_quant_fp4(xp, T, D, ldx, _fp4_group(g), form, factor, _on(codes, "codes", "u8", u8, T * D // 2, dev),
                             _on(scales, "scales", "u8", u8, _fp4_bytes(T, D, form), dev), _raw_stream(stream, dev, torch)),
            "pq_quant_fp4")
 
@@ -546,7 +559,8 @@ def pq_fp4_gemm(codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", alpha=1.0, T=
     form = _fp4_format(fmt)
     T = codes_A.shape[0] if T is None else T
     N = codes_W.shape[0] if N is None else N
-    D = codes_A.shape[1] * 2 if D is None else D
+    given, D = D, codes_A.shape[1] * 2 if D is None else D
+    _fp4_width(codes_W, D, given)
     out, ca, sa, cw, sw, y = _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch)
     _check(lib.pq_fp4_gemm(ca, sa, cw, sw, T, N, D, form, alpha, y, out, _raw_stream(stream, dev, torch)), "pq_fp4_gemm")
 
@@ -561,10 +575,12 @@ def pq_fp4_linear(X, codes_A, scales_A, codes_W, scales_W, Y, fmt="nv", g=0, fac
             return _check(st, "pq_fp4_linear")
     dev, torch = _here()
     form = _fp4_format(fmt)
+    given = D
     xp, T, D, ldx = _rows8(X, T, D, ldx, dev, torch)
+    _fp4_width(codes_W, D, given)
     N = codes_W.shape[0] if N is None else N
     out, ca, sa, cw, sw, y = _fp4_args(codes_A, scales_A, codes_W, scales_W, Y, T, N, D, form, out_dtype, dev, torch)
-    _check(lib.pq_fp4_linear(xp, T, D, ldx, g, form, factor_A, ca, sa, cw, sw, factor_W, N, y, out,
+    _check(lib.pq_fp4_linear(xp, T, D, ldx, _fp4_group(g), form, factor_A, ca, sa, cw, sw, factor_W, N, y, out,
                              _raw_stream(stream, dev, torch)), "pq_fp4_linear")
 
 

@@ -112,3 +112,48 @@ def test_refusals_with_cuda_tensors(pq):
         pq.pq_kv4_attention_masked(cache, Q, Q.clone(), i[:1], i[:1], i[:3].view(1, 3), 1, 1, sinks=1, window=2)
     with pytest.raises(pq.PQError, match="sinks=-1"):
         pq.pq_kv4_attention_masked(cache, Q, Q.clone(), i[:2], i[:1], i[:3].view(1, 3), 1, 1, sinks=-1, window=2)
+
+
+@pytest.mark.gpu
+def test_tensors_without_memory_and_other_layouts_are_refused(pq):
+    """Sparse and fake tensors reach the compiled way too: an error in words, not an exception out of C."""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    X, c, s, Y = (torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 128, dtype=torch.uint8, device="cuda"),
+                  torch.zeros(4096, dtype=torch.uint8, device="cuda"), torch.zeros(4, 4, device="cuda"))
+    with FakeTensorMode(allow_non_fake_inputs=True) as mode:
+        none = {"X": mode.from_tensor(X), "c": mode.from_tensor(c), "s": mode.from_tensor(s), "Y": mode.from_tensor(Y)}
+    thin = {"X": X.to_sparse(), "c": c.to_sparse(), "s": s.to_sparse(), "Y": Y.to_sparse()}
+    call = pq._caller()
+    for other in (none, thin):
+        x, codes, scales, y = other["X"], other["c"], other["s"], other["Y"]
+        for args in ((x, c, s), (X, codes, s), (X, c, scales)):
+            assert call.quant_fp4(*args, "nv", 0, 1.0) != 0
+        for args in ((codes, s, c, s, Y), (c, scales, c, s, Y), (c, s, codes, s, Y), (c, s, c, scales, Y), (c, s, c, s, y)):
+            assert call.fp4_gemm(*args, "nv", 1.0) != 0
+            assert call.fp4_linear(X, *args, "nv", 0, 1.0, 1.0) != 0
+        assert call.fp4_linear(x, c, s, c, s, Y, "nv", 0, 1.0, 1.0) != 0
+
+
+@pytest.mark.gpu
+def test_weights_of_another_width_and_groups_past_an_int(pq):
+    X, c, s, Y = (torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 128, dtype=torch.uint8, device="cuda"),
+                  torch.zeros(4096, dtype=torch.uint8, device="cuda"), torch.zeros(4, 4, device="cuda"))
+    wide = torch.zeros(4, 256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="codes_W: rows of 256 bytes, expected 128"):
+        pq.pq_fp4_gemm(c, s, wide, s, Y)
+    with pytest.raises(ValueError, match="codes_W: rows of 256 bytes, expected 128"):
+        pq.pq_fp4_linear(X, c, s, wide, s, Y)
+    pq.pq_fp4_gemm(c, s, wide, s, Y, D=256)
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(ValueError, match="g=4294967296"):
+            pq.pq_quant_fp4(X, c, s, g=1 << 32, stream=stream)
+        with pytest.raises(ValueError, match="g=4294967360"):
+            pq.pq_fp4_linear(X, c, s, c, s, Y, g=(1 << 32) + 64, stream=stream)
+
+
+def test_products_of_factors_below_normal_numbers_are_refused(pq):
+    """2^-100 * 2^-40 keeps no more than 9 bits in float32: refused before anything is launched; a factor of 0 is a tensor of zeros."""
+    st = pq.lib.pq_fp4_linear(256, 4, 256, 256, 0, 1, 2.0 ** -100, 256, 256, 256, 256, 2.0 ** -40, 4, 256, 0, None)
+    assert st != 0 and b"below float32's normal numbers" in pq.lib.pq_last_error()
+    st = pq.lib.pq_fp4_linear(256, 4, 256, 256, 0, 1, 2.0 ** -100, 256, 256, 256, 256, -(2.0 ** -40), 4, 256, 0, None)
+    assert st != 0 and b"below float32's normal numbers" in pq.lib.pq_last_error()
