@@ -15,19 +15,22 @@
 //   time.
 //   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue; warps 2..5: epilogue.
 //
-// fp4_pair_kernel (many output tiles): persistent, one CTA per SM, clusters of two CTAs that share every MMA (cta_group::2,
-//   M256 N256 K64).  Here tokens are operand A and weights B, so that a thread of the epilogue has 16 channels of one token
-//   side by side and stores them whole.  Scales of 256 columns are wanted in both CTAs, those of 128 rows in each its own.
-//   Tensor memory holds two accumulators of 256 columns only if they share some (128): the scales take the rest.  The epilogue reads the shared columns first and hands them over, and the next tile's reduction runs under
-//   what is left of it.
+// fp4_pair_kernel (many tokens): persistent, one CTA per SM, clusters of two CTAs that share every MMA (cta_group::2, M256 N256
+//   K64).  Here tokens are operand A and weights B, so that a thread of the epilogue has 16 channels of one token side by side
+//   and stores them whole.  Scales of 256 columns are wanted in both CTAs, those of 128 rows in each its own.  Tensor memory
+//   holds two accumulators of 256 columns only if they share some (128): the scales take the rest.  The epilogue reads the
+//   shared columns first and hands them over, and the next tile's reduction runs under what is left of it.
 //   warp 0: TMA producer; warp 1: tensor memory, scale copies and MMA issue (even CTA); warps 4..11: epilogue, two a lane
 //   quarter.
 //
 // Issue bounds the pair kernel before the tensor cores do: a step is 12 scale copies, 4 products and a commit.  From a branch
 // on the lane's number they took 1660 cycles (8192 x 4096 x 14336: 361 us; operands move to uniform registers one by one),
-// from an elected lane with a warp's waits 800 (178 us), with the elected lane walking the steps alone 660 (167 us); the
-// four products take 550.  A warp of its own for the copies costs more in barriers than it saves (185 us), and copies a half
-// step ahead of their products twice as much (326 us: they wait for the products before them).
+// from an elected lane with a warp's waits 800 (178 us), with the elected lane walking the steps alone 660 (167 us, 5.8
+// PFLOP/s); the four products take 550.  A warp of its own for the copies costs more in barriers than it saves (185 us), and
+// copies a half step ahead of their products twice as much (326 us: they wait for the products before them).  In a row of such
+// calls the 1000 W limit lowers the clock, and the same product takes 175 to 200 us.
+// The tile kernel is bound by the weights' bytes and the latencies of one launch: 64 tokens through 14336 x 4096 (33 MB from HBM) take
+// 10.4 us, 3.2 TB/s, of which a launch that only starts, waits once for memory and ends is 4.
 //
 // Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains what it has in flight, meets
 // its cluster, frees tensor memory and returns.
@@ -362,7 +365,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(P_THREADS, 1) fp4_pa
 constexpr int TM = 128;                 // weight rows per tile
 constexpr int T_THREADS = 192;
 
-// NP: token columns of a tile.  DEEP: stages for one CTA per SM (about 220 KB in flight), otherwise for two.
+// NP: token columns of a tile.  DEEP: stages for one CTA per SM (about 220 KB in flight), otherwise for two: where there are
+// more CTAs than SMs (us, deep against two; 64 tokens, D 4096: 14336 channels, 112 tiles, 9.2 : 9.6; 28672, 224, 16.4 : 10.7; 16
+// tokens, 65536, 512, 36.6 : 30.8).
 template <int NP, bool NV, bool DEEP> struct TileGeom {
   static constexpr int SF = kPieces<NV> * PIECE;          // scale bytes of 128 rows a step
   static constexpr uint32_t TX = (TM + NP) * KB + 2 * SF;
@@ -727,7 +732,8 @@ pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, in
 int tile_tokens(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
 // K steps of the tile kernel's reduction, and the ranges it is cut into: as long as every CTA still has an SM of its own and
-// keeps some steps.
+// keeps two steps (us on the device, uncut and by 2, 4 and 8 at most).  1 token, N x D 4096 x 4096: 7.4, 6.8, 5.8, 5.8; 4096 x
+// 14336: 18.9, 12.0, 8.9, 8.9; 16 tokens, 1024 x 14336: 18.6, 11.9, 7.9, 6.4; 391 tokens, 1003 x 4192: 13.3, 11.5, 9.2, 9.2.
 int fp4_ranges(int64_t T, int64_t N, int64_t D, int* split) {
   const int np = tile_tokens(T), sms = device_sm_count(), steps = (int)((D + 2 * KB - 1) / (2 * KB));
   const int64_t tiles = (N + TM - 1) / TM * ((T + np - 1) / np);
@@ -740,16 +746,19 @@ template <bool NV>
 pq_status run(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t T,
               int64_t N, int64_t D, Fp4Call c) {
   const int sms = device_sm_count();
+  const int np = tile_tokens(T);
+  const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
   const int64_t pair_m = (T + 2 * PM - 1) / (2 * PM), pair_n = (N + PN - 1) / PN;
-  if (T > 128 && pair_m * pair_n * 4 >= 3 * (sms / 2)) {
+  // Pairs of CTAs from 129 tokens on, unless so few tiles of 128 x 128 that each may have its reduction cut over several SMs (us on
+  // the device, nv, pairs against tiles).  256 tokens, N x D 4096 x 4096 10.6 : 10.6, 4096 x 14336 22.0 : 16.7; past that border
+  // 6144 x 256 6.3 : 6.8, 5120 x 14336 22.2 : 23.4, 14336 x 4096 11.3 : 14.0; 1024 tokens 4096 x 4096 11.5 : 14.6, 4096 x 14336 24.4 : 31.9.
+  if (T > 128 && 2 * tiles > sms) {
     if (pair_m * pair_n >= ((int64_t)1 << 30)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
     Fp4Maps m;
     const pq_status st = make_maps(&m, codes_A, scales_A, codes_W, scales_W, T, N, D, c.pieces, kPieces<NV>, PM);
     if (st != PQ_OK) return st;
     return launch_pair<NV>(m, c, (int)pair_m, (int)pair_n, sms);
   }
-  const int np = tile_tokens(T);
-  const int64_t m_tiles = (N + TM - 1) / TM, tiles = m_tiles * ((T + np - 1) / np);
   if (tiles >= ((int64_t)1 << 31)) { set_error("too many output tiles"); return PQ_ERR_INVALID_ARG; }
   int split = 1;
   fp4_ranges(T, N, D, &split);
