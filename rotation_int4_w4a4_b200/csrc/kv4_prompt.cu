@@ -410,31 +410,31 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   const int tiles = w.rows - w.r0 > PT ? 2 : 1;          // row tiles that hold rows
   const Interior interior{c_lo, c_hi, p_first, p_last, a.window, MASKED ? a.sinks : 0};
 
-      // ---- of the softmax warps: their rows, whose queries are requested before the block sets itself up
+  // ---- of the softmax warps: their rows, whose queries are requested before the block sets itself up
   const int i = (warp - PR_SOFT0) >> 2;                  // row tile
-      const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
-      const int r = w.r0 + PT * i + row;
-      const bool live = r < w.rows;
-      const int rr = min(r, w.rows - 1);
-      const int head = w.kvh * group + rr % group;
-      // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
-      // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
-      // its fetch.
-      constexpr int LPR = HD / 8, RPI = 32 / LPR;
-      const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
-      auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
-      // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
-      // group is a multiplication by its reciprocal (rows + group below 2^16).
-      const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
-      const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
-      auto each_row = [&](auto body) {
+  const int row = (warp & 3) * 32 + lane;              // lane of tensor memory
+  const int r = w.r0 + PT * i + row;
+  const bool live = r < w.rows;
+  const int rr = min(r, w.rows - 1);
+  const int head = w.kvh * group + rr % group;
+  // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
+  // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
+  // its fetch.
+  constexpr int LPR = HD / 8, RPI = 32 / LPR;
+  const int io_row = (warp & 3) * 32 + lane / LPR, io_chunk = lane % LPR;
+  auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
+  // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
+  // group is a multiplication by its reciprocal (rows + group below 2^16).
+  const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
+  const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
+  auto each_row = [&](auto body) {
 #pragma unroll 4
-        for (int k = 0; k < LPR; ++k) {
-          const int to = io_row + RPI * k, x = to + tile_off;
-          const int t = group == 1 ? x : (int)__umulhi((uint32_t)x, inv_group);
-          if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
-        }
-      };
+    for (int k = 0; k < LPR; ++k) {
+      const int to = io_row + RPI * k, x = to + tile_off;
+      const int t = group == 1 ? x : (int)__umulhi((uint32_t)x, inv_group);
+      if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
+    }
+  };
   if (warp >= PR_SOFT0 && warp < PR_PROD0)
     each_row([&](int to, int64_t t, int hq) {
       ptx::cp_async16(place(to, io_chunk), reinterpret_cast<const uint4*>(a.Q + t * a.ldq + hq * HD) + io_chunk, 16);
@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     {
       ptx::cp_async_wait_all();
       __syncwarp();
-      // largest magnitude, two channels an instruction; infinities and NaN do not count (the rare second pass)
+      // largest magnitude, two channels an instruction; infinities and NaN do not count (the rare second pass; not for rows that
+      // do not exist, whose place holds what was there before: where that was float32 it cost 5 us)
       uint32_t mw = 0u;
 #pragma unroll 4
       for (int c = 0; c < HD / 8; ++c) {
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         mw = __vimax3_u16x2(mw, x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu);
       }
       float mq = __uint_as_float(max(mw << 16, mw & 0xFFFF0000u));
-      if (!(mq < INFINITY)) {
+      if (live && !(mq < INFINITY)) {
         mq = 0.0f;
 #pragma unroll 1
         for (int c = 0; c < HD; ++c)
