@@ -900,13 +900,18 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
   const int group = a.heads_q / a.cache.heads;
   const int64_t max_rows = max_q * group;
   const int sms = device_sm_count();
-  const bool prompt = max_rows > kPromptRows;
   const int64_t walk = (max_len + AT_STEP - 1) / AT_STEP;
-  // Tiles of 8 rows or 16.  Masked calls that leave blocks idle keep to 8, whose blocks are quicker (us, 8 against 16; 8
-  // key/value heads of 128, 32 rows each).  One sequence over 1029 tokens 11.4 : 14.9, 8100 19.5 : 20.2; two over 2048 14.2 :
-  // 16.2, 4300 23.3 : 20.6; four over 1029 14.9 : 17.2, 2048 19.2 : 19.2, 3000 25.6 : 22.1; 16 over 130 17.2 : 12.7.
+  // Masked calls that leave blocks idle.  (1) They keep to tiles of 8 rows, whose blocks are quicker (us, 8 against 16; 8 key/value
+  // heads of 128, 32 rows each).  One sequence over 1029 tokens 11.4 : 14.9, 8100 19.5 : 20.2; two over 2048 14.2 : 16.2, 4300
+  // 23.3 : 20.6; four over 1029 14.9 : 17.2, 2048 19.2 : 19.2, 3000 25.6 : 22.1; 16 over 130 17.2 : 12.7.
   const int64_t eights = a.B * a.cache.heads * ((max_rows + 7) / 8);
   const bool narrow = kv4_masked(a) && 2 * eights <= 3 * sms && eights * walk <= 2048;
+  // (2) They stay here with more rows, a step of 128 tokens an SM for each of 8 tiles (us, this against the prompts' kernel; 8 heads).
+  // One sequence over 300 tokens, 128 rows 9.2 : 14.6; 1029, 64 rows 12.4 : 14.1, 128 rows 14.7 : 15.4; 2048, 64 rows 14.0 :
+  // 14.4, 80 rows 15.6 : 14.6; 8192, 36 rows 23.6 : 21.9.  Two over 1029, 64 rows 14.7 : 15.9, 80 rows 17.1 : 16.7.  Four over
+  // 300, 64 rows 12.5 : 15.2; 1029, 64 rows 19.0 : 18.8.  Eight over 300, 48 rows 13.9 : 15.4, 80 rows 24.9 : 15.9.
+  const bool stay = kv4_masked(a) && max_rows <= 128 && eights <= 3 * sms && eights * walk <= 8 * sms;
+  const bool prompt = max_rows > kPromptRows && !stay;
   const int nt = max_rows > 8 && !narrow ? 2 : 1;
   const bool wide = a.cache.head_dim == 128;
   // Float32 workspace for partial results: [rows][head_dim] outputs, [rows] references and sums, then `extra` bytes.
@@ -936,7 +941,9 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     // One block an SM: chunks only where the tiles (of 256 rows; a sequence's last one half full on average) leave SMs idle,
     // at least two steps of 128 tokens each (400 rows over 1500 tokens: 31 us; 35 with four, 42 uncut; 64 rows over 8192: 32
     // with four or fewer, 39 with eight).
-    const int64_t tiles = a.B == 1 ? kv4_prompt_tiles(a) : std::max<int64_t>((a.T * group + 128 * (int64_t)a.B) / 256, 1);
+    int64_t tiles = a.B == 1 ? kv4_prompt_tiles(a) : std::max<int64_t>((a.T * group + 128 * (int64_t)a.B) / 256, 1);
+    // Sequences of up to 256 rows have a tile each.  (Masked calls alone: the others' parts, and so their bits, stay.)
+    if (kv4_masked(a) && max_rows <= 256) tiles = a.B;
     const int64_t want = sms / (tiles * a.cache.heads);
     Partials part = {};
     part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, (max_len + 255) / 256), 256));
@@ -953,10 +960,13 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
       // GPC holds two of eight) and a block has no more than 28 rows to join (us, cluster against two kernels; 8 key/value heads
       // of 128).  64 rows over 400 tokens 15.7 : 19.4, 2048 15.5 : 21.7; 128 over 2048 20.4 : 21.4; 256 over 1029 20.5 : 20.4; 256
       // over 400, in two, 26.7 : 17.8.  The host saves 4 us of a second launch and the workspace.
-      const int64_t c = std::min<int64_t>(std::min<int64_t>(3 * sms / 4 / (tiles * a.cache.heads), steps), KV4_CLUSTER);
+      const int64_t items = tiles * a.cache.heads;
+      const int64_t c = std::min<int64_t>(std::min<int64_t>(2 * items <= sms ? std::max<int64_t>(3 * sms / 4 / items, 2) : 1, steps), KV4_CLUSTER);
       const int64_t rows = std::min<int64_t>(max_rows, 256);
       if (c > 1 && (rows <= 28 * c || c == KV4_CLUSTER) && (steps + c - 1) / c <= (steps + part.chunks - 1) / part.chunks + 2)
         part.chunks = (int)c, part.cluster = 1;
+      else if (steps - (steps + part.chunks - 1) / part.chunks < 2)
+        part.chunks = 1;                                 // a step saved pays for no second kernel: 8 sequences over 300, uncut 15.9 : 17.2
     }
     if (!part.cluster && a.T * a.heads_q >= ((int64_t)1 << 31)) part.chunks = 1;  // the joining kernel takes a block a row
     part.chunk_len = (int)(((max_len + part.chunks - 1) / part.chunks + 127) / 128 * 128);

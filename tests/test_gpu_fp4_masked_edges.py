@@ -263,3 +263,30 @@ def test_nan_queries_and_scales(pq, q, n, window, bad):
                 assert bool((~got[touched].isfinite()).any(-1).all())
     assert torch.equal(run(), want)
     pq.pq_check_status()
+
+
+# Few sequences of up to 256 rows a head: blocks of 8 rows uncut and in clusters, tiles of 128 rows uncut, in clusters of 2 to 8 and in
+# parts that a second kernel joins; sequences that leave most of a tile empty beside others.
+@pytest.mark.parametrize("window,sinks,tree", [(0, 0, True), (700, 5, True), (300, 70, False)])
+@pytest.mark.parametrize("B,q,n", [(1, 32, 300), (1, 9, 1029), (1, 25, 1500), (2, 32, 300), (2, 18, 1029), (3, 30, 2000), (4, 12, 1029), (4, 24, 2100),
+                                   (8, 12, 300), (8, 12, 1029), (8, 24, 300), (8, 30, 1029), (9, 60, 900), (12, 17, 3000)])
+def test_batches_across_the_borders(pq, B, q, n, window, sinks, tree):
+    qs = [q] + [max(1, (q * (3 * b + 1)) % q) for b in range(1, B)]
+    ls = [n] + [max(qs[b], n * (b + 2) // (B + 3)) for b in range(1, B)]
+    check(pq, make_case(pq, B + q, qs, ls, 32, 8, 128, 32), max(qs), n, window=window, sinks=sinks, trees=trees_of(qs, 5) if tree else None)
+
+
+def test_rows_behind_a_tile_cost_nothing_and_say_nothing(pq):
+    """36 of 128 rows: what the other rows' place held (NaN and infinities of an earlier call) reaches nothing."""
+    cache, Q, starts, lens, table = make_case(pq, 3, [9] * 9, [900] * 9, 32, 8, 128, 32)
+    tree = torch.full((81, 1), 511, dtype=torch.int32, device="cuda")
+    outs = []
+    for bad in (None, float("nan"), float("inf")):
+        if bad is not None:
+            big = make_case(pq, 4, [60] * 9, [900] * 9, 32, 8, 128, 32)
+            big[1].fill_(bad)
+            pq.pq_kv4_attention_masked(big[0], big[1], torch.empty_like(big[1]), *big[2:], 60, 900, tree=torch.ones(540, 2, dtype=torch.int32, device="cuda"))
+        O = torch.empty_like(Q)
+        pq.pq_kv4_attention_masked(cache, Q, O, starts, lens, table, 9, 900, tree=tree)
+        outs.append(O)
+    assert torch.isfinite(outs[0].float()).all() and all(torch.equal(outs[0], o) for o in outs[1:])
