@@ -765,16 +765,20 @@ pq_status run(const uint8_t* codes_A, const uint8_t* scales_A, const uint8_t* co
   Fp4Maps m;
   const pq_status st = make_maps(&m, codes_A, scales_A, codes_W, scales_W, T, N, D, c.pieces, kPieces<NV>, np, c.g >= 0);
   if (st != PQ_OK) return st;
+  // One CTA an SM where all clusters run at once so: those of 4 leave an eighth of the SMs empty, those of 8 a fifth (us, one CTA an
+  // SM, in two waves, against two; 1 token, 2048 x 14336, 16 clusters of 8, 11.8 : 6.9; 4608 x 4096, 36 of 4, 9.6 : 6.1; 64 tokens,
+  // 2048 x 8192 12.7 : 8.7; 391 tokens, 1003 x 4192, 32 of 4, which fit, 9.4 : 9.7).
+  const bool deep = tiles * split <= (split == 8 ? 13 * sms / 16 : split == 4 ? 7 * sms / 8 : sms);
   if (c.g >= 0) {
 #define PQ_FUSED_CASE(G)                                                                     \
-  (tiles * split <= sms ? launch_tile<16, NV, true, G>(m, c, (int)m_tiles, tiles, split) \
-                        : launch_tile<16, NV, false, G>(m, c, (int)m_tiles, tiles, split))
+  (deep ? launch_tile<16, NV, true, G>(m, c, (int)m_tiles, tiles, split)                     \
+        : launch_tile<16, NV, false, G>(m, c, (int)m_tiles, tiles, split))
     return c.g == 0 ? PQ_FUSED_CASE(0) : c.g == 64 ? PQ_FUSED_CASE(64) : c.g == 128 ? PQ_FUSED_CASE(128) : PQ_FUSED_CASE(256);
 #undef PQ_FUSED_CASE
   }
 #define PQ_TILE_CASE(NP)                                                                   \
-  (tiles * split <= sms ? launch_tile<NP, NV, true>(m, c, (int)m_tiles, tiles, split) \
-                        : launch_tile<NP, NV, false>(m, c, (int)m_tiles, tiles, split))
+  (deep ? launch_tile<NP, NV, true>(m, c, (int)m_tiles, tiles, split)                      \
+        : launch_tile<NP, NV, false>(m, c, (int)m_tiles, tiles, split))
   return np == 16 ? PQ_TILE_CASE(16) : np == 32 ? PQ_TILE_CASE(32) : np == 64 ? PQ_TILE_CASE(64) : PQ_TILE_CASE(128);
 #undef PQ_TILE_CASE
 }
