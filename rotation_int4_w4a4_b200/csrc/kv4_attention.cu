@@ -995,7 +995,8 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     int cluster = 1;
     if (kv4_masked(a) && walk >= 4) {
       const int64_t items = (int64_t)a.B * a.cache.heads * row_tiles, fit = (nt == 1 ? 3 : 2) * (int64_t)sms;
-      while (cluster < KV4_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= fit) cluster *= 2;
+      // Clusters of 4 and 8 fill no GPC: 7/8 of the places hold them (51 clusters of 8, in two waves, 23.0; 48: 14.2).
+      while (cluster < KV4_CLUSTER && 2 * cluster <= walk && items * cluster * 2 <= (cluster == 1 ? fit : fit * 7 / 8)) cluster *= 2;
       if (walk > 8 * cluster || walk * (fit - items * cluster) > 4 * cluster * fit) cluster = 1;
     }
     // Under a window walks differ little: a block an item, as long as all run at once and none is long (us, uncut against shares;
