@@ -25,7 +25,7 @@ LIB = os.path.join(LIBDIR, "libpq.so")
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["pq_host.cpp", "transform.cu", "smooth_rows.cu", "rotate_mma.cu", "gemm.cu", "gemm_small.cu", "gemv.cu", "rrs.cu", "rows_small.cu", "gemm_static_scratch.cu",
            "ops_host.cpp", "quant8.cu", "w8a8.cu", "quant_fp4.cu", "fp4.cu", "kv4_append.cu", "kv4_attention.cu", "kv4_prompt.cu"]
-HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh", "quant_fp4.cuh"]
+HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh", "quant_fp4.cuh", "ptx_fp4.cuh"]
 CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
 CALL_LIB = os.path.join(LIBDIR, "_pqcall.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

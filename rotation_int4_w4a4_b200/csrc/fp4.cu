@@ -41,7 +41,7 @@
 #include <cstdint>
 
 #include "internal.h"
-#include "ptx.cuh"
+#include "ptx_fp4.cuh"
 #include "quant_fp4.cuh"
 
 namespace pq {
@@ -673,6 +673,29 @@ pq_status make_maps(Fp4Maps* m, const uint8_t* codes_A, const uint8_t* scales_A,
   return cuda_fail(e, "4-bit operand tensor map");
 }
 
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Y as dense rows: boxes of 128 bytes x 32 rows, 128-byte swizzle; the row stride has to be a multiple of 16 bytes.
+cudaError_t make_out_map(CUtensorMap* map, void* base, int64_t rows, int64_t inner, bool bf16) {
+  static const EncodeTiled enc = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q);
+    return reinterpret_cast<EncodeTiled>(e == cudaSuccess && q == cudaDriverEntryPointSuccess ? p : nullptr);
+  }();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)inner * (bf16 ? 2 : 4)};
+  cuuint32_t box[2] = {bf16 ? 64u : 32u, 32u};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
+                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 struct Fp4Call {
   float alpha;
   void* Y;
@@ -716,7 +739,7 @@ pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, in
   const bool bulk = c.N % (c.bf16 ? 8 : 4) == 0;
   m.y = m.a;
   if (bulk) {
-    const cudaError_t e = make_out_tile_map(&m.y, c.Y, c.T, c.N, c.bf16 != 0);
+    const cudaError_t e = make_out_map(&m.y, c.Y, c.T, c.N, c.bf16 != 0);
     if (e != cudaSuccess) return cuda_fail(e, "output tensor map");
   }
   constexpr size_t smem = sizeof(PairSmem<NV>) + 1024;

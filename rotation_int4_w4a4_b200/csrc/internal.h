@@ -118,9 +118,6 @@ cudaError_t make_bf16_tile_map(CUtensorMap* map, const void* base, int64_t rows,
 // optionally the 128-byte swizzle (rotate_mma.cu).
 cudaError_t make_u8_tile_map(CUtensorMap* map, const void* base, int64_t rows, int64_t inner, int box_inner,
                              int box_rows, bool swizzle128);
-// Tensor map of a dense bf16 or float32 [rows][inner] output: boxes of 128 bytes x 32 rows, 128-byte swizzle; the row stride
-// has to be a multiple of 16 bytes (rotate_mma.cu).
-cudaError_t make_out_tile_map(CUtensorMap* map, void* base, int64_t rows, int64_t inner, bool bf16);
 // bf16 rows [rows][D] as lines of 128 bytes: a box of box_rows whole rows, 128-byte swizzle,
 // rows past the end zero-filled (D / 64 <= 256).
 cudaError_t make_bf16_row_lines_map(CUtensorMap* map, const void* base, int64_t rows, int64_t D, int64_t ld,

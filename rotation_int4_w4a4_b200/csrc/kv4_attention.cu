@@ -10,7 +10,8 @@
 // bytes a token for keys and as much for values.  Bytes are the floor.  Above it lie the instructions (about 650 for 32
 // tokens of a head of 128), but no pipe is full: ALU 58%, issue 55%, DRAM 47%; a quarter of a warp's time is fixed latencies,
 // a fifth its own issue, an eighth each memory, a busy pipe and other warps' turns.  The same time with all pages in L2, and
-// with 16 warps an SM.  256 users of 4096 tokens: 287 us, 61% of the copy's bandwidth; 64 of up to 8192: 74; one of 65536: 33.
+// with 16 warps an SM.  256 users of 4096 tokens: 287 us, 61% of the copy's bandwidth; 64 of up to 8192: 74; one of 65536: 33
+// (call by call).
 // A warp owns blocks of 32 tokens:
 //   - keys are the A operand (16 tokens x 16 channels), the query rows the 8-column B operand: a thread's 16-byte
 //     load of one token is its share of the A operands of all 8 channel steps, because the channels of a dot product
@@ -34,6 +35,12 @@
 // A block's warps join their maxima, sums and outputs through shared memory.  The tokens of all sequences and heads are
 // cut into equal shares, one for each block that runs at once (64 users of 0 to 8192 tokens: 74 us; chunks of fixed length,
 // of which short sequences leave some empty: 89); a second kernel joins the float32 partial results.
+//
+// MASKED instances take sinks (under a window a row also sees the first tokens) and trees of drafted tokens (a list of bits says
+// which of the new tokens a row sees).  They walk steps of 128 tokens: those with sinks, then the window's; the gap is not read.
+// The tokens that a row sees of 32 are one word, made where some token may be hidden: a row of the cache is read once for all
+// of a tree's rows.  64 users of 0 to 8192 tokens under a window of 1024 with 4 sinks: 35 us; one token over 65536 the same 13
+// (of which 9 are a launch, the first loads and the output); 8 drafts over 1029 tokens 11.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>

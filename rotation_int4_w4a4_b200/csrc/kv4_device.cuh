@@ -7,6 +7,27 @@
 #include <cstdint>
 
 namespace pq {
+namespace ptx {
+
+// Float32 from the shared memory of a block of the cluster.
+template <int N>
+__device__ __forceinline__ void ld_cluster(float (&v)[N], uint32_t cluster_addr) {
+  static_assert(N == 2 || N == 4, "8 or 16 bytes");
+  if constexpr (N == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(cluster_addr)
+                 : "memory");
+  else
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+}  // namespace ptx
 
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -20,11 +20,18 @@
 //   warps 12..15       producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
 // Spills in a half step cost much: the operands leave so little of the L1 cache that they come back from L2 (with the next
-// half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).  The compiler reports 40 bytes of stores and 84 of
-// loads (heads of 64: 28 and 56); which code they belong to is not known.
-// 4096 of 8192 tokens, 32 + 8 heads of 128: 505 us, 51% of the library's bf16 rate; a half step takes 2300 cycles, of which
+// half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).  The compiler reports 16 bytes of stores and 44 of
+// loads (heads of 64: 12 and 36); which code they belong to is not known.
+// 4096 of 8192 tokens, 32 + 8 heads of 128: 466 us, 55% of the library's bf16 rate; a half step takes 2000 cycles, of which
 // the matrix instructions need 1400 and the exponentials 1000: the chain scores -> exponentials -> P -> product -> next
 // scores bounds it, with 10% of the SMs' time idle behind the last blocks.
+//
+// MASKED instances take sinks and trees of drafted tokens.  A block walks steps, not tokens: those with sinks, then those from
+// its rows' first window on; what lies between is not looked at.  Rows of a tree all see the tokens in front of the new ones
+// (or their windows of them), and of the new ones those that their bit lists name: 64 bits a half step, read where it is used.
+// Under a window of 1024 to 4096 much of a walk is the hidden-token path, so 32 tokens that none of a warp's rows sees are
+// passed over (4096 of 8192 tokens under a window of 2048 with 4 sinks: 200 us, 43% of what its pairs need at the bf16 rate;
+// 216 without).  Few tiles: the chunks of a tile are a cluster and join over its shared memory.
 //
 // Where the scales go.  Of 32 tokens that every row of the block sees and whose scales are of a size (kScaleSpread), keys
 // and values come with their scales multiplied in, as fp16 relative to a power of two for each 32 tokens (a key: one
@@ -40,7 +47,7 @@
 // Keys are rows of 128 bytes, K-major; values lie the same way and enter as an MN-major operand.
 //
 // Few rows over a long context leave SMs idle: the context is then cut into chunks whose partial results a second
-// kernel joins (kv4_attention.cu).
+// kernel joins (kv4_attention.cu, where the rules stand).
 //
 // Every mbarrier wait is bounded; a timeout sets the library's status word, the CTA drains, frees tensor memory and
 // returns.
@@ -69,7 +76,8 @@ constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 
 // scales (0 counts: such a token's score must not set the reference).  The reference of such a step is its largest score plus
 // the exponent of its largest value scale, which may belong to another token: the largest product is then up to 2^6 below 1
 // and keeps 18 of fp16's 24 places below it.  Within the factor every operand is a normal fp16 number (of scales above 2^-100).
-// 4096 of 8192 tokens: 478 us with every step so, 482 where the first 64 tokens differ by more, 696 where all do.
+// 4096 of 8192 tokens: 466 us with every step so; before its last improvements 478, 482 where the first 64 tokens differ by
+// more, 696 where all do.
 constexpr float kScaleSpread = 64.0f;
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {

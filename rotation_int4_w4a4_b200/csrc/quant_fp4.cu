@@ -9,7 +9,10 @@
 // log2(g) butterfly stages are one matrix instruction (m16n8k16, bf16 x +-1, exact products, float32 sums): lane t of
 // a row's four holds 16 consecutive channels of every 64, of which the matrix turns index bits 0, 1 (within 4 channels)
 // and 4, 5 (the lane), the operands' order being free; bits 2, 3, 6 and 7 are additions within the thread.  No value
-// crosses lanes but a block's maximum (mx: one shuffle) and the scale bytes of a word.
+// crosses lanes but a block's maximum (mx: one shuffle) and the scale bytes of a word (the 8-bit rows, whose butterflies go
+// through shuffles, take 85 us for what is 49 here).
+// 8192 x 14336, g = 128: 48.6 us nv, 47.7 mx (6.2 TB/s, 95% of the copy), g = 256 55.  Issue 67%: the floats'
+// conversion to E2M1 and the scales share a slow pipe, so two blocks' scales are converted by one instruction.
 #include <algorithm>
 #include <cstdint>
 

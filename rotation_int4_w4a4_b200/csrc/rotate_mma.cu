@@ -463,19 +463,6 @@ cudaError_t make_u8_tile_map(CUtensorMap* map, const void* base, int64_t rows, i
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_out_tile_map(CUtensorMap* map, void* base, int64_t rows, int64_t inner, bool bf16) {
-  EncodeTiledFnR enc = encode_fn_r();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)inner * (bf16 ? 2 : 4)};
-  cuuint32_t box[2] = {bf16 ? 64u : 32u, 32u};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
-                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // bf16 rows [rows][D] (row stride ld elements) seen as [rows][D/64][64]: a box of box_rows whole
 // rows lands as D/64 * box_rows lines of 128 bytes with the 128-byte swizzle (line L's 16-byte
 // chunk c at L * 128 + ((c ^ (L mod 8)) * 16)); rows past the end read as zero.  D / 64 <= 256.
