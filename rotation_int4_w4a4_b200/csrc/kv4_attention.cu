@@ -811,6 +811,7 @@ __global__ void __launch_bounds__(32 * JN_WARPS) kv4_join_kernel(const Kv4AttnAr
   const int64_t token = row / a.heads_q;
   ptx::griddep_wait();
   if (token < a.q_start[0] || token >= min((int64_t)a.q_start[a.B], a.T)) return;   // the whole block, or warp
+  if ((a.tree || a.sinks > 0) && part.ml[row].y == kRowDone) return;
   auto at = [&](int k) { return k * total + row; };
   uint16_t* dst = a.O + token * a.ldo + (row - token * a.heads_q) * HD;
   if (warp_a_row) join_row<HD, 1>(part.ml, part.o, part.chunks, at, a.cache.rotate_v, dst);
@@ -953,6 +954,7 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     if (kv4_masked(a) && max_rows <= 256) tiles = a.B;
     const int64_t want = sms / (tiles * a.cache.heads);
     Partials part = {};
+    part.sms = sms;
     part.chunks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want, (max_len + 255) / 256), 256));
     if (kv4_masked(a)) {
       // A masked walk is cut into equal parts by its own length (us on the device, uncut and by the number of parts at most).

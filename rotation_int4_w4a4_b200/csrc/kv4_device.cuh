@@ -38,8 +38,12 @@ struct Partials {
   float2* ml;     // [chunk][T * heads_q]
   int chunks;     // 1: no partials, the output is written directly
   int chunk_len;  // tokens of a chunk
+  int sms;        // the device's
   int cluster;    // masked calls: a tile's chunks are a cluster, which joins them over its shared memory (o and ml are not used)
 };
+
+// The sum beside a row's first piece where a masked call's walk was not cut: its output is written already.
+constexpr float kRowDone = -1.0f;
 
 // Sequence b's new tokens, the first and how many: rows of the call, whatever q_start holds.
 __device__ __forceinline__ void new_tokens(const int32_t* q_start, int T, int b, int& q0, int& qlen) {

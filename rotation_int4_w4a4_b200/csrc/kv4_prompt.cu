@@ -98,6 +98,7 @@ struct __align__(1024) PromptSmem {
   int scaled[SC_RING][4];                                // the 32 tokens' scales are in the operands
   float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
   float2 ml[2 * PT];                                     // cluster: each row's reference and sum
+  int split;                                             // MASKED: the block's walk is a part of its rows'
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
   uint64_t sc_full[SC_RING];
@@ -127,7 +128,55 @@ __device__ __forceinline__ bool pr_warp_wait(uint64_t* bar, uint32_t parity, int
 struct Work {
   int b, kvh, r0, chunk;
   int q0, qlen, rows, n;
+  int parts;                                             // MASKED: into how many the sequence's walks are cut
 };
+
+// MASKED: the steps of a sequence's longest walk (sinks, then from its first row's window on), and the equal parts that it is cut
+// into: as many as it has chunk lengths.
+__device__ __forceinline__ int walk_steps(const Kv4AttnArgs& a, int qlen, int n) {
+  const int lo = a.window > 0 ? max(0, n - qlen - a.window + 1) : 0;
+  return min((min(a.sinks, n) + PT - 1) / PT, lo / PT) + max(0, (n + PT - 1) / PT - lo / PT);
+}
+__device__ __forceinline__ int parts_of(const Partials& part, int steps) {
+  return part.chunks > 1 ? min(part.chunks, max(1, (steps * PT + part.chunk_len - 1) / part.chunk_len)) : 1;
+}
+
+// MASKED calls of up to 32 sequences: a block a part, the sequences with the longest parts first, so that short parts fill the
+// end (16 of 0 to 8192 tokens, 61 drafts: 96 us, in the sequences' order 100; 24 of 0 to 3000, 30 drafts: 53, 61).
+__device__ __forceinline__ bool find_part(const Kv4AttnArgs& a, const Partials& part, Work& w) {
+  const int lane = threadIdx.x & 31, heads = a.cache.heads;
+  int q0 = 0, qlen = 0, n = 0;
+  if (lane < a.B) {
+    n = max(0, a.seq_lens[lane]);
+    new_tokens(a.q_start, (int)a.T, lane, q0, qlen);
+  }
+  const int tiles = (qlen * (a.heads_q / heads) + 2 * PT - 1) / (2 * PT);
+  const int all = walk_steps(a, qlen, (int)min((int64_t)n, (int64_t)a.table_width << a.cache.page_shift));
+  int parts = parts_of(part, all);
+  // Walks that all run at once and are about as long as the mean SM's share stay whole (16 of 8192 tokens, 61 drafts: 167 us,
+  // in three parts 198; 12 of 4000: 90, 106).
+  int longest = tiles > 0 ? all : 0, items = min(tiles * heads, part.sms + 1), work = items * all;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+    items += __shfl_xor_sync(0xffffffffu, items, o);
+    work += __shfl_xor_sync(0xffffffffu, work, o);
+  }
+  if (items <= part.sms && (int64_t)5 * longest * part.sms <= (int64_t)8 * work) parts = 1;
+  const int blocks = tiles * heads * parts, length = (all + parts - 1) / parts;
+  int mine = (int)blockIdx.x;                          // the block's number within this lane's sequence
+#pragma unroll 4
+  for (int s = 0; s < a.B; ++s) {
+    const int other = __shfl_sync(0xffffffffu, length, s), count = __shfl_sync(0xffffffffu, blocks, s);
+    if (other > length || (other == length && s < lane)) mine -= count;
+  }
+  const uint32_t hit = __ballot_sync(0xffffffffu, mine >= 0 && mine < blocks);
+  if (!hit) return false;
+  const int each = heads * parts;
+  w = Work{lane, mine % each % heads, (tiles - 1 - mine / each) * 2 * PT, mine % each / heads, q0, qlen, qlen * (a.heads_q / heads), n, parts};
+  if (lane != __ffs(hit) - 1) w.b = -1;                  // the lane whose sequence it is has the answer
+  return true;
+}
 
 // Tiles are numbered through the sequences; those of one sequence from its last rows (the longest) to its first.
 // Returns false when the block has no tile.  Called by whole warps.
@@ -165,6 +214,7 @@ __device__ __forceinline__ bool find_work(const Kv4AttnArgs& a, const Partials& 
       w.r0 = (__shfl_sync(0xffffffffu, upto, src) - 1 - tile) * 2 * PT;
       w.rows = w.qlen * group;
       w.n = max(0, __shfl_sync(0xffffffffu, n, src));
+      w.parts = 0;
       return true;
     }
     tile -= __shfl_sync(0xffffffffu, upto, 31);
@@ -372,7 +422,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
 
   ptx::griddep_launch_dependents();                      // the kernel that joins chunks waits for this one
   Work w;
-  if (!find_work(a, part, w)) return;                    // the whole block agrees
+  if constexpr (MASKED) {                                // one warp looks for all of the block: sixteen that do cost 2 us a turn
+    __shared__ Work found;
+    if (warp == 0) {
+      const bool sorted = a.B > 1 && a.B <= 32 && !part.cluster;
+      const bool some = sorted ? find_part(a, part, w) : find_work(a, part, w);
+      if (!some) w.b = -1;
+      if (some ? (sorted ? w.b >= 0 : lane == 0) : lane == 0) found = w;
+    }
+    __syncthreads();
+    w = found;
+    if (w.b < 0) return;
+  } else if (!find_work(a, part, w)) {
+    return;                                              // the whole block agrees
+  }
   const int group = a.heads_q / a.cache.heads;
   const int ps = a.cache.page_shift;
   int n = w.n;
@@ -393,17 +456,24 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   int c_lo, c_hi, j0, steps, sink_steps = 0, gap = 0;
   if constexpr (MASKED) {
     // The walk: steps with sinks, then those from lo on.  Step j begins at token (j0 + j) PT, behind the sinks' steps gap
-    // tokens later.  It is cut into as many equal parts as it has chunk lengths; a block behind the last has nothing to do.
+    // tokens later.  It is cut into equal parts, as many as its sequence's longest walk; a block behind the last has nothing to do.
     sink_steps = min((min(a.sinks, hi) + PT - 1) / PT, lo / PT);
     gap = (lo / PT - sink_steps) * PT;
     const int all = sink_steps + max(0, (hi + PT - 1) / PT - lo / PT);
-    const int parts = part.chunks > 1 ? min(part.chunks, max(1, (all * PT + part.chunk_len - 1) / part.chunk_len)) : 1;
-    if (w.chunk >= parts && !part.cluster) {
+    int parts = w.parts > 0 ? w.parts : 1;
+    if (w.parts == 0 && part.chunks > 1) parts = parts_of(part, walk_steps(a, w.qlen, n));
+    if (part.chunks > 1 && !part.cluster) {
+      if (w.chunk >= parts) return;
       const int r = w.r0 + threadIdx.x;
-      if (threadIdx.x < 2 * PT && r < w.rows)
-        part.ml[((int64_t)w.chunk * a.T + w.q0 + r / group) * a.heads_q + w.kvh * group + r % group] = make_float2(-INFINITY, 0.0f);
-      return;
+      if (w.chunk == parts - 1 && threadIdx.x < 2 * PT && r < w.rows) {
+        float2* ml = part.ml + ((int64_t)w.q0 + r / group) * a.heads_q + w.kvh * group + r % group;
+        const int64_t chunk = (int64_t)a.T * a.heads_q;
+        if (parts == 1) *ml = make_float2(-INFINITY, kRowDone);   // its output is written here
+        else
+          for (int c = parts; c < part.chunks; ++c) ml[c * chunk] = make_float2(-INFINITY, 0.0f);   // parts that the walk does not have
+      }
     }
+    if (threadIdx.x == 0) S.split = part.chunks > 1 && parts > 1;   // read at the end: a register less until then
     const int per = (all + parts - 1) / parts;
     j0 = min(all, w.chunk * per);
     steps = min(all, j0 + per) - j0;
@@ -662,7 +732,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       };
       if (MASKED && part.cluster) {                      // joined below, when every product has been made
         S.ml[PT * i + row] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
-      } else if (part.chunks > 1) {
+      } else if (MASKED ? S.split != 0 : part.chunks > 1) {   // one result of several
         const int64_t token = w.q0 + rr / group, first = (int64_t)w.chunk * a.T;
         if (live) part.ml[(first + token) * a.heads_q + head] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
         if (some) {

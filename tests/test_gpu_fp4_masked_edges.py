@@ -290,3 +290,15 @@ def test_rows_behind_a_tile_cost_nothing_and_say_nothing(pq):
         pq.pq_kv4_attention_masked(cache, Q, O, starts, lens, table, 9, 900, tree=tree)
         outs.append(O)
     assert torch.isfinite(outs[0].float()).all() and all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+@pytest.mark.parametrize("window,sinks,tree", [(0, 0, True), (2500, 9, True), (3000, 200, False)])
+@pytest.mark.parametrize("qs,ls,hq,hkv", [
+    ([61] * 5, [5000, 130, 61, 2600, 4100], 16, 4), ([40, 1, 70, 0, 64, 33], [6000, 5000, 70, 0, 4500, 6000], 8, 2),      # parts of uneven walks
+    ([50] * 12, [4300 - 7 * b for b in range(12)], 8, 2), ([64] * 33, [100 + 130 * b for b in range(33)], 4, 1),            # whole walks; more than 32 sequences
+    ([300, 20, 200], [4000, 4500, 900], 8, 2),
+])
+def test_walks_in_parts_and_whole(pq, qs, ls, hq, hkv, window, sinks, tree):
+    """Sequences whose walks are cut beside ones that are not, sorted by length, with the rows of the others left alone."""
+    check(pq, make_case(pq, len(qs) + window, qs, ls, hq, hkv, 128, 64), max(qs), max(ls), window=window, sinks=sinks,
+          trees=trees_of(qs, 6) if tree else None)
