@@ -410,8 +410,9 @@ struct Interior {
   }
 };
 
-// MASKED: with sinks, or a tree of drafted tokens.
-template <int HD, bool MASKED>
+// MASKED: with sinks, or a tree of drafted tokens.  SORTED: parts in find_part's order; an instance of its own, since that code
+// in front of a block's start costs the others 2%.
+template <int HD, bool MASKED, bool SORTED>
 __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4AttnArgs a, const Partials part) {
   using Smem = PromptSmem<HD>;
   constexpr int HB = HD / 2;
@@ -425,10 +426,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   if constexpr (MASKED) {                                // one warp looks for all of the block: sixteen that do cost 2 us a turn
     __shared__ Work found;
     if (warp == 0) {
-      const bool sorted = a.B > 1 && a.B <= 32 && !part.cluster;
-      const bool some = sorted ? find_part(a, part, w) : find_work(a, part, w);
+      const bool some = SORTED ? find_part(a, part, w) : find_work(a, part, w);
       if (!some) w.b = -1;
-      if (some ? (sorted ? w.b >= 0 : lane == 0) : lane == 0) found = w;
+      if (some && SORTED ? w.b >= 0 : lane == 0) found = w;
     }
     __syncthreads();
     w = found;
@@ -1017,12 +1017,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   }
 }
 
-template <int HD, bool MASKED>
+template <int HD, bool MASKED, bool SORTED = false>
 pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tiles, cudaStream_t stream) {
   constexpr size_t smem = sizeof(PromptSmem<HD>) + 1024;
   static_assert(smem <= 232448, "shared memory exceeds 227 KB");
   static std::atomic<bool> done[kMaxDevices];
-  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(kv4_prompt_kernel<HD, MASKED>), (int)smem, done);
+  cudaError_t e = set_kernel_attributes(reinterpret_cast<const void*>(kv4_prompt_kernel<HD, MASKED, SORTED>), (int)smem, done);
   if (e != cudaSuccess) return cuda_fail(e, "kv4_prompt_kernel attributes");
   const int64_t grid = tiles * a.cache.heads * part.chunks;
   if (grid >= ((int64_t)1 << 31)) { set_error("too many query tiles for one call"); return PQ_ERR_INVALID_ARG; }
@@ -1038,9 +1038,9 @@ pq_status launch_prompt(const Kv4AttnArgs& a, const Partials& part, int64_t tile
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cuda_fail(cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<HD, MASKED>, a, part), "kv4_prompt_kernel launch");
+    return cuda_fail(cudaLaunchKernelEx(&cfg, kv4_prompt_kernel<HD, MASKED, SORTED>, a, part), "kv4_prompt_kernel launch");
   }
-  kv4_prompt_kernel<HD, MASKED><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);
+  kv4_prompt_kernel<HD, MASKED, SORTED><<<(unsigned)grid, PR_THREADS, smem, stream>>>(a, part);
   return cuda_fail(cudaGetLastError(), "kv4_prompt_kernel launch");
 }
 
@@ -1053,6 +1053,8 @@ int64_t kv4_prompt_tiles(const Kv4AttnArgs& a) {
 
 pq_status launch_kv4_prompt(const Kv4AttnArgs& a, const Partials& part, cudaStream_t stream) {
   const int64_t tiles = kv4_prompt_tiles(a);
+  if (kv4_masked(a) && a.B > 1 && a.B <= 32 && !part.cluster)
+    return a.cache.head_dim == 128 ? launch_prompt<128, true, true>(a, part, tiles, stream) : launch_prompt<64, true, true>(a, part, tiles, stream);
   if (kv4_masked(a))
     return a.cache.head_dim == 128 ? launch_prompt<128, true>(a, part, tiles, stream) : launch_prompt<64, true>(a, part, tiles, stream);
   return a.cache.head_dim == 128 ? launch_prompt<128, false>(a, part, tiles, stream) : launch_prompt<64, false>(a, part, tiles, stream);
