@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
 
   ptx::griddep_launch_dependents();                      // the kernel that joins chunks waits for this one
   Work w;
-  if constexpr (MASKED) {                                // one warp looks for all of the block: sixteen that do cost 2 us a turn
+  {                                                      // one warp looks for all of the block: sixteen that do cost up to 2 us a turn
     __shared__ Work found;
     if (warp == 0) {
       const bool some = SORTED ? find_part(a, part, w) : find_work(a, part, w);
@@ -433,8 +433,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
     __syncthreads();
     w = found;
     if (w.b < 0) return;
-  } else if (!find_work(a, part, w)) {
-    return;                                              // the whole block agrees
   }
   const int group = a.heads_q / a.cache.heads;
   const int ps = a.cache.page_shift;
