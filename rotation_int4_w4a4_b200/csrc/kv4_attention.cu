@@ -959,8 +959,8 @@ pq_status kv4_attention_run(const Kv4AttnArgs& a, int64_t max_q, int64_t max_len
     if (kv4_masked(a)) {
       // A masked walk is cut into equal parts by its own length (us on the device, uncut and by the number of parts at most).
       // Of several sequences the longest keeps one SM busy: 16 of 0 to 8192 tokens, 61 drafts on 32 + 8 heads of 128: 168; 2
-      // parts 137, 3 112, 4 111, 6 127, 8 140 in the sequences' order, longest first 2 107, 3 96, 5 109.  Not where the walks are short: chunks of up to 801 under a window of 700: 29; 34,
-      // 33, 39.  Short walks of few tiles go down to a step a part: 5 sequences under a window of 512, 25 drafts: 23; 4 parts
+      // parts 137, 3 112, 4 111, 6 127, 8 140 in the sequences' order, longest first 2 107, 3 96, 5 109.  Not where the walks are short:
+      // chunks of up to 801 under a window of 700: 29; 34, 33, 39.  Short walks of few tiles go down to a step a part: 5 sequences under a window of 512, 25 drafts: 23; 4 parts
       // 17.1, 8 14.7.
       const int64_t steps = (max_len + 127) / 128, share = std::max<int64_t>(16, tiles * a.cache.heads * steps / (2 * sms));
       if (a.B > 1 && steps >= 32) part.chunks = std::max<int>(part.chunks, (int)std::min<int64_t>((steps + share - 1) / share, 16));
