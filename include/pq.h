@@ -542,7 +542,7 @@ pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq
  *               tokens in front of the new ones a row sees all, or with a window those that a row at position
  *               p = (those tokens) + max(bits, 1) - 1 sees: a drafted token's position is its depth, whatever slot it lies
  *               in (append it with that position; once a branch is accepted, append its tokens again to their own slots).
- *   tree_words  1..1024.
+ *   tree_words  1..1024 (without a tree it says nothing).
  *   A row that sees nothing becomes 0.  Pages whose tokens lie all behind the sinks and in front of every row's window are not
  *   looked at, nor are their entries in block_table followed.  Everything else, roundings and scratch included, is as told
  *   for pq_kv4_attention; a call without sinks and tree is that call.

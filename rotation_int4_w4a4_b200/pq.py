@@ -719,7 +719,7 @@ def pq_kv4_attention(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_
 def pq_kv4_attention_masked(cache: KV4Cache, Q, O, q_start, seq_lens, block_table, max_q, max_len, scale=None, window=0, sinks=0,
                             tree=None, stream=None) -> None:
     """:func:`pq_kv4_attention` with sinks (under a window the first `sinks` tokens stay visible) and a tree of drafted tokens
-    (int32 [T, words]: bit j of a row's words, the lowest first, says that it sees its sequence's new token j)."""
+    (int32 [T, words], 1 to 1024 words: bit j of a row's words, the lowest first, says that it sees its sequence's new token j)."""
     if stream is None:
         st = (_call or _caller()).attention_masked(cache.handle, cache.device, Q, O, q_start, seq_lens, block_table, max_q, max_len,
                                                    scale, window, sinks, tree)
@@ -736,8 +736,8 @@ def pq_kv4_attention_masked(cache: KV4Cache, Q, O, q_start, seq_lens, block_tabl
     i32 = torch.int32
     words = 0
     if tree is not None:
-        if tree.dim() != 2 or tree.shape[0] != T:
-            raise ValueError(f"tree: expected [{T}, words]")
+        if tree.dim() != 2 or tree.shape[0] != T or tree.shape[1] < 1:   # without words it has no address: the library would see no tree
+            raise ValueError(f"tree: expected [{T}, words], one word or more")
         words = tree.shape[1]
     _check(lib.pq_kv4_attention_masked(cache.on(dev), qp, ldq, wq // hd, _on(q_start, "q_start", "i32", i32, B + 1, dev),
                                        _on(seq_lens, "seq_lens", "i32", i32, B, dev),
