@@ -47,7 +47,7 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _call_command() -> list[str] | None:
+def _call_command(source: str = CALL_SOURCE, target: str = CALL_LIB) -> list[str] | None:
     """The compiler's command for _pqcall.so (torch is found, not imported), None without torch: the library needs none."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
@@ -57,7 +57,7 @@ def _call_command() -> list[str] | None:
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"] + ["-isystem" + d for d in include] +
-            [CALL_SOURCE, "-o", CALL_LIB, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+            [source, "-o", target, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

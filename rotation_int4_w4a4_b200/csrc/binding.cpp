@@ -107,12 +107,23 @@ PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
 }
 
+// The library's entry without the interpreter's lock.  What it throws ends here, where the lock can be taken again, and becomes
+// Python's: the call may have had its effect, so it is not one that was not taken.
 template <typename F>
 PyObject* call(F f) {
-  pq_status st;
+  pq_status st = PQ_OK;
+  bool threw = false;
   Py_BEGIN_ALLOW_THREADS
-  st = f();
+  try {
+    st = f();
+  } catch (...) {
+    threw = true;
+  }
   Py_END_ALLOW_THREADS
+  if (threw) {
+    PyErr_SetString(PyExc_RuntimeError, "the library ended with a C++ exception; whether the call was made is not known");
+    return nullptr;
+  }
   return PyLong_FromLong((long)st);
 }
 
