@@ -9,6 +9,8 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cxxabi.h>
+
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -97,11 +99,14 @@ int device() {
 }
 void* stream_of(int dev) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 
-// Tensors without memory (fake ones, functional ones) throw when asked for it, and no exception may leave a C entry.
+// Tensors without memory (fake ones, functional ones) throw when asked for it, and no exception may leave a C entry.  What
+// unwinds a thread that ends (a daemon thread that asks for the lock after the interpreter's end) is none and goes on.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
   try {
     return F(a, n);
+  } catch (abi::__forced_unwind&) {
+    throw;
   } catch (...) {
     return not_taken();
   }
@@ -116,6 +121,8 @@ PyObject* call(F f) {
   Py_BEGIN_ALLOW_THREADS
   try {
     st = f();
+  } catch (abi::__forced_unwind&) {
+    throw;
   } catch (...) {
     threw = true;
   }

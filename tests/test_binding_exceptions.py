@@ -66,3 +66,15 @@ print("then", s.answers())
 
 def test_an_exception_before_the_library_is_a_call_not_taken(folder):
     assert python(folder, "print(s.throws_before(), s.throws_before())")[:2] == (0, "-1 -1\n")
+
+
+def test_python_may_end_while_a_call_runs(folder):
+    """A daemon thread's call outlasts the interpreter: the thread ends where it asks for the lock, by an unwinding that nothing may
+    hold up (a handler that swallows it goes on without the lock)."""
+    code = """
+import threading, time
+threading.Thread(target=s.waits, daemon=True).start()
+time.sleep(0.1)
+"""
+    rc, out, err = python(folder, code)
+    assert rc == 0, (rc, out, err)
