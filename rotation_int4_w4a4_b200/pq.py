@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import numpy as np
 
@@ -462,6 +463,11 @@ def pq_w8a8_linear(X, codes_A, scales_A, codes_W, scales_W, Y, g=0, T=None, N=No
 _call = None
 
 
+class _NoModule:
+    """In the compiled module's place where it is missing or does not load: no call is taken, so each is checked and made below."""
+    quant_fp4 = fp4_gemm = fp4_linear = attention_masked = staticmethod(lambda *args: -1)
+
+
 def _caller():
     """The compiled module behind the quickest calls (csrc/binding.cpp), loaded at the first of them: it needs torch."""
     global _call
@@ -470,11 +476,14 @@ def _caller():
 
     import torch  # noqa: F401  (its libraries have to be there first)
     path = os.path.join(os.path.dirname(_LIB_PATH), "_pqcall.so")
-    if not os.path.exists(path):
-        raise ImportError(f"_pqcall.so is not built ({path}); run python -m rotation_int4_w4a4_b200.build")
     loader = importlib.machinery.ExtensionFileLoader("_pqcall", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pqcall", loader))
-    module.bind(*(_c.cast(f, _vp).value for f in (lib.pq_quant_fp4, lib.pq_fp4_gemm, lib.pq_fp4_linear, lib.pq_kv4_attention_masked)))
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pqcall", loader))
+        module.bind(*(_c.cast(f, _vp).value for f in (lib.pq_quant_fp4, lib.pq_fp4_gemm, lib.pq_fp4_linear, lib.pq_kv4_attention_masked)))
+    except ImportError as e:
+        warnings.warn(f"calls go through ctypes, some 5 us slower: {e}; python -m rotation_int4_w4a4_b200.build makes {path}",
+                      RuntimeWarning, stacklevel=3)
+        module = _NoModule
     _call = module
     return module
 
