@@ -5,7 +5,8 @@
 Objects go to ``_build/`` at the repository root; the shared library to
 ``rotation_int4_w4a4_b200/_lib/libpq.so``.  The CUDA runtime is linked statically, so the
 library depends only on the driver (``libcuda``) at run time.  Beside it lies ``_pqcall.so``, the
-Python module through which pq.py makes its quickest calls, compiled against the installed torch.
+Python module through which pq.py makes its quickest calls, compiled against the installed torch;
+where that fails the library is built all the same.
 """
 from __future__ import annotations
 
@@ -47,7 +48,7 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _call_command(source: str = CALL_SOURCE, target: str = CALL_LIB) -> list[str] | None:
+def _call_command(source: str | None = None, target: str | None = None) -> list[str] | None:
     """The compiler's command for _pqcall.so (torch is found, not imported), None without torch: the library needs none."""
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
@@ -57,7 +58,17 @@ def _call_command(source: str = CALL_SOURCE, target: str = CALL_LIB) -> list[str
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"] + ["-isystem" + d for d in include] +
-            [source, "-o", target, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+            [source or CALL_SOURCE, "-o", target or CALL_LIB, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+
+
+def _run(cmd: list[str], verbose: bool) -> subprocess.CompletedProcess:
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:                                 # no such compiler
+        res = subprocess.CompletedProcess(cmd, 127, "", f"{e}\n")
+    if verbose or res.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
+    return res
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -73,23 +84,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + hdrs):
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc()] + NVCC_FLAGS + extra + ["-c", s, "-o", o])
-    call = [_call_command()] if force or _stale(CALL_LIB, [CALL_SOURCE, hdrs[-1]]) else []
-    if call == [None]:
+    stale = force or _stale(CALL_LIB, [CALL_SOURCE, hdrs[-1]])
+    call = _call_command() if stale else None
+    if stale and call is None:
         sys.stderr.write("torch is not installed: _pqcall.so, which reads its tensors, is left out\n")
-        call = []
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        for cmd, res in zip(call + jobs, ex.map(lambda c: subprocess.run(c, capture_output=True, text=True), call + jobs)):
-            if verbose or res.returncode != 0:
-                sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
+        made = ex.submit(_run, call, verbose) if call else None
+        for cmd, res in zip(jobs, ex.map(lambda c: _run(c, verbose), jobs)):
             if res.returncode != 0:
                 raise RuntimeError(f"compilation failed: {' '.join(cmd)}")
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc()] + ARCH + ["-shared", "-o", LIB] + objs + ["-cudart", "static"]
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        if verbose or res.returncode != 0:
-            sys.stderr.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-        if res.returncode != 0:
+        if _run(cmd, verbose).returncode != 0:
             raise RuntimeError("link of libpq.so failed")
+    # The module only makes calls quicker: the library does without it.  One of other sources goes: it might call by other signatures.
+    if stale and (made is None or made.result().returncode != 0):
+        if os.path.exists(CALL_LIB):
+            os.remove(CALL_LIB)
+        if made:
+            sys.stderr.write("_pqcall.so could not be compiled (above): calls go through ctypes, some 5 us slower\n")
     return LIB
 
 
