@@ -4,16 +4,18 @@
 
 Objects go to ``_build/`` at the repository root; the shared library to
 ``rotation_int4_w4a4_b200/_lib/libpq.so``.  The CUDA runtime is linked statically, so the
-library depends only on the driver (``libcuda``) at run time.  Beside it lies ``_pqcall.so``, the
-Python module through which pq.py makes its quickest calls, compiled against the installed torch;
-where that fails the library is built all the same.
+library depends only on the driver (``libcuda``) at run time.  Beside it lies ``_pqcall-<torch><Python>.so``,
+the Python module through which pq.py makes its quickest calls, compiled against the installed torch, whose
+version its name holds; where that fails the library is built all the same.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import glob
 import importlib.util
 import os
+import re
 import subprocess
 import sys
 import sysconfig
@@ -28,7 +30,7 @@ SOURCES = ["pq_host.cpp", "transform.cu", "smooth_rows.cu", "rotate_mma.cu", "ge
            "ops_host.cpp", "quant8.cu", "w8a8.cu", "quant_fp4.cu", "fp4.cu", "kv4_append.cu", "kv4_attention.cu", "kv4_prompt.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "rows.cuh", "nan_max.cuh", "kv4.h", "kv4_device.cuh", "quant_fp4.cuh", "ptx_fp4.cuh"]
 CALL_SOURCE = os.path.join(CSRC, "binding.cpp")
-CALL_LIB = os.path.join(LIBDIR, "_pqcall.so")
+
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-Wall",
                      "-I" + os.path.join(ROOT, "include")]
@@ -48,12 +50,35 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _call_command(source: str | None = None, target: str | None = None) -> list[str] | None:
-    """The compiler's command for _pqcall.so (torch is found, not imported), None without torch: the library needs none."""
+def _torch_folder() -> str | None:
+    """Where torch lies (found, not imported), None without it."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
+    return list(spec.submodule_search_locations)[0] if spec and spec.submodule_search_locations else None
+
+
+def torch_version() -> str:
+    """The installed torch's version, "none" without one."""
+    try:
+        with open(os.path.join(_torch_folder() or "", "version.py")) as f:
+            found = re.search(r"^__version__\s*=\s*['\"]([^'\"]+)", f.read(), re.M)
+    except OSError:
+        found = None
+    return found.group(1) if found else "none"
+
+
+def call_lib_name(version: str) -> str:
+    """The compiled module's file for this Python and a torch of that version, whose objects it reads in place."""
+    return "_pqcall-" + re.sub(r"[^\w.+]", "_", version) + sysconfig.get_config_var("EXT_SUFFIX")
+
+
+CALL_LIB = os.path.join(LIBDIR, call_lib_name(torch_version()))
+
+
+def _call_command(source: str | None = None, target: str | None = None) -> list[str] | None:
+    """The compiler's command for the module, None without torch: the library needs none."""
+    torch = _torch_folder()
+    if torch is None:
         return None
-    torch = list(spec.submodule_search_locations)[0]
     cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
     include = [os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
@@ -84,10 +109,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(o, [s] + hdrs):
             extra = ["-Xptxas", "-v"] if verbose and src.endswith(".cu") else []
             jobs.append([nvcc()] + NVCC_FLAGS + extra + ["-c", s, "-o", o])
+    for other in glob.glob(os.path.join(glob.escape(LIBDIR), "_pqcall*.so")):   # of another torch, and of other sources
+        if other != CALL_LIB and _stale(other, [CALL_SOURCE, hdrs[-1]]):
+            os.remove(other)
     stale = force or _stale(CALL_LIB, [CALL_SOURCE, hdrs[-1]])
     call = _call_command() if stale else None
     if stale and call is None:
-        sys.stderr.write("torch is not installed: _pqcall.so, which reads its tensors, is left out\n")
+        sys.stderr.write("torch is not installed: the module _pqcall, which reads its tensors, is left out\n")
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         made = ex.submit(_run, call, verbose) if call else None
         for cmd, res in zip(jobs, ex.map(lambda c: _run(c, verbose), jobs)):
@@ -102,7 +130,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if os.path.exists(CALL_LIB):
             os.remove(CALL_LIB)
         if made:
-            sys.stderr.write("_pqcall.so could not be compiled (above): calls go through ctypes, some 5 us slower\n")
+            sys.stderr.write("the module _pqcall could not be compiled (above): calls go through ctypes, some 5 us slower\n")
     return LIB
 
 

@@ -474,8 +474,10 @@ def _caller():
     import importlib.machinery
     import importlib.util
 
-    import torch  # noqa: F401  (its libraries have to be there first)
-    path = os.path.join(os.path.dirname(_LIB_PATH), "_pqcall.so")
+    import torch                               # its libraries have to be there first
+
+    from .build import call_lib_name
+    path = os.path.join(os.path.dirname(_LIB_PATH), call_lib_name(torch.version.__version__))
     loader = importlib.machinery.ExtensionFileLoader("_pqcall", path)
     try:
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pqcall", loader))

@@ -75,3 +75,39 @@ def test_without_torch(build, monkeypatch, capsys):
     os.utime(build.module.CALL_LIB, (0, 0))
     monkeypatch.setattr(build.module.importlib.util, "find_spec", lambda name: None)
     assert build.module.build() and os.listdir(build.lib) == ["libpq.so"] and "torch is not installed" in capsys.readouterr().err
+
+
+def test_another_torch_or_python_has_another_module(monkeypatch, tmp_path):
+    """The module reads torch's C++ objects in place: one built for another torch is not loaded, whatever its file's age."""
+    import sysconfig
+    from rotation_int4_w4a4_b200 import build as b
+    import torch
+    assert os.path.basename(b.CALL_LIB) == b.call_lib_name(torch.version.__version__)
+    assert b.CALL_LIB.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    (tmp_path / "version.py").write_text("from typing import Optional\n__version__ = '9.8.7+cu999'\ncuda = None\n")
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: types.SimpleNamespace(submodule_search_locations=[str(tmp_path)]))
+    assert b.torch_version() == "9.8.7+cu999"
+    assert b.call_lib_name("9.8.7+cu999") != b.call_lib_name(torch.version.__version__)
+
+
+def test_modules_of_other_sources_are_removed(build):
+    """Those for other torches too: they would be loaded again when that torch comes back, against the new library."""
+    build.module.build()
+    for name, when in (("_pqcall-1.0.so", 0), ("_pqcall.so", 0), ("_pqcall-2.0.so", None)):
+        (build.lib / name).touch()
+        if when is not None:
+            os.utime(build.lib / name, (when, when))
+    build.module.build()
+    assert sorted(os.listdir(build.lib)) == sorted(["libpq.so", os.path.basename(build.call), "_pqcall-2.0.so"])
+
+
+def test_a_module_of_another_torch_is_not_loaded(monkeypatch):
+    from rotation_int4_w4a4_b200 import build as b
+    b.build()
+    from rotation_int4_w4a4_b200 import pq
+    import torch
+    monkeypatch.setattr(pq, "_call", None)
+    assert pq._caller() is not pq._NoModule
+    monkeypatch.setattr(torch.version, "__version__", "9.8.7+cu999")
+    with pytest.warns(RuntimeWarning, match="9.8.7"):
+        assert pq._caller() is pq._NoModule
