@@ -679,7 +679,7 @@ def pq_kv4_append(cache: KV4Cache, Q, K, V, Q_out, positions, slots, rope=None, 
     vp, ldv = _rows_of(V, "V", wk, T, dev, torch)
     rope_rows = rope_dim = 0
     if rope is not None:
-        if rope.dim() != 2:
+        if rope.dim() != 2 or rope.numel() == 0:   # without elements it has no address: the library would see no table
             raise ValueError("rope: expected [positions, rope_dim]")
         rope_rows, rope_dim = rope.shape
     bf16 = torch.bfloat16
