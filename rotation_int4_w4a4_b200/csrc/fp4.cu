@@ -764,18 +764,25 @@ pq_status launch_pair(Fp4Maps& m, const Fp4Call& c, int m_tiles, int n_tiles, in
 
 int tile_tokens(int64_t T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
 
-// K steps of the tile kernel's reduction, and the ranges it is cut into: as long as every CTA still has an SM of its own and
-// keeps two steps (us on the device, uncut and by 2, 4 and 8 at most).  1 token, N x D 4096 x 4096: 7.4, 6.8, 5.8, 5.8; 4096 x
-// 14336: 18.9, 12.0, 8.9, 8.9; 16 tokens, 1024 x 14336: 18.6, 11.9, 7.9, 6.4; 391 tokens, 1003 x 4192: 13.3, 11.5, 9.2, 9.2.
-// Up to 16 tokens, whose join is short, two CTAs an SM of four steps each where it is cut at all (weights from HBM, against one).  1 token 8192 x 8192
-// 10.1 : 11.2, 5120 x 5120 7.7 : 8.6; 16 tokens 10.8 : 12.1, 8.0 : 9.0; 4096 x 4096, two steps each, with the
-// quantisation 7.0 : 7.3, from L2 7.0 : 6.7; 64 tokens 9.3 : 8.1; 16 tokens 14336 x 4096, not cut otherwise, 11.5 : 11.2.
+// K steps of the tile kernel's reduction, and the ranges it is cut into (figures: us on the device).
+// It is cut by twos as long as every CTA still has an SM of its own and keeps two steps.  Uncut, and by 2, 4 and 8 at most: 1 token,
+// N x D 4096 x 4096 7.4, 6.8, 5.8, 5.8; 4096 x 14336 18.9, 12.0, 8.9, 8.9; 16 tokens, 1024 x 14336 18.6, 11.9, 7.9, 6.4; 391
+// tokens, 1003 x 4192 13.3, 11.5, 9.2, 9.2.
+// Where it is cut and the tokens are up to 16, whose join is short, it is cut on, to two CTAs an SM, as long as each keeps four
+// steps and all clusters run at once.  Two CTAs an SM : one, nv, weights from HBM:
+//   taken       1 token 8192 x 8192 10.0 : 11.0, 5120 x 5120 7.3 : 8.6; 16 tokens 10.3 : 11.3, 7.7 : 8.7
+//   two steps   1 token 4096 x 4096, with the quantisation 7.2 : 7.0; 16 tokens 7.6 : 7.2
+//   more tokens 64, 5120 x 5120 9.4 : 9.7, but 4096 x 8192 10.7 : 9.7, 4096 x 14336 12.4 : 11.3; 128, 4096 x 8192 13.3 : 11.0
+//   uncut       16 tokens 14336 x 4096 10.2 : 9.9
+//   at once     a 25th of the places stays empty beside clusters of 4: 1 token, 71 tiles, 9088 x 4096 8.1 : 8.9, 72 tiles, 9216
+//               10.8 : 8.9; an eighth beside those of 8: 32 tiles, 4096 x 8192 7.9 : 8.5, 36 tiles, 4608 11.5 : 8.2
 int fp4_ranges(int64_t T, int64_t N, int64_t D, int* split) {
   const int np = tile_tokens(T), sms = device_sm_count(), steps = (int)((D + 2 * KB - 1) / (2 * KB));
   const int64_t tiles = (N + TM - 1) / TM * ((T + np - 1) / np);
   *split = 1;
   while (*split < 8 && tiles * *split * 2 <= sms && steps >= 4 * *split) *split *= 2;
-  while (T <= 16 && *split > 1 && *split < 8 && tiles * *split * 2 <= 2 * sms && steps >= 8 * *split) *split *= 2;
+  while (T <= 16 && *split > 1 && *split < 8 && tiles * *split * 2 <= (*split == 2 ? 48 * sms / 25 : 7 * sms / 4) && steps >= 8 * *split)
+    *split *= 2;
   return steps;
 }
 
@@ -838,8 +845,8 @@ pq_status fp4_linear_launch(const void* X, int64_t T, int64_t D, int64_t ldx, in
                             uint8_t* scales_A, const uint8_t* codes_W, const uint8_t* scales_W, int64_t N, float alpha, void* Y,
                             pq_out_dtype out_dtype, cudaStream_t stream) {
   // Up to 16 tokens one kernel does both, where no block has more than 4 steps of them to quantise and an SM has one block (us on the
-  // device, one kernel against two; one token).  4096 x 4096, 4 steps a block: 6.7 : 6.3, and 3 less of the host for the second
-  // launch; 2048 x 2048, 2 steps: 5.3 : 5.6; 6144 x 4096, 4 steps and two blocks an SM: 8.2 : 7.6; 14336 x 4096, 16 steps: 12.9 :
+  // device, one kernel against two; one token).  4096 x 4096, 4 steps a block: 7.0 : 7.1 with weights from HBM, 6.7 : 6.3 from L2, and
+  // 3 less of the host for the second launch; 2048 x 2048, 2 steps: 5.0 : 5.7; 6144 x 4096, 4 steps and two blocks an SM: 8.2 : 7.6; 14336 x 4096, 16 steps: 12.9 :
   // 8.8; 4096 x 14336, 14 steps: 13.9 : 10.3.
   int split = 1;
   const int steps = fp4_ranges(T, N, D, &split);
