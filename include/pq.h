@@ -544,8 +544,11 @@ pq_status pq_kv4_attention(const pq_kv4_cache* cache, const void* Q, int64_t ldq
  *               in (append it with that position; once a branch is accepted, append its tokens again to their own slots).
  *   tree_words  1..1024 (without a tree it says nothing).
  *   A row that sees nothing becomes 0.  Pages whose tokens lie all behind the sinks and in front of every row's window are not
- *   looked at, nor are their entries in block_table followed.  Everything else, roundings and scratch included, is as told
- *   for pq_kv4_attention; a call without sinks and tree is that call.
+ *   looked at, nor are their entries in block_table followed.
+ *   max_q chooses one kernel for the whole call here too, but not at 32 query rows a key/value head alone: calls whose blocks
+ *   would leave the device partly idle stay with the kernel of fewer rows up to 128 of them, and so with its roundings (codes
+ *   exact whatever the scales).  Scratch: none where the blocks that share a sequence's tokens are a cluster.  Everything
+ *   else is as told for pq_kv4_attention; a call without sinks and tree is that call.
  */
 pq_status pq_kv4_attention_masked(const pq_kv4_cache* cache, const void* Q, int64_t ldq, int heads_q, const int32_t* q_start,
                                   const int32_t* seq_lens, const int32_t* block_table, int64_t table_width, int64_t B,
