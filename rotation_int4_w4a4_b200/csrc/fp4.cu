@@ -846,7 +846,7 @@ pq_status fp4_linear_launch(const void* X, int64_t T, int64_t D, int64_t ldx, in
                             pq_out_dtype out_dtype, cudaStream_t stream) {
   // Up to 16 tokens one kernel does both, where no block has more than 4 steps of them to quantise and an SM has one block (us on the
   // device, one kernel against two; one token).  4096 x 4096, 4 steps a block: 7.0 : 7.1 with weights from HBM, 6.7 : 6.3 from L2, and
-  // 3 less of the host for the second launch; 2048 x 2048, 2 steps: 5.0 : 5.7; 6144 x 4096, 4 steps and two blocks an SM: 8.2 : 7.6; 14336 x 4096, 16 steps: 12.9 :
+  // 3 less of the host for the second launch; at worst 4608 x 4096, the same, 8.0 : 7.3; 2048 x 2048, 2 steps: 5.0 : 5.7; 6144 x 4096, 4 steps and two blocks an SM: 8.2 : 7.6; 14336 x 4096, 16 steps: 12.9 :
   // 8.8; 4096 x 14336, 14 steps: 13.9 : 10.3.
   int split = 1;
   const int steps = fp4_ranges(T, N, D, &split);
