@@ -20,9 +20,9 @@
 //   warps 12..15       producers: 128 tokens' codes from the pages, unpacked to fp16 keys and values in the swizzled
 //                      operand layout, two stages each; their scales beside them.
 // Spills in a half step cost much: the operands leave so little of the L1 cache that they come back from L2 (with the next
-// half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).  The compiler reports 16 bytes of stores and 44 of
-// loads (heads of 64: 12 and 36); which code they belong to is not known.
-// 4096 of 8192 tokens, 32 + 8 heads of 128: 466 us, 55% of the library's bf16 rate; a half step takes 2000 cycles, of which
+// half's scores loaded ahead, 400 bytes spilled: 655 us instead of 564).  The compiler reports none: what the end needs of the
+// block's work it reads again (kept over the half steps, 12 bytes of stores and 24 of loads: 459 us instead of 447).
+// 4096 of 8192 tokens, 32 + 8 heads of 128: 447 us, 57% of the library's bf16 rate; a half step takes 1900 cycles, of which
 // the matrix instructions need 1400 and the exponentials 1000: the chain scores -> exponentials -> P -> product -> next
 // scores bounds it, with 10% of the SMs' time idle behind the last blocks.
 //
@@ -76,8 +76,7 @@ constexpr float kTop = 32768.0f;         // sum of 64 probabilities (fp16 holds 
 // scales (0 counts: such a token's score must not set the reference).  The reference of such a step is its largest score plus
 // the exponent of its largest value scale, which may belong to another token: the largest product is then up to 2^6 below 1
 // and keeps 18 of fp16's 24 places below it.  Within the factor every operand is a normal fp16 number (of scales above 2^-100).
-// 4096 of 8192 tokens: 466 us with every step so; before its last improvements 478, 482 where the first 64 tokens differ by
-// more, 696 where all do.
+// 4096 of 8192 tokens: 447 us with every step so; an earlier form 478, 482 where the first 64 tokens differ by more, 696 where all do.
 constexpr float kScaleSpread = 64.0f;
 // kind::f16 on fp16 operands (types 0 at bits 7 and 10) with a float32 accumulator, B MN-major at bit 16.
 __host__ __device__ constexpr uint32_t idesc_f16(int b_mn_major, int N) {
@@ -99,6 +98,7 @@ struct __align__(1024) PromptSmem {
   float k_pow[SC_RING][4], v_exp[SC_RING][4];            // 2^e of each 32 keys, e of each 32 values
   float2 ml[2 * PT];                                     // cluster: each row's reference and sum
   int split;                                             // MASKED: the block's walk is a part of its rows'
+  int2 at[2 * PT];                                       // MASKED: each row's position and its row of Q
   uint64_t q_full;
   uint64_t k_full[PR_STAGES], k_empty[PR_STAGES], v_full[PR_STAGES], v_empty[PR_STAGES];
   uint64_t sc_full[SC_RING];
@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
 
   ptx::griddep_launch_dependents();                      // the kernel that joins chunks waits for this one
   Work w;
+  __shared__ Work found;
   {                                                      // one warp looks for all of the block: sixteen that do cost up to 2 us a turn
-    __shared__ Work found;
     if (warp == 0) {
       const bool some = SORTED ? find_part(a, part, w) : find_work(a, part, w);
       if (!some) w.b = -1;
@@ -492,7 +492,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   const int r = w.r0 + PT * i + row;
   const bool live = r < w.rows;
   const int rr = min(r, w.rows - 1);
-  const int head = w.kvh * group + rr % group;
   // Rows come from and go to memory RPI at a time, LPR lanes a row (a row a lane touches 32 lines an instruction), and
   // pass through shared memory, where a thread reaches its own.  Loops stay rolled: code that runs once is bound by
   // its fetch.
@@ -501,9 +500,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
   auto place = [&](int r_, int c) { return reinterpret_cast<uint4*>(S.q[i][c / 8] + sw128(r_, c % 8)); };
   // body(row of the tile, token, query head) over the warp's rows that exist.  Rows of the tile are few: dividing by the
   // group is a multiplication by its reciprocal (rows + group below 2^16).
-  const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
-  const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
-  auto each_row = [&](auto body) {
+  auto each_row = [&](const Work& w, auto body) {
+    const int tile_tok = (w.r0 + PT * i) / group, tile_off = (w.r0 + PT * i) % group;
+    const uint32_t inv_group = group == 1 ? 0u : 0xffffffffu / (uint32_t)group + 1u;
 #pragma unroll 4
     for (int k = 0; k < LPR; ++k) {
       const int to = io_row + RPI * k, x = to + tile_off;
@@ -511,10 +510,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       if (w.r0 + PT * i + to < w.rows) body(to, (int64_t)w.q0 + tile_tok + t, w.kvh * group + x - t * group);
     }
   };
-  if (warp >= PR_SOFT0 && warp < PR_PROD0)
-    each_row([&](int to, int64_t t, int hq) {
+  if (warp >= PR_SOFT0 && warp < PR_PROD0) {
+    each_row(w, [&](int to, int64_t t, int hq) {
       ptx::cp_async16(place(to, io_chunk), reinterpret_cast<const uint4*>(a.Q + t * a.ldq + hq * HD) + io_chunk, 16);
     });
+    if constexpr (MASKED) {
+      // A list is read once for its length (in every half step: 4000 drafts behind 4000 tokens under a window of 512 took 6.8 ms, now 0.53).
+      const int t = rr / group;
+      const int deep = tree && a.window > 0 ? tree_depth(a.tree + (int64_t)(w.q0 + t) * a.tree_words, a.tree_words, w.qlen) : t;
+      S.at[threadIdx.x - 32 * PR_SOFT0] = make_int2(old + deep, w.q0 + t);
+    }
+  }
 
   if (threadIdx.x == 32) {
     ptx::mbar_init(&S.q_full, 8);
@@ -649,19 +655,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
         // each sum without its values' power of two
         l = fmaf(sum0, ex2(-v2.x), fmaf(sum1, ex2(-v2.y), l));
       } else {
-        int pos = n - w.qlen + rr / group;
         uint64_t bits;
         if constexpr (MASKED) {
           const int first = first_of(j) + t0;
-          const uint32_t* list = tree ? a.tree + (int64_t)(w.q0 + rr / group) * a.tree_words : nullptr;
-          if (tree && a.window > 0) pos = old + tree_depth(list, a.tree_words, w.qlen);
+          const int2 at = S.at[threadIdx.x - 32 * PR_SOFT0];
+          const int pos = at.x;
           const int last = tree ? old - 1 : min(pos, c_hi - 1);
           bits = token_bits(first, a.window > 0 ? max(pos - a.window + 1, 0) : 0, last) | token_bits(first, 0, min(a.sinks - 1, last));
           if (tree && first + HT > old) {
-            const uint64_t mine = tree_bits(list, a.tree_words, first - old);
+            const uint64_t mine = tree_bits(a.tree + (int64_t)at.y * a.tree_words, a.tree_words, first - old);
             bits |= first >= old ? mine : mine & (~0ull << (old - first));
           }
         } else {
+          const int pos = n - w.qlen + rr / group;
           bits = token_bits(first_of(j) + t0, a.window > 0 ? max(pos - a.window + 1, c_lo) : c_lo, min(pos, c_hi - 1));
         }
         const uint32_t sa = (uint32_t)bits & va, sb = (uint32_t)(bits >> 32) & vb;
@@ -720,19 +726,22 @@ __global__ void __launch_bounds__(PR_THREADS, 1) kv4_prompt_kernel(const Kv4Attn
       if (ok && steps > 0) ok = pr_warp_wait(&S.o_full[i][1], (uint32_t)(steps - 1) & 1u, &S.abort_flag, a.status);
       ptx::tc_fence_after();
       const bool some = ok && steps > 0;
+      asm volatile("" ::: "memory");
+      const Work e = found;                              // again, so that the half steps need not keep it in registers
       // The queries' place (their products are done) takes each row's output, HD / 8 chunks of 16 bytes; rows leave from
       // there whole.  A warp touches its own rows only.
       auto stage = [&](int c, uint4 x) { *place(row, c) = x; };
       auto flush = [&](auto dst_of) {                    // dst_of(token, head): where the row goes
         __syncwarp();
-        each_row([&](int from, int64_t t, int hq) { reinterpret_cast<uint4*>(dst_of(t, hq))[io_chunk] = *place(from, io_chunk); });
+        each_row(e, [&](int from, int64_t t, int hq) { reinterpret_cast<uint4*>(dst_of(t, hq))[io_chunk] = *place(from, io_chunk); });
         __syncwarp();
       };
       if (MASKED && part.cluster) {                      // joined below, when every product has been made
         S.ml[PT * i + row] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
       } else if (MASKED ? S.split != 0 : part.chunks > 1) {   // one result of several
-        const int64_t token = w.q0 + rr / group, first = (int64_t)w.chunk * a.T;
-        if (live) part.ml[(first + token) * a.heads_q + head] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
+        const int64_t first = (int64_t)e.chunk * a.T;
+        const int t = MASKED ? S.at[threadIdx.x - 32 * PR_SOFT0].y - e.q0 : rr / group;
+        if (r < e.rows) part.ml[(first + e.q0 + t) * a.heads_q + e.kvh * group + rr - t * group] = make_float2(some ? m : -INFINITY, some ? l : 0.0f);
         if (some) {
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {         // HD / 2 channels in float32 fill the place
