@@ -68,7 +68,7 @@ def torch_version() -> str:
 
 def call_lib_name(version: str) -> str:
     """The compiled module's file for this Python and a torch of that version, whose objects it reads in place."""
-    return "_pqcall-" + re.sub(r"[^\w.+]", "_", version) + sysconfig.get_config_var("EXT_SUFFIX")
+    return "_pqcall-" + re.sub(r"[^\w.+]", "_", version) + (sysconfig.get_config_var("EXT_SUFFIX") or ".so")
 
 
 CALL_LIB = os.path.join(LIBDIR, call_lib_name(torch_version()))

@@ -483,11 +483,12 @@ def _caller():
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pqcall", loader))
         module.bind(*(_c.cast(f, _vp).value for f in (lib.pq_quant_fp4, lib.pq_fp4_gemm, lib.pq_fp4_linear, lib.pq_kv4_attention_masked)))
     except ImportError as e:
+        _call = _NoModule
         warnings.warn(f"calls go through ctypes, some 5 us slower: {e}; python -m rotation_int4_w4a4_b200.build makes {path}",
                       RuntimeWarning, stacklevel=3)
-        module = _NoModule
-    _call = module
-    return module
+    else:
+        _call = module
+    return _call
 
 
 def _fp4_format(fmt):

@@ -81,3 +81,14 @@ def test_the_same_bits(pq, monkeypatch):
         assert bool(told) != module
         outs.append((*buffers, Y))
     assert all(torch.equal(a, b) for a, b in zip(*outs)) and outs[0][4].abs().sum() > 0
+
+
+def test_a_warning_that_is_an_error_stops_one_call_only(pq, monkeypatch):
+    names = reached(pq, monkeypatch)
+    X, c, s = fake(4, 256), fake(4, 128, dtype=torch.uint8), fake(4096, dtype=torch.uint8)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(RuntimeWarning):
+            pq.pq_quant_fp4(X, c, s)
+        pq.pq_quant_fp4(X, c, s)
+    assert names == ["pq_quant_fp4"]
